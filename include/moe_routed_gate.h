@@ -467,6 +467,137 @@ MOE_API moe_status_t moe_forward_w4a16(const void *x, const void *w_g, const flo
 MOE_API int64_t moe_forward_workspace_offset(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
                                      moe_dtype_t dtype, int index);
 
+/*
+ * Norms before and after a block, fused with its gate and residual scale.
+ * For every row t of H elements, in fp32, each output rounded once:
+ *   z   = w_post ? y * rstd(y) * w_post : y        (the block's own output norm)
+ *   out = y ? res + alpha * gate * z : res          (residual add)
+ *   u   = out * rstd(out) * w_next                  (the norm before the next block,
+ *                                                    of the unrounded out)
+ *   rstd(v) = 1 / sqrt(mean(v^2) + eps)
+ * y NULL: only u, the norm of res (w_post, gate, out and rstd_post must be
+ * NULL).  w_next NULL: no u (u and rstd_next must be NULL).  gate_kind says how
+ * gate is laid out: MOE_GATE_NONE (gate NULL, factor 1), MOE_GATE_CHANNEL [H],
+ * MOE_GATE_TOKEN [T], MOE_GATE_FULL [T, H].  rstd_post, rstd_next: fp32 [T] or
+ * NULL; a backward pass needs them.
+ * y, res, out, u [T, H] and the weights and gate in `dtype` (f16, bf16, f32);
+ * 1 <= H <= 16384, any T >= 0, eps >= 0.  `out` may be the same buffer as
+ * `res`; no other output may overlap an input.
+ */
+typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_t;
+MOE_API moe_status_t moe_residual_norm(const void *y, const void *res, const void *w_post, const void *gate,
+                                       moe_gate_t gate_kind, float alpha, const void *w_next, float eps,
+                                       int64_t T, int64_t H, moe_dtype_t dtype, void *out, void *u,
+                                       float *rstd_post, float *rstd_next, moe_stream_t stream);
+
+/*
+ * Gradients of moe_residual_norm.  d_out: gradient of `out` (NULL: zero); d_u:
+ * of `u`, given exactly when w_next is.  With v = d_u * w_next and r = rstd_next:
+ *   d      = d_out + r * v - out * r^3 / H * sum_h(v * out)
+ *   d_res  = d
+ *   d_gate = alpha * d * z summed over the axes gate was broadcast over
+ *   dz     = alpha * gate * d;  v2 = dz * w_post, r2 = rstd_post:
+ *   d_y    = w_post ? r2 * v2 - y * r2^3 / H * sum_h(v2 * y) : dz
+ *   d_w_post[h] = sum_t dz * y * r2;  d_w_next[h] = sum_t d_u * out * r
+ * in fp32; out is the stored (rounded) forward output, or res where the forward
+ * had no y.  `out` may be NULL when w_next is.  d_res, d_y [T, H] in `dtype`;
+ * d_gate fp32 [H] or [T], for MOE_GATE_FULL [T, H] in `dtype`; d_w_post,
+ * d_w_next fp32 [H].  d_gate, d_w_post, d_w_next may be NULL (not computed).
+ * Column sums are added in a fixed order: the same inputs give the same bits.
+ * For T = 0 the column sums are written as zeros.  d_res may be the same buffer
+ * as d_out.  ws: moe_residual_norm_backward_workspace_bytes(T, H) bytes, 16-byte
+ * aligned.
+ */
+MOE_API size_t moe_residual_norm_backward_workspace_bytes(int64_t T, int64_t H);
+MOE_API moe_status_t moe_residual_norm_backward(const void *d_out, const void *d_u, const void *y, const void *out,
+                                                const void *w_post, const void *gate, moe_gate_t gate_kind,
+                                                float alpha, const void *w_next, const float *rstd_post,
+                                                const float *rstd_next, int64_t T, int64_t H, moe_dtype_t dtype,
+                                                void *d_res, void *d_y, void *d_gate, float *d_w_post,
+                                                float *d_w_next, void *ws, size_t ws_bytes,
+                                                moe_stream_t stream);
+
+/*
+ * The whole routed-expert layer for a few tokens (1 <= T <= MOE_FEW_MAX_T, more
+ * is MOE_ERR_UNSUPPORTED): the results of moe_forward without its tables and
+ * 128-row tiles.  Routing as moe_gate_topk (the fixed summation order, ties to
+ * the lower id).  Every chosen expert's weights are read once for all its
+ * tokens; h = silu(G) * U, scaled by its routing weight, is kept as two values
+ * of `dtype` (the rounded value and the rest), the outputs are summed over the
+ * experts in fp32 and rounded once, so the result is closer to exact than
+ * moe_forward's, which rounds h and each expert's output.
+ * Arguments as moe_forward; d_h % 256 == 0, d_e % 64 == 0, k <= min(E, 32),
+ * E <= 1024.  ws: moe_forward_few_workspace_bytes(...) bytes, 256-byte aligned,
+ * needs no clearing.
+ */
+#define MOE_FEW_MAX_T 16
+MOE_API size_t moe_forward_few_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
+                                               moe_dtype_t dtype);
+MOE_API moe_status_t moe_forward_few(const void *x, const void *w_g, const float *bias, const void *w_gate,
+                                     const void *w_up, const void *w_down, int64_t T, int64_t d_h, int64_t d_e,
+                                     int64_t E, int64_t k, moe_dtype_t dtype, void *ws, size_t ws_bytes,
+                                     void *out, int32_t *err_flag, moe_stream_t stream);
+
+/*
+ * Microscaled 4-bit floating point ("mx4"): 32 consecutive elements of a row
+ * share a scale 2^(s - 127), s one byte (255: NaN), and each is a 4-bit e2m1
+ * number (sign; 0, 0.5, 1, 1.5, 2, 3, 4, 6).  A matrix [R, K], K % 32 == 0, is
+ * q [R, K/2] (element j in byte j/2, the even one in the low nibble) and
+ * sf [R, K/32].
+ *
+ * moe_quantize_mx4: row r of q, sf from row row_idx[r] of x [T, K] (row_idx
+ * NULL: row r, n_rows <= T), so that one call gathers and quantises the routed
+ * rows.  s = floor(log2(max |x|)) - 2 + 127 over the 32 (at least 0; 0 where
+ * all are zero), elements rounded to nearest even and limited to 6.  A block
+ * that holds a NaN or an infinity gets s = 255.  A row_idx entry outside [0, T)
+ * sets *err_flag = MOE_ERR_DEVICE_FLAG and its row is zeros.  x in f16, bf16 or f32.
+ * moe_dequantize_mx4: the values, rounded to `dtype` (bf16 and f32 hold all of
+ * them exactly).
+ *
+ * moe_grouped_gemm_mx4: C[r, :] = A_r B[g]^T for the rows r of expert g, over
+ * the dispatch tables as moe_grouped_down: q_a, sf_a [n_rows, K], q_b, sf_b
+ * [E, N, K], sums in fp32, C [n_rows, N] rounded once to `out_dtype` (f16, bf16,
+ * f32).  N >= 1, K % 32 == 0.
+ * moe_grouped_gate_up_silu_mx4: h = silu(A W_gate^T) * (A W_up^T) from the fp32
+ * sums, quantised as moe_quantize_mx4 would its fp32 values: q_h, sf_h
+ * [n_rows, d_e].  d_h % 32 == 0, d_e % 32 == 0.
+ * q_* 16-byte aligned.
+ */
+MOE_API moe_status_t moe_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T, int64_t K,
+                                      moe_dtype_t dtype, uint8_t *q, uint8_t *sf, int32_t *err_flag,
+                                      moe_stream_t stream);
+MOE_API moe_status_t moe_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K,
+                                        moe_dtype_t dtype, void *out, moe_stream_t stream);
+MOE_API moe_status_t moe_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b,
+                                          const uint8_t *sf_b, const int32_t *group_sizes,
+                                          const int32_t *group_offsets, const int32_t *group_padded_offsets,
+                                          const int32_t *group_idx_for_bx, int64_t m_blocks, int64_t n_rows,
+                                          int64_t N, int64_t K, int64_t E, moe_dtype_t out_dtype, void *C,
+                                          int32_t *err_flag, moe_stream_t stream);
+MOE_API moe_status_t moe_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
+                                                  const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                                  const int32_t *group_sizes, const int32_t *group_offsets,
+                                                  const int32_t *group_padded_offsets,
+                                                  const int32_t *group_idx_for_bx, int64_t m_blocks,
+                                                  int64_t n_rows, int64_t d_h, int64_t d_e, int64_t E,
+                                                  uint8_t *q_h, uint8_t *sf_h, int32_t *err_flag,
+                                                  moe_stream_t stream);
+
+/*
+ * moe_forward with mx4 experts and mx4 activations: moe_gate_topk and
+ * moe_build_dispatch on x in `dtype`, then moe_quantize_mx4 of the routed rows,
+ * moe_grouped_gate_up_silu_mx4, moe_grouped_gemm_mx4 (down, into `dtype`) and
+ * moe_reduce_fused.  d_h % 256 == 0, d_e % 64 == 0.  ws:
+ * moe_forward_mx4_workspace_bytes(...) bytes, 256-byte aligned.
+ */
+MOE_API size_t moe_forward_mx4_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
+                                               moe_dtype_t dtype);
+MOE_API moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float *bias, const uint8_t *q_gate,
+                                     const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                     const uint8_t *q_down, const uint8_t *sf_down, int64_t T, int64_t d_h,
+                                     int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype, void *ws,
+                                     size_t ws_bytes, void *out, int32_t *err_flag, moe_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -47,6 +47,7 @@ def lib():
                            "(python -c 'import __graft_entry__ as g; g.build()')")
     L = ctypes.CDLL(path)
     P, I64, SZ, I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    F = ctypes.c_float
     sigs = {
         "moe_status_string": (ctypes.c_char_p, [I]),
         "moe_num_m_blocks": (I64, [I64, I64, I64, I64]),
@@ -76,6 +77,17 @@ def lib():
         "moe_gemm_w4a8": (I, [P, P, I64, I64, I64, P, P, I64, P, P]),
         "moe_grouped_gemm_w4a8_workspace_bytes": (I64, [I64, I64, I64]),
         "moe_grouped_gemm_w4a8": (I, [P, P, I64, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, I64, P, P]),
+        "moe_residual_norm": (I, [P, P, P, P, I, F, P, F, I64, I64, I, P, P, P, P, P]),
+        "moe_residual_norm_backward_workspace_bytes": (SZ, [I64, I64]),
+        "moe_residual_norm_backward": (I, [P, P, P, P, P, P, I, F, P, P, P, I64, I64, I, P, P, P, P, P, P, SZ, P]),
+        "moe_forward_few_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
+        "moe_forward_few": (I, [P, P, P, P, P, P, I64, I64, I64, I64, I64, I, P, SZ, P, P, P]),
+        "moe_quantize_mx4": (I, [P, P, I64, I64, I64, I, P, P, P, P]),
+        "moe_dequantize_mx4": (I, [P, P, I64, I64, I, P, P]),
+        "moe_grouped_gemm_mx4": (I, [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, P, P, P]),
+        "moe_grouped_gate_up_silu_mx4": (I, [P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, P, P]),
+        "moe_forward_mx4_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
+        "moe_forward_mx4": (I, [P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, P, SZ, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -95,7 +107,11 @@ def exported_symbols():
             "moe_grouped_mlp", "moe_pack_int4_bytes", "moe_pack_int4_weights", "moe_grouped_mlp_w4a16",
             "moe_forward_w4a16", "moe_gemm_w4a8_workspace_bytes", "moe_gemm_w4a8",
             "moe_grouped_gemm_w4a8_workspace_bytes", "moe_grouped_gemm_w4a8", "moe_reduce_fused",
-            "moe_reduce_fused_scaled", "moe_forward"]
+            "moe_reduce_fused_scaled", "moe_forward",
+            "moe_residual_norm", "moe_residual_norm_backward_workspace_bytes", "moe_residual_norm_backward",
+            "moe_forward_few_workspace_bytes", "moe_forward_few", "moe_quantize_mx4", "moe_dequantize_mx4",
+            "moe_grouped_gemm_mx4", "moe_grouped_gate_up_silu_mx4", "moe_forward_mx4_workspace_bytes",
+            "moe_forward_mx4"]
 
 
 # --------------------------------------------------------------------------- helpers
@@ -701,6 +717,337 @@ def moe_forward(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=None, e
                                  _ptr(w_down), T, d_h, d_e, E, k, _dtype_code(x, "x"), _ptr(ws),
                                  ws.numel(), _ptr(out), _ptr(err), _stream(x.device)),
                "moe_forward")
+    return out
+
+
+# --------------------------------------------------------------------------- norms around a block
+
+GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
+
+
+def _gate_kind(gate, T, H, dtype):
+    """[H] per channel, [T, 1] per token, [T, H] per element, None for 1."""
+    if gate is None:
+        return GATE_NONE
+    _cuda(gate, "gate", dtype=dtype)
+    shape = tuple(gate.shape)
+    if shape == (H,):
+        return GATE_CHANNEL
+    if shape == (T, H):
+        return GATE_FULL
+    if shape == (T, 1):
+        return GATE_TOKEN
+    raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {shape}")
+
+
+def _like(t, ref, name):
+    _cuda(t, name, dtype=ref.dtype)
+    if t.shape != ref.shape or t.device != ref.device:
+        raise ValueError(f"{name} must be {tuple(ref.shape)} on {ref.device}, got {tuple(t.shape)} on {t.device}")
+    return t
+
+
+def _norm_weight(w, H, dtype, name):
+    if w is not None:
+        _cuda(w, name, dtype=dtype)
+        if tuple(w.shape) != (H,):
+            raise ValueError(f"{name} must be [{H}], got {tuple(w.shape)}")
+
+
+def _row_stat(t, T, name):
+    _cuda(t, name, dtype=torch.float32)
+    if tuple(t.shape) != (T,):
+        raise ValueError(f"{name} must be [{T}], got {tuple(t.shape)}")
+
+
+def moe_residual_norm(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next=None, eps: float = 1e-6,
+                      out=None, u=None):
+    """The norms after one block and before the next: with z = y, normalised and
+    weighted by w_post when that is given, out = res + alpha * gate * z and
+    u = out / rms(out) * w_next.  Returns a dict with ``out`` (unless y is None),
+    ``u`` and ``rstd_next`` (with w_next) and ``rstd_post`` (with w_post).
+    gate: [H], [T, 1], [T, H] or None; y None: u is the norm of res.  ``out``
+    may be ``res`` itself."""
+    _cuda(res, "res", ndim=2)
+    T, H = res.shape
+    dt, dev = res.dtype, res.device
+    if y is None and w_next is None:
+        raise ValueError("nothing to compute: give y, w_next or both")
+    if y is None and (w_post is not None or gate is not None or out is not None):
+        raise ValueError("w_post, gate and out need y")
+    if u is not None and w_next is None:
+        raise ValueError("u needs w_next")
+    if y is not None:
+        _like(y, res, "y")
+        out = torch.empty_like(res) if out is None else _like(out, res, "out")
+    _norm_weight(w_post, H, dt, "w_post")
+    _norm_weight(w_next, H, dt, "w_next")
+    kind = _gate_kind(gate, T, H, dt)
+    got = {}
+    if y is not None:
+        got["out"] = out
+    if w_next is not None:
+        got["u"] = u = torch.empty_like(res) if u is None else _like(u, res, "u")
+        got["rstd_next"] = torch.empty(T, dtype=torch.float32, device=dev)
+    if w_post is not None:
+        got["rstd_post"] = torch.empty(T, dtype=torch.float32, device=dev)
+    with torch.cuda.device(dev):
+        _check(lib().moe_residual_norm(_ptr(y), _ptr(res), _ptr(w_post), _ptr(gate), kind, alpha, _ptr(w_next), eps,
+                                       T, H, _dtype_code(res, "res"), _ptr(out), _ptr(u), _ptr(got.get("rstd_post")),
+                                       _ptr(got.get("rstd_next")), _stream(dev)), "moe_residual_norm")
+    return got
+
+
+def moe_residual_norm_backward(d_out, d_u, y, out, w_post=None, gate=None, alpha: float = 1.0, w_next=None,
+                               rstd_post=None, rstd_next=None, ws=None):
+    """Gradients of :func:`moe_residual_norm`.  ``out`` is its stored output (res
+    where it had no y), d_out or d_u may be None where nothing flows back there.
+    Returns a dict with ``d_res`` and, where they apply, ``d_y``, ``d_gate``
+    (fp32 [H] or [T, 1]; [T, H] in the activations' dtype), ``d_w_post`` and
+    ``d_w_next`` (fp32 [H])."""
+    ref = d_u if d_out is None else d_out
+    if ref is None:
+        raise ValueError("d_out or d_u is needed")
+    _cuda(ref, "d_out" if d_out is not None else "d_u", ndim=2)
+    T, H = ref.shape
+    dt, dev = ref.dtype, ref.device
+    for t, name in ((d_u, "d_u"), (y, "y"), (out, "out")):
+        if t is not None:
+            _like(t, ref, name)
+    if (d_u is None) != (w_next is None):
+        raise ValueError("d_u and w_next go together")
+    if w_next is not None and (out is None or rstd_next is None):
+        raise ValueError("w_next needs out and rstd_next")
+    if y is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need y")
+    if w_post is not None and rstd_post is None:
+        raise ValueError("w_post needs rstd_post")
+    _norm_weight(w_post, H, dt, "w_post")
+    _norm_weight(w_next, H, dt, "w_next")
+    if w_post is not None:
+        _row_stat(rstd_post, T, "rstd_post")
+    if w_next is not None:
+        _row_stat(rstd_next, T, "rstd_next")
+    kind = _gate_kind(gate, T, H, dt)
+    f32 = dict(dtype=torch.float32, device=dev)
+    got = {"d_res": torch.empty_like(ref)}
+    if y is not None:
+        got["d_y"] = torch.empty_like(ref)
+    if kind == GATE_FULL:
+        got["d_gate"] = torch.empty_like(ref)
+    elif kind != GATE_NONE:
+        got["d_gate"] = torch.empty(gate.shape, **f32)
+    if w_post is not None:
+        got["d_w_post"] = torch.empty(H, **f32)
+    if w_next is not None:
+        got["d_w_next"] = torch.empty(H, **f32)
+    if ws is None:
+        need = _ws_bytes(lib().moe_residual_norm_backward_workspace_bytes(T, H), "moe_residual_norm_backward")
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _cuda(ws, "ws", dtype=torch.uint8)
+    with torch.cuda.device(dev):
+        _check(lib().moe_residual_norm_backward(
+            _ptr(d_out), _ptr(d_u), _ptr(y), _ptr(out), _ptr(w_post), _ptr(gate), kind, alpha, _ptr(w_next),
+            _ptr(rstd_post), _ptr(rstd_next), T, H, _dtype_code(ref, "d_out"), _ptr(got["d_res"]), _ptr(got.get("d_y")),
+            _ptr(got.get("d_gate")), _ptr(got.get("d_w_post")), _ptr(got.get("d_w_next")), _ptr(ws), ws.numel(),
+            _stream(dev)), "moe_residual_norm_backward")
+    return got
+
+
+# --------------------------------------------------------------------------- a few tokens
+
+FEW_MAX_T = 16
+
+
+def _ws_bytes(n: int, what: str) -> int:
+    if n == ctypes.c_size_t(-1).value:
+        raise ValueError(f"{what}: unsupported sizes or dtype")
+    return n
+
+
+def forward_few_workspace_bytes(T, d_h, d_e, E, k, dtype) -> int:
+    return _ws_bytes(lib().moe_forward_few_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]), "moe_forward_few")
+
+
+def moe_forward_few(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=None, err=None):
+    """The routed layer for at most FEW_MAX_T tokens, as :func:`moe_forward`
+    (the same routing, less rounding); returns out [T, d_hidden]."""
+    _cuda(x, "x", ndim=2)
+    for n, t, nd in (("w_g", w_g, 2), ("w_gate", w_gate, 3), ("w_up", w_up, 3), ("w_down", w_down, 3)):
+        _cuda(t, n, dtype=x.dtype, ndim=nd)
+    T, d_h = x.shape
+    E, d_e, _ = w_gate.shape
+    if tuple(w_gate.shape) != (E, d_e, d_h) or w_up.shape != w_gate.shape:
+        raise ValueError("w_gate / w_up must be [E, d_expert, d_hidden]")
+    if tuple(w_down.shape) != (E, d_h, d_e) or tuple(w_g.shape) != (E, d_h):
+        raise ValueError("w_down must be [E, d_hidden, d_expert] and w_g [E, d_hidden]")
+    if bias is not None:
+        _cuda(bias, "bias", dtype=torch.float32, ndim=1)
+        if bias.numel() != E:
+            raise ValueError("bias must be [E]")
+    if ws is None:
+        ws = torch.empty(forward_few_workspace_bytes(T, d_h, d_e, E, k, x.dtype), dtype=torch.uint8, device=x.device)
+    _cuda(ws, "ws", dtype=torch.uint8)
+    out = torch.empty_like(x) if out is None else _like(out, x, "out")
+    if err is not None:
+        _cuda(err, "err", dtype=torch.int32)
+    with torch.cuda.device(x.device):
+        _check(lib().moe_forward_few(_ptr(x), _ptr(w_g), _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down), T, d_h,
+                                     d_e, E, k, _dtype_code(x, "x"), _ptr(ws), ws.numel(), _ptr(out), _ptr(err),
+                                     _stream(x.device)), "moe_forward_few")
+    return out
+
+
+# --------------------------------------------------------------------------- microscaled 4-bit floating point
+
+def _mx4(q, sf, name, lead):
+    """q [*lead, K / 2], sf [*lead, K / 32]: returns K."""
+    _cuda(q, f"q{name}", dtype=torch.uint8, ndim=len(lead) + 1)
+    _cuda(sf, f"sf{name}", dtype=torch.uint8, ndim=len(lead) + 1)
+    K = 2 * q.shape[-1]
+    if K % 32 != 0 or tuple(q.shape[:-1]) != tuple(lead) or tuple(sf.shape) != (*lead, K // 32):
+        raise ValueError(f"q{name} / sf{name} must be {(*lead, 'K / 2')} / {(*lead, 'K / 32')} with K % 32 == 0, "
+                         f"got {tuple(q.shape)} / {tuple(sf.shape)}")
+    return K
+
+
+def moe_quantize_mx4(x, row_idx=None, q=None, sf=None, err=None):
+    """Rows of x [T, K] (row_idx: those rows, in that order) as e2m1 elements
+    q uint8 [R, K / 2] with one scale byte per 32, sf uint8 [R, K / 32]."""
+    _cuda(x, "x", ndim=2)
+    T, K = x.shape
+    if K == 0 or K % 32 != 0:
+        raise ValueError("K must be a multiple of 32")
+    if row_idx is not None:
+        _cuda(row_idx, "row_idx", dtype=torch.int32, ndim=1)
+    R = T if row_idx is None else row_idx.numel()
+    u8 = dict(dtype=torch.uint8, device=x.device)
+    q = torch.empty((R, K // 2), **u8) if q is None else q
+    sf = torch.empty((R, K // 32), **u8) if sf is None else sf
+    _mx4(q, sf, "", (R,))
+    if err is not None:
+        _cuda(err, "err", dtype=torch.int32)
+    with torch.cuda.device(x.device):
+        _check(lib().moe_quantize_mx4(_ptr(x), _ptr(row_idx), R, T, K, _dtype_code(x, "x"), _ptr(q), _ptr(sf),
+                                      _ptr(err), _stream(x.device)), "moe_quantize_mx4")
+    return q, sf
+
+
+def moe_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None):
+    """The values of q [R, K / 2], sf [R, K / 32] as [R, K] in dtype."""
+    _cuda(q, "q", dtype=torch.uint8, ndim=2)
+    K = _mx4(q, sf, "", (q.shape[0],))
+    if out is None:
+        out = torch.empty((q.shape[0], K), dtype=dtype, device=q.device)
+    _cuda(out, "out", dtype=dtype, ndim=2)
+    if tuple(out.shape) != (q.shape[0], K):
+        raise ValueError(f"out must be {(q.shape[0], K)}, got {tuple(out.shape)}")
+    with torch.cuda.device(q.device):
+        _check(lib().moe_dequantize_mx4(_ptr(q), _ptr(sf), q.shape[0], K, _dtype_code(out, "out"), _ptr(out),
+                                        _stream(q.device)), "moe_dequantize_mx4")
+    return out
+
+
+def moe_grouped_gemm_mx4(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16, out=None, err=None):
+    """C[r] = A_r B[g]^T over the dispatch tables, both sides mx4: q_a, sf_a
+    [rows, .], q_b, sf_b [E, N, .]; returns C [rows, N] in out_dtype."""
+    _cuda(q_a, "q_a", dtype=torch.uint8, ndim=2)
+    _cuda(q_b, "q_b", dtype=torch.uint8, ndim=3)
+    rows, (E, N, _) = q_a.shape[0], q_b.shape
+    K = _mx4(q_a, sf_a, "_a", (rows,))
+    if _mx4(q_b, sf_b, "_b", (E, N)) != K:
+        raise ValueError("the two sides disagree on K")
+    s, o, p, g = _tables(tables)
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=q_a.device)
+    _cuda(out, "out", dtype=out_dtype)
+    if tuple(out.shape) != (rows, N):
+        raise ValueError(f"out must be [{rows}, {N}], got {tuple(out.shape)}")
+    if err is not None:
+        _cuda(err, "err", dtype=torch.int32)
+    with torch.cuda.device(q_a.device):
+        _check(lib().moe_grouped_gemm_mx4(_ptr(q_a), _ptr(sf_a), _ptr(q_b), _ptr(sf_b), _ptr(s), _ptr(o), _ptr(p),
+                                          _ptr(g), g.numel(), rows, N, K, E, _dtype_code(out, "out"), _ptr(out),
+                                          _ptr(err), _stream(q_a.device)), "moe_grouped_gemm_mx4")
+    return out
+
+
+class Mx4Experts:
+    """The three expert weights of a layer as mx4 elements and scales."""
+
+    def __init__(self, q_gate, sf_gate, q_up, sf_up, q_down, sf_down):
+        self.E, self.d_e, half = q_gate.shape
+        self.d_h = 2 * half
+        for q, sf, name, lead in ((q_gate, sf_gate, "_gate", (self.E, self.d_e)), (q_up, sf_up, "_up", (self.E, self.d_e)),
+                                  (q_down, sf_down, "_down", (self.E, self.d_h))):
+            if _mx4(q, sf, name, lead) != (self.d_e if name == "_down" else self.d_h):
+                raise ValueError("q_gate / q_up must be [E, d_e, d_h // 2] and q_down [E, d_h, d_e // 2]")
+        self.q_gate, self.sf_gate, self.q_up, self.sf_up = q_gate, sf_gate, q_up, sf_up
+        self.q_down, self.sf_down = q_down, sf_down
+
+    @classmethod
+    def from_weights(cls, w_gate, w_up, w_down):
+        """Quantise the layer's weights [E, N, K] on the GPU."""
+        parts = []
+        for w in (w_gate, w_up, w_down):
+            E, N, K = w.shape
+            q, sf = moe_quantize_mx4(w.reshape(E * N, K))
+            parts += [q.view(E, N, K // 2), sf.view(E, N, K // 32)]
+        return cls(*parts)
+
+
+def moe_grouped_gate_up_silu_mx4(q_a, sf_a, experts: "Mx4Experts", tables, q_h=None, sf_h=None, err=None):
+    """h = silu(A W_gate^T) * (A W_up^T) over the dispatch tables, quantised:
+    returns q_h [rows, d_e / 2], sf_h [rows, d_e / 32]."""
+    _cuda(q_a, "q_a", dtype=torch.uint8, ndim=2)
+    rows = q_a.shape[0]
+    if _mx4(q_a, sf_a, "_a", (rows,)) != experts.d_h:
+        raise ValueError("the rows and the experts disagree on d_hidden")
+    s, o, p, g = _tables(tables)
+    u8 = dict(dtype=torch.uint8, device=q_a.device)
+    q_h = torch.empty((rows, experts.d_e // 2), **u8) if q_h is None else q_h
+    sf_h = torch.empty((rows, experts.d_e // 32), **u8) if sf_h is None else sf_h
+    if _mx4(q_h, sf_h, "_h", (rows,)) != experts.d_e:
+        raise ValueError("q_h must be [rows, d_expert / 2]")
+    if err is not None:
+        _cuda(err, "err", dtype=torch.int32)
+    e = experts
+    with torch.cuda.device(q_a.device):
+        _check(lib().moe_grouped_gate_up_silu_mx4(
+            _ptr(q_a), _ptr(sf_a), _ptr(e.q_gate), _ptr(e.sf_gate), _ptr(e.q_up), _ptr(e.sf_up), _ptr(s), _ptr(o),
+            _ptr(p), _ptr(g), g.numel(), rows, e.d_h, e.d_e, e.E, _ptr(q_h), _ptr(sf_h), _ptr(err),
+            _stream(q_a.device)), "moe_grouped_gate_up_silu_mx4")
+    return q_h, sf_h
+
+
+def forward_mx4_workspace_bytes(T, d_h, d_e, E, k, dtype) -> int:
+    return _ws_bytes(lib().moe_forward_mx4_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]), "moe_forward_mx4")
+
+
+def moe_forward_mx4(x, w_g, bias, experts: "Mx4Experts", k: int, ws=None, out=None, err=None):
+    """The routed forward with mx4 experts and activations; returns out [T, d_hidden]."""
+    _cuda(x, "x", ndim=2)
+    _cuda(w_g, "w_g", dtype=x.dtype, ndim=2)
+    T, d_h = x.shape
+    e = experts
+    if d_h != e.d_h or tuple(w_g.shape) != (e.E, d_h):
+        raise ValueError("x, w_g and the experts disagree on d_hidden or the number of experts")
+    if bias is not None:
+        _cuda(bias, "bias", dtype=torch.float32, ndim=1)
+        if bias.numel() != e.E:
+            raise ValueError("bias must be [E]")
+    if ws is None:
+        ws = torch.empty(forward_mx4_workspace_bytes(T, d_h, e.d_e, e.E, k, x.dtype), dtype=torch.uint8,
+                         device=x.device)
+    _cuda(ws, "ws", dtype=torch.uint8)
+    out = torch.empty_like(x) if out is None else _like(out, x, "out")
+    if err is not None:
+        _cuda(err, "err", dtype=torch.int32)
+    with torch.cuda.device(x.device):
+        _check(lib().moe_forward_mx4(_ptr(x), _ptr(w_g), _ptr(bias), _ptr(e.q_gate), _ptr(e.sf_gate), _ptr(e.q_up),
+                                     _ptr(e.sf_up), _ptr(e.q_down), _ptr(e.sf_down), T, d_h, e.d_e, e.E, k,
+                                     _dtype_code(x, "x"), _ptr(ws), ws.numel(), _ptr(out), _ptr(err),
+                                     _stream(x.device)), "moe_forward_mx4")
     return out
 
 

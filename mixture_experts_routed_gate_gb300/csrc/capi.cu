@@ -5,6 +5,7 @@
 
 #include <atomic>
 #include <cstdlib>
+#include <initializer_list>
 
 #include "../../include/moe_routed_gate.h"
 #include "internal.h"
@@ -658,5 +659,251 @@ moe_status_t moe_forward_w4a16(const void *x, const void *w_g, const float *bias
                          stream, false, true);
 }
 
+
+// ---------------------------------------------------------------------------
+// norms before and after a block
+// ---------------------------------------------------------------------------
+static bool is_norm_type(moe_dtype_t d) { return d == MOE_F16 || d == MOE_BF16 || d == MOE_F32; }
+
+// nullptr is aligned: optional arguments pass
+static bool all_aligned16(std::initializer_list<const void *> ps) {
+    for (const void *p : ps)
+        if (!aligned16(p)) return false;
+    return true;
+}
+
+static moe_status_t check_norm(const void *y, const void *w_post, const void *gate, moe_gate_t gate_kind, float alpha,
+                               int64_t T, int64_t H, moe_dtype_t dtype) {
+    if (!is_norm_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (T < 0 || H < 1 || alpha != alpha) return MOE_ERR_INVALID_ARG;
+    if (H > 16384 || T > INT32_MAX) return MOE_ERR_UNSUPPORTED;
+    if (gate_kind < MOE_GATE_NONE || gate_kind > MOE_GATE_FULL) return MOE_ERR_INVALID_ARG;
+    if (gate_kind == MOE_GATE_NONE && gate) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;  // [0, H] tensors may be null
+    if (gate_kind != MOE_GATE_NONE && !gate) return MOE_ERR_INVALID_ARG;
+    if (!y && (w_post || gate)) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+moe_status_t moe_residual_norm(const void *y, const void *res, const void *w_post, const void *gate,
+                               moe_gate_t gate_kind, float alpha, const void *w_next, float eps, int64_t T, int64_t H,
+                               moe_dtype_t dtype, void *out, void *u, float *rstd_post, float *rstd_next,
+                               moe_stream_t stream) {
+    const moe_status_t st = check_norm(y, w_post, gate, gate_kind, alpha, T, H, dtype);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.0f)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!res || (y == nullptr) != (out == nullptr) || (w_next == nullptr) != (u == nullptr) || (!out && !u))
+        return MOE_ERR_INVALID_ARG;
+    if ((rstd_post && !w_post) || (rstd_next && !w_next)) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({y, res, w_post, gate, w_next, out, u})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_residual_norm(y, res, w_post, gate, gate_kind, alpha, w_next, eps, T, H, dtype, out,
+                                                 u, rstd_post, rstd_next, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_residual_norm_backward_workspace_bytes(int64_t T, int64_t H) {
+    if (T < 0 || H < 1 || H > 16384) return static_cast<size_t>(-1);
+    return moe::residual_norm_backward_ws_bytes(T, H);
+}
+
+moe_status_t moe_residual_norm_backward(const void *d_out, const void *d_u, const void *y, const void *out,
+                                        const void *w_post, const void *gate, moe_gate_t gate_kind, float alpha,
+                                        const void *w_next, const float *rstd_post, const float *rstd_next, int64_t T,
+                                        int64_t H, moe_dtype_t dtype, void *d_res, void *d_y, void *d_gate,
+                                        float *d_w_post, float *d_w_next, void *ws, size_t ws_bytes,
+                                        moe_stream_t stream) {
+    const moe_status_t st = check_norm(y, w_post, gate, gate_kind, alpha, T, H, dtype);
+    if (st != MOE_OK) return st;
+    if ((d_w_post && !w_post) || (d_w_next && !w_next) || (d_gate && gate_kind == MOE_GATE_NONE))
+        return MOE_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (d_y && !y) return MOE_ERR_INVALID_ARG;
+        if ((!d_out && !d_u) || !d_res || (y && !d_y)) return MOE_ERR_INVALID_ARG;
+        if ((w_next == nullptr) != (d_u == nullptr) || (w_next && (!out || !rstd_next))) return MOE_ERR_INVALID_ARG;
+        if (w_post && !rstd_post) return MOE_ERR_INVALID_ARG;
+        if (!all_aligned16({d_out, d_u, y, out, w_post, gate, w_next, d_res, d_y, d_gate})) return MOE_ERR_INVALID_ARG;
+    }
+    if (!ws || !aligned16(ws)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe_residual_norm_backward_workspace_bytes(T, H)) return MOE_ERR_WORKSPACE;
+    return cuda_status(moe::launch_residual_norm_backward(
+        d_out, d_u, y, out, w_post, gate, gate_kind, alpha, w_next, rstd_post, rstd_next, T, H, dtype, d_res, d_y,
+        d_gate, d_w_post, d_w_next, ws, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// the whole layer for a few tokens
+// ---------------------------------------------------------------------------
+size_t moe_forward_few_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype) {
+    if (T < 0 || T > MOE_FEW_MAX_T || d_h <= 0 || d_e <= 0 || E <= 0 || E > 1024 || k <= 0 || k > 32 ||
+        !is_half_type(dtype))
+        return static_cast<size_t>(-1);
+    return moe::forward_few_ws_bytes(T, d_h, d_e, E, k);
+}
+
+moe_status_t moe_forward_few(const void *x, const void *w_g, const float *bias, const void *w_gate, const void *w_up,
+                             const void *w_down, int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
+                             moe_dtype_t dtype, void *ws, size_t ws_bytes, void *out, int32_t *err_flag,
+                             moe_stream_t stream) {
+    if (!is_half_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || k > E || k > 32 || E > 1024) return MOE_ERR_INVALID_ARG;
+    if (d_h % 256 != 0 || d_e % 64 != 0) return MOE_ERR_INVALID_ARG;
+    if (T > MOE_FEW_MAX_T || d_h > (1 << 20) || d_e > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (T == 0) return MOE_OK;
+    if (!x || !w_g || !w_gate || !w_up || !w_down || !out || !ws) return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, w_g, w_gate, w_up, w_down, out})) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe_forward_few_workspace_bytes(T, d_h, d_e, E, k, dtype)) return MOE_ERR_WORKSPACE;
+    return cuda_status(moe::launch_forward_few(x, w_g, bias, w_gate, w_up, w_down, T, d_h, d_e, E, k, dtype, ws, out,
+                                               err_flag, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// microscaled 4-bit floating point
+// ---------------------------------------------------------------------------
+moe_status_t moe_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T, int64_t K,
+                              moe_dtype_t dtype, uint8_t *q, uint8_t *sf, int32_t *err_flag, moe_stream_t stream) {
+    if (!is_norm_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows < 0 || T < 0 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (!row_idx && n_rows > T) return MOE_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX || T > INT32_MAX || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    if ((T > 0 && !x) || !q || !sf || !all_aligned16({x, q})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_quantize_mx4(x, row_idx, n_rows, T, K, dtype, q, sf, err_flag,
+                                                reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K, moe_dtype_t dtype,
+                                void *out, moe_stream_t stream) {
+    if (!is_norm_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows < 0 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    if (!q || !sf || !out || !all_aligned16({q, out})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_dequantize_mx4(q, sf, n_rows, K, dtype, out,
+                                                  reinterpret_cast<cudaStream_t>(stream)));
+}
+
+static moe_status_t check_mx4_gemm(std::initializer_list<const void *> need, int64_t N, int64_t K) {
+    if (N < 1 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (N > (1 << 20) || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    for (const void *p : need)
+        if (!p) return MOE_ERR_INVALID_ARG;
+    return MOE_OK;
+}
+
+moe_status_t moe_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
+                                  const int32_t *group_sizes, const int32_t *group_offsets,
+                                  const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx,
+                                  int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K, int64_t E,
+                                  moe_dtype_t out_dtype, void *C, int32_t *err_flag, moe_stream_t stream) {
+    if (!is_norm_type(out_dtype)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
+                                        n_rows, E);
+    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_b, sf_b, C}, N, K);
+    if (st != MOE_OK) return st;
+    if (!all_aligned16({q_a, q_b, C})) return MOE_ERR_INVALID_ARG;
+    const moe::Mx4Tables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
+    return cuda_status(moe::launch_grouped_gemm_mx4(q_a, sf_a, q_b, sf_b, tab, m_blocks, n_rows, N, K, E, out_dtype, C,
+                                                    err_flag, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
+                                          const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                          const int32_t *group_sizes, const int32_t *group_offsets,
+                                          const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx,
+                                          int64_t m_blocks, int64_t n_rows, int64_t d_h, int64_t d_e, int64_t E,
+                                          uint8_t *q_h, uint8_t *sf_h, int32_t *err_flag, moe_stream_t stream) {
+    if (n_rows == 0) return MOE_OK;
+    moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
+                                        n_rows, E);
+    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h);
+    if (st != MOE_OK) return st;
+    if (d_e % 32 != 0 || !all_aligned16({q_a, q_gate, q_up, q_h})) return MOE_ERR_INVALID_ARG;
+    const moe::Mx4Tables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
+    return cuda_status(moe::launch_grouped_gate_up_silu_mx4(q_a, sf_a, q_gate, sf_gate, q_up, sf_up, tab, m_blocks,
+                                                            n_rows, d_h, d_e, E, q_h, sf_h, err_flag,
+                                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// the 16-bit forward's routing sections, then the 4-bit rows, h and y
+struct Mx4Layout {
+    size_t logits, idx, w, sizes, offsets, padded, gidx, stok, sw, pos, scratch, qa, sa, qh, sh, y, total;
+};
+
+static bool mx4_layout(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype, Mx4Layout *L) {
+    if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || !is_half_type(dtype)) return false;
+    const size_t Tk = static_cast<size_t>(T * k), e4 = static_cast<size_t>(E) * 4;
+    size_t cur = 0;
+    auto take = [&cur](size_t bytes) {
+        const size_t off = cur;
+        cur += align_up(bytes > 0 ? bytes : 1);
+        return off;
+    };
+    L->logits = take(moe_gate_topk_workspace_bytes(T, E));
+    L->idx = take(Tk * 4);
+    L->w = take(Tk * 4);
+    L->sizes = take(e4);
+    L->offsets = take(e4);
+    L->padded = take(e4);
+    L->gidx = take(static_cast<size_t>(m_blocks_of(T, k, E, MOE_BLOCK_M)) * 4);
+    L->stok = take(Tk * 4);
+    L->sw = take(Tk * 4);
+    L->pos = take(Tk * 4);
+    L->scratch = take(moe::dispatch_scratch_bytes(static_cast<int64_t>(Tk), E));
+    L->qa = take(Tk * static_cast<size_t>(d_h / 2));
+    L->sa = take(Tk * static_cast<size_t>(d_h / 32));
+    L->qh = take(Tk * static_cast<size_t>(d_e / 2));
+    L->sh = take(Tk * static_cast<size_t>(d_e / 32));
+    L->y = take(Tk * static_cast<size_t>(d_h) * 2);
+    L->total = cur;
+    return true;
+}
+
+size_t moe_forward_mx4_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype) {
+    Mx4Layout L;
+    return mx4_layout(T, d_h, d_e, E, k, dtype, &L) ? L.total : static_cast<size_t>(-1);
+}
+
+moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float *bias, const uint8_t *q_gate,
+                             const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up, const uint8_t *q_down,
+                             const uint8_t *sf_down, int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
+                             moe_dtype_t dtype, void *ws, size_t ws_bytes, void *out, int32_t *err_flag,
+                             moe_stream_t stream) {
+    if (!is_half_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || k > E || k > 32 || E > 1024) return MOE_ERR_INVALID_ARG;
+    if (d_h % 256 != 0 || d_e % 64 != 0) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!x || !w_g || !q_gate || !sf_gate || !q_up || !sf_up || !q_down || !sf_down || !out || !ws)
+        return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, w_g, q_gate, q_up, q_down, out})) return MOE_ERR_INVALID_ARG;
+    Mx4Layout L;
+    if (!mx4_layout(T, d_h, d_e, E, k, dtype, &L)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    char *w = static_cast<char *>(ws);
+    auto i32 = [w](size_t off) { return reinterpret_cast<int32_t *>(w + off); };
+    auto u8 = [w](size_t off) { return reinterpret_cast<uint8_t *>(w + off); };
+    float *topk_w = reinterpret_cast<float *>(w + L.w);
+    int32_t *sizes = i32(L.sizes), *offsets = i32(L.offsets), *padded = i32(L.padded), *gidx = i32(L.gidx);
+    const int64_t Tk = T * k, mb = m_blocks_of(T, k, E, MOE_BLOCK_M);
+    moe_status_t st = gate_topk(x, w_g, bias, T, d_h, E, k, dtype, i32(L.idx), topk_w, w + L.logits,
+                                moe_gate_topk_workspace_bytes(T, E), err_flag, stream);
+    if (st != MOE_OK) return st;
+    st = build_dispatch(i32(L.idx), topk_w, T, k, E, MOE_BLOCK_M, sizes, offsets, padded, gidx, i32(L.stok),
+                        reinterpret_cast<float *>(w + L.sw), i32(L.pos), w + L.scratch,
+                        moe::dispatch_scratch_bytes(Tk, E), nullptr, stream);
+    if (st != MOE_OK) return st;
+    st = moe_quantize_mx4(x, i32(L.stok), Tk, T, d_h, dtype, u8(L.qa), u8(L.sa), err_flag, stream);
+    if (st != MOE_OK) return st;
+    st = moe_grouped_gate_up_silu_mx4(u8(L.qa), u8(L.sa), q_gate, sf_gate, q_up, sf_up, sizes, offsets, padded, gidx,
+                                      mb, Tk, d_h, d_e, E, u8(L.qh), u8(L.sh), err_flag, stream);
+    if (st != MOE_OK) return st;
+    st = moe_grouped_gemm_mx4(u8(L.qh), u8(L.sh), q_down, sf_down, sizes, offsets, padded, gidx, mb, Tk, d_h, d_e, E,
+                              dtype, w + L.y, err_flag, stream);
+    if (st != MOE_OK) return st;
+    return reduce_common(w + L.y, Tk, i32(L.pos), topk_w, nullptr, nullptr, T, k, d_h, dtype, dtype, out, err_flag,
+                         stream, false);
+}
 
 }  // extern "C"

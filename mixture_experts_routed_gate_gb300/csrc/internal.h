@@ -161,4 +161,39 @@ cudaError_t launch_gemm_w4a8(const int8_t *x, const int32_t *gather_idx, int64_t
                              int64_t ld_row, int64_t ld_col, int64_t out_elems, int32_t *err,
                              cudaStream_t stream);
 
+// norm.cu: out = res + alpha * gate * norm(y), u = norm(out), and the
+// gradients (gate_kind as moe_gate_t; absent parts are null)
+cudaError_t launch_residual_norm(const void *y, const void *res, const void *w_post, const void *gate, int gate_kind,
+                                 float alpha, const void *w_next, float eps, int64_t T, int64_t H, int dtype,
+                                 void *out, void *u, float *rstd_post, float *rstd_next, cudaStream_t stream);
+size_t residual_norm_backward_ws_bytes(int64_t T, int64_t H);
+cudaError_t launch_residual_norm_backward(const void *d_out, const void *d_u, const void *y, const void *out,
+                                          const void *w_post, const void *gate, int gate_kind, float alpha,
+                                          const void *w_next, const float *rstd_post, const float *rstd_next,
+                                          int64_t T, int64_t H, int dtype, void *d_res, void *d_y, void *d_gate,
+                                          float *d_w_post, float *d_w_next, void *ws, cudaStream_t stream);
+
+// few_tokens.cu: the whole layer for T <= 16 tokens
+size_t forward_few_ws_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k);
+cudaError_t launch_forward_few(const void *x, const void *w_g, const float *bias, const void *w_gate, const void *w_up,
+                               const void *w_down, int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
+                               int dtype, void *ws, void *out, int32_t *err, cudaStream_t stream);
+
+// mx4.cu: 4-bit rows with a power-of-two scale per 32 elements
+struct Mx4Tables {
+    const int32_t *sizes, *offsets, *padded, *gidx;
+};
+cudaError_t launch_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T, int64_t K,
+                                int dtype, uint8_t *q, uint8_t *sf, int32_t *err, cudaStream_t stream);
+cudaError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K, int dtype, void *out,
+                                  cudaStream_t stream);
+cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
+                                    const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
+                                    int64_t E, int out_dtype, void *C, int32_t *err, cudaStream_t stream);
+cudaError_t launch_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
+                                            const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                            const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t d_h,
+                                            int64_t d_e, int64_t E, uint8_t *q_h, uint8_t *sf_h, int32_t *err,
+                                            cudaStream_t stream);
+
 }  // namespace moe
