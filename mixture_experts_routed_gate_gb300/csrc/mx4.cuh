@@ -1,0 +1,56 @@
+// mx4.cuh -- the arithmetic of the 4-bit block-scaled format, shared by the
+// quantiser and the grouped product.
+#pragma once
+
+#include "common.cuh"
+#include "internal.h"
+
+namespace moe {
+
+constexpr int MX_BLOCK = 32;
+
+// the scale byte of a block whose largest magnitude is `top`: floor(log2) is
+// in the exponent field; 255 for a NaN or an infinity
+__device__ __forceinline__ uint32_t mx4_scale(float top) {
+    const int field = static_cast<int>(__float_as_uint(top) >> 23) & 255;
+    if (field == 255) return 255u;
+    return static_cast<uint32_t>(max(field - 2, 0));
+}
+
+// 2^(127 - byte) for byte <= 252, exact
+__device__ __forceinline__ float mx4_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// 2^(byte - 127); byte 255 is NaN
+__device__ __forceinline__ float mx4_factor(uint32_t byte) {
+    if (byte == 255u) return __uint_as_float(0x7fc00000u);
+    return __uint_as_float(byte ? byte << 23 : 1u << 22);
+}
+
+// two elements to a byte, `lo` in the low nibble: nearest even, limited to 6
+__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ float e2m1_value(uint32_t code) {
+    const uint32_t m = code & 7u;
+    const float v = m < 4u ? 0.5f * m : (m < 6u ? m - 2.0f : 2.0f * m - 8.0f);
+    return (code & 8u) ? -v : v;
+}
+
+struct Mx4Block {
+    int g, m_start, rows;
+};
+
+// rows of M block bx of the dispatch tables: expert, first row, count
+__device__ __forceinline__ Mx4Block mx4_block_of(const Mx4Tables &t, int bx) {
+    Mx4Block b;
+    b.g = t.gidx[bx];
+    const int off = bx * 128 - t.padded[b.g];
+    b.m_start = off + t.offsets[b.g];
+    b.rows = max(0, min(t.sizes[b.g] - off, 128));
+    return b;
+}
+
+}  // namespace moe

@@ -1,0 +1,594 @@
+// mx4_gemm.cu -- the grouped product of 4-bit rows with 4-bit expert weights
+// on the block-scaled tensor cores (tcgen05.mma kind::mxf4):
+//
+//   C[r, n] = sum over k of (qa 2^sa)[r, k] * (qb 2^sb)[expert of r][n, k]
+//
+// and the gate/up form, h = silu(A Wg^T) * (A Wu^T), whose epilogue quantises
+// h (a thread holds 32 consecutive features of a row: one scale block).
+//
+// A persistent CTA works on tiles of 128 rows of a dispatch block by BN
+// columns.  Roles:
+//   warp 0      TMA: 128-byte (256-element) slices of the rows and the weights
+//               into a ring of 128-byte-swizzled stages;
+//   warps 6-9   scales: each thread loads its row's 8 scale bytes of a slice
+//               (several slices ahead) and stores them in the order that
+//               tcgen05.cp takes to tensor memory;
+//   warp 1      one thread: scales to tensor memory, then four K = 64 MMAs a slice;
+//   warps 2-5   epilogue, from one of two accumulators while the other fills.
+#include "common.cuh"
+#include "internal.h"
+#include "mx4.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int MG_BM = 128;
+constexpr int MG_SLICE = 256;       // elements of K per stage: 128 bytes of a row
+constexpr int MG_A_BYTES = MG_BM * 128;
+constexpr int MG_THREADS = 320;
+constexpr int MG_EPI_WARP0 = 2, MG_SF_WARP0 = 6;
+constexpr int MG_AHEAD = 4;         // slices of scales in registers ahead of the ring
+constexpr int MG_LIST = 2048;       // M blocks the shared-memory list holds
+constexpr int MG_FEW_ROWS = 32;     // a block of at most so many rows loads a short box
+
+template <int BN> struct MgLayout {
+    static constexpr int B_BYTES = BN * 128;
+    static constexpr int SF_HALVES = (BN + 127) / 128;          // 128-row groups of B's scales
+    static constexpr int SF_BYTES = 2 * (1 + SF_HALVES) * 512;  // two 128-element groups of K
+    static constexpr int STAGE = MG_A_BYTES + B_BYTES + SF_BYTES;
+    static constexpr int LIST_BYTES = MG_LIST * 12;
+    static constexpr int STAGES = (232448 - 2048 - LIST_BYTES) / STAGE;
+    static constexpr int SMEM = 1024 + STAGES * STAGE + 512 + LIST_BYTES;
+    static constexpr int SF_COLS = 2 * 4 * (1 + SF_HALVES);     // tensor-memory columns of a slice's scales
+    static constexpr int SF_COL0 = 2 * BN;                      // after the two accumulators
+    static_assert(SF_COL0 + 2 * SF_COLS <= 512, "tensor memory");
+    static_assert(STAGE % 1024 == 0, "swizzle atoms");
+    static_assert(SMEM <= 232448 && STAGES >= 3, "shared memory");
+};
+
+struct MgParams {
+    const uint8_t *sf_a, *sf_b0, *sf_b1;  // b1: the up weights of the gate/up form
+    Mx4Tables tab;
+    void *out;
+    uint8_t *q_h, *sf_h;
+    int32_t *err;
+    int m_blocks, n_tiles, slices;
+    int64_t n_rows, N, K;
+};
+
+struct MgTile {
+    int g, m_start, rows, n0;
+};
+
+// kind::mxf4: e2m1 by e2m1, e8m0 scales; the scale id (0 or 2: which two of a
+// cell's four bytes) is added per MMA.
+//   bits 4-5 B scale id; 7-9 A format, 10-12 B format (1 = e2m1); 17-22 N >> 3;
+//   23 scale type (1 = e8m0); 24-28 M >> 4; 29-30 A scale id; 31 K (0 = 64)
+__host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N) {
+    return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24);
+}
+
+__device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                            uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// 512 bytes of scales (32 rows of 16) to four columns, in each of the four
+// 32-lane quarters of tensor memory
+__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+// no swizzle: 8-row groups of 16-byte rows, 128 bytes apart
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
+           (static_cast<uint64_t>(1) << 46);
+}
+
+__device__ __forceinline__ void mg_drain(uint32_t bar, uint32_t parity) {
+    const unsigned long long start = global_timer_ns();
+    while (!mbar_try_wait(bar, parity))
+        if (global_timer_ns() - start > kWaitTimeoutNs) return;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+
+// The 8 scale bytes of row `row` of a [rows, kb] byte matrix from byte b0 on;
+// bytes past kb are 0 (their elements are zeros too).  V: the load width that
+// kb and the base's alignment allow.
+template <int V> __device__ __forceinline__ uint2 load_scales(const uint8_t *base, int64_t row, int kb, int b0) {
+    const uint8_t *p = base + row * kb + b0;
+    uint2 v = make_uint2(0u, 0u);
+    if constexpr (V == 8) {
+        v = __ldg(reinterpret_cast<const uint2 *>(p));
+    } else if constexpr (V == 4) {
+        v.x = __ldg(reinterpret_cast<const uint32_t *>(p));
+        if (b0 + 4 < kb) v.y = __ldg(reinterpret_cast<const uint32_t *>(p + 4));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (b0 + i < kb) v.x |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
+            if (b0 + 4 + i < kb) v.y |= static_cast<uint32_t>(__ldg(p + 4 + i)) << (8 * i);
+        }
+    }
+    return v;
+}
+
+template <typename TOut, int CNT>
+__device__ __forceinline__ void store_row(TOut *dst, const uint32_t (&r)[CNT], int64_t left, bool wide) {
+    // `wide`: the row's start is 16-byte aligned
+    if (wide && left >= CNT) {
+        if constexpr (sizeof(TOut) == 4) {
+#pragma unroll
+            for (int i = 0; i < CNT / 4; ++i)
+                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+        } else {
+            constexpr int DT = std::is_same<TOut, __half>::value ? kF16 : kBF16;
+#pragma unroll
+            for (int i = 0; i < CNT / 8; ++i) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = pack2<DT>(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]));
+                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < CNT; ++i)
+            if (i < left) dst[i] = from_f32<TOut>(__uint_as_float(r[i]));
+    }
+}
+
+template <typename TOut, bool GATE_UP, int BN, int V>
+__global__ void __launch_bounds__(MG_THREADS, 1)
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA_few,
+                    const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                    const MgParams p) {
+    using L = MgLayout<BN>;
+    constexpr int OUT_N = GATE_UP ? BN / 2 : BN;  // output columns of a tile
+    extern __shared__ uint8_t mg_smem_raw[];
+    uint8_t *smem = mg_smem_raw + ((1024u - (smem_u32(mg_smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::STAGES * L::STAGE);
+    int *list_g = reinterpret_cast<int *>(smem + L::STAGES * L::STAGE + 512);
+    int *list_m = list_g + MG_LIST, *list_rows = list_m + MG_LIST;
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, n_listed;
+    volatile int *abort_flag = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (L::STAGES + i); };
+    auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * L::STAGES + i); };
+    auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * L::STAGES + 2 + i); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < L::STAGES; ++i) {
+            mbar_init(full_bar(i), 1 + 4);  // the copies' thread and the scale warps
+            mbar_init(empty_bar(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull_bar(i), 1);
+            mbar_init(tempty_bar(i), 4);
+        }
+        abort_word = 0;
+        n_listed = -1;
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(&tmem_slot), 512);
+        tmem_relinquish();
+    }
+    if (warp == 0 && lane == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB0);
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // the blocks that hold rows, in order, when they fit the list
+    if (warp == 2 && p.m_blocks <= MG_LIST) {
+        int n = 0;
+        for (int b0 = 0; b0 < p.m_blocks; b0 += 32) {
+            const int bx = b0 + lane;
+            const Mx4Block b = bx < p.m_blocks ? mx4_block_of(p.tab, bx) : Mx4Block{0, 0, 0};
+            const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
+            if (b.rows > 0) {
+                const int at = n + __popc(has & ((1u << lane) - 1u));
+                list_g[at] = b.g;
+                list_m[at] = b.m_start;
+                list_rows[at] = b.rows;
+            }
+            n += __popc(has);
+        }
+        if (lane == 0) n_listed = n;
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    const int listed = n_listed;
+    const int64_t total = static_cast<int64_t>(listed >= 0 ? listed : p.m_blocks) * p.n_tiles;
+    auto tile_at = [&](int64_t t) {
+        const int b = static_cast<int>(t / p.n_tiles);
+        MgTile ti;
+        ti.n0 = static_cast<int>(t - static_cast<int64_t>(b) * p.n_tiles) * OUT_N;
+        if (listed >= 0) {
+            ti.g = list_g[b];
+            ti.m_start = list_m[b];
+            ti.rows = list_rows[b];
+        } else {
+            const Mx4Block k = mx4_block_of(p.tab, b);
+            ti.g = k.g;
+            ti.m_start = k.m_start;
+            ti.rows = k.rows;
+        }
+        return ti;
+    };
+
+    if (warp == 0) {
+        // -------------------------------- copies --------------------------------
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
+            int stage = 0;
+            uint32_t phase = 0;
+            long issued = 0;
+            bool ok = true;
+            for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const MgTile ti = tile_at(t);
+                if (ti.rows == 0) continue;
+                const bool few = ti.rows <= MG_FEW_ROWS;
+                // one row block: its weights are read once
+                const uint64_t pol_b = few ? pass : keep;
+                for (int s = 0; s < p.slices; ++s) {
+                    if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a = smem_u32(smem + stage * L::STAGE), b = a + MG_A_BYTES, fb = full_bar(stage);
+                    mbar_arrive_expect_tx(fb, (few ? MG_FEW_ROWS * 128 : MG_A_BYTES) + L::B_BYTES);
+                    tma_load_2d_hint(a, few ? &tmA_few : &tmA, fb, s * 128, ti.m_start, keep);
+                    if (GATE_UP) {
+                        tma_load_3d_hint(b, &tmB0, fb, s * 128, ti.n0, ti.g, pol_b);
+                        tma_load_3d_hint(b + L::B_BYTES / 2, &tmB1, fb, s * 128, ti.n0, ti.g, pol_b);
+                    } else {
+                        tma_load_3d_hint(b, &tmB0, fb, s * 128, ti.n0, ti.g, pol_b);
+                    }
+                    ++issued;
+                    if (++stage == L::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (!ok || *abort_flag) {
+                // copies in flight land before shared memory goes away (a
+                // stage whose scales never came stays incomplete: bounded)
+                for (long j = 1; j <= L::STAGES && j <= issued; ++j) {
+                    const long i = issued - j;
+                    mg_drain(full_bar(static_cast<int>(i % L::STAGES)), static_cast<uint32_t>((i / L::STAGES) & 1));
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        if (lane == 0) {
+            constexpr uint32_t IDESC = idesc_mxf4(MG_BM, BN);
+            int stage = 0, local = 0, buf = 0;
+            uint32_t phase = 0, last_bar = 0, last_parity = 0;
+            bool ok = true, committed = false;
+            for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+                const MgTile ti = tile_at(t);
+                if (ti.rows == 0) continue;
+                const int acc = local & 1;
+                if (!mbar_wait_bounded(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag, p.err)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+                for (int s = 0; s < p.slices; ++s) {
+                    if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t a = smem_u32(smem + stage * L::STAGE), sf = a + MG_A_BYTES + L::B_BYTES;
+                    const uint64_t a_desc = smem_desc_sw128(a), b_desc = smem_desc_sw128(a + MG_A_BYTES);
+                    const uint32_t sfa = tmem + L::SF_COL0 + buf * L::SF_COLS, sfb = sfa + 8u;
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        tc_cp_scales(sfa + 4u * j, smem_desc_scales(sf + 512u * j));
+#pragma unroll
+                        for (int h = 0; h < L::SF_HALVES; ++h)
+                            tc_cp_scales(sfb + 4u * (j * L::SF_HALVES + h),
+                                         smem_desc_scales(sf + 1024u + 512u * (j * L::SF_HALVES + h)));
+                    }
+                    const int64_t left = p.K - static_cast<int64_t>(s) * MG_SLICE;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k * 64 >= left) break;
+                        const uint32_t id = (k & 1) * 2u;
+                        tc_mma_mxf4(d, a_desc + 2u * k, b_desc + 2u * k, IDESC | (id << 29) | (id << 4),
+                                    sfa + 4u * (k >> 1), sfb + 4u * L::SF_HALVES * (k >> 1), (s | k) != 0 ? 1u : 0u);
+                    }
+                    tc_commit(empty_bar(stage));
+                    last_bar = empty_bar(stage);
+                    last_parity = phase;
+                    committed = true;
+                    buf ^= 1;
+                    if (++stage == L::STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+                if (!ok) break;
+                tc_commit(tfull_bar(acc));
+                ++local;
+            }
+            if (!ok && committed) mg_drain(last_bar, last_parity);
+        }
+    } else if (warp >= MG_SF_WARP0) {
+        // -------------------------------- scales --------------------------------
+        const int r = threadIdx.x - MG_SF_WARP0 * 32;
+        const int kb = static_cast<int>(p.K / 32);
+        const uint32_t cell = (r & 31) * 16u + (r >> 5) * 4u;  // of row r within 512 bytes
+        uint2 va[MG_AHEAD], vb[MG_AHEAD][L::SF_HALVES];
+        int64_t lt = blockIdx.x;  // next slice to load: tile, slice
+        int ls = 0;
+        MgTile li{0, 0, 0, 0};
+        auto next_tile = [&]() {
+            for (; lt < total; lt += gridDim.x) {
+                li = tile_at(lt);
+                if (li.rows > 0) return;
+            }
+        };
+        next_tile();
+        auto load = [&](uint2 &a, uint2(&b)[L::SF_HALVES]) {
+            const int64_t row = static_cast<int64_t>(li.m_start) + r;
+            a = r < li.rows ? load_scales<V>(p.sf_a, row, kb, ls * 8) : make_uint2(0u, 0u);
+#pragma unroll
+            for (int h = 0; h < L::SF_HALVES; ++h) {
+                const int n = h * 128 + r;  // row of the stage's B box
+                b[h] = make_uint2(0u, 0u);
+                if (GATE_UP) {
+                    const int f = li.n0 + (n < OUT_N ? n : n - OUT_N);
+                    if (n < BN && f < p.N)
+                        b[h] = load_scales<V>(n < OUT_N ? p.sf_b0 : p.sf_b1, static_cast<int64_t>(li.g) * p.N + f, kb, ls * 8);
+                } else if (n < BN && li.n0 + n < p.N) {
+                    b[h] = load_scales<V>(p.sf_b0, static_cast<int64_t>(li.g) * p.N + li.n0 + n, kb, ls * 8);
+                }
+            }
+            if (++ls == p.slices) {
+                ls = 0;
+                lt += gridDim.x;
+                next_tile();
+            }
+        };
+        int ahead = 0;  // slices in registers
+#pragma unroll
+        for (int j = 0; j < MG_AHEAD; ++j)
+            if (lt < total) {
+                load(va[j], vb[j]);
+                ++ahead;
+            }
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && ahead > 0) {
+#pragma unroll
+            for (int j = 0; j < MG_AHEAD; ++j) {
+                if (!ok || ahead == 0) continue;
+                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+                    ok = false;
+                    continue;
+                }
+                uint8_t *sf = smem + stage * L::STAGE + MG_A_BYTES + L::B_BYTES;
+                *reinterpret_cast<uint32_t *>(sf + cell) = va[j].x;
+                *reinterpret_cast<uint32_t *>(sf + 512 + cell) = va[j].y;
+#pragma unroll
+                for (int h = 0; h < L::SF_HALVES; ++h) {
+                    *reinterpret_cast<uint32_t *>(sf + 1024 + h * 512 + cell) = vb[j][h].x;
+                    *reinterpret_cast<uint32_t *>(sf + 1024 + (L::SF_HALVES + h) * 512 + cell) = vb[j][h].y;
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full_bar(stage));
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+                --ahead;
+                if (lt < total) {
+                    load(va[j], vb[j]);
+                    ++ahead;
+                }
+            }
+        }
+    } else {
+        // ------------------------------- epilogue -------------------------------
+        const int q = warp & 3;  // the lane quarter this warp may read
+        const int row = q * 32 + lane;
+        int local = 0;
+        for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
+            const MgTile ti = tile_at(t);
+            if (ti.rows == 0) continue;
+            const int acc = local & 1;
+            int ready = 1;
+            if (lane == 0) ready = mbar_wait_bounded(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err) ? 1 : 0;
+            ready = __shfl_sync(0xffffffffu, ready, 0);
+            if (!ready) break;
+            tc_fence_after();
+            const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * BN);
+            const int64_t r = static_cast<int64_t>(ti.m_start) + row;
+            const bool valid = row < ti.rows;
+            if (q * 32 < ti.rows) {
+#pragma unroll 1
+                for (int c = 0; c < OUT_N; c += 32) {
+                    const int64_t n = ti.n0 + c;
+                    if (n >= p.N) break;
+                    uint32_t v[32];
+                    tmem_ld32(d + c, v);
+                    if constexpr (GATE_UP) {
+                        uint32_t u[32];
+                        tmem_ld32(d + OUT_N + c, u);
+                        tmem_ld_wait();
+                        float top = 0.0f;
+                        bool odd = false;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float g = __uint_as_float(v[i]);
+                            const float h = __fdividef(g, 1.0f + __expf(-g)) * __uint_as_float(u[i]);
+                            odd |= !(fabsf(h) < INFINITY);
+                            top = fmaxf(top, fabsf(h));
+                            v[i] = __float_as_uint(h);
+                        }
+                        const uint32_t s = odd ? 255u : mx4_scale(top);
+                        const float inv = odd ? 0.0f : mx4_inverse(s);
+                        uint32_t w[4] = {0u, 0u, 0u, 0u};
+                        if (!odd) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                w[i >> 2] |= e2m1x2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv)
+                                             << (8 * (i & 3));
+                        }
+                        if (valid) {
+                            const int64_t o = r * (p.N / 32) + n / 32;
+                            *reinterpret_cast<uint4 *>(p.q_h + o * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                            p.sf_h[o] = static_cast<uint8_t>(s);
+                        }
+                    } else {
+                        tmem_ld_wait();
+                        if (valid) {
+                            constexpr int per16 = 16 / sizeof(TOut);
+                            store_row(static_cast<TOut *>(p.out) + r * p.N + n, v, p.N - n, p.N % per16 == 0);
+                        }
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(acc));
+            ++local;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+bool rows_map(CUtensorMap *m, const uint8_t *q, int64_t K, int64_t rows, uint32_t box_rows) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(K / 2), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(K / 2)};
+    const uint32_t box[2] = {128, box_rows};
+    return encode_tma_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, dims, strides, box, 1);
+}
+
+bool weights_map(CUtensorMap *m, const uint8_t *q, int64_t K, int64_t N, int64_t E, uint32_t box_rows) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(K / 2), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(K / 2), static_cast<uint64_t>(N * (K / 2))};
+    const uint32_t box[3] = {128, box_rows, 1};
+    return encode_tma_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box, 1);
+}
+
+template <typename TOut, bool GATE_UP, int BN, int V>
+cudaError_t launch_v(const CUtensorMap *maps, const MgParams &p, cudaStream_t stream) {
+    using L = MgLayout<BN>;
+    auto kern = mx4_gemm_kernel<TOut, GATE_UP, BN, V>;
+    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    }
+    const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_tiles;
+    const int64_t grid = tiles < device_sm_count() ? tiles : device_sm_count();
+    return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(MG_THREADS), L::SMEM, stream, maps[0], maps[1],
+                      maps[2], maps[3], p);
+}
+
+// the widest scale loads that K and the bases' alignment allow
+template <typename TOut, bool GATE_UP, int BN>
+cudaError_t launch_n(const CUtensorMap *maps, const MgParams &p, cudaStream_t stream) {
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(p.sf_a) | reinterpret_cast<uintptr_t>(p.sf_b0) |
+                            reinterpret_cast<uintptr_t>(p.sf_b1);
+    if (p.K % 256 == 0 && (bases & 7u) == 0) return launch_v<TOut, GATE_UP, BN, 8>(maps, p, stream);
+    if (p.K % 128 == 0 && (bases & 3u) == 0) return launch_v<TOut, GATE_UP, BN, 4>(maps, p, stream);
+    return launch_v<TOut, GATE_UP, BN, 1>(maps, p, stream);
+}
+
+MgParams params(const uint8_t *sf_a, const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
+                int out_n, int32_t *err) {
+    MgParams p{};
+    p.sf_a = sf_a;
+    p.tab = tab;
+    p.m_blocks = static_cast<int>(m_blocks);
+    p.n_rows = n_rows;
+    p.N = N;
+    p.K = K;
+    p.n_tiles = static_cast<int>((N + out_n - 1) / out_n);
+    p.slices = static_cast<int>((K + MG_SLICE - 1) / MG_SLICE);
+    p.err = err;
+    return p;
+}
+
+}  // namespace
+
+cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
+                                    const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
+                                    int64_t E, int out_dtype, void *C, int32_t *err, cudaStream_t stream) {
+    constexpr int BN = 128;
+    CUtensorMap maps[4];
+    if (!rows_map(&maps[0], q_a, K, n_rows, MG_BM) || !rows_map(&maps[1], q_a, K, n_rows, MG_FEW_ROWS) ||
+        !weights_map(&maps[2], q_b, K, N, E, BN))
+        return cudaErrorInvalidValue;
+    maps[3] = maps[2];
+    MgParams p = params(sf_a, tab, m_blocks, n_rows, N, K, BN, err);
+    p.sf_b0 = sf_b;
+    p.sf_b1 = sf_b;
+    p.out = C;
+    if (out_dtype == kF32) return launch_n<float, false, BN>(maps, p, stream);
+    if (out_dtype == kBF16) return launch_n<__nv_bfloat16, false, BN>(maps, p, stream);
+    return launch_n<__half, false, BN>(maps, p, stream);
+}
+
+cudaError_t launch_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
+                                            const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                            const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t d_h,
+                                            int64_t d_e, int64_t E, uint8_t *q_h, uint8_t *sf_h, int32_t *err,
+                                            cudaStream_t stream) {
+    constexpr int BN = 128;
+    CUtensorMap maps[4];
+    if (!rows_map(&maps[0], q_a, d_h, n_rows, MG_BM) || !rows_map(&maps[1], q_a, d_h, n_rows, MG_FEW_ROWS) ||
+        !weights_map(&maps[2], q_gate, d_h, d_e, E, BN / 2) || !weights_map(&maps[3], q_up, d_h, d_e, E, BN / 2))
+        return cudaErrorInvalidValue;
+    MgParams p = params(sf_a, tab, m_blocks, n_rows, d_e, d_h, BN / 2, err);
+    p.sf_b0 = sf_gate;
+    p.sf_b1 = sf_up;
+    p.q_h = q_h;
+    p.sf_h = sf_h;
+    return launch_n<float, true, BN>(maps, p, stream);
+}
+
+}  // namespace moe
