@@ -9,81 +9,179 @@
 namespace moe {
 namespace {
 
-__device__ __forceinline__ float warp_max(float v) {
+constexpr int MX_THREADS = 256;
+constexpr int MX_UNIT = 8;    // elements per thread and step: four lanes hold a block
+constexpr int MX_STEPS = 4;   // loads in flight per thread
+
+template <typename T> struct Unit;  // 8 elements as loaded
+template <> struct Unit<float> {
+    uint4 w[2];
+    __device__ __forceinline__ void load(const float *p) {
+        w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
+        w[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+    }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t b[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, s));
-    return v;
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(b[i]);
+    }
+};
+template <int DT> struct HalfUnit {
+    uint4 w;
+    __device__ __forceinline__ void load(const void *p) { w = __ldg(static_cast<const uint4 *>(p)); }
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        const uint32_t b[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2<DT>(b[i]);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+};
+template <> struct Unit<__half> : HalfUnit<kF16> {};
+template <> struct Unit<__nv_bfloat16> : HalfUnit<kBF16> {};
+
+// Four lanes quantise 32 values, 8 each (every lane of the warp takes part):
+// returns the lane's 4 bytes of elements and, through s, the scale byte.
+__device__ __forceinline__ uint32_t quad_quantize(const float (&v)[8], uint32_t &s) {
+    // fmaxf drops a NaN, so a block that holds one is told by a flag
+    float top = 0.0f;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        top = fmaxf(top, fabsf(v[i]));
+        odd |= v[i] != v[i];
+    }
+    if (odd) top = INFINITY;
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    s = mx4_scale(top);
+    if (s == 255u) return 0u;
+    const float inv = mx4_inverse(s);
+    uint32_t q = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+    return q;
 }
 
-// One warp quantises 32 values, one per lane; lanes 0, 2, ... write their bytes.
-__device__ __forceinline__ void warp_quantize(float v, uint8_t *q, uint8_t *sf, int lane) {
-    // fmaxf drops a NaN, so a block with one is found by a vote
-    const bool odd = __any_sync(0xffffffffu, !(fabsf(v) < INFINITY));
-    const uint32_t s = odd ? 255u : mx4_scale(warp_max(fabsf(v)));
-    const float a = odd ? 0.0f : v * mx4_inverse(s);
-    const float b = __shfl_down_sync(0xffffffffu, a, 1);
-    if ((lane & 1) == 0) q[lane >> 1] = static_cast<uint8_t>(e2m1x2(a, b));
-    if (lane == 0) *sf = static_cast<uint8_t>(s);
+// A CTA holds rows_per_cta rows at a time, `width` threads (a power of two,
+// at least four) on each.  Memory bound: 2 bytes in, 0.53 out per 16-bit
+// element, every access 16 (4 out) bytes a lane and contiguous over the warp.
+template <typename T>
+__global__ void __launch_bounds__(MX_THREADS)
+    quantize_kernel(const T *__restrict__ x, const int32_t *__restrict__ row_idx, int64_t n_rows, int64_t T_rows,
+                    int units, int width, uint8_t *__restrict__ q, uint8_t *__restrict__ sf, int32_t *err) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int rows_per_cta = MX_THREADS / width;
+    const int u0 = threadIdx.x & (width - 1);
+    for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * rows_per_cta; r0 < n_rows;
+         r0 += static_cast<int64_t>(gridDim.x) * rows_per_cta) {
+        const int64_t r = r0 + threadIdx.x / width;
+        const bool here = r < n_rows;
+        int64_t src = here ? (row_idx ? static_cast<int64_t>(__ldg(row_idx + r)) : r) : 0;
+        const bool in = here && src >= 0 && src < T_rows;
+        if (here && !in && err && u0 == 0) atomicExch(err, kErrDeviceFlag);
+        const T *row = x + (in ? src : 0) * units * MX_UNIT;
+        uint32_t *qr = reinterpret_cast<uint32_t *>(q) + (here ? r : 0) * units;
+        uint8_t *sr = sf + (here ? r : 0) * (units / 4);
+        for (int u = u0; u - u0 < units; u += width * MX_STEPS) {  // every lane the same number of steps
+            Unit<T> raw[MX_STEPS];
+#pragma unroll
+            for (int i = 0; i < MX_STEPS; ++i)
+                if (in && u + i * width < units) raw[i].load(row + static_cast<int64_t>(u + i * width) * MX_UNIT);
+#pragma unroll
+            for (int i = 0; i < MX_STEPS; ++i) {
+                const int at = u + i * width;
+                if (at - u0 >= units) break;  // the same for the whole CTA
+                float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
+                if (in && at < units) raw[i].values(v);
+                uint32_t s;
+                const uint32_t w = quad_quantize(v, s);
+                if (here && at < units) {
+                    qr[at] = w;
+                    if ((at & 3) == 0) sr[at >> 2] = static_cast<uint8_t>(s);
+                }
+            }
+        }
+    }
+}
+
+// 8 elements a thread
+template <typename T>
+__global__ void __launch_bounds__(MX_THREADS)
+    dequantize_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ sf, int64_t words, T *__restrict__ out) {
+    griddep_wait();
+    griddep_launch_dependents();
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (MX_THREADS * MX_STEPS) + threadIdx.x;
+    uint32_t w[MX_STEPS], s[MX_STEPS];
+#pragma unroll
+    for (int i = 0; i < MX_STEPS; ++i) {
+        const int64_t at = first + i * MX_THREADS;
+        if (at < words) {
+            w[i] = __ldg(q + at);
+            s[i] = __ldg(sf + (at >> 2));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MX_STEPS; ++i) {
+        const int64_t at = first + i * MX_THREADS;
+        if (at >= words) return;
+        const float f = mx4_factor(s[i]);
+        float v[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 pair = e2m1x2_values((w[i] >> (8 * j)) & 255u);
+            v[2 * j] = pair.x * f;
+            v[2 * j + 1] = pair.y * f;
+        }
+        uint4 *dst = reinterpret_cast<uint4 *>(out + at * MX_UNIT);
+        if constexpr (sizeof(T) == 4) {
+            dst[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+            dst[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
+        } else {
+            constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
+            dst[0] = make_uint4(pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7]));
+        }
+    }
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
-    quantize_kernel(const T *x, const int32_t *row_idx, int64_t n_rows, int64_t T_rows, int64_t blocks, uint8_t *q,
-                    uint8_t *sf, int32_t *err) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (i >= n_rows * blocks) return;
-    const int64_t r = i / blocks, b = i % blocks;
-    const int64_t src = row_idx ? row_idx[r] : r;
-    float v = 0.0f;
-    if (src >= 0 && src < T_rows)
-        v = to_f32(x[(src * blocks + b) * MX_BLOCK + lane]);
-    else if (err && lane == 0)
-        atomicExch(err, kErrDeviceFlag);
-    warp_quantize(v, q + i * (MX_BLOCK / 2), sf + i, lane);
+cudaError_t launch_quantize_typed(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T_rows, int64_t K,
+                                  uint8_t *q, uint8_t *sf, int32_t *err, cudaStream_t stream) {
+    const int units = static_cast<int>(K / MX_UNIT);
+    int width = 4;
+    while (width < units && width < MX_THREADS) width *= 2;
+    const int64_t groups = (n_rows + MX_THREADS / width - 1) / (MX_THREADS / width);
+    const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
+    return launch_pdl(quantize_kernel<T>, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(MX_THREADS),
+                      0, stream, static_cast<const T *>(x), row_idx, n_rows, T_rows, units, width, q, sf, err);
 }
 
 template <typename T>
-__global__ void __launch_bounds__(256)
-    dequantize_kernel(const uint8_t *q, const uint8_t *sf, int64_t bytes, T *out) {
-    griddep_wait();
-    griddep_launch_dependents();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
-    if (i >= bytes) return;
-    const float f = mx4_factor(sf[i / 16]);
-    out[2 * i] = from_f32<T>(e2m1_value(q[i] & 15u) * f);
-    out[2 * i + 1] = from_f32<T>(e2m1_value(q[i] >> 4) * f);
+cudaError_t launch_dequantize_typed(const uint8_t *q, const uint8_t *sf, int64_t words, void *out, cudaStream_t stream) {
+    constexpr int64_t per_cta = MX_THREADS * MX_STEPS;
+    return launch_pdl(dequantize_kernel<T>, dim3(static_cast<unsigned>((words + per_cta - 1) / per_cta)),
+                      dim3(MX_THREADS), 0, stream, reinterpret_cast<const uint32_t *>(q), sf, words,
+                      static_cast<T *>(out));
 }
 
 }  // namespace
 
 cudaError_t launch_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T, int64_t K,
                                 int dtype, uint8_t *q, uint8_t *sf, int32_t *err, cudaStream_t stream) {
-    const int64_t blocks = K / MX_BLOCK, warps = n_rows * blocks;
-    const dim3 grid(static_cast<unsigned>((warps + 7) / 8));
-    if (dtype == kF32)
-        return launch_pdl(quantize_kernel<float>, grid, dim3(256), 0, stream, static_cast<const float *>(x), row_idx,
-                          n_rows, T, blocks, q, sf, err);
-    if (dtype == kBF16)
-        return launch_pdl(quantize_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream,
-                          static_cast<const __nv_bfloat16 *>(x), row_idx, n_rows, T, blocks, q, sf, err);
-    return launch_pdl(quantize_kernel<__half>, grid, dim3(256), 0, stream, static_cast<const __half *>(x), row_idx,
-                      n_rows, T, blocks, q, sf, err);
+    if (dtype == kF32) return launch_quantize_typed<float>(x, row_idx, n_rows, T, K, q, sf, err, stream);
+    if (dtype == kBF16) return launch_quantize_typed<__nv_bfloat16>(x, row_idx, n_rows, T, K, q, sf, err, stream);
+    return launch_quantize_typed<__half>(x, row_idx, n_rows, T, K, q, sf, err, stream);
 }
 
 cudaError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K, int dtype, void *out,
                                   cudaStream_t stream) {
-    const int64_t bytes = n_rows * (K / 2);
-    const dim3 grid(static_cast<unsigned>((bytes + 255) / 256));
-    if (dtype == kF32)
-        return launch_pdl(dequantize_kernel<float>, grid, dim3(256), 0, stream, q, sf, bytes,
-                          static_cast<float *>(out));
-    if (dtype == kBF16)
-        return launch_pdl(dequantize_kernel<__nv_bfloat16>, grid, dim3(256), 0, stream, q, sf, bytes,
-                          static_cast<__nv_bfloat16 *>(out));
-    return launch_pdl(dequantize_kernel<__half>, grid, dim3(256), 0, stream, q, sf, bytes, static_cast<__half *>(out));
+    const int64_t words = n_rows * (K / MX_UNIT);
+    if (dtype == kF32) return launch_dequantize_typed<float>(q, sf, words, out, stream);
+    if (dtype == kBF16) return launch_dequantize_typed<__nv_bfloat16>(q, sf, words, out, stream);
+    return launch_dequantize_typed<__half>(q, sf, words, out, stream);
 }
 
 }  // namespace moe

@@ -7,8 +7,6 @@
 
 namespace moe {
 
-constexpr int MX_BLOCK = 32;
-
 // the scale byte of a block whose largest magnitude is `top`: floor(log2) is
 // in the exponent field; 255 for a NaN or an infinity
 __device__ __forceinline__ uint32_t mx4_scale(float top) {
@@ -33,10 +31,11 @@ __device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
     return r;
 }
 
-__device__ __forceinline__ float e2m1_value(uint32_t code) {
-    const uint32_t m = code & 7u;
-    const float v = m < 4u ? 0.5f * m : (m < 6u ? m - 2.0f : 2.0f * m - 8.0f);
-    return (code & 8u) ? -v : v;
+// the two elements of a byte, low nibble first
+__device__ __forceinline__ float2 e2m1x2_values(uint32_t byte) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(r) : "r"(byte));
+    return unpack2<kF16>(r);
 }
 
 struct Mx4Block {
