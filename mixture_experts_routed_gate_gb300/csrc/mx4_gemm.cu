@@ -10,8 +10,8 @@
 // columns.  Roles:
 //   warp 0      TMA: 128-byte (256-element) slices of the rows and the weights
 //               into a ring of 128-byte-swizzled stages;
-//   warps 6-9   scales: each thread loads its row's 8 scale bytes of a slice
-//               (several slices ahead) and stores them in the order that
+//   warps 6-13  scales, two groups in turn: each thread loads its row's 8 scale
+//               bytes of a slice (several slices ahead) and stores them in the order that
 //               tcgen05.cp takes to tensor memory;
 //   warp 1      one thread: scales to tensor memory, then four K = 64 MMAs a slice;
 //   warps 2-5   epilogue, from one of two accumulators while the other fills.
@@ -25,7 +25,7 @@ namespace {
 constexpr int MG_BM = 128;
 constexpr int MG_SLICE = 256;       // elements of K per stage: 128 bytes of a row
 constexpr int MG_A_BYTES = MG_BM * 128;
-constexpr int MG_THREADS = 320;
+constexpr int MG_THREADS = 448;
 constexpr int MG_EPI_WARP0 = 2, MG_SF_WARP0 = 6;
 constexpr int MG_AHEAD = 4;         // slices of scales in registers ahead of the ring
 constexpr int MG_LIST = 2048;       // M blocks the shared-memory list holds
@@ -68,12 +68,17 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(uint32_t M, uint32_t N) {
     return (1u << 7) | (1u << 10) | ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24);
 }
 
+// The MMA warp runs whole, its operands the same in every lane, and one
+// elected lane issues: the operands then come from uniform registers.  Issued
+// by one lane of a divergent branch instead, each operand is moved there
+// first, and an MMA took 113 cycles to issue, a copy 71.
 __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                             uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, e;\n\t"
         "setp.ne.b32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
         "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
         : "memory");
 }
@@ -81,7 +86,13 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, ui
 // 512 bytes of scales (32 rows of 16) to four columns, in each of the four
 // 32-lane quarters of tensor memory
 __device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc) : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
 }
 
 // no swizzle: 8-row groups of 16-byte rows, 128 bytes apart
@@ -108,22 +119,23 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
         : "r"(taddr));
 }
 
-// The 8 scale bytes of row `row` of a [rows, kb] byte matrix from byte b0 on;
-// bytes past kb are 0 (their elements are zeros too).  V: the load width that
-// kb and the base's alignment allow.
-template <int V> __device__ __forceinline__ uint2 load_scales(const uint8_t *base, int64_t row, int kb, int b0) {
-    const uint8_t *p = base + row * kb + b0;
+// 8 scale bytes from byte `at` on of a row of kb of them (null: zeros); bytes
+// past kb are 0 (their elements are zeros too).  V: the load width that kb and
+// the bases' alignment allow.
+template <int V> __device__ __forceinline__ uint2 load_scales(const uint8_t *row, int kb, int at) {
     uint2 v = make_uint2(0u, 0u);
+    if (!row) return v;
+    const uint8_t *p = row + at;
     if constexpr (V == 8) {
         v = __ldg(reinterpret_cast<const uint2 *>(p));
     } else if constexpr (V == 4) {
         v.x = __ldg(reinterpret_cast<const uint32_t *>(p));
-        if (b0 + 4 < kb) v.y = __ldg(reinterpret_cast<const uint32_t *>(p + 4));
+        if (at + 4 < kb) v.y = __ldg(reinterpret_cast<const uint32_t *>(p + 4));
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            if (b0 + i < kb) v.x |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
-            if (b0 + 4 + i < kb) v.y |= static_cast<uint32_t>(__ldg(p + 4 + i)) << (8 * i);
+            if (at + i < kb) v.x |= static_cast<uint32_t>(__ldg(p + i)) << (8 * i);
+            if (at + 4 + i < kb) v.y |= static_cast<uint32_t>(__ldg(p + 4 + i)) << (8 * i);
         }
     }
     return v;
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     const int listed = n_listed;
     const int64_t total = static_cast<int64_t>(listed >= 0 ? listed : p.m_blocks) * p.n_tiles;
     auto tile_at = [&](int64_t t) {
@@ -287,98 +299,100 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         }
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
-        if (lane == 0) {
-            constexpr uint32_t IDESC = idesc_mxf4(MG_BM, BN);
-            int stage = 0, local = 0, buf = 0;
-            uint32_t phase = 0, last_bar = 0, last_parity = 0;
-            bool ok = true, committed = false;
-            for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
-                const MgTile ti = tile_at(t);
-                if (ti.rows == 0) continue;
-                const int acc = local & 1;
-                if (!mbar_wait_bounded(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u, abort_flag, p.err)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
-                for (int s = 0; s < p.slices; ++s) {
-                    if (!mbar_wait_bounded(full_bar(stage), phase, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t a = smem_u32(smem + stage * L::STAGE), sf = a + MG_A_BYTES + L::B_BYTES;
-                    const uint64_t a_desc = smem_desc_sw128(a), b_desc = smem_desc_sw128(a + MG_A_BYTES);
-                    const uint32_t sfa = tmem + L::SF_COL0 + buf * L::SF_COLS, sfb = sfa + 8u;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        tc_cp_scales(sfa + 4u * j, smem_desc_scales(sf + 512u * j));
-#pragma unroll
-                        for (int h = 0; h < L::SF_HALVES; ++h)
-                            tc_cp_scales(sfb + 4u * (j * L::SF_HALVES + h),
-                                         smem_desc_scales(sf + 1024u + 512u * (j * L::SF_HALVES + h)));
-                    }
-                    const int64_t left = p.K - static_cast<int64_t>(s) * MG_SLICE;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        if (k * 64 >= left) break;
-                        const uint32_t id = (k & 1) * 2u;
-                        tc_mma_mxf4(d, a_desc + 2u * k, b_desc + 2u * k, IDESC | (id << 29) | (id << 4),
-                                    sfa + 4u * (k >> 1), sfb + 4u * L::SF_HALVES * (k >> 1), (s | k) != 0 ? 1u : 0u);
-                    }
-                    tc_commit(empty_bar(stage));
-                    last_bar = empty_bar(stage);
-                    last_parity = phase;
-                    committed = true;
-                    buf ^= 1;
-                    if (++stage == L::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
-                }
+        constexpr uint32_t IDESC = idesc_mxf4(MG_BM, BN);
+        const uint32_t ring = smem_u32(smem);
+        auto wait = [&](uint32_t bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, p.err)) != 0;
+        };
+        int stage = 0, local = 0, buf = 0;
+        uint32_t phase = 0, last_bar = 0, last_parity = 0;
+        bool ok = true, committed = false;
+        for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
+            if (__all_sync(0xffffffffu, tile_at(t).rows == 0)) continue;
+            const int acc = local & 1;
+            ok = wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t d = tmem + static_cast<uint32_t>(acc * BN);
+            for (int s = 0; s < p.slices; ++s) {
+                ok = wait(full_bar(stage), phase);
                 if (!ok) break;
-                tc_commit(tfull_bar(acc));
-                ++local;
+                tc_fence_after();
+                // the scale warps' stores, seen through the barrier, before
+                // tcgen05.cp reads them
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                const uint32_t a = ring + stage * L::STAGE, sf = a + MG_A_BYTES + L::B_BYTES;
+                const uint64_t a_desc = smem_desc_sw128(a), b_desc = smem_desc_sw128(a + MG_A_BYTES);
+                const uint64_t sf_desc = smem_desc_scales(sf);
+                const uint32_t sfa = tmem + L::SF_COL0 + buf * L::SF_COLS, sfb = sfa + 8u;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    tc_cp_scales(sfa + 4u * j, sf_desc + 32u * j);  // 512 bytes on
+#pragma unroll
+                    for (int h = 0; h < L::SF_HALVES; ++h)
+                        tc_cp_scales(sfb + 4u * (j * L::SF_HALVES + h), sf_desc + 32u * (2 + j * L::SF_HALVES + h));
+                }
+                const int left = static_cast<int>(p.K) - s * MG_SLICE;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if (k * 64 >= left) break;
+                    const uint32_t id = (k & 1) * 2u;
+                    tc_mma_mxf4(d, a_desc + 2u * k, b_desc + 2u * k, IDESC | (id << 29) | (id << 4),
+                                sfa + 4u * (k >> 1), sfb + 4u * L::SF_HALVES * (k >> 1), (s | k) != 0 ? 1u : 0u);
+                }
+                tc_commit_elect(empty_bar(stage));
+                last_bar = empty_bar(stage);
+                last_parity = phase;
+                committed = true;
+                buf ^= 1;
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-            if (!ok && committed) mg_drain(last_bar, last_parity);
+            if (!ok) break;
+            tc_commit_elect(tfull_bar(acc));
+            ++local;
         }
+        if (!ok && committed && lane == 0) mg_drain(last_bar, last_parity);
     } else if (warp >= MG_SF_WARP0) {
         // -------------------------------- scales --------------------------------
-        const int r = threadIdx.x - MG_SF_WARP0 * 32;
+        // two groups of four warps take the slices in turn
+        const int r = (threadIdx.x - MG_SF_WARP0 * 32) & 127;
+        const int group = (warp - MG_SF_WARP0) >> 2;
         const int kb = static_cast<int>(p.K / 32);
         const uint32_t cell = (r & 31) * 16u + (r >> 5) * 4u;  // of row r within 512 bytes
         uint2 va[MG_AHEAD], vb[MG_AHEAD][L::SF_HALVES];
-        int64_t lt = blockIdx.x;  // next slice to load: tile, slice
-        int ls = 0;
-        MgTile li{0, 0, 0, 0};
+        int64_t lt = blockIdx.x;  // next slice to load: its tile, its scale bytes
+        int at = group * 8;       // byte offset of that slice in its row
+        const uint8_t *pa = nullptr, *pb[L::SF_HALVES];  // the thread's rows; null where there is none
         auto next_tile = [&]() {
             for (; lt < total; lt += gridDim.x) {
-                li = tile_at(lt);
-                if (li.rows > 0) return;
+                const MgTile ti = tile_at(lt);
+                if (ti.rows == 0) continue;
+                if (at >= p.slices * 8) {  // past this tile: the slices go on in the next one
+                    at -= p.slices * 8;
+                    continue;
+                }
+                pa = r < ti.rows ? p.sf_a + (static_cast<int64_t>(ti.m_start) + r) * kb : nullptr;
+#pragma unroll
+                for (int h = 0; h < L::SF_HALVES; ++h) {
+                    const int n = h * 128 + r;  // row of the stage's B box
+                    const bool up = GATE_UP && n >= OUT_N;
+                    const int64_t f = ti.n0 + (up ? n - OUT_N : n);
+                    pb[h] = n < BN && f < p.N ? (up ? p.sf_b1 : p.sf_b0) + (static_cast<int64_t>(ti.g) * p.N + f) * kb
+                                              : nullptr;
+                }
+                return;
             }
         };
         next_tile();
         auto load = [&](uint2 &a, uint2(&b)[L::SF_HALVES]) {
-            const int64_t row = static_cast<int64_t>(li.m_start) + r;
-            a = r < li.rows ? load_scales<V>(p.sf_a, row, kb, ls * 8) : make_uint2(0u, 0u);
+            a = load_scales<V>(pa, kb, at);
 #pragma unroll
-            for (int h = 0; h < L::SF_HALVES; ++h) {
-                const int n = h * 128 + r;  // row of the stage's B box
-                b[h] = make_uint2(0u, 0u);
-                if (GATE_UP) {
-                    const int f = li.n0 + (n < OUT_N ? n : n - OUT_N);
-                    if (n < BN && f < p.N)
-                        b[h] = load_scales<V>(n < OUT_N ? p.sf_b0 : p.sf_b1, static_cast<int64_t>(li.g) * p.N + f, kb, ls * 8);
-                } else if (n < BN && li.n0 + n < p.N) {
-                    b[h] = load_scales<V>(p.sf_b0, static_cast<int64_t>(li.g) * p.N + li.n0 + n, kb, ls * 8);
-                }
-            }
-            if (++ls == p.slices) {
-                ls = 0;
-                lt += gridDim.x;
-                next_tile();
-            }
+            for (int h = 0; h < L::SF_HALVES; ++h) b[h] = load_scales<V>(pb[h], kb, at);
+            at += 16;
+            if (at >= p.slices * 8) next_tile();
         };
         int ahead = 0;  // slices in registers
 #pragma unroll
@@ -387,17 +401,17 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 load(va[j], vb[j]);
                 ++ahead;
             }
-        int stage = 0;
+        int stage = group;
         uint32_t phase = 0;
         bool ok = true;
         while (ok && ahead > 0) {
 #pragma unroll
             for (int j = 0; j < MG_AHEAD; ++j) {
                 if (!ok || ahead == 0) continue;
-                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
-                    ok = false;
-                    continue;
-                }
+                int free = 1;
+                if (lane == 0) free = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err) ? 1 : 0;
+                ok = __shfl_sync(0xffffffffu, free, 0) != 0;
+                if (!ok) continue;
                 uint8_t *sf = smem + stage * L::STAGE + MG_A_BYTES + L::B_BYTES;
                 *reinterpret_cast<uint32_t *>(sf + cell) = va[j].x;
                 *reinterpret_cast<uint32_t *>(sf + 512 + cell) = va[j].y;
@@ -406,11 +420,11 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                     *reinterpret_cast<uint32_t *>(sf + 1024 + h * 512 + cell) = vb[j][h].x;
                     *reinterpret_cast<uint32_t *>(sf + 1024 + (L::SF_HALVES + h) * 512 + cell) = vb[j][h].y;
                 }
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_bar(stage));
-                if (++stage == L::STAGES) {
-                    stage = 0;
+                stage += 2;
+                if (stage >= L::STAGES) {
+                    stage -= L::STAGES;
                     phase ^= 1u;
                 }
                 --ahead;
