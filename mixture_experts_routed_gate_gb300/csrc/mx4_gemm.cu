@@ -10,11 +10,12 @@
 // columns.  Roles:
 //   warp 0      TMA: 128-byte (256-element) slices of the rows and the weights
 //               into a ring of 128-byte-swizzled stages;
-//   warps 6-13  scales, two groups in turn: each thread loads its row's 8 scale
-//               bytes of a slice (several slices ahead) and stores them in the order that
-//               tcgen05.cp takes to tensor memory;
-//   warp 1      one thread: scales to tensor memory, then four K = 64 MMAs a slice;
-//   warps 2-5   epilogue, from one of two accumulators while the other fills.
+//   warps 10-17 scales, two groups in turn: each thread loads its row's 8 scale
+//               bytes of a slice, several slices ahead; through shared memory
+//               each warp gets every row's and stores them to its quarter of
+//               tensor memory;
+//   warp 1      one elected lane: four K = 64 MMAs a slice;
+//   warps 2-9   epilogue, from one of two accumulators while the other fills.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"
@@ -25,25 +26,27 @@ namespace {
 constexpr int MG_BM = 128;
 constexpr int MG_SLICE = 256;       // elements of K per stage: 128 bytes of a row
 constexpr int MG_A_BYTES = MG_BM * 128;
-constexpr int MG_THREADS = 448;
-constexpr int MG_EPI_WARP0 = 2, MG_SF_WARP0 = 6;
+constexpr int MG_THREADS = 576;
+constexpr int MG_EPI_WARP0 = 2, MG_EPI_WARPS = 8, MG_SF_WARP0 = 10, MG_SF_GROUPS = 2;
 constexpr int MG_AHEAD = 4;         // slices of scales in registers ahead of the ring
-constexpr int MG_LIST = 2048;       // M blocks the shared-memory list holds
+constexpr int MG_LIST = 512;        // M blocks with rows that the shared-memory list holds
+constexpr int MG_BN = 192;         // columns of a tile
 constexpr int MG_FEW_ROWS = 32;     // a block of at most so many rows loads a short box
 
 template <int BN> struct MgLayout {
     static constexpr int B_BYTES = BN * 128;
+    static constexpr int STAGE = MG_A_BYTES + B_BYTES;
     static constexpr int SF_HALVES = (BN + 127) / 128;          // 128-row groups of B's scales
-    static constexpr int SF_BYTES = 2 * (1 + SF_HALVES) * 512;  // two 128-element groups of K
-    static constexpr int STAGE = MG_A_BYTES + B_BYTES + SF_BYTES;
-    static constexpr int LIST_BYTES = MG_LIST * 12;
-    static constexpr int STAGES = (232448 - 2048 - LIST_BYTES) / STAGE;
-    static constexpr int SMEM = 1024 + STAGES * STAGE + 512 + LIST_BYTES;
-    static constexpr int SF_COLS = 2 * 4 * (1 + SF_HALVES);     // tensor-memory columns of a slice's scales
+    static constexpr int SF_BYTES = 2 * (1 + SF_HALVES) * 512;  // a slice's scales: two 128-element groups of K
+    static constexpr int SF_COLS = 2 * 4 * (1 + SF_HALVES);     // and their tensor-memory columns
+    static constexpr int LIST_BYTES = MG_LIST * 8;
+    static constexpr int FIXED = 1024 + 512 + LIST_BYTES + 2 * MG_SF_GROUPS * SF_BYTES;
+    static constexpr int STAGES = (232448 - 256 - FIXED) / STAGE;
+    static constexpr int SMEM = FIXED + STAGES * STAGE;
     static constexpr int SF_COL0 = 2 * BN;                      // after the two accumulators
-    static_assert(SF_COL0 + 2 * SF_COLS <= 512, "tensor memory");
+    static_assert(SF_COL0 + STAGES * SF_COLS <= 512, "tensor memory");
     static_assert(STAGE % 1024 == 0, "swizzle atoms");
-    static_assert(SMEM <= 232448 && STAGES >= 3, "shared memory");
+    static_assert(STAGES > MG_SF_GROUPS, "the groups work on different stages");
 };
 
 struct MgParams {
@@ -83,22 +86,36 @@ __device__ __forceinline__ void tc_mma_mxf4(uint32_t d_tmem, uint64_t a_desc, ui
         : "memory");
 }
 
-// 512 bytes of scales (32 rows of 16) to four columns, in each of the four
-// 32-lane quarters of tensor memory
-__device__ __forceinline__ void tc_cp_scales(uint32_t taddr, uint64_t desc) {
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-                 "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(desc) : "memory");
-}
-
 __device__ __forceinline__ void tc_commit_elect(uint32_t bar) {
     asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
                  "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar) : "memory");
 }
 
-// no swizzle: 8-row groups of 16-byte rows, 128 bytes apart
-__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
-    return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(128u >> 4) << 32) |
-           (static_cast<uint64_t>(1) << 46);
+// A barrier of one scale group: whether `yes` holds in all its 128 threads.
+__device__ __forceinline__ bool mg_group_all(int id, bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(yes ? 1u : 0u)
+        : "memory");
+    return all != 0;
+}
+
+// the scales of rows i, 32 + i, 64 + i and 96 + i, p at row i
+__device__ __forceinline__ uint4 quarter_scales(const uint8_t *p) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+    return make_uint4(w[0], w[32], w[64], w[96]);
+}
+
+// 8 consecutive columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4 &a, const uint4 &b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
 }
 
 __device__ __forceinline__ void mg_drain(uint32_t bar, uint32_t parity) {
@@ -177,10 +194,9 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     extern __shared__ uint8_t mg_smem_raw[];
     uint8_t *smem = mg_smem_raw + ((1024u - (smem_u32(mg_smem_raw) & 1023u)) & 1023u);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::STAGES * L::STAGE);
-    int *list_g = reinterpret_cast<int *>(smem + L::STAGES * L::STAGE + 512);
-    int *list_m = list_g + MG_LIST, *list_rows = list_m + MG_LIST;
+    int2 *list = reinterpret_cast<int2 *>(smem + L::STAGES * L::STAGE + 512);  // first row; expert and row count
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word, n_listed;
+    __shared__ int abort_word, warp_blocks[MG_THREADS / 32];
     volatile int *abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bar0 = smem_u32(bars);
@@ -191,15 +207,14 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < L::STAGES; ++i) {
-            mbar_init(full_bar(i), 1 + 4);  // the copies' thread and the scale warps
+            mbar_init(full_bar(i), 1 + 4);  // the copies' thread and a group's scale warps
             mbar_init(empty_bar(i), 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(tfull_bar(i), 1);
-            mbar_init(tempty_bar(i), 4);
+            mbar_init(tempty_bar(i), MG_EPI_WARPS);
         }
         abort_word = 0;
-        n_listed = -1;
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -213,37 +228,38 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // the blocks that hold rows, in order, when they fit the list
-    if (warp == 2 && p.m_blocks <= MG_LIST) {
-        int n = 0;
-        for (int b0 = 0; b0 < p.m_blocks; b0 += 32) {
-            const int bx = b0 + lane;
-            const Mx4Block b = bx < p.m_blocks ? mx4_block_of(p.tab, bx) : Mx4Block{0, 0, 0};
-            const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
-            if (b.rows > 0) {
-                const int at = n + __popc(has & ((1u << lane) - 1u));
-                list_g[at] = b.g;
-                list_m[at] = b.m_start;
-                list_rows[at] = b.rows;
-            }
-            n += __popc(has);
+    // the blocks that hold rows, in order, when they fit the list (the whole
+    // CTA looks at MG_THREADS blocks at a time: the tables' latency is paid once)
+    int n_blocks = 0;
+    for (int b0 = 0; b0 < p.m_blocks && n_blocks <= MG_LIST; b0 += MG_THREADS) {
+        const int bx = b0 + static_cast<int>(threadIdx.x);
+        const Mx4Block b = bx < p.m_blocks ? mx4_block_of(p.tab, bx) : Mx4Block{0, 0, 0};
+        const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
+        if (lane == 0) warp_blocks[warp] = __popc(has);
+        __syncthreads();
+        int at = n_blocks + __popc(has & ((1u << lane) - 1u));
+        for (int w = 0; w < MG_THREADS / 32; ++w) {
+            at += w < warp ? warp_blocks[w] : 0;
+            n_blocks += warp_blocks[w];
         }
-        if (lane == 0) n_listed = n;
+        if (b.rows > 0 && at < MG_LIST) list[at] = make_int2(b.m_start, b.g << 8 | b.rows);
+        __syncthreads();
     }
+    const int listed = n_blocks <= MG_LIST ? n_blocks : -1;
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-    const int listed = n_listed;
     const int64_t total = static_cast<int64_t>(listed >= 0 ? listed : p.m_blocks) * p.n_tiles;
     auto tile_at = [&](int64_t t) {
         const int b = static_cast<int>(t / p.n_tiles);
         MgTile ti;
         ti.n0 = static_cast<int>(t - static_cast<int64_t>(b) * p.n_tiles) * OUT_N;
         if (listed >= 0) {
-            ti.g = list_g[b];
-            ti.m_start = list_m[b];
-            ti.rows = list_rows[b];
+            const int2 e = list[b];
+            ti.g = e.y >> 8;
+            ti.m_start = e.x;
+            ti.rows = e.y & 255;
         } else {
             const Mx4Block k = mx4_block_of(p.tab, b);
             ti.g = k.g;
@@ -304,7 +320,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         auto wait = [&](uint32_t bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, p.err)) != 0;
         };
-        int stage = 0, local = 0, buf = 0;
+        int stage = 0, local = 0;
         uint32_t phase = 0, last_bar = 0, last_parity = 0;
         bool ok = true, committed = false;
         for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
@@ -318,20 +334,9 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 ok = wait(full_bar(stage), phase);
                 if (!ok) break;
                 tc_fence_after();
-                // the scale warps' stores, seen through the barrier, before
-                // tcgen05.cp reads them
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                const uint32_t a = ring + stage * L::STAGE, sf = a + MG_A_BYTES + L::B_BYTES;
+                const uint32_t a = ring + stage * L::STAGE;
                 const uint64_t a_desc = smem_desc_sw128(a), b_desc = smem_desc_sw128(a + MG_A_BYTES);
-                const uint64_t sf_desc = smem_desc_scales(sf);
-                const uint32_t sfa = tmem + L::SF_COL0 + buf * L::SF_COLS, sfb = sfa + 8u;
-#pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    tc_cp_scales(sfa + 4u * j, sf_desc + 32u * j);  // 512 bytes on
-#pragma unroll
-                    for (int h = 0; h < L::SF_HALVES; ++h)
-                        tc_cp_scales(sfb + 4u * (j * L::SF_HALVES + h), sf_desc + 32u * (2 + j * L::SF_HALVES + h));
-                }
+                const uint32_t sfa = tmem + L::SF_COL0 + stage * L::SF_COLS, sfb = sfa + 8u;
                 const int left = static_cast<int>(p.K) - s * MG_SLICE;
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
@@ -344,7 +349,6 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 last_bar = empty_bar(stage);
                 last_parity = phase;
                 committed = true;
-                buf ^= 1;
                 if (++stage == L::STAGES) {
                     stage = 0;
                     phase ^= 1u;
@@ -357,11 +361,13 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         if (!ok && committed && lane == 0) mg_drain(last_bar, last_parity);
     } else if (warp >= MG_SF_WARP0) {
         // -------------------------------- scales --------------------------------
-        // two groups of four warps take the slices in turn
+        // groups of four warps take the slices in turn
         const int r = (threadIdx.x - MG_SF_WARP0 * 32) & 127;
         const int group = (warp - MG_SF_WARP0) >> 2;
         const int kb = static_cast<int>(p.K / 32);
-        const uint32_t cell = (r & 31) * 16u + (r >> 5) * 4u;  // of row r within 512 bytes
+        const uint32_t cell = r * 4u;  // of row r within 512 bytes
+        uint8_t *staging = smem + L::STAGES * L::STAGE + 512 + L::LIST_BYTES + group * 2 * L::SF_BYTES;
+        static_assert(MG_AHEAD % 2 == 0, "the staging buffers alternate");
         uint2 va[MG_AHEAD], vb[MG_AHEAD][L::SF_HALVES];
         int64_t lt = blockIdx.x;  // next slice to load: its tile, its scale bytes
         int at = group * 8;       // byte offset of that slice in its row
@@ -391,7 +397,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             a = load_scales<V>(pa, kb, at);
 #pragma unroll
             for (int h = 0; h < L::SF_HALVES; ++h) b[h] = load_scales<V>(pb[h], kb, at);
-            at += 16;
+            at += 8 * MG_SF_GROUPS;
             if (at >= p.slices * 8) next_tile();
         };
         int ahead = 0;  // slices in registers
@@ -410,9 +416,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 if (!ok || ahead == 0) continue;
                 int free = 1;
                 if (lane == 0) free = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err) ? 1 : 0;
-                ok = __shfl_sync(0xffffffffu, free, 0) != 0;
-                if (!ok) continue;
-                uint8_t *sf = smem + stage * L::STAGE + MG_A_BYTES + L::B_BYTES;
+                free = __shfl_sync(0xffffffffu, free, 0);
+                uint8_t *sf = staging + (j & 1) * L::SF_BYTES;
                 *reinterpret_cast<uint32_t *>(sf + cell) = va[j].x;
                 *reinterpret_cast<uint32_t *>(sf + 512 + cell) = va[j].y;
 #pragma unroll
@@ -420,9 +425,24 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                     *reinterpret_cast<uint32_t *>(sf + 1024 + h * 512 + cell) = vb[j][h].x;
                     *reinterpret_cast<uint32_t *>(sf + 1024 + (L::SF_HALVES + h) * 512 + cell) = vb[j][h].y;
                 }
+                // every thread of the group has stored; two buffers in turn, so
+                // the next slice's stores cannot pass this one's reads.  A warp
+                // whose wait gave up comes here too and takes the group along
+                ok = mg_group_all(1 + group, free != 0);
+                if (!ok) continue;
+                // each warp puts all rows' scales into its own lane quarter:
+                // lane i, column c holds row 32 c + i
+                tc_fence_after();
+                const uint32_t col = tmem + ((warp & 3u) << 21) + L::SF_COL0 + stage * L::SF_COLS;
+#pragma unroll
+                for (int i = 0; i < L::SF_COLS / 8; ++i)
+                    tmem_st8(col + 8u * i, quarter_scales(sf + 1024 * i + lane * 4),
+                             quarter_scales(sf + 1024 * i + 512 + lane * 4));
+                tmem_st_wait();
+                tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(full_bar(stage));
-                stage += 2;
+                stage += MG_SF_GROUPS;
                 if (stage >= L::STAGES) {
                     stage -= L::STAGES;
                     phase ^= 1u;
@@ -436,7 +456,10 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
         }
     } else {
         // ------------------------------- epilogue -------------------------------
+        // two warps to a lane quarter, each with half of the columns
         const int q = warp & 3;  // the lane quarter this warp may read
+        constexpr int HALF = (OUT_N / 2 + 31) / 32 * 32;
+        const int c0 = ((warp - MG_EPI_WARP0) >> 2) * HALF, c1 = c0 + HALF < OUT_N ? c0 + HALF : OUT_N;
         const int row = q * 32 + lane;
         int local = 0;
         for (int64_t t = blockIdx.x; t < total; t += gridDim.x) {
@@ -444,7 +467,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             if (ti.rows == 0) continue;
             const int acc = local & 1;
             int ready = 1;
-            if (lane == 0) ready = mbar_wait_bounded(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err) ? 1 : 0;
+            if (lane == 0)
+                ready = mbar_wait_bounded(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err) ? 1 : 0;
             ready = __shfl_sync(0xffffffffu, ready, 0);
             if (!ready) break;
             tc_fence_after();
@@ -453,7 +477,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             const bool valid = row < ti.rows;
             if (q * 32 < ti.rows) {
 #pragma unroll 1
-                for (int c = 0; c < OUT_N; c += 32) {
+                for (int c = c0; c < c1; c += 32) {
                     const int64_t n = ti.n0 + c;
                     if (n >= p.N) break;
                     uint32_t v[32];
@@ -572,7 +596,7 @@ MgParams params(const uint8_t *sf_a, const Mx4Tables &tab, int64_t m_blocks, int
 cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
                                     const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
                                     int64_t E, int out_dtype, void *C, int32_t *err, cudaStream_t stream) {
-    constexpr int BN = 128;
+    constexpr int BN = MG_BN;
     CUtensorMap maps[4];
     if (!rows_map(&maps[0], q_a, K, n_rows, MG_BM) || !rows_map(&maps[1], q_a, K, n_rows, MG_FEW_ROWS) ||
         !weights_map(&maps[2], q_b, K, N, E, BN))
@@ -592,7 +616,7 @@ cudaError_t launch_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *s
                                             const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t d_h,
                                             int64_t d_e, int64_t E, uint8_t *q_h, uint8_t *sf_h, int32_t *err,
                                             cudaStream_t stream) {
-    constexpr int BN = 128;
+    constexpr int BN = MG_BN;
     CUtensorMap maps[4];
     if (!rows_map(&maps[0], q_a, d_h, n_rows, MG_BM) || !rows_map(&maps[1], q_a, d_h, n_rows, MG_FEW_ROWS) ||
         !weights_map(&maps[2], q_gate, d_h, d_e, E, BN / 2) || !weights_map(&maps[3], q_up, d_h, d_e, E, BN / 2))
