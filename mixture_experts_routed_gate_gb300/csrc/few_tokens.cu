@@ -1,16 +1,48 @@
-// few_tokens.cu -- the whole routed-expert layer for a few tokens.
+// few_tokens.cu -- the whole routed-expert layer for a few tokens (T <= 16).
 //
 //   out_t = sum over the k experts e of token t of p_te * W_down[e] h_te,
 //   h_te  = silu(W_gate[e] x_t) * (W_up[e] x_t)
-// with the routing of moe_gate_topk.  One warp per dot product; h is kept,
-// scaled by its routing weight, as a 16-bit value and the rest of it.
+// with the routing of moe_gate_topk.  The weights of the chosen experts are
+// the cost: each is read once and meets at most 16 tokens.  Two launches:
+//
+// 1. few_logits_kernel: a warp per expert, all tokens, in the gate's fixed
+//    summation order.
+// 2. few_layer_kernel: one CTA per SM.  Every CTA chooses the experts from the
+//    logits itself (T warps' work, no further launch), then takes tiles from a
+//    shared counter: first the stage-1 tiles (8 features of an expert: 8 gate
+//    and 8 up rows), then the stage-2 tiles (16 output rows, all experts).
+//    A tile is 16 weight rows, streamed 512 columns at a time through a ring
+//    of shared-memory stages: one warp copies weights (two 8-row boxes of TMA,
+//    each eight 64-column slabs with the 128-byte swizzle), another the rows
+//    that meet them (x, or h once its expert's tiles are done), so the weights
+//    of a stage-2 tile are under way before h is.  Eight warps multiply, each
+//    its 64-column slab of a stage, with m16n8k16 MMAs (weights as the 16
+//    rows, tokens as the 8 columns; 1 or 2 column groups): the tensor path
+//    only has to keep up with the stream, and 16 rows suit short tiles.  Four
+//    more warps join their sums in a fixed order.
+//    h is scaled by its routing weight and kept as a 16-bit value and the
+//    16-bit rest, both multiplied, so that the stage-2 accumulators hold the
+//    weighted sum over the experts and the output is rounded once.
+// Tiles are taken in order, so a stage-2 tile waits only on tiles that running
+// CTAs hold: the launch completes whether or not all CTAs are resident.
 #include "common.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int FEW_WARPS = 8;
+constexpr int FEW_COLS = 512;                        // columns of a stage
+constexpr int FEW_ROW = FEW_COLS * 2 + 16;           // bytes of an x or h row; the pad puts the rows in other banks
+constexpr int FEW_HALF = 8 * FEW_COLS * 2;           // bytes of eight weight rows
+constexpr int FEW_CONSUMERS = 8;                     // multiplying warps
+constexpr int FEW_FINISHERS = 4;                     // warps that join the multiplying warps' sums
+constexpr int FEW_THREADS = (FEW_CONSUMERS + 2 + FEW_FINISHERS) * 32;
+constexpr int FEW_PARTS = 4;                         // tiles whose sums may wait to be joined
+constexpr int FEW_MAX_STAGES = 12;
+constexpr int FEW_QUEUE = 4;                         // tiles handed from the copying to the other warps
+constexpr int FEW_BARS = 2 * FEW_MAX_STAGES + 2 * FEW_QUEUE + 2 * FEW_PARTS;
+constexpr int FEW_SMEM_MAX = 232448 - 1024;
+constexpr int LOGIT_WARPS = 4;
 
 template <int DT>
 __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float c) {
@@ -27,6 +59,53 @@ __device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int s = 16; s >= 1; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
     return v;
+}
+
+// logits[t, e] in the gate's fixed order (lane L sums its 8-element chunks
+// L, L + 32, ... in ascending order, then the butterfly), a warp per expert;
+// also clears the counters of the second launch.  TT tokens at a time.
+template <int DT, int TT>
+__global__ void __launch_bounds__(LOGIT_WARPS * 32)
+    few_logits_kernel(const uint4 *__restrict__ x, const uint4 *__restrict__ w_g, const float *__restrict__ bias,
+                      int tokens, int chunks, int E, float *__restrict__ logits, int *__restrict__ counters,
+                      int n_counters) {
+    griddep_launch_dependents();
+    const int lane = threadIdx.x & 31, e = blockIdx.x * LOGIT_WARPS + (threadIdx.x >> 5);
+    const uint4 *w = w_g + static_cast<int64_t>(e < E ? e : 0) * chunks;
+    for (int c = lane * 8; c < chunks; c += 256)  // 128 bytes a lane
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(w + c));
+    griddep_wait();
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_counters; i += gridDim.x * blockDim.x) counters[i] = 0;
+    if (e >= E) return;
+    constexpr int U = TT <= 2 ? 7 : (TT <= 4 ? 4 : 2);  // chunks in flight
+    for (int t0 = 0; t0 < tokens; t0 += TT) {
+        float acc[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[t] = 0.0f;
+        for (int c0 = lane; c0 < chunks; c0 += 32 * U) {
+            uint4 wv[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < chunks) wv[u] = __ldg(w + c0 + 32 * u);
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+                const uint4 *xr = x + static_cast<int64_t>(min(t0 + t, tokens - 1)) * chunks + c0;
+                uint4 xv[U];
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < chunks) xv[u] = __ldg(xr + 32 * u);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (c0 + 32 * u < chunks) acc[t] = dot8<DT>(xv[u], wv[u], acc[t]);
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            float l = warp_sum(acc[t]);
+            if (bias) l = l + bias[e];
+            if (lane == 0 && t0 + t < tokens) logits[static_cast<int64_t>(t0 + t) * E + e] = l;
+        }
+    }
 }
 
 // Order-preserving key of a logit: larger is better, 0 is below every logit's.
@@ -84,100 +163,492 @@ __device__ __forceinline__ void warp_route(const float *row, int E, int k, int l
     *my_w = expf(mine - top) / sum;
 }
 
-__global__ void __launch_bounds__(32) few_route_kernel(const float *logits, int E, int k, int32_t *idx, float *w) {
-    griddep_wait();
-    griddep_launch_dependents();
-    int e;
-    float p;
-    warp_route<32>(logits + static_cast<int64_t>(blockIdx.x) * E, E, k, threadIdx.x, &e, &p);
-    if (static_cast<int>(threadIdx.x) < k) {
-        idx[blockIdx.x * k + threadIdx.x] = e;
-        w[blockIdx.x * k + threadIdx.x] = p;
-    }
+struct FewParams {
+    const void *x, *w_gate, *w_up, *w_down;
+    const float *logits;
+    int *counters;  // the next tile, then per chosen expert the stage-1 warps that stored h
+    void *h_hi, *h_lo, *out;
+    int32_t *err;
+    int T, k, E, d_h, d_e;
+    int stages, stage_bytes;
+};
+
+// D (16 x 8 fp32) += A (16 x 16) B (16 x 8)
+template <int DT>
+__device__ __forceinline__ void mma_16816(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    if constexpr (DT == kBF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+                     "{%0, %1, %2, %3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
 }
 
-// one warp per (routed pair, feature)
-template <int DT>
-__global__ void __launch_bounds__(FEW_WARPS * 32)
-    few_gate_up_kernel(const void *x, const void *w_gate, const void *w_up, const int32_t *idx, const float *w,
-                       int pairs, int k, int d_h, int d_e, void *h_hi, void *h_lo) {
-    using T = typename Elem<DT>::T;
-    griddep_wait();
-    griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * FEW_WARPS + (threadIdx.x >> 5);
-    const int pair = static_cast<int>(job / d_e), f = static_cast<int>(job % d_e);
-    if (pair >= pairs) return;
-    const int64_t row = (static_cast<int64_t>(idx[pair]) * d_e + f) * d_h;
-    const uint4 *xr = reinterpret_cast<const uint4 *>(static_cast<const T *>(x) + static_cast<int64_t>(pair / k) * d_h);
-    const uint4 *gr = reinterpret_cast<const uint4 *>(static_cast<const T *>(w_gate) + row);
-    const uint4 *ur = reinterpret_cast<const uint4 *>(static_cast<const T *>(w_up) + row);
-    float g = 0.0f, u = 0.0f;
-    for (int c = lane; c < d_h / 8; c += 32) {
-        const uint4 xv = xr[c];
-        g = dot8<DT>(xv, gr[c], g);
-        u = dot8<DT>(xv, ur[c], u);
-    }
-    g = warp_sum(g);
-    u = warp_sum(u);
-    if (lane == 0) {
-        const float h = g / (1.0f + __expf(-g)) * u * w[pair];
-        const T hi = from_f32<T>(h);
-        const int64_t o = static_cast<int64_t>(pair) * d_e + f;
-        static_cast<T *>(h_hi)[o] = hi;
-        static_cast<T *>(h_lo)[o] = from_f32<T>(h - to_f32(hi));
-    }
+// four 8 x 8 matrices, each lane giving the address of one row of one of them
+__device__ __forceinline__ uint4 ldmatrix_x4(uint32_t addr) {
+    uint4 r;
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "r"(addr)
+                 : "memory");
+    return r;
 }
 
-// one warp per (token, output)
-template <int DT>
-__global__ void __launch_bounds__(FEW_WARPS * 32)
-    few_down_kernel(const void *h_hi, const void *h_lo, const void *w_down, const int32_t *idx, int tokens, int k,
-                    int d_h, int d_e, void *out) {
-    using T = typename Elem<DT>::T;
+__device__ __forceinline__ void row_copy(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar, uint64_t policy) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(policy)
+        : "memory");
+}
+
+// shared memory after the ring: chosen experts and pairs (at most T * k of each)
+struct FewSmem {
+    uint8_t *ring, *zeros;  // zeros: a row of x or h for a token that is not routed here
+    uint64_t *bars;
+    float4 *partial;  // [FEW_PARTS][FEW_CONSUMERS][NT][32]
+    int *queue, *act_e, *act_base, *topk_e;
+    uint32_t *act_mask;
+    float *pair_w, *topk_w;
+};
+__host__ __device__ constexpr int few_fixed_bytes(int nt, int pairs) {
+    return FEW_BARS * 8 + FEW_ROW + FEW_PARTS * FEW_CONSUMERS * nt * 512 + FEW_QUEUE * 4 + pairs * 24;
+}
+
+template <int DT, int NT>
+__global__ void __launch_bounds__(FEW_THREADS, 1)
+    few_layer_kernel(const __grid_constant__ CUtensorMap tm_gate, const __grid_constant__ CUtensorMap tm_up,
+                     const __grid_constant__ CUtensorMap tm_down, const FewParams p) {
+    using El = typename Elem<DT>::T;
+    extern __shared__ uint8_t few_unaligned[];
+    uint8_t *few_raw = few_unaligned + ((1024u - (smem_u32(few_unaligned) & 1023u)) & 1023u);
+    const int pairs = p.T * p.k;
+    FewSmem sm;
+    sm.ring = few_raw;
+    sm.bars = reinterpret_cast<uint64_t *>(few_raw + p.stages * p.stage_bytes);
+    sm.zeros = reinterpret_cast<uint8_t *>(sm.bars + FEW_BARS);
+    sm.partial = reinterpret_cast<float4 *>(sm.zeros + FEW_ROW);
+    sm.queue = reinterpret_cast<int *>(sm.partial + FEW_PARTS * FEW_CONSUMERS * NT * 32);
+    sm.act_e = sm.queue + FEW_QUEUE;
+    sm.act_base = sm.act_e + pairs;
+    sm.topk_e = sm.act_base + pairs;
+    sm.act_mask = reinterpret_cast<uint32_t *>(sm.topk_e + pairs);
+    sm.pair_w = reinterpret_cast<float *>(sm.act_mask + pairs);
+    sm.topk_w = sm.pair_w + pairs;
+    __shared__ int abort_word, n_act_word;
+    volatile int *abort_flag = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t bar0 = smem_u32(sm.bars);
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (FEW_MAX_STAGES + i); };
+    auto tqf_bar = [&](int i) { return bar0 + 8u * (2 * FEW_MAX_STAGES + i); };
+    auto tqe_bar = [&](int i) { return bar0 + 8u * (2 * FEW_MAX_STAGES + FEW_QUEUE + i); };
+    auto pf_bar = [&](int i) { return bar0 + 8u * (2 * FEW_MAX_STAGES + 2 * FEW_QUEUE + i); };
+    auto pe_bar = [&](int i) { return bar0 + 8u * (2 * FEW_MAX_STAGES + 2 * FEW_QUEUE + FEW_PARTS + i); };
+    uint32_t *mask = reinterpret_cast<uint32_t *>(sm.ring);  // [E] while routing
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < p.stages; ++i) {
+            mbar_init(full_bar(i), 2);  // the weights' and the rows' copying warps
+            mbar_init(empty_bar(i), FEW_CONSUMERS);
+        }
+        for (int i = 0; i < FEW_QUEUE; ++i) {
+            mbar_init(tqf_bar(i), 1);
+            mbar_init(tqe_bar(i), FEW_CONSUMERS + 1 + FEW_FINISHERS);
+        }
+        for (int i = 0; i < FEW_PARTS; ++i) {
+            mbar_init(pf_bar(i), FEW_CONSUMERS);
+            mbar_init(pe_bar(i), FEW_FINISHERS);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+    }
+    for (int e = threadIdx.x; e < p.E; e += FEW_THREADS) mask[e] = 0u;
+    for (int i = threadIdx.x; i < FEW_ROW / 4; i += FEW_THREADS) reinterpret_cast<uint32_t *>(sm.zeros)[i] = 0u;
+    __syncthreads();
     griddep_wait();
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31;
-    const int64_t job = static_cast<int64_t>(blockIdx.x) * FEW_WARPS + (threadIdx.x >> 5);
-    const int t = static_cast<int>(job / d_h), j = static_cast<int>(job % d_h);
-    if (t >= tokens) return;
-    float acc = 0.0f;
-    for (int s = 0; s < k; ++s) {
-        const int64_t pair = static_cast<int64_t>(t) * k + s;
-        const uint4 *hi = reinterpret_cast<const uint4 *>(static_cast<const T *>(h_hi) + pair * d_e);
-        const uint4 *lo = reinterpret_cast<const uint4 *>(static_cast<const T *>(h_lo) + pair * d_e);
-        const uint4 *wr = reinterpret_cast<const uint4 *>(static_cast<const T *>(w_down) +
-                                                          (static_cast<int64_t>(idx[pair]) * d_h + j) * d_e);
-        for (int c = lane; c < d_e / 8; c += 32) {
-            acc = dot8<DT>(hi[c], wr[c], acc);
-            acc = dot8<DT>(lo[c], wr[c], acc);
+
+    // ------------------------------- routing -------------------------------
+    for (int t = warp; t < p.T; t += FEW_THREADS / 32) {
+        const float *row = p.logits + static_cast<int64_t>(t) * p.E;
+        int e;
+        float w;
+        if (p.E <= 64)
+            warp_route<2>(row, p.E, p.k, lane, &e, &w);
+        else if (p.E <= 256)
+            warp_route<8>(row, p.E, p.k, lane, &e, &w);
+        else
+            warp_route<32>(row, p.E, p.k, lane, &e, &w);
+        if (lane < p.k) {
+            sm.topk_e[t * p.k + lane] = e;
+            sm.topk_w[t * p.k + lane] = w;
+            atomicOr(&mask[e], 1u << t);
         }
     }
-    acc = warp_sum(acc);
-    if (lane == 0) static_cast<T *>(out)[static_cast<int64_t>(t) * d_h + j] = from_f32<T>(acc);
-}
+    __syncthreads();
+    if (warp == 0) {  // the chosen experts in ascending order, their tokens, their first row of h
+        int n = 0, base = 0;
+        for (int e0 = 0; e0 < p.E; e0 += 32) {
+            const int e = e0 + lane;
+            const uint32_t m = e < p.E ? mask[e] : 0u;
+            const uint32_t has = __ballot_sync(0xffffffffu, m != 0u);
+            if (has == 0u) continue;
+            int rows = __popc(m), before = rows;
+#pragma unroll
+            for (int s = 1; s < 32; s <<= 1) {
+                const int v = __shfl_up_sync(0xffffffffu, before, s);
+                if (lane >= s) before += v;
+            }
+            if (m != 0u) {
+                const int a = n + __popc(has & ((1u << lane) - 1u));
+                sm.act_e[a] = e;
+                sm.act_mask[a] = m;
+                sm.act_base[a] = base + before - rows;
+                mask[e] = static_cast<uint32_t>(a);
+            }
+            n += __popc(has);
+            base += __shfl_sync(0xffffffffu, before, 31);
+        }
+        if (lane == 0) n_act_word = n;
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < pairs; i += FEW_THREADS) {
+        const uint32_t a = mask[sm.topk_e[i]];
+        sm.pair_w[sm.act_base[a] + __popc(sm.act_mask[a] & ((1u << (i / p.k)) - 1u))] = sm.topk_w[i];
+    }
+    // the ring was written through the generic proxy; bulk copies follow
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncthreads();
+    const int n_act = n_act_word;
+    const int tiles_e = p.d_e / 8;           // stage-1 tiles of an expert
+    const int n1 = n_act * tiles_e, total = n1 + p.d_h / 16;
+    const int steps1 = (p.d_h + FEW_COLS - 1) / FEW_COLS, steps2 = (p.d_e + FEW_COLS - 1) / FEW_COLS;
 
-template <int DT>
-cudaError_t launch_typed(const void *x, const void *w_gate, const void *w_up, const void *w_down, int64_t T,
-                         int64_t d_h, int64_t d_e, int64_t k, const int32_t *idx, const float *w, void *h_hi,
-                         void *h_lo, void *out, cudaStream_t stream) {
-    const int64_t pairs = T * k;
-    cudaError_t e = launch_pdl(few_gate_up_kernel<DT>, dim3(static_cast<unsigned>((pairs * d_e + FEW_WARPS - 1) / FEW_WARPS)),
-                               dim3(FEW_WARPS * 32), 0, stream, x, w_gate, w_up, idx, w, (int)pairs, (int)k,
-                               (int)d_h, (int)d_e, h_hi, h_lo);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(few_down_kernel<DT>, dim3(static_cast<unsigned>((T * d_h + FEW_WARPS - 1) / FEW_WARPS)),
-                      dim3(FEW_WARPS * 32), 0, stream, (const void *)h_hi, (const void *)h_lo, w_down, idx, (int)T,
-                      (int)k, (int)d_h, (int)d_e, out);
+    if (warp == FEW_CONSUMERS || warp == FEW_CONSUMERS + 1) {
+        const bool rows_warp = warp > FEW_CONSUMERS;
+        const uint64_t policy = rows_warp ? l2_policy_evict_last() : l2_policy_evict_first();
+        int stage = 0, slot = 0, next = 0, ready = -1;  // ready: experts up to here have their h
+        uint32_t phase = 0, qphase = 0;
+        bool ok = true;
+        auto advance = [&]() {
+            if (++stage == p.stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+        };
+        // the next stage, once free, gets `bytes` of this warp's copies
+        auto open = [&](uint32_t bytes) {
+            int free = 1;
+            if (lane == 0) {
+                free = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err) ? 1 : 0;
+                if (free) mbar_arrive_expect_tx(full_bar(stage), bytes);
+            }
+            return __shfl_sync(0xffffffffu, free, 0) != 0;
+        };
+        // `n` rows of `bytes` from each lane's src
+        auto copy_rows = [&](int n, uint32_t bytes, const uint8_t *src) {
+            if (!open(n * bytes)) return false;
+            if (lane < n)
+                row_copy(smem_u32(sm.ring + stage * p.stage_bytes + 2 * FEW_HALF + lane * FEW_ROW), src, bytes, full_bar(stage),
+                         policy);
+            advance();
+            return true;
+        };
+        // 16 weight rows: 8 of row r0 of map m0, 8 of row r1 of map m1 (columns past the end read as zeros)
+        auto copy_weights = [&](const CUtensorMap *m0, const CUtensorMap *m1, int r0, int r1, int c) {
+            if (!open(2 * FEW_HALF)) return false;
+            if (lane == 0) {
+                const uint32_t dst = smem_u32(sm.ring + stage * p.stage_bytes);
+                tma_load_3d_hint(dst, m0, full_bar(stage), 0, r0, c * (FEW_COLS / 64), policy);
+                tma_load_3d_hint(dst + FEW_HALF, m1, full_bar(stage), 0, r1, c * (FEW_COLS / 64), policy);
+            }
+            advance();
+            return true;
+        };
+        auto bytes_of = [](int K, int c) { return static_cast<uint32_t>(min(FEW_COLS, K - c * FEW_COLS)) * 2u; };
+        if (!rows_warp && lane == 0) next = atomicAdd(p.counters, 1);
+        while (ok) {
+            int tile = 0, free = 1;
+            if (!rows_warp) {
+                if (lane == 0) {
+                    free = mbar_wait_bounded(tqe_bar(slot), qphase ^ 1u, abort_flag, p.err) ? 1 : 0;
+                    if (free) {
+                        sm.queue[slot] = next;
+                        mbar_arrive(tqf_bar(slot));
+                    }
+                    tile = next;
+                    if (tile < total) next = atomicAdd(p.counters, 1);  // its latency passes under this tile
+                }
+            } else if (lane == 0) {
+                free = mbar_wait_bounded(tqf_bar(slot), qphase, abort_flag, p.err) ? 1 : 0;
+                if (free) {
+                    tile = sm.queue[slot];
+                    mbar_arrive(tqe_bar(slot));
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, free, 0)) break;
+            tile = __shfl_sync(0xffffffffu, tile, 0);
+            if (tile >= total) break;
+            if (++slot == FEW_QUEUE) {
+                slot = 0;
+                qphase ^= 1u;
+            }
+            if (tile < n1) {
+                const int a = tile / tiles_e, row = sm.act_e[a] * p.d_e + (tile - a * tiles_e) * 8;
+                const uint32_t m = sm.act_mask[a];
+                const int n = __popc(m), t = lane < n ? static_cast<int>(__fns(m, 0, lane + 1)) : 0;
+                const uint8_t *src = static_cast<const uint8_t *>(p.x) + static_cast<int64_t>(t) * p.d_h * 2;
+                for (int c = 0; c < steps1 && ok; ++c)
+                    ok = rows_warp ? copy_rows(n, bytes_of(p.d_h, c), src + c * FEW_COLS * 2)
+                                   : copy_weights(&tm_gate, &tm_up, row, row, c);
+            } else {
+                for (int a = 0; a < n_act && ok; ++a) {
+                    const int row = sm.act_e[a] * p.d_h + (tile - n1) * 16;
+                    const int rows = __popc(sm.act_mask[a]);
+                    const int r = sm.act_base[a] + (lane < rows ? lane : lane - rows);
+                    const uint8_t *src =
+                        static_cast<const uint8_t *>(lane < rows ? p.h_hi : p.h_lo) + static_cast<int64_t>(r) * p.d_e * 2;
+                    if (rows_warp && a > ready) {  // h of this expert: every stage-1 warp has stored it
+                        int have = 1;
+                        if (lane == 0)
+                            have = counter_wait_bounded(p.counters + 1 + a, tiles_e * 2 * NT, abort_flag, p.err) ? 1 : 0;
+                        ok = __shfl_sync(0xffffffffu, have, 0) != 0;
+                        __syncwarp();
+                        asm volatile("fence.proxy.async.global;" ::: "memory");
+                        ready = a;
+                    }
+                    for (int c = 0; c < steps2 && ok; ++c)
+                        ok = rows_warp ? copy_rows(2 * rows, bytes_of(p.d_e, c), src + c * FEW_COLS * 2)
+                                       : copy_weights(&tm_down, &tm_down, row, row + 8, c);
+                }
+            }
+        }
+        if (*abort_flag && lane == 0) {
+            // copies in flight land before shared memory goes away; a stage
+            // that the other warp never filled stays open: 10 ms each
+            for (int i = 0; i < p.stages; ++i) {
+                const int st = (stage + i) % p.stages;
+                const uint32_t par = stage + i < p.stages ? phase ^ 1u : phase;
+                const unsigned long long start = global_timer_ns();
+                while (!mbar_try_wait(full_bar(st), par) && global_timer_ns() - start < 10000000ull) {
+                }
+            }
+        }
+        return;
+    }
+
+    // the other warps take every tile; every lane polls, which on the usual
+    // first try needs no broadcast
+    int slot = 0, local = 0;
+    uint32_t qphase = 0;
+    auto wait = [&](uint32_t bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+        return __all_sync(0xffffffffu, mbar_wait_bounded(bar, parity, abort_flag, p.err)) != 0;
+    };
+    auto take = [&]() {  // the next tile, `total` or more when there is none
+        if (!wait(tqf_bar(slot), qphase)) return total;
+        const int tile = sm.queue[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tqe_bar(slot));
+        if (++slot == FEW_QUEUE) {
+            slot = 0;
+            qphase ^= 1u;
+        }
+        return tile;
+    };
+    if (warp >= FEW_CONSUMERS + 2) {
+        // -------------------------------- joining --------------------------------
+        const int fin = warp - FEW_CONSUMERS - 2;
+        for (int tile = take(); tile < total; tile = take(), ++local) {
+            const int buf = local % FEW_PARTS;
+            if (!wait(pf_bar(buf), static_cast<uint32_t>(local / FEW_PARTS) & 1u)) break;
+            const float *f = reinterpret_cast<const float *>(sm.partial + buf * FEW_CONSUMERS * NT * 32);
+            if (tile < n1) {
+                const int a = tile / tiles_e;
+                if (fin < 2 * NT) {
+                    const int i = fin * 32 + lane, n = i >> 6, feat = i & 7, t8 = (i >> 3) & 7, t = n * 8 + t8;
+                    const uint32_t m = sm.act_mask[a];
+                    if ((m >> t) & 1u) {
+                        float gate = 0.0f, up = 0.0f;
+                        const int at = (n * 32 + feat * 4 + (t8 >> 1)) * 4 + (t8 & 1);
+#pragma unroll
+                        for (int w = 0; w < FEW_CONSUMERS; ++w) {
+                            gate += f[w * NT * 128 + at];
+                            up += f[w * NT * 128 + at + 2];
+                        }
+                        const int r = sm.act_base[a] + __popc(m & ((1u << t) - 1u));
+                        const float h = gate / (1.0f + __expf(-gate)) * up * sm.pair_w[r];
+                        const El top = from_f32<El>(h);
+                        const int64_t o = static_cast<int64_t>(r) * p.d_e + (tile - a * tiles_e) * 8 + feat;
+                        static_cast<El *>(p.h_hi)[o] = top;
+                        static_cast<El *>(p.h_lo)[o] = from_f32<El>(h - to_f32(top));
+                    }
+                    __threadfence();
+                    asm volatile("fence.proxy.async.global;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) counter_publish(p.counters + 1 + a);
+                }
+            } else {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int i = fin * 32 + lane, r = i & 15, t8 = i >> 4, t = n * 8 + t8;
+                    if (t < p.T) {
+                        float v = 0.0f;
+                        const int at = (n * 32 + (r & 7) * 4 + (t8 >> 1)) * 4 + (t8 & 1) + (r >> 3) * 2;
+#pragma unroll
+                        for (int w = 0; w < FEW_CONSUMERS; ++w) v += f[w * NT * 128 + at];
+                        static_cast<El *>(p.out)[static_cast<int64_t>(t) * p.d_h + (tile - n1) * 16 + r] = from_f32<El>(v);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(pe_bar(buf));
+        }
+        return;
+    }
+
+    // ------------------------------ multiplying ------------------------------
+    // a lane gives the address of row lane % 8 of matrix lane / 8.  Weights:
+    // the matrices are rows 0-7, then 8-15, of 8 columns, then of the next 8;
+    // tokens: four times 8 columns
+    const int mrow = lane & 7, mat = lane >> 3;
+    const uint32_t ring = smem_u32(sm.ring), zeros = smem_u32(sm.zeros) + mat * 16;
+    const uint32_t wrow = (mat & 1) * FEW_HALF + warp * 1024 + mrow * 128;
+    const uint32_t trow = 2 * FEW_HALF + warp * 128 + mat * 16;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int tile = take(); tile < total; tile = take(), ++local) {
+        float acc[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+        const bool first = tile < n1;
+        const int a0 = first ? tile / tiles_e : 0, a1 = first ? a0 + 1 : n_act;
+        const int K = first ? p.d_h : p.d_e, steps = first ? steps1 : steps2;
+        for (int a = a0; a < a1 && ok; ++a) {
+            const uint32_t m = sm.act_mask[a];
+            const uint32_t rest = __popc(m) * FEW_ROW;  // from a row of h to its rest
+            uint32_t token[NT];                         // the lane's token's row in a stage
+            bool here[NT], any[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int t = n * 8 + mrow;
+                here[n] = (m >> t) & 1u;
+                any[n] = ((m >> (8 * n)) & 255u) != 0u;
+                token[n] = trow + __popc(m & ((1u << t) - 1u)) * FEW_ROW;
+            }
+            for (int c = 0; c < steps; ++c) {
+                ok = wait(full_bar(stage), phase);
+                if (!ok) break;
+                if (warp * 64 < K - c * FEW_COLS) {
+                    const uint32_t st = ring + stage * p.stage_bytes;
+                    uint4 w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) w[j] = ldmatrix_x4(st + wrow + (((2 * j + (mat >> 1)) ^ mrow) << 4));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        if (!any[n]) continue;
+                        const uint32_t b = here[n] ? st + token[n] : zeros;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const uint4 v = ldmatrix_x4(b + j * 64);
+                            mma_16816<DT>(acc[n], w[2 * j], v.x, v.y);
+                            mma_16816<DT>(acc[n], w[2 * j + 1], v.z, v.w);
+                        }
+                        if (!first) {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const uint4 v = ldmatrix_x4((here[n] ? b + rest : zeros) + j * 64);
+                                mma_16816<DT>(acc[n], w[2 * j], v.x, v.y);
+                                mma_16816<DT>(acc[n], w[2 * j + 1], v.z, v.w);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty_bar(stage));
+                if (++stage == p.stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+        if (!ok) break;
+        const int buf = local % FEW_PARTS;
+        if (!wait(pe_bar(buf), (static_cast<uint32_t>(local / FEW_PARTS) & 1u) ^ 1u)) break;
+        float4 *part = sm.partial + buf * FEW_CONSUMERS * NT * 32;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+            part[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(pf_bar(buf));
+    }
 }
 
 size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
+
+template <int DT, int TT>
+cudaError_t launch_logits(const void *x, const void *w_g, const float *bias, int64_t T, int64_t d_h, int64_t E,
+                          float *logits, int *counters, int n_counters, cudaStream_t stream) {
+    return launch_pdl(few_logits_kernel<DT, TT>, dim3(static_cast<unsigned>((E + LOGIT_WARPS - 1) / LOGIT_WARPS)),
+                      dim3(LOGIT_WARPS * 32), 0, stream, static_cast<const uint4 *>(x), static_cast<const uint4 *>(w_g),
+                      bias, (int)T, (int)(d_h / 8), (int)E, logits, counters, n_counters);
+}
+
+// [E, N, K] weights as 64 columns x (E N) rows x K / 64 slabs; a box is 8 rows
+// of 8 slabs, slab by slab
+bool weight_map(CUtensorMap *m, const void *w, int64_t E, int64_t N, int64_t K) {
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(E * N), static_cast<uint64_t>(K / 64)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(K) * 2, 128};
+    const uint32_t box[3] = {64, 8, FEW_COLS / 64};
+    return encode_tma_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 3, w, dims, strides, box, 1);
+}
+
+template <int DT, int NT> cudaError_t launch_layer(FewParams p, cudaStream_t stream) {
+    const int pairs = p.T * p.k;
+    p.stage_bytes = (2 * FEW_HALF + 2 * p.T * FEW_ROW + 1023) / 1024 * 1024;
+    const int stages = (FEW_SMEM_MAX - 1024 - few_fixed_bytes(NT, pairs)) / p.stage_bytes;
+    p.stages = stages < FEW_MAX_STAGES ? stages : FEW_MAX_STAGES;
+    const int smem = 1024 + p.stages * p.stage_bytes + few_fixed_bytes(NT, pairs);
+    CUtensorMap maps[3];
+    if (!weight_map(&maps[0], p.w_gate, p.E, p.d_e, p.d_h) || !weight_map(&maps[1], p.w_up, p.E, p.d_e, p.d_h) ||
+        !weight_map(&maps[2], p.w_down, p.E, p.d_h, p.d_e))
+        return cudaErrorInvalidValue;
+    auto kern = few_layer_kernel<DT, NT>;
+    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, FEW_SMEM_MAX);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    }
+    const int64_t experts = pairs < p.E ? pairs : p.E;
+    const int64_t tiles = experts * (p.d_e / 8) + p.d_h / 16;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(mlp_grid(tiles))), dim3(FEW_THREADS), static_cast<size_t>(smem),
+                      stream, maps[0], maps[1], maps[2], p);
+}
+
+template <int DT>
+cudaError_t launch_typed(const void *w_g, const float *bias, FewParams p, float *logits, int n_counters,
+                         cudaStream_t stream) {
+    auto run = [&](auto logits_of) { return logits_of(p.x, w_g, bias, p.T, p.d_h, p.E, logits, p.counters, n_counters, stream); };
+    cudaError_t e = p.T == 1 ? run(launch_logits<DT, 1>) : p.T == 2 ? run(launch_logits<DT, 2>)
+                    : p.T <= 4 ? run(launch_logits<DT, 4>) : run(launch_logits<DT, 8>);
+    if (e != cudaSuccess) return e;
+    return p.T <= 8 ? launch_layer<DT, 1>(p, stream) : launch_layer<DT, 2>(p, stream);
+}
 
 }  // namespace
 
 size_t forward_few_ws_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k) {
     (void)d_h;
-    return round_up(static_cast<size_t>(T * E) * 4) + 2 * round_up(static_cast<size_t>(T * k) * 4) +
+    return round_up(static_cast<size_t>(T * E) * 4) + round_up(static_cast<size_t>(T * k + 1) * 4) +
            2 * round_up(static_cast<size_t>(T * k * d_e) * 2);
 }
 
@@ -187,20 +658,26 @@ cudaError_t launch_forward_few(const void *x, const void *w_g, const float *bias
     char *at = static_cast<char *>(ws);
     float *logits = reinterpret_cast<float *>(at);
     at += round_up(static_cast<size_t>(T * E) * 4);
-    int32_t *idx = reinterpret_cast<int32_t *>(at);
-    at += round_up(static_cast<size_t>(T * k) * 4);
-    float *w = reinterpret_cast<float *>(at);
-    at += round_up(static_cast<size_t>(T * k) * 4);
-    void *h_hi = at;
-    void *h_lo = at + round_up(static_cast<size_t>(T * k * d_e) * 2);
-    cudaError_t e = launch_gate_topk(x, w_g, bias, T, d_h, E, k, dtype, logits, idx, w, nullptr, err, stream);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(few_route_kernel, dim3(static_cast<unsigned>(T)), dim3(32), 0, stream, (const float *)logits, (int)E,
-                   (int)k, idx, w);
-    if (e != cudaSuccess) return e;
-    if (dtype == kBF16)
-        return launch_typed<kBF16>(x, w_gate, w_up, w_down, T, d_h, d_e, k, idx, w, h_hi, h_lo, out, stream);
-    return launch_typed<kF16>(x, w_gate, w_up, w_down, T, d_h, d_e, k, idx, w, h_hi, h_lo, out, stream);
+    FewParams p{};
+    p.x = x;
+    p.w_gate = w_gate;
+    p.w_up = w_up;
+    p.w_down = w_down;
+    p.logits = logits;
+    p.counters = reinterpret_cast<int *>(at);
+    at += round_up(static_cast<size_t>(T * k + 1) * 4);
+    p.h_hi = at;
+    p.h_lo = at + round_up(static_cast<size_t>(T * k * d_e) * 2);
+    p.out = out;
+    p.err = err;
+    p.T = static_cast<int>(T);
+    p.k = static_cast<int>(k);
+    p.E = static_cast<int>(E);
+    p.d_h = static_cast<int>(d_h);
+    p.d_e = static_cast<int>(d_e);
+    const int n_counters = static_cast<int>(T * k + 1);
+    if (dtype == kBF16) return launch_typed<kBF16>(w_g, bias, p, logits, n_counters, stream);
+    return launch_typed<kF16>(w_g, bias, p, logits, n_counters, stream);
 }
 
 }  // namespace moe
