@@ -62,49 +62,48 @@ __device__ __forceinline__ float warp_sum(float v) {
 }
 
 // logits[t, e] in the gate's fixed order (lane L sums its 8-element chunks
-// L, L + 32, ... in ascending order, then the butterfly), a warp per expert;
-// also clears the counters of the second launch.  TT tokens at a time.
+// L, L + 32, ... in ascending order, then the butterfly), a warp for one expert
+// and TT tokens; also clears the counters of the second launch.
 template <int DT, int TT>
 __global__ void __launch_bounds__(LOGIT_WARPS * 32)
     few_logits_kernel(const uint4 *__restrict__ x, const uint4 *__restrict__ w_g, const float *__restrict__ bias,
                       int tokens, int chunks, int E, float *__restrict__ logits, int *__restrict__ counters,
                       int n_counters) {
     griddep_launch_dependents();
-    const int lane = threadIdx.x & 31, e = blockIdx.x * LOGIT_WARPS + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, e = blockIdx.x * LOGIT_WARPS + (threadIdx.x >> 5), t0 = blockIdx.y * TT;
     const uint4 *w = w_g + static_cast<int64_t>(e < E ? e : 0) * chunks;
     for (int c = lane * 8; c < chunks; c += 256)  // 128 bytes a lane
         asm volatile("prefetch.global.L2 [%0];" ::"l"(w + c));
     griddep_wait();
-    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < n_counters; i += gridDim.x * blockDim.x) counters[i] = 0;
+    if (blockIdx.x == 0 && blockIdx.y == 0)
+        for (int i = threadIdx.x; i < n_counters; i += LOGIT_WARPS * 32) counters[i] = 0;
     if (e >= E) return;
-    constexpr int U = TT <= 2 ? 7 : (TT <= 4 ? 4 : 2);  // chunks in flight
-    for (int t0 = 0; t0 < tokens; t0 += TT) {
-        float acc[TT];
+    constexpr int U = TT == 1 ? 8 : (TT == 2 ? 6 : 4);  // chunks in flight, each of w and of TT tokens
+    float acc[TT];
 #pragma unroll
-        for (int t = 0; t < TT; ++t) acc[t] = 0.0f;
-        for (int c0 = lane; c0 < chunks; c0 += 32 * U) {
-            uint4 wv[U];
+    for (int t = 0; t < TT; ++t) acc[t] = 0.0f;
+    for (int c0 = lane; c0 < chunks; c0 += 32 * U) {
+        uint4 wv[U], xv[TT][U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (c0 + 32 * u < chunks) wv[u] = __ldg(w + c0 + 32 * u);
+#pragma unroll
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (c0 + 32 * u < chunks) wv[u] = __ldg(w + c0 + 32 * u);
+                if (c0 + 32 * u < chunks)
+                    xv[t][u] = __ldg(x + static_cast<int64_t>(min(t0 + t, tokens - 1)) * chunks + c0 + 32 * u);
 #pragma unroll
-            for (int t = 0; t < TT; ++t) {
-                const uint4 *xr = x + static_cast<int64_t>(min(t0 + t, tokens - 1)) * chunks + c0;
-                uint4 xv[U];
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + 32 * u < chunks) xv[u] = __ldg(xr + 32 * u);
+            for (int u = 0; u < U; ++u)
+                if (c0 + 32 * u < chunks) acc[t] = dot8<DT>(xv[t][u], wv[u], acc[t]);
+    }
 #pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (c0 + 32 * u < chunks) acc[t] = dot8<DT>(xv[u], wv[u], acc[t]);
-            }
-        }
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            float l = warp_sum(acc[t]);
-            if (bias) l = l + bias[e];
-            if (lane == 0 && t0 + t < tokens) logits[static_cast<int64_t>(t0 + t) * E + e] = l;
-        }
+    for (int t = 0; t < TT; ++t) {
+        float l = warp_sum(acc[t]);
+        if (bias) l = l + bias[e];
+        if (lane == 0 && t0 + t < tokens) logits[static_cast<int64_t>(t0 + t) * E + e] = l;
     }
 }
 
@@ -163,6 +162,32 @@ __device__ __forceinline__ void warp_route(const float *row, int E, int k, int l
     *my_w = expf(mine - top) / sum;
 }
 
+// Waits until counter `a` has reached `target` and returns the last expert up
+// to which all have (a - 1 when the wait gave up).  The lanes look at 32
+// counters at once: one at a time, each look cost its latency (about 1 us an
+// expert, in the way of the copies).
+__device__ __forceinline__ int experts_ready(const int *counters, int a, int n_act, int target, int lane,
+                                             volatile int *abort_flag, int *err) {
+    const unsigned long long start = global_timer_ns();
+    for (;;) {
+        const bool yes = a + lane < n_act && counter_load_acquire(counters + a + lane) >= target;
+        const uint32_t done = __ballot_sync(0xffffffffu, yes);
+        if (done & 1u) {
+            // the copies of h that follow read through the async proxy
+            asm volatile("fence.proxy.async.global;" ::: "memory");
+            __syncwarp();
+            return a + __ffs(~done) - 2 + (done == 0xffffffffu ? 33 : 0);
+        }
+        const bool late = *abort_flag || global_timer_ns() - start > kWaitTimeoutNs;
+        if (__any_sync(0xffffffffu, late)) {
+            *abort_flag = 1;
+            if (err && lane == 0) atomicExch(err, kErrTimeout);
+            return a - 1;
+        }
+        __nanosleep(50);
+    }
+}
+
 struct FewParams {
     const void *x, *w_gate, *w_up, *w_down;
     const float *logits;
@@ -170,7 +195,7 @@ struct FewParams {
     void *h_hi, *h_lo, *out;
     int32_t *err;
     int T, k, E, d_h, d_e;
-    int stages, stage_bytes;
+    int ring_bytes;
 };
 
 // D (16 x 8 fp32) += A (16 x 16) B (16 x 8)
@@ -214,9 +239,13 @@ struct FewSmem {
     uint32_t *act_mask;
     float *pair_w, *topk_w;
 };
+__host__ __device__ constexpr int few_stage_bytes(int tokens) {
+    return (2 * FEW_HALF + 2 * tokens * FEW_ROW + 1023) / 1024 * 1024;
+}
 __host__ __device__ constexpr int few_fixed_bytes(int nt, int pairs) {
     return FEW_BARS * 8 + FEW_ROW + FEW_PARTS * FEW_CONSUMERS * nt * 512 + FEW_QUEUE * 4 + pairs * 24;
 }
+static_assert(1024 + 3 * few_stage_bytes(16) + few_fixed_bytes(2, 16 * 32) <= FEW_SMEM_MAX, "three stages at least");
 
 template <int DT, int NT>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
@@ -228,7 +257,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     const int pairs = p.T * p.k;
     FewSmem sm;
     sm.ring = few_raw;
-    sm.bars = reinterpret_cast<uint64_t *>(few_raw + p.stages * p.stage_bytes);
+    sm.bars = reinterpret_cast<uint64_t *>(few_raw + p.ring_bytes);
     sm.zeros = reinterpret_cast<uint8_t *>(sm.bars + FEW_BARS);
     sm.partial = reinterpret_cast<float4 *>(sm.zeros + FEW_ROW);
     sm.queue = reinterpret_cast<int *>(sm.partial + FEW_PARTS * FEW_CONSUMERS * NT * 32);
@@ -238,7 +267,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     sm.act_mask = reinterpret_cast<uint32_t *>(sm.topk_e + pairs);
     sm.pair_w = reinterpret_cast<float *>(sm.act_mask + pairs);
     sm.topk_w = sm.pair_w + pairs;
-    __shared__ int abort_word, n_act_word;
+    __shared__ int abort_word, n_act_word, most_word;
     volatile int *abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t bar0 = smem_u32(sm.bars);
@@ -250,7 +279,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     auto pe_bar = [&](int i) { return bar0 + 8u * (2 * FEW_MAX_STAGES + 2 * FEW_QUEUE + FEW_PARTS + i); };
     uint32_t *mask = reinterpret_cast<uint32_t *>(sm.ring);  // [E] while routing
     if (threadIdx.x == 0) {
-        for (int i = 0; i < p.stages; ++i) {
+        for (int i = 0; i < FEW_MAX_STAGES; ++i) {
             mbar_init(full_bar(i), 2);  // the weights' and the rows' copying warps
             mbar_init(empty_bar(i), FEW_CONSUMERS);
         }
@@ -264,6 +293,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
         abort_word = 0;
         fence_mbar_init();
+        tma_prefetch_desc(&tm_gate);
+        tma_prefetch_desc(&tm_up);
+        tma_prefetch_desc(&tm_down);
     }
     for (int e = threadIdx.x; e < p.E; e += FEW_THREADS) mask[e] = 0u;
     for (int i = threadIdx.x; i < FEW_ROW / 4; i += FEW_THREADS) reinterpret_cast<uint32_t *>(sm.zeros)[i] = 0u;
@@ -290,13 +322,15 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     }
     __syncthreads();
     if (warp == 0) {  // the chosen experts in ascending order, their tokens, their first row of h
-        int n = 0, base = 0;
+        int n = 0, base = 0, most = 0;
         for (int e0 = 0; e0 < p.E; e0 += 32) {
             const int e = e0 + lane;
             const uint32_t m = e < p.E ? mask[e] : 0u;
             const uint32_t has = __ballot_sync(0xffffffffu, m != 0u);
             if (has == 0u) continue;
-            int rows = __popc(m), before = rows;
+            const int rows = __popc(m);
+            int before = rows;
+            most = max(most, rows);
 #pragma unroll
             for (int s = 1; s < 32; s <<= 1) {
                 const int v = __shfl_up_sync(0xffffffffu, before, s);
@@ -312,7 +346,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             n += __popc(has);
             base += __shfl_sync(0xffffffffu, before, 31);
         }
-        if (lane == 0) n_act_word = n;
+        most = __reduce_max_sync(0xffffffffu, most);
+        if (lane == 0) {
+            n_act_word = n;
+            most_word = most;
+        }
     }
     __syncthreads();
     for (int i = threadIdx.x; i < pairs; i += FEW_THREADS) {
@@ -323,6 +361,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncthreads();
     const int n_act = n_act_word;
+    // a stage holds 16 weight rows and the rows of the expert with the most tokens
+    const int stage_bytes = few_stage_bytes(most_word);
+    const int stages = min(FEW_MAX_STAGES, p.ring_bytes / stage_bytes);
     const int tiles_e = p.d_e / 8;           // stage-1 tiles of an expert
     const int n1 = n_act * tiles_e, total = n1 + p.d_h / 16;
     const int steps1 = (p.d_h + FEW_COLS - 1) / FEW_COLS, steps2 = (p.d_e + FEW_COLS - 1) / FEW_COLS;
@@ -334,7 +375,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         uint32_t phase = 0, qphase = 0;
         bool ok = true;
         auto advance = [&]() {
-            if (++stage == p.stages) {
+            if (++stage == stages) {
                 stage = 0;
                 phase ^= 1u;
             }
@@ -352,7 +393,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         auto copy_rows = [&](int n, uint32_t bytes, const uint8_t *src) {
             if (!open(n * bytes)) return false;
             if (lane < n)
-                row_copy(smem_u32(sm.ring + stage * p.stage_bytes + 2 * FEW_HALF + lane * FEW_ROW), src, bytes, full_bar(stage),
+                row_copy(smem_u32(sm.ring + stage * stage_bytes + 2 * FEW_HALF + lane * FEW_ROW), src, bytes, full_bar(stage),
                          policy);
             advance();
             return true;
@@ -361,7 +402,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         auto copy_weights = [&](const CUtensorMap *m0, const CUtensorMap *m1, int r0, int r1, int c) {
             if (!open(2 * FEW_HALF)) return false;
             if (lane == 0) {
-                const uint32_t dst = smem_u32(sm.ring + stage * p.stage_bytes);
+                const uint32_t dst = smem_u32(sm.ring + stage * stage_bytes);
                 tma_load_3d_hint(dst, m0, full_bar(stage), 0, r0, c * (FEW_COLS / 64), policy);
                 tma_load_3d_hint(dst + FEW_HALF, m1, full_bar(stage), 0, r1, c * (FEW_COLS / 64), policy);
             }
@@ -412,13 +453,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     const uint8_t *src =
                         static_cast<const uint8_t *>(lane < rows ? p.h_hi : p.h_lo) + static_cast<int64_t>(r) * p.d_e * 2;
                     if (rows_warp && a > ready) {  // h of this expert: every stage-1 warp has stored it
-                        int have = 1;
-                        if (lane == 0)
-                            have = counter_wait_bounded(p.counters + 1 + a, tiles_e * 2 * NT, abort_flag, p.err) ? 1 : 0;
-                        ok = __shfl_sync(0xffffffffu, have, 0) != 0;
-                        __syncwarp();
-                        asm volatile("fence.proxy.async.global;" ::: "memory");
-                        ready = a;
+                        ready = experts_ready(p.counters + 1, a, n_act, tiles_e * 2 * NT, lane, abort_flag, p.err);
+                        ok = ready >= a;
                     }
                     for (int c = 0; c < steps2 && ok; ++c)
                         ok = rows_warp ? copy_rows(2 * rows, bytes_of(p.d_e, c), src + c * FEW_COLS * 2)
@@ -429,9 +465,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         if (*abort_flag && lane == 0) {
             // copies in flight land before shared memory goes away; a stage
             // that the other warp never filled stays open: 10 ms each
-            for (int i = 0; i < p.stages; ++i) {
-                const int st = (stage + i) % p.stages;
-                const uint32_t par = stage + i < p.stages ? phase ^ 1u : phase;
+            for (int i = 0; i < stages; ++i) {
+                const int st = (stage + i) % stages;
+                const uint32_t par = stage + i < stages ? phase ^ 1u : phase;
                 const unsigned long long start = global_timer_ns();
                 while (!mbar_try_wait(full_bar(st), par) && global_timer_ns() - start < 10000000ull) {
                 }
@@ -468,8 +504,10 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             const float *f = reinterpret_cast<const float *>(sm.partial + buf * FEW_CONSUMERS * NT * 32);
             if (tile < n1) {
                 const int a = tile / tiles_e;
-                if (fin < 2 * NT) {
-                    const int i = fin * 32 + lane, n = i >> 6, feat = i & 7, t8 = (i >> 3) & 7, t = n * 8 + t8;
+                // 2 NT warps have values; at NT = 1 two pairs of warps take the
+                // tiles in turn, since making h visible costs 1 to 2 us
+                if (NT == 2 || (fin >> 1) == (local & 1)) {
+                    const int i = (NT == 2 ? fin : fin & 1) * 32 + lane, n = i >> 6, feat = i & 7, t8 = (i >> 3) & 7, t = n * 8 + t8;
                     const uint32_t m = sm.act_mask[a];
                     if ((m >> t) & 1u) {
                         float gate = 0.0f, up = 0.0f;
@@ -486,9 +524,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                         static_cast<El *>(p.h_hi)[o] = top;
                         static_cast<El *>(p.h_lo)[o] = from_f32<El>(h - to_f32(top));
                     }
-                    __threadfence();
                     asm volatile("fence.proxy.async.global;" ::: "memory");
-                    __syncwarp();
+                    __syncwarp();  // the publishing add releases the whole warp's stores
                     if (lane == 0) counter_publish(p.counters + 1 + a);
                 }
             } else {
@@ -546,7 +583,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 ok = wait(full_bar(stage), phase);
                 if (!ok) break;
                 if (warp * 64 < K - c * FEW_COLS) {
-                    const uint32_t st = ring + stage * p.stage_bytes;
+                    const uint32_t st = ring + stage * stage_bytes;
                     uint4 w[4];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) w[j] = ldmatrix_x4(st + wrow + (((2 * j + (mat >> 1)) ^ mrow) << 4));
@@ -572,7 +609,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(stage));
-                if (++stage == p.stages) {
+                if (++stage == stages) {
                     stage = 0;
                     phase ^= 1u;
                 }
@@ -595,7 +632,7 @@ size_t round_up(size_t v) { return (v + 255) / 256 * 256; }
 template <int DT, int TT>
 cudaError_t launch_logits(const void *x, const void *w_g, const float *bias, int64_t T, int64_t d_h, int64_t E,
                           float *logits, int *counters, int n_counters, cudaStream_t stream) {
-    return launch_pdl(few_logits_kernel<DT, TT>, dim3(static_cast<unsigned>((E + LOGIT_WARPS - 1) / LOGIT_WARPS)),
+    return launch_pdl(few_logits_kernel<DT, TT>, dim3(static_cast<unsigned>((E + LOGIT_WARPS - 1) / LOGIT_WARPS), static_cast<unsigned>((T + TT - 1) / TT)),
                       dim3(LOGIT_WARPS * 32), 0, stream, static_cast<const uint4 *>(x), static_cast<const uint4 *>(w_g),
                       bias, (int)T, (int)(d_h / 8), (int)E, logits, counters, n_counters);
 }
@@ -611,10 +648,8 @@ bool weight_map(CUtensorMap *m, const void *w, int64_t E, int64_t N, int64_t K) 
 
 template <int DT, int NT> cudaError_t launch_layer(FewParams p, cudaStream_t stream) {
     const int pairs = p.T * p.k;
-    p.stage_bytes = (2 * FEW_HALF + 2 * p.T * FEW_ROW + 1023) / 1024 * 1024;
-    const int stages = (FEW_SMEM_MAX - 1024 - few_fixed_bytes(NT, pairs)) / p.stage_bytes;
-    p.stages = stages < FEW_MAX_STAGES ? stages : FEW_MAX_STAGES;
-    const int smem = 1024 + p.stages * p.stage_bytes + few_fixed_bytes(NT, pairs);
+    p.ring_bytes = (FEW_SMEM_MAX - 1024 - few_fixed_bytes(NT, pairs)) / 1024 * 1024;
+    const int smem = 1024 + p.ring_bytes + few_fixed_bytes(NT, pairs);
     CUtensorMap maps[3];
     if (!weight_map(&maps[0], p.w_gate, p.E, p.d_e, p.d_h) || !weight_map(&maps[1], p.w_up, p.E, p.d_e, p.d_h) ||
         !weight_map(&maps[2], p.w_down, p.E, p.d_h, p.d_e))
@@ -638,8 +673,9 @@ template <int DT>
 cudaError_t launch_typed(const void *w_g, const float *bias, FewParams p, float *logits, int n_counters,
                          cudaStream_t stream) {
     auto run = [&](auto logits_of) { return logits_of(p.x, w_g, bias, p.T, p.d_h, p.E, logits, p.counters, n_counters, stream); };
-    cudaError_t e = p.T == 1 ? run(launch_logits<DT, 1>) : p.T == 2 ? run(launch_logits<DT, 2>)
-                    : p.T <= 4 ? run(launch_logits<DT, 4>) : run(launch_logits<DT, 8>);
+    // few warps: one token each; more: a row of w for two or four tokens
+    const int64_t dots = static_cast<int64_t>(p.T) * p.E;
+    cudaError_t e = dots <= 1024 ? run(launch_logits<DT, 1>) : dots <= 2048 ? run(launch_logits<DT, 2>) : run(launch_logits<DT, 4>);
     if (e != cudaSuccess) return e;
     return p.T <= 8 ? launch_layer<DT, 1>(p, stream) : launch_layer<DT, 2>(p, stream);
 }
