@@ -15,8 +15,9 @@
 //    of shared-memory stages: one warp copies weights (two 8-row boxes of TMA,
 //    each eight 64-column slabs with the 128-byte swizzle), another the rows
 //    that meet them (x, or h once its expert's tiles are done), so the weights
-//    of a stage-2 tile are under way before h is.  Eight warps multiply, each
-//    its 64-column slab of a stage, with m16n8k16 MMAs (weights as the 16
+//    of a stage-2 tile are under way before h is.  Two groups of eight warps
+//    take the stages in turn (one group needs about 600 cycles a stage, and
+//    16 KB arrive every 370 ns), each warp its 64-column slab, with m16n8k16 MMAs (weights as the 16
 //    rows, tokens as the 8 columns; 1 or 2 column groups): the tensor path
 //    only has to keep up with the stream, and 16 rows suit short tiles.  Four
 //    more warps join their sums in a fixed order.
@@ -34,10 +35,12 @@ namespace {
 constexpr int FEW_COLS = 512;                        // columns of a stage
 constexpr int FEW_ROW = FEW_COLS * 2 + 16;           // bytes of an x or h row; the pad puts the rows in other banks
 constexpr int FEW_HALF = 8 * FEW_COLS * 2;           // bytes of eight weight rows
-constexpr int FEW_CONSUMERS = 8;                     // multiplying warps
+constexpr int FEW_SLABS = 8;                         // multiplying warps on a stage, 64 columns each
+constexpr int FEW_GROUPS = 2;                        // groups of them, which take the stages in turn
+constexpr int FEW_CONSUMERS = FEW_SLABS * FEW_GROUPS;
 constexpr int FEW_FINISHERS = 4;                     // warps that join the multiplying warps' sums
 constexpr int FEW_THREADS = (FEW_CONSUMERS + 2 + FEW_FINISHERS) * 32;
-constexpr int FEW_PARTS = 4;                         // tiles whose sums may wait to be joined
+constexpr int FEW_PARTS = 2;                         // tiles whose sums may wait to be joined
 constexpr int FEW_MAX_STAGES = 12;
 constexpr int FEW_QUEUE = 4;                         // tiles handed from the copying to the other warps
 constexpr int FEW_BARS = 2 * FEW_MAX_STAGES + 2 * FEW_QUEUE + 2 * FEW_PARTS;
@@ -116,50 +119,50 @@ __device__ __forceinline__ uint32_t logit_key(float v) {
     return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+__device__ __forceinline__ float logit_of(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
 // The k best of one token's E logits (descending, ties to the lower id) and
 // their softmax weights, by one warp; lane j < k gets slot j.
 template <int SLOTS>
 __device__ __forceinline__ void warp_route(const float *row, int E, int k, int lane, int *my_e, float *my_w) {
-    float v[SLOTS];
-    uint32_t key[SLOTS];
+    uint32_t key[SLOTS], most = 0u;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
         const int e = s * 32 + lane;
-        v[s] = e < E ? row[e] : 0.0f;
-        key[s] = e < E ? logit_key(v[s]) : 0u;
+        key[s] = e < E ? logit_key(__ldcg(row + e)) : 0u;
+        most = max(most, key[s]);
     }
-    float top = 0.0f, mine = 0.0f;
+    const float top = logit_of(__reduce_max_sync(0xffffffffu, most));
+    float sum = 0.0f;
+#pragma unroll
+    for (int s = 0; s < SLOTS; ++s)
+        if (s * 32 + lane < E) sum += expf(logit_of(key[s]) - top);
+    sum = warp_sum(sum);
+    uint32_t mine = 0u;
     int id = 0;
     for (int j = 0; j < k; ++j) {
         uint32_t best = 0;
         int slot = 0;
-        float val = 0.0f;
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s)
             if (key[s] > best) {
                 best = key[s];
                 slot = s;
-                val = v[s];
             }
-        const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-        const uint32_t e = __reduce_min_sync(0xffffffffu, best == most ? slot * 32u + lane : 0xffffffffu);
-        val = __shfl_sync(0xffffffffu, val, e & 31u);
+        const uint32_t win = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t e = __reduce_min_sync(0xffffffffu, best == win ? slot * 32u + lane : 0xffffffffu);
 #pragma unroll
         for (int s = 0; s < SLOTS; ++s)
             if (s * 32u + lane == e) key[s] = 0u;
-        if (j == 0) top = val;
         if (j == lane) {
-            mine = val;
+            mine = win;
             id = static_cast<int>(e);
         }
     }
-    float sum = 0.0f;
-#pragma unroll
-    for (int s = 0; s < SLOTS; ++s)
-        if (s * 32 + lane < E) sum += expf(v[s] - top);
-    sum = warp_sum(sum);
     *my_e = id;
-    *my_w = expf(mine - top) / sum;
+    *my_w = expf(logit_of(mine) - top) / sum;
 }
 
 // Waits until counter `a` has reached `target` and returns the last expert up
@@ -185,6 +188,19 @@ __device__ __forceinline__ int experts_ready(const int *counters, int a, int n_a
             return a - 1;
         }
         __nanosleep(50);
+    }
+}
+
+// After an abort: copies in flight land before shared memory goes away; a
+// stage that the other copying warp never filled stays open, 10 ms each.
+// `stage`, `phase`: where the copying warp would go on.
+__device__ __forceinline__ void few_drain(uint32_t full_bars, int stages, int stage, uint32_t phase) {
+    for (int i = 0; i < stages; ++i) {
+        const int st = (stage + i) % stages;
+        const uint32_t par = stage + i < stages ? phase ^ 1u : phase;
+        const unsigned long long start = global_timer_ns();
+        while (!mbar_try_wait(full_bars + 8u * st, par) && global_timer_ns() - start < 10000000ull) {
+        }
     }
 }
 
@@ -245,7 +261,9 @@ __host__ __device__ constexpr int few_stage_bytes(int tokens) {
 __host__ __device__ constexpr int few_fixed_bytes(int nt, int pairs) {
     return FEW_BARS * 8 + FEW_ROW + FEW_PARTS * FEW_CONSUMERS * nt * 512 + FEW_QUEUE * 4 + pairs * 24;
 }
-static_assert(1024 + 3 * few_stage_bytes(16) + few_fixed_bytes(2, 16 * 32) <= FEW_SMEM_MAX, "three stages at least");
+static_assert(1024 + FEW_GROUPS * few_stage_bytes(16) + few_fixed_bytes(2, 16 * 32) <= FEW_SMEM_MAX,
+              "a stage for each group at least");
+static_assert(FEW_MAX_STAGES % FEW_GROUPS == 0, "stages belong to groups");
 
 template <int DT, int NT>
 __global__ void __launch_bounds__(FEW_THREADS, 1)
@@ -281,7 +299,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     if (threadIdx.x == 0) {
         for (int i = 0; i < FEW_MAX_STAGES; ++i) {
             mbar_init(full_bar(i), 2);  // the weights' and the rows' copying warps
-            mbar_init(empty_bar(i), FEW_CONSUMERS);
+            mbar_init(empty_bar(i), FEW_SLABS);
         }
         for (int i = 0; i < FEW_QUEUE; ++i) {
             mbar_init(tqf_bar(i), 1);
@@ -363,120 +381,68 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     const int n_act = n_act_word;
     // a stage holds 16 weight rows and the rows of the expert with the most tokens
     const int stage_bytes = few_stage_bytes(most_word);
-    const int stages = min(FEW_MAX_STAGES, p.ring_bytes / stage_bytes);
+    // A multiple of the groups, so that a stage always belongs to one group: a
+    // group a whole ring ahead of another on the other's stage would take the
+    // barrier's phase before last for its own (they have the same parity).
+    const int stages = min(FEW_MAX_STAGES, p.ring_bytes / stage_bytes) / FEW_GROUPS * FEW_GROUPS;
+    const uint32_t ring = smem_u32(sm.ring);
     const int tiles_e = p.d_e / 8;           // stage-1 tiles of an expert
     const int n1 = n_act * tiles_e, total = n1 + p.d_h / 16;
     const int steps1 = (p.d_h + FEW_COLS - 1) / FEW_COLS, steps2 = (p.d_e + FEW_COLS - 1) / FEW_COLS;
 
-    if (warp == FEW_CONSUMERS || warp == FEW_CONSUMERS + 1) {
-        const bool rows_warp = warp > FEW_CONSUMERS;
-        const uint64_t policy = rows_warp ? l2_policy_evict_last() : l2_policy_evict_first();
-        int stage = 0, slot = 0, next = 0, ready = -1;  // ready: experts up to here have their h
+    if (warp == FEW_CONSUMERS) {
+        // -------------------- weights: one thread, no broadcasts --------------------
+        // (a whole warp with its shuffles took about 900 cycles a step and
+        // was what paced the stream)
+        if (lane != 0) return;
+        const uint64_t policy = l2_policy_evict_first();
+        int stage = 0, slot = 0;
         uint32_t phase = 0, qphase = 0;
         bool ok = true;
-        auto advance = [&]() {
-            if (++stage == stages) {
-                stage = 0;
-                phase ^= 1u;
+        // 512 columns of 16 weight rows: 8 from row r0 of map m0, 8 from row r1
+        // of map m1 (columns past the end read as zeros)
+        auto copy = [&](const CUtensorMap *m0, const CUtensorMap *m1, int r0, int r1, int steps) {
+            for (int c = 0; c < steps; ++c) {
+                if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) return false;
+                const uint32_t dst = ring + stage * stage_bytes, bar = full_bar(stage);
+                mbar_arrive_expect_tx(bar, 2 * FEW_HALF);
+                tma_load_3d_hint(dst, m0, bar, 0, r0, c * (FEW_COLS / 64), policy);
+                tma_load_3d_hint(dst + FEW_HALF, m1, bar, 0, r1, c * (FEW_COLS / 64), policy);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
             }
-        };
-        // the next stage, once free, gets `bytes` of this warp's copies
-        auto open = [&](uint32_t bytes) {
-            int free = 1;
-            if (lane == 0) {
-                free = mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err) ? 1 : 0;
-                if (free) mbar_arrive_expect_tx(full_bar(stage), bytes);
-            }
-            return __shfl_sync(0xffffffffu, free, 0) != 0;
-        };
-        // `n` rows of `bytes` from each lane's src
-        auto copy_rows = [&](int n, uint32_t bytes, const uint8_t *src) {
-            if (!open(n * bytes)) return false;
-            if (lane < n)
-                row_copy(smem_u32(sm.ring + stage * stage_bytes + 2 * FEW_HALF + lane * FEW_ROW), src, bytes, full_bar(stage),
-                         policy);
-            advance();
             return true;
         };
-        // 16 weight rows: 8 of row r0 of map m0, 8 of row r1 of map m1 (columns past the end read as zeros)
-        auto copy_weights = [&](const CUtensorMap *m0, const CUtensorMap *m1, int r0, int r1, int c) {
-            if (!open(2 * FEW_HALF)) return false;
-            if (lane == 0) {
-                const uint32_t dst = smem_u32(sm.ring + stage * stage_bytes);
-                tma_load_3d_hint(dst, m0, full_bar(stage), 0, r0, c * (FEW_COLS / 64), policy);
-                tma_load_3d_hint(dst + FEW_HALF, m1, full_bar(stage), 0, r1, c * (FEW_COLS / 64), policy);
-            }
-            advance();
-            return true;
-        };
-        auto bytes_of = [](int K, int c) { return static_cast<uint32_t>(min(FEW_COLS, K - c * FEW_COLS)) * 2u; };
-        if (!rows_warp && lane == 0) next = atomicAdd(p.counters, 1);
+        int next = atomicAdd(p.counters, 1);
         while (ok) {
-            int tile = 0, free = 1;
-            if (!rows_warp) {
-                if (lane == 0) {
-                    free = mbar_wait_bounded(tqe_bar(slot), qphase ^ 1u, abort_flag, p.err) ? 1 : 0;
-                    if (free) {
-                        sm.queue[slot] = next;
-                        mbar_arrive(tqf_bar(slot));
-                    }
-                    tile = next;
-                    if (tile < total) next = atomicAdd(p.counters, 1);  // its latency passes under this tile
-                }
-            } else if (lane == 0) {
-                free = mbar_wait_bounded(tqf_bar(slot), qphase, abort_flag, p.err) ? 1 : 0;
-                if (free) {
-                    tile = sm.queue[slot];
-                    mbar_arrive(tqe_bar(slot));
-                }
-            }
-            if (!__shfl_sync(0xffffffffu, free, 0)) break;
-            tile = __shfl_sync(0xffffffffu, tile, 0);
+            ok = mbar_wait_bounded(tqe_bar(slot), qphase ^ 1u, abort_flag, p.err);
+            if (!ok) break;
+            const int tile = next;
+            sm.queue[slot] = tile;
+            mbar_arrive(tqf_bar(slot));
             if (tile >= total) break;
+            next = atomicAdd(p.counters, 1);  // its latency passes under this tile
             if (++slot == FEW_QUEUE) {
                 slot = 0;
                 qphase ^= 1u;
             }
             if (tile < n1) {
                 const int a = tile / tiles_e, row = sm.act_e[a] * p.d_e + (tile - a * tiles_e) * 8;
-                const uint32_t m = sm.act_mask[a];
-                const int n = __popc(m), t = lane < n ? static_cast<int>(__fns(m, 0, lane + 1)) : 0;
-                const uint8_t *src = static_cast<const uint8_t *>(p.x) + static_cast<int64_t>(t) * p.d_h * 2;
-                for (int c = 0; c < steps1 && ok; ++c)
-                    ok = rows_warp ? copy_rows(n, bytes_of(p.d_h, c), src + c * FEW_COLS * 2)
-                                   : copy_weights(&tm_gate, &tm_up, row, row, c);
+                ok = copy(&tm_gate, &tm_up, row, row, steps1);
             } else {
                 for (int a = 0; a < n_act && ok; ++a) {
                     const int row = sm.act_e[a] * p.d_h + (tile - n1) * 16;
-                    const int rows = __popc(sm.act_mask[a]);
-                    const int r = sm.act_base[a] + (lane < rows ? lane : lane - rows);
-                    const uint8_t *src =
-                        static_cast<const uint8_t *>(lane < rows ? p.h_hi : p.h_lo) + static_cast<int64_t>(r) * p.d_e * 2;
-                    if (rows_warp && a > ready) {  // h of this expert: every stage-1 warp has stored it
-                        ready = experts_ready(p.counters + 1, a, n_act, tiles_e * 2 * NT, lane, abort_flag, p.err);
-                        ok = ready >= a;
-                    }
-                    for (int c = 0; c < steps2 && ok; ++c)
-                        ok = rows_warp ? copy_rows(2 * rows, bytes_of(p.d_e, c), src + c * FEW_COLS * 2)
-                                       : copy_weights(&tm_down, &tm_down, row, row + 8, c);
+                    ok = copy(&tm_down, &tm_down, row, row + 8, steps2);
                 }
             }
         }
-        if (*abort_flag && lane == 0) {
-            // copies in flight land before shared memory goes away; a stage
-            // that the other warp never filled stays open: 10 ms each
-            for (int i = 0; i < stages; ++i) {
-                const int st = (stage + i) % stages;
-                const uint32_t par = stage + i < stages ? phase ^ 1u : phase;
-                const unsigned long long start = global_timer_ns();
-                while (!mbar_try_wait(full_bar(st), par) && global_timer_ns() - start < 10000000ull) {
-                }
-            }
-        }
+        if (*abort_flag) few_drain(bar0, stages, stage, phase);
         return;
     }
 
-    // the other warps take every tile; every lane polls, which on the usual
+    // the other warps take every tile and run whole; every lane polls, which on the usual
     // first try needs no broadcast
     int slot = 0, local = 0;
     uint32_t qphase = 0;
@@ -495,6 +461,51 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         }
         return tile;
     };
+    if (warp == FEW_CONSUMERS + 1) {
+        // ------------------ the rows that meet the weights: x or h ------------------
+        const uint64_t policy = l2_policy_evict_last();
+        int stage = 0, ready = -1;  // ready: experts up to here have their h
+        uint32_t phase = 0;
+        bool ok = true;
+        // `n` rows of K columns from each lane's src, step by step.  The
+        // lanes' copies may start before lane 0 has announced their bytes: its
+        // arrival is what lets the phase complete
+        auto copy = [&](int n, int K, const uint8_t *src, int steps) {
+            for (int c = 0; c < steps; ++c) {
+                if (!wait(empty_bar(stage), phase ^ 1u)) return false;
+                const uint32_t bytes = static_cast<uint32_t>(min(FEW_COLS, K - c * FEW_COLS)) * 2u, bar = full_bar(stage);
+                if (lane == 0) mbar_arrive_expect_tx(bar, n * bytes);
+                if (lane < n)
+                    row_copy(ring + stage * stage_bytes + 2 * FEW_HALF + lane * FEW_ROW, src + c * FEW_COLS * 2, bytes, bar, policy);
+                if (++stage == stages) {
+                    stage = 0;
+                    phase ^= 1u;
+                }
+            }
+            return true;
+        };
+        for (int tile = take(); tile < total && ok; tile = take()) {
+            if (tile < n1) {
+                const uint32_t m = sm.act_mask[tile / tiles_e];
+                const int n = __popc(m), t = lane < n ? static_cast<int>(__fns(m, 0, lane + 1)) : 0;
+                ok = copy(n, p.d_h, static_cast<const uint8_t *>(p.x) + static_cast<int64_t>(t) * p.d_h * 2, steps1);
+            } else {
+                for (int a = 0; a < n_act && ok; ++a) {
+                    const int rows = __popc(sm.act_mask[a]);
+                    const int r = sm.act_base[a] + (lane < rows ? lane : lane - rows);
+                    if (a > ready) {  // h of this expert: every stage-1 warp has stored it
+                        ready = experts_ready(p.counters + 1, a, n_act, tiles_e * 2 * NT, lane, abort_flag, p.err);
+                        ok = ready >= a;
+                    }
+                    const void *h = lane < rows ? p.h_hi : p.h_lo;
+                    ok = ok && copy(2 * rows, p.d_e, static_cast<const uint8_t *>(h) + static_cast<int64_t>(r) * p.d_e * 2, steps2);
+                }
+            }
+        }
+        if (*abort_flag && lane == 0) few_drain(bar0, stages, stage, phase);
+        return;
+    }
+
     if (warp >= FEW_CONSUMERS + 2) {
         // -------------------------------- joining --------------------------------
         const int fin = warp - FEW_CONSUMERS - 2;
@@ -552,18 +563,28 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     // the matrices are rows 0-7, then 8-15, of 8 columns, then of the next 8;
     // tokens: four times 8 columns
     const int mrow = lane & 7, mat = lane >> 3;
-    const uint32_t ring = smem_u32(sm.ring), zeros = smem_u32(sm.zeros) + mat * 16;
-    const uint32_t wrow = (mat & 1) * FEW_HALF + warp * 1024 + mrow * 128;
-    const uint32_t trow = 2 * FEW_HALF + warp * 128 + mat * 16;
-    int stage = 0;
+    const uint32_t zeros = smem_u32(sm.zeros) + mat * 16;
+    const int slab = warp % FEW_SLABS;
+    const uint32_t wrow = (mat & 1) * FEW_HALF + slab * 1024 + mrow * 128;
+    const uint32_t trow = 2 * FEW_HALF + slab * 128 + mat * 16;
+    int stage = 0, turn = warp / FEW_SLABS;  // turn 0: the next stage is this group's
     uint32_t phase = 0;
     bool ok = true;
+    auto advance = [&]() {
+        if (++stage == stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        turn = turn == 0 ? FEW_GROUPS - 1 : turn - 1;
+    };
     for (int tile = take(); tile < total; tile = take(), ++local) {
-        float acc[NT][4];
+        // four independent chains of MMAs a column group: in one chain their
+        // latencies add up to most of a step
+        float acc[NT][4][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+            for (int i = 0; i < 16; ++i) acc[n][i >> 2][i & 3] = 0.0f;
         const bool first = tile < n1;
         const int a0 = first ? tile / tiles_e : 0, a1 = first ? a0 + 1 : n_act;
         const int K = first ? p.d_h : p.d_e, steps = first ? steps1 : steps2;
@@ -579,10 +600,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 any[n] = ((m >> (8 * n)) & 255u) != 0u;
                 token[n] = trow + __popc(m & ((1u << t) - 1u)) * FEW_ROW;
             }
-            for (int c = 0; c < steps; ++c) {
+            for (int c = 0; c < steps; ++c, advance()) {
+                if (turn != 0) continue;
                 ok = wait(full_bar(stage), phase);
                 if (!ok) break;
-                if (warp * 64 < K - c * FEW_COLS) {
+                if (slab * 64 < K - c * FEW_COLS) {
                     const uint32_t st = ring + stage * stage_bytes;
                     uint4 w[4];
 #pragma unroll
@@ -594,25 +616,21 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const uint4 v = ldmatrix_x4(b + j * 64);
-                            mma_16816<DT>(acc[n], w[2 * j], v.x, v.y);
-                            mma_16816<DT>(acc[n], w[2 * j + 1], v.z, v.w);
+                            mma_16816<DT>(acc[n][j], w[2 * j], v.x, v.y);
+                            mma_16816<DT>(acc[n][2 + j], w[2 * j + 1], v.z, v.w);
                         }
                         if (!first) {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
                                 const uint4 v = ldmatrix_x4((here[n] ? b + rest : zeros) + j * 64);
-                                mma_16816<DT>(acc[n], w[2 * j], v.x, v.y);
-                                mma_16816<DT>(acc[n], w[2 * j + 1], v.z, v.w);
+                                mma_16816<DT>(acc[n][2 + j], w[2 * j], v.x, v.y);
+                                mma_16816<DT>(acc[n][j], w[2 * j + 1], v.z, v.w);
                             }
                         }
                     }
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(stage));
-                if (++stage == stages) {
-                    stage = 0;
-                    phase ^= 1u;
-                }
             }
         }
         if (!ok) break;
@@ -621,7 +639,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         float4 *part = sm.partial + buf * FEW_CONSUMERS * NT * 32;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
-            part[(warp * NT + n) * 32 + lane] = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+            part[(warp * NT + n) * 32 + lane] =
+                make_float4((acc[n][0][0] + acc[n][1][0]) + (acc[n][2][0] + acc[n][3][0]),
+                            (acc[n][0][1] + acc[n][1][1]) + (acc[n][2][1] + acc[n][3][1]),
+                            (acc[n][0][2] + acc[n][1][2]) + (acc[n][2][2] + acc[n][3][2]),
+                            (acc[n][0][3] + acc[n][1][3]) + (acc[n][2][3] + acc[n][3][3]));
         __syncwarp();
         if (lane == 0) mbar_arrive(pf_bar(buf));
     }
