@@ -10,13 +10,24 @@
 //   d_y = r2 * v2 - y * r2^3 / H * sum(v2 * y)
 // and the weights' and the gate's gradients are column (or row) sums of
 // products of these.
+//
+// Memory bound: every tensor is read once and written once.  A CTA holds one
+// row at a time in registers, 8 (wide rows: 16) elements a thread, and walks
+// the rows with the grid's stride; the rows to come arrive through a ring of
+// shared-memory stages by bulk copies, so loads go on under the row's two
+// reductions.  Rows whose bytes are no multiple of 16, and rows too wide for
+// two stages, are loaded by the threads themselves.  The backward pass keeps
+// the column sums of its rows in registers; a second kernel adds the CTAs'
+// sums in a fixed order.
 #include "common.cuh"
 #include "internal.h"
 
 namespace moe {
 namespace {
 
-constexpr int NORM_THREADS = 256;
+constexpr int NORM_MAX_TENSORS = 5;
+constexpr int NORM_MAX_STAGES = 8;
+constexpr int NORM_RING_BYTES = 200 * 1024;  // of one SM, shared by its CTAs
 
 struct NormParams {
     const void *y, *res, *w_post, *gate, *w_next;
@@ -24,162 +35,470 @@ struct NormParams {
     const float *r_post, *r_next;
     void *out, *u, *d_res, *d_y, *d_gate;
     float *rstd_post, *rstd_next, *d_w_post, *d_w_next;
-    float *row_sum;  // backward: r^3 / H * sum(v * out) of each row
+    float *partial;  // backward: [CTAs][3][H] column sums of d_w_next, d_w_post, d_gate
     int gate_kind;
     float alpha, eps;
     int64_t T;
     int H;
+    int stages, tensors;  // the ring: tensors a row (in the order of the kernel's reads)
+    const void *ring[NORM_MAX_TENSORS];
 };
 
-template <typename T> __device__ __forceinline__ float at(const void *p, int64_t i) {
-    return to_f32(static_cast<const T *>(p)[i]);
-}
+// A thread's EPT elements of a row.  RING: 16-byte vectors, `threads` apart,
+// kept packed; otherwise single elements, `threads` apart, in fp32.
+template <typename T, int EPT, bool RING> struct Part;
 
-template <typename T> __device__ __forceinline__ float gate_at(const NormParams &p, int64_t t, int h) {
-    if (p.gate_kind == 1) return at<T>(p.gate, h);
-    if (p.gate_kind == 2) return at<T>(p.gate, t);
-    if (p.gate_kind == 3) return at<T>(p.gate, t * p.H + h);
-    return 1.0f;
-}
-
-__device__ __forceinline__ float cta_sum(float v, float *scratch) {
+template <typename T, int EPT> struct Part<T, EPT, true> {
+    static constexpr int EV = 16 / sizeof(T), V = EPT / EV;
+    uint4 q[V];
+    static __device__ __forceinline__ int at(int v) { return (v * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * EV; }
+    __device__ __forceinline__ void load(const void *row, int H) {  // global or shared
 #pragma unroll
-    for (int s = 16; s >= 1; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) scratch[threadIdx.x >> 5] = v;
-    __syncthreads();
-    float total = 0.0f;
+        for (int v = 0; v < V; ++v)
+            q[v] = at(v) < H ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + at(v)) : make_uint4(0u, 0u, 0u, 0u);
+    }
+    __device__ __forceinline__ void put(void *row, int H) const {
 #pragma unroll
-    for (int w = 0; w < NORM_THREADS / 32; ++w) total += scratch[w];
-    return total;
+        for (int v = 0; v < V; ++v)
+            if (at(v) < H) *reinterpret_cast<uint4 *>(static_cast<T *>(row) + at(v)) = q[v];
+    }
+    __device__ __forceinline__ float get(int i) const {
+        const uint4 &w = q[i / EV];
+        const int j = i % EV;
+        if constexpr (sizeof(T) == 4) {
+            return __uint_as_float(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w);
+        } else {
+            constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
+            const uint32_t b = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
+            const float2 f = unpack2<DT>(b);
+            return j & 1 ? f.y : f.x;
+        }
+    }
+    static __device__ __forceinline__ void store(void *row, int H, const float (&f)[EPT]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            if (at(v) >= H) continue;
+            uint4 w;
+            if constexpr (sizeof(T) == 4) {
+                w = make_uint4(__float_as_uint(f[4 * v]), __float_as_uint(f[4 * v + 1]), __float_as_uint(f[4 * v + 2]),
+                               __float_as_uint(f[4 * v + 3]));
+            } else {
+                constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
+                w = make_uint4(pack2<DT>(f[8 * v], f[8 * v + 1]), pack2<DT>(f[8 * v + 2], f[8 * v + 3]),
+                               pack2<DT>(f[8 * v + 4], f[8 * v + 5]), pack2<DT>(f[8 * v + 6], f[8 * v + 7]));
+            }
+            *reinterpret_cast<uint4 *>(static_cast<T *>(row) + at(v)) = w;
+        }
+    }
+    static __device__ __forceinline__ void store_sums(float *row, int H, const float (&f)[EPT]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int j = 0; j < EV; j += 4)
+                if (at(v) < H)
+                    *reinterpret_cast<float4 *>(row + at(v) + j) =
+                        make_float4(f[v * EV + j], f[v * EV + j + 1], f[v * EV + j + 2], f[v * EV + j + 3]);
+    }
+};
+
+template <typename T, int EPT> struct Part<T, EPT, false> {
+    float f[EPT];
+    static __device__ __forceinline__ int at(int i) { return i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); }
+    __device__ __forceinline__ void load(const void *row, int H) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) f[i] = at(i) < H ? to_f32(static_cast<const T *>(row)[at(i)]) : 0.0f;
+    }
+    __device__ __forceinline__ void put(void *, int) const {}
+    __device__ __forceinline__ float get(int i) const { return f[i]; }
+    static __device__ __forceinline__ void store(void *row, int H, const float (&v)[EPT]) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i)
+            if (at(i) < H) static_cast<T *>(row)[at(i)] = from_f32<T>(v[i]);
+    }
+    static __device__ __forceinline__ void store_sums(float *row, int H, const float (&v)[EPT]) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i)
+            if (at(i) < H) row[at(i)] = v[i];
+    }
+};
+
+// Sums over the CTA with one barrier each: two scratch buffers in turn.
+struct RowSums {
+    float2 *scratch;  // [2][32]
+    int turn = 0;
+    __device__ __forceinline__ float2 operator()(float a, float b) {
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) {
+            a += __shfl_xor_sync(0xffffffffu, a, s);
+            b += __shfl_xor_sync(0xffffffffu, b, s);
+        }
+        float2 *buf = scratch + turn * 32;
+        turn ^= 1;
+        const int warps = static_cast<int>(blockDim.x) >> 5, lane = threadIdx.x & 31;
+        if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+        __syncthreads();
+        float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int s = 16; s >= 1; s >>= 1) {
+            v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
+            v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
+        }
+        return v;
+    }
+};
+
+// The rows of p.ring's tensors, this CTA's in order.  next() waits for the
+// next row's stage; refill() is called once every thread has read it.
+template <bool RING> struct RowRing;
+
+template <> struct RowRing<true> {
+    const NormParams &p;
+    uint8_t *smem;
+    uint32_t bars, row_bytes, stage_bytes;
+    int64_t row, ahead;  // the current row; the next one to ask for
+    int stage = -1;
+    uint32_t phase = 0;
+    __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *smem, uint64_t *bar, int elem)
+        : p(p), smem(smem), bars(smem_u32(bar)), row_bytes(static_cast<uint32_t>(p.H * elem)),
+          stage_bytes(row_bytes * p.tensors), row(blockIdx.x), ahead(blockIdx.x) {
+        if (threadIdx.x == 0) {
+            for (int i = 0; i < p.stages; ++i) mbar_init(bars + 8u * i, 1);
+            fence_mbar_init();
+        }
+        __syncthreads();
+    }
+    __device__ __forceinline__ void ask(int st) {  // thread 0
+        if (ahead >= p.T) return;
+        const uint32_t bar = bars + 8u * st, dst = smem_u32(smem) + st * stage_bytes;
+        mbar_arrive_expect_tx(bar, stage_bytes);
+        for (int i = 0; i < p.tensors; ++i)
+            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                             dst + i * row_bytes),
+                         "l"(static_cast<const uint8_t *>(p.ring[i]) + ahead * row_bytes), "r"(row_bytes), "r"(bar)
+                         : "memory");
+        ahead += gridDim.x;
+    }
+    __device__ __forceinline__ void start() {
+        if (threadIdx.x == 0)
+            for (int i = 0; i < p.stages; ++i) ask(i);
+    }
+    // A copy of this CTA's own, asked for before: bounded, and without an
+    // error word to report to a row that never came would be left as it is.
+    __device__ __forceinline__ bool next() {
+        if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+        }
+        const unsigned long long start = global_timer_ns();
+        while (!mbar_try_wait(bars + 8u * stage, phase))
+            if (global_timer_ns() - start > kWaitTimeoutNs) return false;
+        return true;
+    }
+    __device__ __forceinline__ const void *tensor(int i) const { return smem + stage * stage_bytes + i * row_bytes; }
+    __device__ __forceinline__ void refill() {
+        if (threadIdx.x == 0) ask(stage);
+    }
+};
+
+template <> struct RowRing<false> {
+    const NormParams &p;
+    int64_t row, bytes;
+    bool first = true;
+    __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *, uint64_t *, int elem)
+        : p(p), row(blockIdx.x), bytes(static_cast<int64_t>(p.H) * elem) {}
+    __device__ __forceinline__ void start() {}
+    __device__ __forceinline__ bool next() { return true; }
+    __device__ __forceinline__ const void *tensor(int i) const { return static_cast<const uint8_t *>(p.ring[i]) + row * bytes; }
+    __device__ __forceinline__ void refill() {}
+};
+
+// The [H] tensors (weights, gate per channel): with the ring, a thread keeps
+// its elements in shared memory after the stages, else it reads them again for
+// every row; either way they take no registers between their uses.
+template <typename P, bool RING>
+__device__ __forceinline__ const void *keep_row(const void *row, uint8_t *&room, int H, int elem) {
+    if (!RING || !row) return row;
+    P part;
+    part.load(row, H);
+    uint8_t *at = room;
+    room += H * elem;
+    part.put(at, H);
+    return at;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(NORM_THREADS) norm_kernel(NormParams p) {
-    __shared__ float scratch[NORM_THREADS / 32];
+template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __grid_constant__ NormParams p) {
+    using P = Part<T, EPT, RING>;
+    extern __shared__ __align__(128) uint8_t norm_smem[];
+    __shared__ float2 scratch[64];
+    __shared__ uint64_t bars[NORM_MAX_STAGES];
+    RowRing<RING> ring(p, norm_smem, bars, sizeof(T));
+    RowSums sums{scratch};
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t t = blockIdx.x, base = t * p.H;
-    float r2 = 1.0f;
-    if (p.w_post) {
-        float s = 0.0f;
-        for (int h = threadIdx.x; h < p.H; h += NORM_THREADS) {
-            const float v = at<T>(p.y, base + h);
-            s += v * v;
+    ring.start();
+    const int H = p.H;
+    const bool has_y = p.y != nullptr, post = p.w_post != nullptr, nxt = p.w_next != nullptr;
+    const float per = 1.0f / static_cast<float>(H);
+    uint8_t *room = norm_smem + static_cast<int64_t>(p.stages) * p.tensors * H * sizeof(T);
+    const void *w_post = keep_row<P, RING>(p.w_post, room, H, sizeof(T));
+    const void *w_next = keep_row<P, RING>(p.w_next, room, H, sizeof(T));
+    const void *gate_row = keep_row<P, RING>(p.gate_kind == 1 ? p.gate : nullptr, room, H, sizeof(T));
+    for (; ring.row < p.T; ring.row += gridDim.x) {
+        const int64_t t = ring.row, base = t * H;
+        if (!ring.next()) return;
+        float scale = p.alpha;
+        if (p.gate_kind == 2) scale *= to_f32(static_cast<const T *>(p.gate)[t]);
+        P res, y, gate;
+        res.load(ring.tensor(0), H);
+        if (has_y) y.load(ring.tensor(1), H);
+        if (p.gate_kind == 3) gate.load(ring.tensor(2), H);
+        if (p.gate_kind == 1) gate.load(gate_row, H);
+        bool read = false;  // every thread has read the stage
+        float o[EPT];
+        if (has_y) {
+            float r2 = 1.0f;
+            if (post) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) s += y.get(i) * y.get(i);
+                r2 = 1.0f / sqrtf(sums(s, 0.0f).x * per + p.eps);
+                if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
+                ring.refill();
+                read = true;
+            }
+            P w;
+            if (post) w.load(w_post, H);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) {
+                float z = y.get(i);
+                if (post) z = z * r2 * w.get(i);
+                if (p.gate_kind & 1) z *= gate.get(i);
+                o[i] = res.get(i) + scale * z;
+            }
+            P::store(static_cast<T *>(p.out) + base, H, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) o[i] = res.get(i);
         }
-        r2 = 1.0f / sqrtf(cta_sum(s, scratch) / static_cast<float>(p.H) + p.eps);
-        if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
-    }
-    auto value = [&](int h) {
-        float o = at<T>(p.res, base + h);
-        if (p.y) {
-            float z = at<T>(p.y, base + h);
-            if (p.w_post) z = z * r2 * at<T>(p.w_post, h);
-            o += p.alpha * gate_at<T>(p, t, h) * z;
+        if (nxt) {
+            float s = 0.0f;
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) s += o[i] * o[i];
+            const float r = 1.0f / sqrtf(sums(s, 0.0f).x * per + p.eps);
+            if (p.rstd_next && threadIdx.x == 0) p.rstd_next[t] = r;
+            if (!read) ring.refill();
+            read = true;
+            P w;
+            w.load(w_next, H);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) o[i] = o[i] * r * w.get(i);
+            P::store(static_cast<T *>(p.u) + base, H, o);
         }
-        return o;
-    };
-    float r = 0.0f;
-    if (p.w_next) {
-        float s = 0.0f;
-        for (int h = threadIdx.x; h < p.H; h += NORM_THREADS) {
-            const float o = value(h);
-            s += o * o;
+        if (!read) {
+            if (RING) __syncthreads();
+            ring.refill();
         }
-        r = 1.0f / sqrtf(cta_sum(s, scratch) / static_cast<float>(p.H) + p.eps);
-        if (p.rstd_next && threadIdx.x == 0) p.rstd_next[t] = r;
-    }
-    for (int h = threadIdx.x; h < p.H; h += NORM_THREADS) {
-        const float o = value(h);
-        if (p.w_next) static_cast<T *>(p.u)[base + h] = from_f32<T>(o * r * at<T>(p.w_next, h));
-        if (p.y) static_cast<T *>(p.out)[base + h] = from_f32<T>(o);
     }
 }
 
-// d at one element, given the row's sum term
-template <typename T>
-__device__ __forceinline__ float upstream(const NormParams &p, int64_t t, int h, float sum) {
-    const int64_t i = t * p.H + h;
-    float d = p.d_out ? at<T>(p.d_out, i) : 0.0f;
-    if (p.w_next) d += p.r_next[t] * at<T>(p.d_u, i) * at<T>(p.w_next, h) - at<T>(p.saved_out, i) * sum;
-    return d;
-}
-
-template <typename T>
-__global__ void __launch_bounds__(NORM_THREADS) norm_backward_rows(NormParams p) {
-    __shared__ float scratch[NORM_THREADS / 32];
+template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(const __grid_constant__ NormParams p) {
+    using P = Part<T, EPT, RING>;
+    extern __shared__ __align__(128) uint8_t norm_smem[];
+    __shared__ float2 scratch[64];
+    __shared__ uint64_t bars[NORM_MAX_STAGES];
+    RowRing<RING> ring(p, norm_smem, bars, sizeof(T));
+    RowSums sums{scratch};
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t t = blockIdx.x, base = t * p.H;
-    float sum1 = 0.0f;
-    if (p.w_next) {
-        float s = 0.0f;
-        for (int h = threadIdx.x; h < p.H; h += NORM_THREADS)
-            s += at<T>(p.d_u, base + h) * at<T>(p.w_next, h) * at<T>(p.saved_out, base + h);
-        const float r = p.r_next[t];
-        sum1 = cta_sum(s, scratch) * (r * r * r / static_cast<float>(p.H));
-        if (threadIdx.x == 0) p.row_sum[t] = sum1;
-    }
-    const float r2 = p.w_post ? p.r_post[t] : 1.0f;
-    float sum2 = 0.0f, dg = 0.0f;
-    if (p.y) {
-        for (int h = threadIdx.x; h < p.H; h += NORM_THREADS) {
-            const float d = upstream<T>(p, t, h, sum1), y = at<T>(p.y, base + h);
-            const float w = p.w_post ? at<T>(p.w_post, h) : 1.0f;
-            dg += d * (y * r2 * w);
-            sum2 += p.alpha * gate_at<T>(p, t, h) * d * w * y;
+    ring.start();
+    const int H = p.H;
+    const bool has_y = p.y != nullptr, post = p.w_post != nullptr, nxt = p.w_next != nullptr, above = p.d_out != nullptr;
+    const float per = 1.0f / static_cast<float>(H);
+    uint8_t *room = norm_smem + static_cast<int64_t>(p.stages) * p.tensors * H * sizeof(T);
+    const void *w_post = keep_row<P, RING>(p.w_post, room, H, sizeof(T));
+    const void *w_next = keep_row<P, RING>(p.w_next, room, H, sizeof(T));
+    const void *gate_row = keep_row<P, RING>(p.gate_kind == 1 ? p.gate : nullptr, room, H, sizeof(T));
+    float sum_next[EPT], sum_post[EPT], sum_gate[EPT];  // columns, over this CTA's rows
+#pragma unroll
+    for (int i = 0; i < EPT; ++i) sum_next[i] = sum_post[i] = sum_gate[i] = 0.0f;
+    for (; ring.row < p.T; ring.row += gridDim.x) {
+        const int64_t t = ring.row, base = t * H;
+        if (!ring.next()) return;
+        int at = 0;
+        bool read = false;
+        float d[EPT];
+        if (above) {
+            P d_out;
+            d_out.load(ring.tensor(at++), H);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) d[i] = d_out.get(i);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) d[i] = 0.0f;
         }
-        sum2 = cta_sum(sum2, scratch) * (r2 * r2 * r2 / static_cast<float>(p.H));
-        if (p.gate_kind == 2 && p.d_gate) {
-            dg = cta_sum(dg, scratch);
-            if (threadIdx.x == 0) static_cast<float *>(p.d_gate)[t] = p.alpha * dg;
+        P d_u, out, y, gate;
+        if (nxt) {
+            d_u.load(ring.tensor(at++), H);
+            out.load(ring.tensor(at++), H);
+        }
+        if (has_y) y.load(ring.tensor(at++), H);
+        if (p.gate_kind == 3) gate.load(ring.tensor(at), H);
+        if (nxt) {
+            const float r = p.r_next[t];
+            float s = 0.0f;
+            P w;
+            w.load(w_next, H);
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) s += d_u.get(i) * w.get(i) * out.get(i);
+            const float back = sums(s, 0.0f).x * (r * r * r * per);
+            ring.refill();
+            read = true;
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) {
+                d[i] += r * d_u.get(i) * w.get(i) - out.get(i) * back;
+                sum_next[i] += d_u.get(i) * out.get(i) * r;
+            }
+        }
+        P::store(static_cast<T *>(p.d_res) + base, H, d);
+        if (has_y) {
+            const float r2 = post ? p.r_post[t] : 1.0f;
+            const float g_row = p.gate_kind == 2 ? to_f32(static_cast<const T *>(p.gate)[t]) : 1.0f;
+            float s = 0.0f, sg = 0.0f;
+            P w;
+            if (post) w.load(w_post, H);
+            if (p.gate_kind == 1) gate.load(gate_row, H);
+            if (p.gate_kind == 3 && p.d_gate) {
+                float dg[EPT];
+#pragma unroll
+                for (int i = 0; i < EPT; ++i) dg[i] = p.alpha * d[i] * (y.get(i) * r2 * (post ? w.get(i) : 1.0f));
+                P::store(static_cast<T *>(p.d_gate) + base, H, dg);
+            }
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) {  // d becomes dz
+                const float n = y.get(i) * r2, wi = post ? w.get(i) : 1.0f;
+                const float dg = p.alpha * d[i] * (n * wi);
+                sg += dg;
+                if (p.gate_kind == 1) sum_gate[i] += dg;
+                d[i] = p.alpha * ((p.gate_kind & 1) ? gate.get(i) : g_row) * d[i];
+                s += d[i] * wi * y.get(i);
+                sum_post[i] += d[i] * n;
+            }
+            if (post || p.gate_kind == 2) {
+                const float2 row = sums(s, sg);
+                if (!read) ring.refill();
+                read = true;
+                if (p.gate_kind == 2 && p.d_gate && threadIdx.x == 0) static_cast<float *>(p.d_gate)[t] = row.y;
+                if (post) {
+                    const float back = row.x * (r2 * r2 * r2 * per);
+#pragma unroll
+                    for (int i = 0; i < EPT; ++i) d[i] = r2 * d[i] * w.get(i) - y.get(i) * back;
+                }
+            }
+            P::store(static_cast<T *>(p.d_y) + base, H, d);
+        }
+        if (!read) {
+            if (RING) __syncthreads();
+            ring.refill();
         }
     }
-    for (int h = threadIdx.x; h < p.H; h += NORM_THREADS) {
-        const float d = upstream<T>(p, t, h, sum1);
-        if (p.y) {
-            const float y = at<T>(p.y, base + h), w = p.w_post ? at<T>(p.w_post, h) : 1.0f;
-            const float dz = p.alpha * gate_at<T>(p, t, h) * d;
-            static_cast<T *>(p.d_y)[base + h] = from_f32<T>(p.w_post ? r2 * dz * w - y * sum2 : dz);
-            if (p.gate_kind == 3 && p.d_gate) static_cast<T *>(p.d_gate)[base + h] = from_f32<T>(p.alpha * d * (y * r2 * w));
-        }
-    }
+    float *part = p.partial + static_cast<int64_t>(blockIdx.x) * 3 * H;
+    if (p.d_w_next) P::store_sums(part, H, sum_next);
+    if (p.d_w_post) P::store_sums(part + H, H, sum_post);
+    if (p.gate_kind == 1 && p.d_gate) P::store_sums(part + 2 * H, H, sum_gate);
 }
 
-template <typename T>
-__global__ void __launch_bounds__(32) norm_backward_columns(NormParams p) {
+// The CTAs' column sums added: 32 columns a CTA, 8 threads a column each with
+// every 8th CTA's sum, then those in order.
+__global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant__ NormParams p, int ctas) {
+    __shared__ float part[8][33];
     griddep_wait();
     griddep_launch_dependents();
-    const int h = blockIdx.x * 32 + threadIdx.x;
-    if (h >= p.H) return;
-    float dwn = 0.0f, dwp = 0.0f, dg = 0.0f;
-    for (int64_t t = 0; t < p.T; ++t) {
-        const int64_t i = t * p.H + h;
-        const float d = upstream<T>(p, t, h, p.w_next ? p.row_sum[t] : 0.0f);
-        if (p.w_next) dwn += at<T>(p.d_u, i) * at<T>(p.saved_out, i) * p.r_next[t];
-        if (p.y) {
-            const float n = at<T>(p.y, i) * (p.w_post ? p.r_post[t] : 1.0f);
-            dwp += p.alpha * gate_at<T>(p, t, h) * d * n;
-            dg += p.alpha * d * n * (p.w_post ? at<T>(p.w_post, h) : 1.0f);
-        }
-        static_cast<T *>(p.d_res)[i] = from_f32<T>(d);  // after its last read of d_out: they may be one buffer
+    const int which = blockIdx.y, c = threadIdx.x & 31, k = threadIdx.x >> 5, h = blockIdx.x * 32 + c;
+    float *dst = which == 0 ? p.d_w_next : which == 1 ? p.d_w_post : (p.gate_kind == 1 ? static_cast<float *>(p.d_gate) : nullptr);
+    if (!dst) return;
+    float s = 0.0f;
+    if (h < p.H) {
+        const float *src = p.partial + static_cast<int64_t>(which) * p.H + h;
+#pragma unroll 8
+        for (int i = k; i < ctas; i += 8) s += src[static_cast<int64_t>(i) * 3 * p.H];
     }
-    if (p.d_w_next) p.d_w_next[h] = dwn;
-    if (p.d_w_post) p.d_w_post[h] = dwp;
-    if (p.gate_kind == 1 && p.d_gate) static_cast<float *>(p.d_gate)[h] = dg;
+    part[k][c] = s;
+    __syncthreads();
+    if (k == 0 && h < p.H) {
+#pragma unroll
+        for (int i = 1; i < 8; ++i) s += part[i][c];
+        dst[h] = s;
+    }
 }
 
-template <typename T> cudaError_t launch_forward(const NormParams &p, cudaStream_t stream) {
-    return launch_pdl(norm_kernel<T>, dim3(static_cast<unsigned>(p.T)), dim3(NORM_THREADS), 0, stream, p);
+// Threads of a CTA, CTAs of an SM and of the grid, and whether the rows go
+// through the ring, by H, the type and the tensors of a row.
+struct NormShape {
+    int ept, threads, ctas, stages;
+    bool ring;
+    size_t smem;
+};
+
+NormShape norm_shape(const NormParams &p, int elem, bool backward) {
+    NormShape s{};
+    const int64_t row_bytes = static_cast<int64_t>(p.H) * elem;
+    s.ept = p.H <= 8192 ? 8 : 16;
+    s.threads = ((p.H + s.ept - 1) / s.ept + 31) / 32 * 32;
+    // narrow rows: several CTAs an SM (the backward pass holds more registers)
+    int per_sm = (backward ? 896 : 1024) / s.threads;
+    per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
+    const int64_t all = static_cast<int64_t>(device_sm_count()) * per_sm;
+    s.ctas = static_cast<int>(p.T < all ? p.T : all);
+    const int kept = (p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0);
+    const int64_t stage = row_bytes * p.tensors, room = NORM_RING_BYTES / per_sm - kept * row_bytes;
+    s.ring = row_bytes % 16 == 0 && room >= 2 * stage;
+    if (s.ring) {
+        const int64_t rows = (p.T + s.ctas - 1) / (s.ctas > 0 ? s.ctas : 1), fit = room / stage;
+        s.stages = static_cast<int>(fit < NORM_MAX_STAGES ? fit : NORM_MAX_STAGES);
+        if (rows < s.stages) s.stages = static_cast<int>(rows);
+        s.smem = static_cast<size_t>(s.stages * stage + kept * row_bytes);
+    }
+    return s;
 }
 
-template <typename T> cudaError_t launch_backward(const NormParams &p, cudaStream_t stream) {
+// Registers by the CTA's threads: 80 and 128 for the backward pass up to 256
+// and 512 threads, 72 up to 896 (rows of 7168); 64 above and for the forward.
+template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+cudaError_t launch_rows(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
+    constexpr int FORWARD_CTAS = MAX_THREADS > 512 ? 1 : 1024 / MAX_THREADS;
+    auto kern = backward ? norm_backward_kernel<T, EPT, RING, MAX_THREADS, MIN_CTAS>
+                         : norm_kernel<T, EPT, RING, MAX_THREADS, FORWARD_CTAS>;
+    static std::atomic<bool> attr_done[64][2];  // zero-initialised; several host threads may launch
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (RING && (dev < 0 || dev >= 64 || !attr_done[dev][backward])) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_RING_BYTES);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev][backward] = true;
+    }
+    return launch_pdl(kern, dim3(static_cast<unsigned>(s.ctas)), dim3(static_cast<unsigned>(s.threads)), s.smem, stream, p);
+}
+
+template <typename T, bool RING>
+cudaError_t launch_sized(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
+    if (s.ept == 16) return launch_rows<T, 16, RING, 1024, 1>(p, s, backward, stream);
+    if (s.threads <= 256) return launch_rows<T, 8, RING, 256, 3>(p, s, backward, stream);
+    if (s.threads <= 512) return launch_rows<T, 8, RING, 512, 1>(p, s, backward, stream);
+    if (s.threads <= 896) return launch_rows<T, 8, RING, 896, 1>(p, s, backward, stream);
+    return launch_rows<T, 8, RING, 1024, 1>(p, s, backward, stream);
+}
+
+template <typename T> cudaError_t launch_typed(NormParams p, bool backward, cudaStream_t stream) {
+    const NormShape s = norm_shape(p, sizeof(T), backward);
+    p.stages = s.stages;
     if (p.T > 0) {
-        cudaError_t e = launch_pdl(norm_backward_rows<T>, dim3(static_cast<unsigned>(p.T)), dim3(NORM_THREADS), 0,
-                                   stream, p);
+        const cudaError_t e = s.ring ? launch_sized<T, true>(p, s, backward, stream) : launch_sized<T, false>(p, s, backward, stream);
         if (e != cudaSuccess) return e;
     }
-    return launch_pdl(norm_backward_columns<T>, dim3((p.H + 31) / 32), dim3(32), 0, stream, p);
+    if (!backward || (!p.d_w_next && !p.d_w_post && !(p.d_gate && p.gate_kind == 1))) return cudaSuccess;
+    return launch_pdl(norm_columns_kernel, dim3(static_cast<unsigned>((p.H + 31) / 32), 3), dim3(256), 0, stream, p, s.ctas);
 }
 
 }  // namespace
@@ -202,14 +521,18 @@ cudaError_t launch_residual_norm(const void *y, const void *res, const void *w_p
     p.u = u;
     p.rstd_post = rstd_post;
     p.rstd_next = rstd_next;
-    if (dtype == kF32) return launch_forward<float>(p, stream);
-    if (dtype == kBF16) return launch_forward<__nv_bfloat16>(p, stream);
-    return launch_forward<__half>(p, stream);
+    p.ring[p.tensors++] = res;
+    if (y) p.ring[p.tensors++] = y;
+    if (gate_kind == 3) p.ring[p.tensors++] = gate;
+    if (dtype == kF32) return launch_typed<float>(p, false, stream);
+    if (dtype == kBF16) return launch_typed<__nv_bfloat16>(p, false, stream);
+    return launch_typed<__half>(p, false, stream);
 }
 
 size_t residual_norm_backward_ws_bytes(int64_t T, int64_t H) {
-    (void)H;
-    return static_cast<size_t>(T) * 4 + 16;
+    // three rows of column sums for each CTA of the largest grid
+    const int64_t ctas = static_cast<int64_t>(device_sm_count()) * 16;
+    return static_cast<size_t>((T < ctas ? T : ctas) * 3 * H * 4 + 16);
 }
 
 cudaError_t launch_residual_norm_backward(const void *d_out, const void *d_u, const void *y, const void *out,
@@ -236,10 +559,18 @@ cudaError_t launch_residual_norm_backward(const void *d_out, const void *d_u, co
     p.d_gate = d_gate;
     p.d_w_post = d_w_post;
     p.d_w_next = d_w_next;
-    p.row_sum = static_cast<float *>(ws);
-    if (dtype == kF32) return launch_backward<float>(p, stream);
-    if (dtype == kBF16) return launch_backward<__nv_bfloat16>(p, stream);
-    return launch_backward<__half>(p, stream);
+    p.partial = static_cast<float *>(ws);
+    // in the order of the kernel's reads
+    if (d_out) p.ring[p.tensors++] = d_out;
+    if (w_next) {
+        p.ring[p.tensors++] = d_u;
+        p.ring[p.tensors++] = out;
+    }
+    if (y) p.ring[p.tensors++] = y;
+    if (gate_kind == 3) p.ring[p.tensors++] = gate;
+    if (dtype == kF32) return launch_typed<float>(p, true, stream);
+    if (dtype == kBF16) return launch_typed<__nv_bfloat16>(p, true, stream);
+    return launch_typed<__half>(p, true, stream);
 }
 
 }  // namespace moe
