@@ -50,6 +50,7 @@ template <typename T, int EPT, bool RING> struct Part;
 
 template <typename T, int EPT> struct Part<T, EPT, true> {
     static constexpr int EV = 16 / sizeof(T), V = EPT / EV;
+    static constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
     uint4 q[V];
     static __device__ __forceinline__ int at(int v) { return (v * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * EV; }
     __device__ __forceinline__ void load(const void *row, int H) {  // global or shared
@@ -62,17 +63,40 @@ template <typename T, int EPT> struct Part<T, EPT, true> {
         for (int v = 0; v < V; ++v)
             if (at(v) < H) *reinterpret_cast<uint4 *>(static_cast<T *>(row) + at(v)) = q[v];
     }
-    __device__ __forceinline__ float get(int i) const {
+    __device__ __forceinline__ void fill(float v) {
+        uint32_t w;
+        if constexpr (sizeof(T) == 4)
+            w = __float_as_uint(v);
+        else
+            w = pack2<DT>(v, v);
+#pragma unroll
+        for (int i = 0; i < V; ++i) q[i] = make_uint4(w, w, w, w);
+    }
+    // The packed words as if read anew: otherwise the compiler keeps the
+    // unpacked values across the reductions, twice the registers, and spills.
+    __device__ __forceinline__ void again() {
+#pragma unroll
+        for (int v = 0; v < V; ++v) asm volatile("" : "+r"(q[v].x), "+r"(q[v].y), "+r"(q[v].z), "+r"(q[v].w));
+    }
+    __device__ __forceinline__ uint32_t word(int i) const {  // the one that holds element i
         const uint4 &w = q[i / EV];
-        const int j = i % EV;
+        const int j = i % EV * static_cast<int>(sizeof(T)) / 4;
+        return j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
+    }
+    __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) {
-            return __uint_as_float(j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w);
+            return __uint_as_float(word(i));
         } else {
-            constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
-            const uint32_t b = j < 2 ? w.x : j < 4 ? w.y : j < 6 ? w.z : w.w;
-            const float2 f = unpack2<DT>(b);
-            return j & 1 ? f.y : f.x;
+            const float2 f = unpack2<DT>(word(i));
+            return i & 1 ? f.y : f.x;
         }
+    }
+    // this[i] * o[i], exact for 16-bit types: one mixed FMA, no unpacking
+    __device__ __forceinline__ float times(const Part &o, int i) const {
+        if constexpr (sizeof(T) == 4)
+            return get(i) * o.get(i);
+        else
+            return i & 1 ? fma_mixed<DT, true>(word(i), o.word(i), 0.0f) : fma_mixed<DT, false>(word(i), o.word(i), 0.0f);
     }
     static __device__ __forceinline__ void store(void *row, int H, const float (&f)[EPT]) {
 #pragma unroll
@@ -83,7 +107,6 @@ template <typename T, int EPT> struct Part<T, EPT, true> {
                 w = make_uint4(__float_as_uint(f[4 * v]), __float_as_uint(f[4 * v + 1]), __float_as_uint(f[4 * v + 2]),
                                __float_as_uint(f[4 * v + 3]));
             } else {
-                constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
                 w = make_uint4(pack2<DT>(f[8 * v], f[8 * v + 1]), pack2<DT>(f[8 * v + 2], f[8 * v + 3]),
                                pack2<DT>(f[8 * v + 4], f[8 * v + 5]), pack2<DT>(f[8 * v + 6], f[8 * v + 7]));
             }
@@ -109,7 +132,13 @@ template <typename T, int EPT> struct Part<T, EPT, false> {
         for (int i = 0; i < EPT; ++i) f[i] = at(i) < H ? to_f32(static_cast<const T *>(row)[at(i)]) : 0.0f;
     }
     __device__ __forceinline__ void put(void *, int) const {}
+    __device__ __forceinline__ void fill(float v) {
+#pragma unroll
+        for (int i = 0; i < EPT; ++i) f[i] = v;
+    }
+    __device__ __forceinline__ void again() {}
     __device__ __forceinline__ float get(int i) const { return f[i]; }
+    __device__ __forceinline__ float times(const Part &o, int i) const { return f[i] * o.f[i]; }
     static __device__ __forceinline__ void store(void *row, int H, const float (&v)[EPT]) {
 #pragma unroll
         for (int i = 0; i < EPT; ++i)
@@ -189,6 +218,8 @@ template <> struct RowRing<true> {
             stage = 0;
             phase ^= 1u;
         }
+        for (int i = 0; i < 64; ++i)  // before the slow read of the timer
+            if (mbar_try_wait(bars + 8u * stage, phase)) return true;
         const unsigned long long start = global_timer_ns();
         while (!mbar_try_wait(bars + 8u * stage, phase))
             if (global_timer_ns() - start > kWaitTimeoutNs) return false;
@@ -262,7 +293,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
                 float s = 0.0f;
 #pragma unroll
                 for (int i = 0; i < EPT; ++i) s += y.get(i) * y.get(i);
-                r2 = 1.0f / sqrtf(sums(s, 0.0f).x * per + p.eps);
+                r2 = rsqrtf(sums(s, 0.0f).x * per + p.eps);
                 if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
                 ring.refill();
                 read = true;
@@ -285,7 +316,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < EPT; ++i) s += o[i] * o[i];
-            const float r = 1.0f / sqrtf(sums(s, 0.0f).x * per + p.eps);
+            const float r = rsqrtf(sums(s, 0.0f).x * per + p.eps);
             if (p.rstd_next && threadIdx.x == 0) p.rstd_next[t] = r;
             if (!read) ring.refill();
             read = true;
@@ -302,9 +333,15 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
     }
 }
 
-template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+// The instructions of a row take as long as its bytes, so what a call has or
+// lacks is no test per element: an absent weight is a row of ones, and the
+// gate's three forms (a row, of ones where there is none; one factor a token;
+// a factor an element) are three kernels.  4096 x 7168 bf16: 117 us with the
+// tests, 84 us without.
+template <typename T, int EPT, bool RING, int GATE, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(const __grid_constant__ NormParams p) {
     using P = Part<T, EPT, RING>;
+    constexpr bool TOKEN = GATE == 2, FULL = GATE == 3, ROW = !TOKEN && !FULL;
     extern __shared__ __align__(128) uint8_t norm_smem[];
     __shared__ float2 scratch[64];
     __shared__ uint64_t bars[NORM_MAX_STAGES];
@@ -314,7 +351,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
     griddep_launch_dependents();
     ring.start();
     const int H = p.H;
-    const bool has_y = p.y != nullptr, post = p.w_post != nullptr, nxt = p.w_next != nullptr, above = p.d_out != nullptr;
+    const bool has_y = p.y != nullptr, post = p.w_post != nullptr, nxt = p.w_next != nullptr;
     const float per = 1.0f / static_cast<float>(H);
     uint8_t *room = norm_smem + static_cast<int64_t>(p.stages) * p.tensors * H * sizeof(T);
     const void *w_post = keep_row<P, RING>(p.w_post, room, H, sizeof(T));
@@ -327,73 +364,82 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
         const int64_t t = ring.row, base = t * H;
         if (!ring.next()) return;
         int at = 0;
-        bool read = false;
+        bool read = false;  // every thread has read the stage
         float d[EPT];
-        if (above) {
-            P d_out;
+        P d_out, d_u, out, y, gate, w;
+        if (p.d_out)
             d_out.load(ring.tensor(at++), H);
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) d[i] = d_out.get(i);
-        } else {
-#pragma unroll
-            for (int i = 0; i < EPT; ++i) d[i] = 0.0f;
-        }
-        P d_u, out, y, gate;
+        else
+            d_out.fill(0.0f);
         if (nxt) {
             d_u.load(ring.tensor(at++), H);
             out.load(ring.tensor(at++), H);
         }
         if (has_y) y.load(ring.tensor(at++), H);
-        if (p.gate_kind == 3) gate.load(ring.tensor(at), H);
+        if (FULL) gate.load(ring.tensor(at), H);
         if (nxt) {
             const float r = p.r_next[t];
             float s = 0.0f;
-            P w;
             w.load(w_next, H);
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) s += d_u.get(i) * w.get(i) * out.get(i);
-            const float back = sums(s, 0.0f).x * (r * r * r * per);
+            for (int i = 0; i < EPT; ++i) s = fmaf(d_u.times(w, i), out.get(i), s);
+            const float back = -(sums(s, 0.0f).x * (r * r * r * per));
             ring.refill();
             read = true;
+            d_u.again();
+            w.again();
+            out.again();
 #pragma unroll
             for (int i = 0; i < EPT; ++i) {
-                d[i] += r * d_u.get(i) * w.get(i) - out.get(i) * back;
-                sum_next[i] += d_u.get(i) * out.get(i) * r;
+                d[i] = fmaf(out.get(i), back, fmaf(r, d_u.times(w, i), d_out.get(i)));
+                sum_next[i] = fmaf(r, d_u.times(out, i), sum_next[i]);
             }
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) d[i] = d_out.get(i);
         }
         P::store(static_cast<T *>(p.d_res) + base, H, d);
         if (has_y) {
             const float r2 = post ? p.r_post[t] : 1.0f;
-            const float g_row = p.gate_kind == 2 ? to_f32(static_cast<const T *>(p.gate)[t]) : 1.0f;
+            const float factor = TOKEN ? p.alpha * to_f32(static_cast<const T *>(p.gate)[t]) : p.alpha;
             float s = 0.0f, sg = 0.0f;
-            P w;
-            if (post) w.load(w_post, H);
-            if (p.gate_kind == 1) gate.load(gate_row, H);
-            if (p.gate_kind == 3 && p.d_gate) {
+            if (post)
+                w.load(w_post, H);
+            else
+                w.fill(1.0f);
+            if (ROW) {
+                if (p.gate_kind == 1)
+                    gate.load(gate_row, H);
+                else
+                    gate.fill(1.0f);
+            }
+            if (FULL && p.d_gate) {
                 float dg[EPT];
 #pragma unroll
-                for (int i = 0; i < EPT; ++i) dg[i] = p.alpha * d[i] * (y.get(i) * r2 * (post ? w.get(i) : 1.0f));
+                for (int i = 0; i < EPT; ++i) dg[i] = p.alpha * d[i] * (r2 * y.times(w, i));
                 P::store(static_cast<T *>(p.d_gate) + base, H, dg);
             }
+            const float alpha2 = p.alpha * r2;
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {  // d becomes dz
-                const float n = y.get(i) * r2, wi = post ? w.get(i) : 1.0f;
-                const float dg = p.alpha * d[i] * (n * wi);
-                sg += dg;
-                if (p.gate_kind == 1) sum_gate[i] += dg;
-                d[i] = p.alpha * ((p.gate_kind & 1) ? gate.get(i) : g_row) * d[i];
-                s += d[i] * wi * y.get(i);
-                sum_post[i] += d[i] * n;
+            for (int i = 0; i < EPT; ++i) {  // d becomes dz * w_post
+                if (ROW) sum_gate[i] = fmaf(alpha2 * d[i], y.times(w, i), sum_gate[i]);
+                if (TOKEN) sg = fmaf(alpha2 * d[i], y.times(w, i), sg);
+                float dz = factor * d[i];
+                if (!TOKEN) dz *= gate.get(i);
+                sum_post[i] = fmaf(dz * r2, y.get(i), sum_post[i]);
+                d[i] = dz * w.get(i);
+                s = fmaf(d[i], y.get(i), s);
             }
-            if (post || p.gate_kind == 2) {
+            if (post || TOKEN) {
                 const float2 row = sums(s, sg);
                 if (!read) ring.refill();
                 read = true;
-                if (p.gate_kind == 2 && p.d_gate && threadIdx.x == 0) static_cast<float *>(p.d_gate)[t] = row.y;
+                if (TOKEN && p.d_gate && threadIdx.x == 0) static_cast<float *>(p.d_gate)[t] = row.y;
                 if (post) {
-                    const float back = row.x * (r2 * r2 * r2 * per);
+                    const float back = -(row.x * (r2 * r2 * r2 * per));
+                    y.again();
 #pragma unroll
-                    for (int i = 0; i < EPT; ++i) d[i] = r2 * d[i] * w.get(i) - y.get(i) * back;
+                    for (int i = 0; i < EPT; ++i) d[i] = fmaf(y.get(i), back, r2 * d[i]);
                 }
             }
             P::store(static_cast<T *>(p.d_y) + base, H, d);
@@ -443,17 +489,25 @@ struct NormShape {
 
 NormShape norm_shape(const NormParams &p, int elem, bool backward) {
     NormShape s{};
-    const int64_t row_bytes = static_cast<int64_t>(p.H) * elem;
-    s.ept = p.H <= 8192 ? 8 : 16;
-    s.threads = ((p.H + s.ept - 1) / s.ept + 31) / 32 * 32;
-    // narrow rows: several CTAs an SM (the backward pass holds more registers)
-    int per_sm = (backward ? 896 : 1024) / s.threads;
-    per_sm = per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
+    const int64_t row_bytes = static_cast<int64_t>(p.H) * elem, stage = row_bytes * p.tensors;
+    const int kept = (p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0);
+    int64_t room = 0;
+    int per_sm = 1;
+    auto size = [&](int ept) {
+        s.ept = ept;
+        s.threads = ((p.H + ept - 1) / ept + 31) / 32 * 32;
+        // narrow rows: several CTAs an SM (the backward pass holds more registers)
+        per_sm = (backward ? 896 : 1024) / s.threads;
+        per_sm = per_sm < 1 || (backward && ept == 16) ? 1 : per_sm > 16 ? 16 : per_sm;
+        room = NORM_RING_BYTES / per_sm - kept * row_bytes;
+        s.ring = row_bytes % 16 == 0 && room >= 2 * stage;
+    };
+    // Forward: 16 elements a thread above 4096, for two CTAs an SM.  Backward:
+    // 8 with the ring as long as the registers allow (72 at 896 threads).
+    size(p.H <= (backward ? 7168 : 4096) ? 8 : 16);
+    if (!s.ring && p.H > 4096) size(16);
     const int64_t all = static_cast<int64_t>(device_sm_count()) * per_sm;
     s.ctas = static_cast<int>(p.T < all ? p.T : all);
-    const int kept = (p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0);
-    const int64_t stage = row_bytes * p.tensors, room = NORM_RING_BYTES / per_sm - kept * row_bytes;
-    s.ring = row_bytes % 16 == 0 && room >= 2 * stage;
     if (s.ring) {
         const int64_t rows = (p.T + s.ctas - 1) / (s.ctas > 0 ? s.ctas : 1), fit = room / stage;
         s.stages = static_cast<int>(fit < NORM_MAX_STAGES ? fit : NORM_MAX_STAGES);
@@ -463,38 +517,61 @@ NormShape norm_shape(const NormParams &p, int elem, bool backward) {
     return s;
 }
 
-// Registers by the CTA's threads: 80 and 128 for the backward pass up to 256
-// and 512 threads, 72 up to 896 (rows of 7168); 64 above and for the forward.
-template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
-cudaError_t launch_rows(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
-    constexpr int FORWARD_CTAS = MAX_THREADS > 512 ? 1 : 1024 / MAX_THREADS;
-    auto kern = backward ? norm_backward_kernel<T, EPT, RING, MAX_THREADS, MIN_CTAS>
-                         : norm_kernel<T, EPT, RING, MAX_THREADS, FORWARD_CTAS>;
-    static std::atomic<bool> attr_done[64][2];  // zero-initialised; several host threads may launch
+cudaError_t launch_kernel(void (*kern)(NormParams), std::atomic<bool> *attr_done, const NormParams &p, const NormShape &s,
+                          cudaStream_t stream) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    if (RING && (dev < 0 || dev >= 64 || !attr_done[dev][backward])) {
+    if (s.ring && (dev < 0 || dev >= 64 || !attr_done[dev])) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_RING_BYTES);
         if (e != cudaSuccess) return e;
-        if (dev >= 0 && dev < 64) attr_done[dev][backward] = true;
+        if (dev >= 0 && dev < 64) attr_done[dev] = true;
     }
     return launch_pdl(kern, dim3(static_cast<unsigned>(s.ctas)), dim3(static_cast<unsigned>(s.threads)), s.smem, stream, p);
 }
 
-template <typename T, bool RING>
-cudaError_t launch_sized(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
-    if (s.ept == 16) return launch_rows<T, 16, RING, 1024, 1>(p, s, backward, stream);
-    if (s.threads <= 256) return launch_rows<T, 8, RING, 256, 3>(p, s, backward, stream);
-    if (s.threads <= 512) return launch_rows<T, 8, RING, 512, 1>(p, s, backward, stream);
-    if (s.threads <= 896) return launch_rows<T, 8, RING, 896, 1>(p, s, backward, stream);
-    return launch_rows<T, 8, RING, 1024, 1>(p, s, backward, stream);
+template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+cudaError_t launch_forward(const NormParams &p, const NormShape &s, cudaStream_t stream) {
+    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
+    return launch_kernel(norm_kernel<T, EPT, RING, MAX_THREADS, MIN_CTAS>, attr_done, p, s, stream);
+}
+
+template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+cudaError_t launch_backward(const NormParams &p, const NormShape &s, cudaStream_t stream) {
+    static std::atomic<bool> attr_done[3][64];  // zero-initialised; several host threads may launch
+    if (p.gate_kind == 2)
+        return launch_kernel(norm_backward_kernel<T, EPT, RING, 2, MAX_THREADS, MIN_CTAS>, attr_done[1], p, s, stream);
+    if (p.gate_kind == 3)
+        return launch_kernel(norm_backward_kernel<T, EPT, RING, 3, MAX_THREADS, MIN_CTAS>, attr_done[2], p, s, stream);
+    return launch_kernel(norm_backward_kernel<T, EPT, RING, 1, MAX_THREADS, MIN_CTAS>, attr_done[0], p, s, stream);
+}
+
+// Registers by the CTA's threads: the forward pass has 64; the backward pass
+// 80 up to 256 threads, 128 up to 512, 72 up to 896 (rows of 7168), 64 above.
+template <typename T> cudaError_t launch_shape(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
+    if (!backward) {
+        if (s.ept == 16) {
+            if (s.threads <= 512)
+                return s.ring ? launch_forward<T, 16, true, 512, 2>(p, s, stream) : launch_forward<T, 16, false, 512, 2>(p, s, stream);
+            return s.ring ? launch_forward<T, 16, true, 1024, 1>(p, s, stream) : launch_forward<T, 16, false, 1024, 1>(p, s, stream);
+        }
+        return s.ring ? launch_forward<T, 8, true, 512, 2>(p, s, stream) : launch_forward<T, 8, false, 512, 2>(p, s, stream);
+    }
+    if (s.ept == 16) {
+        if (s.threads <= 512)
+            return s.ring ? launch_backward<T, 16, true, 512, 1>(p, s, stream) : launch_backward<T, 16, false, 512, 1>(p, s, stream);
+        return s.ring ? launch_backward<T, 16, true, 1024, 1>(p, s, stream) : launch_backward<T, 16, false, 1024, 1>(p, s, stream);
+    }
+    if (!s.ring) return launch_backward<T, 8, false, 512, 1>(p, s, stream);
+    if (s.threads <= 256) return launch_backward<T, 8, true, 256, 3>(p, s, stream);
+    if (s.threads <= 512) return launch_backward<T, 8, true, 512, 1>(p, s, stream);
+    return launch_backward<T, 8, true, 896, 1>(p, s, stream);
 }
 
 template <typename T> cudaError_t launch_typed(NormParams p, bool backward, cudaStream_t stream) {
     const NormShape s = norm_shape(p, sizeof(T), backward);
     p.stages = s.stages;
     if (p.T > 0) {
-        const cudaError_t e = s.ring ? launch_sized<T, true>(p, s, backward, stream) : launch_sized<T, false>(p, s, backward, stream);
+        const cudaError_t e = launch_shape<T>(p, s, backward, stream);
         if (e != cudaSuccess) return e;
     }
     if (!backward || (!p.d_w_next && !p.d_w_post && !(p.d_gate && p.gate_kind == 1))) return cudaSuccess;
