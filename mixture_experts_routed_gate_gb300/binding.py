@@ -720,6 +720,64 @@ def moe_forward(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=None, e
     return out
 
 
+# --------------------------------------------------------------------------- checks and calls of the entry points below
+# (a decode step's calls take about as long on the host as on the GPU: the
+# checks look at each tensor once, and a call switches devices only when it must)
+
+def _need(t, name, dtype, shape):
+    """t is a contiguous CUDA tensor of this dtype and shape."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+        return t
+    _cuda(t, name, dtype=dtype)
+    raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _want(t, name, dtype, shape, dev):
+    """An output: the caller's, checked, or a new one."""
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _need(t, name, dtype, shape)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+# the current stream's handle without a Stream object (about 5 us a call)
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    lambda i: torch.cuda.current_stream(i).cuda_stream
+
+
+def _call(what, dev, *args):
+    """The library's `what` with these arguments and the device's current stream."""
+    fn = getattr(_lib or lib(), what)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(*args, _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(*args, _raw_stream(dev.index))
+    if status != 0:
+        raise MoEError(status, what)
+
+
+def _err(err):
+    if err is not None:
+        _cuda(err, "err", dtype=torch.int32)
+    return _at(err)
+
+
+def _ws(ws, dev, what, *sizes):
+    """The caller's workspace or a new one, and its bytes."""
+    if ws is None:
+        n = getattr(_lib or lib(), what + "_workspace_bytes")(*sizes)
+        if n == _NO_BYTES:
+            raise ValueError(f"{what}: unsupported sizes or dtype")
+        return torch.empty(n, dtype=torch.uint8, device=dev), n
+    _cuda(ws, "ws", dtype=torch.uint8)
+    return ws, ws.numel()
+
+
+_NO_BYTES = ctypes.c_size_t(-1).value
+
+
 # --------------------------------------------------------------------------- norms around a block
 
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
@@ -737,27 +795,7 @@ def _gate_kind(gate, T, H, dtype):
         return GATE_FULL
     if shape == (T, 1):
         return GATE_TOKEN
-    raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {shape}")
-
-
-def _like(t, ref, name):
-    _cuda(t, name, dtype=ref.dtype)
-    if t.shape != ref.shape or t.device != ref.device:
-        raise ValueError(f"{name} must be {tuple(ref.shape)} on {ref.device}, got {tuple(t.shape)} on {t.device}")
-    return t
-
-
-def _norm_weight(w, H, dtype, name):
-    if w is not None:
-        _cuda(w, name, dtype=dtype)
-        if tuple(w.shape) != (H,):
-            raise ValueError(f"{name} must be [{H}], got {tuple(w.shape)}")
-
-
-def _row_stat(t, T, name):
-    _cuda(t, name, dtype=torch.float32)
-    if tuple(t.shape) != (T,):
-        raise ValueError(f"{name} must be [{T}], got {tuple(t.shape)}")
+    raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {list(shape)}")
 
 
 def moe_residual_norm(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next=None, eps: float = 1e-6,
@@ -769,32 +807,29 @@ def moe_residual_norm(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next
     gate: [H], [T, 1], [T, H] or None; y None: u is the norm of res.  ``out``
     may be ``res`` itself."""
     _cuda(res, "res", ndim=2)
-    T, H = res.shape
-    dt, dev = res.dtype, res.device
+    shape, dt, dev = res.shape, res.dtype, res.device
+    T, H = shape
     if y is None and w_next is None:
         raise ValueError("nothing to compute: give y, w_next or both")
     if y is None and (w_post is not None or gate is not None or out is not None):
         raise ValueError("w_post, gate and out need y")
     if u is not None and w_next is None:
         raise ValueError("u needs w_next")
-    if y is not None:
-        _like(y, res, "y")
-        out = torch.empty_like(res) if out is None else _like(out, res, "out")
-    _norm_weight(w_post, H, dt, "w_post")
-    _norm_weight(w_next, H, dt, "w_next")
-    kind = _gate_kind(gate, T, H, dt)
+    code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt)
     got = {}
     if y is not None:
-        got["out"] = out
-    if w_next is not None:
-        got["u"] = u = torch.empty_like(res) if u is None else _like(u, res, "u")
-        got["rstd_next"] = torch.empty(T, dtype=torch.float32, device=dev)
+        _need(y, "y", dt, shape)
+        got["out"] = out = _want(out, "out", dt, shape, dev)
+    r_post = r_next = None
     if w_post is not None:
-        got["rstd_post"] = torch.empty(T, dtype=torch.float32, device=dev)
-    with torch.cuda.device(dev):
-        _check(lib().moe_residual_norm(_ptr(y), _ptr(res), _ptr(w_post), _ptr(gate), kind, alpha, _ptr(w_next), eps,
-                                       T, H, _dtype_code(res, "res"), _ptr(out), _ptr(u), _ptr(got.get("rstd_post")),
-                                       _ptr(got.get("rstd_next")), _stream(dev)), "moe_residual_norm")
+        _need(w_post, "w_post", dt, (H,))
+        got["rstd_post"] = r_post = torch.empty(T, dtype=torch.float32, device=dev)
+    if w_next is not None:
+        _need(w_next, "w_next", dt, (H,))
+        got["u"] = u = _want(u, "u", dt, shape, dev)
+        got["rstd_next"] = r_next = torch.empty(T, dtype=torch.float32, device=dev)
+    _call("moe_residual_norm", dev, _at(y), _at(res), _at(w_post), _at(gate), kind, alpha, _at(w_next), eps, T, H, code,
+          _at(out), _at(u), _at(r_post), _at(r_next))
     return got
 
 
@@ -808,12 +843,9 @@ def moe_residual_norm_backward(d_out, d_u, y, out, w_post=None, gate=None, alpha
     ref = d_u if d_out is None else d_out
     if ref is None:
         raise ValueError("d_out or d_u is needed")
-    _cuda(ref, "d_out" if d_out is not None else "d_u", ndim=2)
-    T, H = ref.shape
-    dt, dev = ref.dtype, ref.device
-    for t, name in ((d_u, "d_u"), (y, "y"), (out, "out")):
-        if t is not None:
-            _like(t, ref, name)
+    _cuda(ref, "d_u" if d_out is None else "d_out", ndim=2)
+    shape, dt, dev, f32 = ref.shape, ref.dtype, ref.device, torch.float32
+    T, H = shape
     if (d_u is None) != (w_next is None):
         raise ValueError("d_u and w_next go together")
     if w_next is not None and (out is None or rstd_next is None):
@@ -822,35 +854,30 @@ def moe_residual_norm_backward(d_out, d_u, y, out, w_post=None, gate=None, alpha
         raise ValueError("w_post and gate need y")
     if w_post is not None and rstd_post is None:
         raise ValueError("w_post needs rstd_post")
-    _norm_weight(w_post, H, dt, "w_post")
-    _norm_weight(w_next, H, dt, "w_next")
-    if w_post is not None:
-        _row_stat(rstd_post, T, "rstd_post")
-    if w_next is not None:
-        _row_stat(rstd_next, T, "rstd_next")
-    kind = _gate_kind(gate, T, H, dt)
-    f32 = dict(dtype=torch.float32, device=dev)
-    got = {"d_res": torch.empty_like(ref)}
+    code, kind = _dtype_code(ref, "d_out"), _gate_kind(gate, T, H, dt)
+    if out is not None:
+        _need(out, "out", dt, shape)
+    d_res = torch.empty(shape, dtype=dt, device=dev)
+    got = {"d_res": d_res}
+    d_y = d_gate = d_w_post = d_w_next = None
     if y is not None:
-        got["d_y"] = torch.empty_like(ref)
-    if kind == GATE_FULL:
-        got["d_gate"] = torch.empty_like(ref)
-    elif kind != GATE_NONE:
-        got["d_gate"] = torch.empty(gate.shape, **f32)
+        _need(y, "y", dt, shape)
+        got["d_y"] = d_y = torch.empty(shape, dtype=dt, device=dev)
+    if kind != GATE_NONE:
+        got["d_gate"] = d_gate = torch.empty(gate.shape, dtype=dt if kind == GATE_FULL else f32, device=dev)
     if w_post is not None:
-        got["d_w_post"] = torch.empty(H, **f32)
+        _need(w_post, "w_post", dt, (H,))
+        _need(rstd_post, "rstd_post", f32, (T,))
+        got["d_w_post"] = d_w_post = torch.empty(H, dtype=f32, device=dev)
     if w_next is not None:
-        got["d_w_next"] = torch.empty(H, **f32)
-    if ws is None:
-        need = _ws_bytes(lib().moe_residual_norm_backward_workspace_bytes(T, H), "moe_residual_norm_backward")
-        ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _cuda(ws, "ws", dtype=torch.uint8)
-    with torch.cuda.device(dev):
-        _check(lib().moe_residual_norm_backward(
-            _ptr(d_out), _ptr(d_u), _ptr(y), _ptr(out), _ptr(w_post), _ptr(gate), kind, alpha, _ptr(w_next),
-            _ptr(rstd_post), _ptr(rstd_next), T, H, _dtype_code(ref, "d_out"), _ptr(got["d_res"]), _ptr(got.get("d_y")),
-            _ptr(got.get("d_gate")), _ptr(got.get("d_w_post")), _ptr(got.get("d_w_next")), _ptr(ws), ws.numel(),
-            _stream(dev)), "moe_residual_norm_backward")
+        _need(d_u, "d_u", dt, shape)
+        _need(w_next, "w_next", dt, (H,))
+        _need(rstd_next, "rstd_next", f32, (T,))
+        got["d_w_next"] = d_w_next = torch.empty(H, dtype=f32, device=dev)
+    ws, nws = _ws(ws, dev, "moe_residual_norm_backward", T, H)
+    _call("moe_residual_norm_backward", dev, _at(d_out), _at(d_u), _at(y), _at(out), _at(w_post), _at(gate), kind, alpha,
+          _at(w_next), _at(rstd_post), _at(rstd_next), T, H, code, _at(d_res), _at(d_y), _at(d_gate), _at(d_w_post),
+          _at(d_w_next), _at(ws), nws)
     return got
 
 
@@ -859,42 +886,29 @@ def moe_residual_norm_backward(d_out, d_u, y, out, w_post=None, gate=None, alpha
 FEW_MAX_T = 16
 
 
-def _ws_bytes(n: int, what: str) -> int:
-    if n == ctypes.c_size_t(-1).value:
-        raise ValueError(f"{what}: unsupported sizes or dtype")
-    return n
-
-
 def forward_few_workspace_bytes(T, d_h, d_e, E, k, dtype) -> int:
-    return _ws_bytes(lib().moe_forward_few_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]), "moe_forward_few")
+    return int(lib().moe_forward_few_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]))
 
 
 def moe_forward_few(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=None, err=None):
     """The routed layer for at most FEW_MAX_T tokens, as :func:`moe_forward`
     (the same routing, less rounding); returns out [T, d_hidden]."""
     _cuda(x, "x", ndim=2)
-    for n, t, nd in (("w_g", w_g, 2), ("w_gate", w_gate, 3), ("w_up", w_up, 3), ("w_down", w_down, 3)):
-        _cuda(t, n, dtype=x.dtype, ndim=nd)
     T, d_h = x.shape
+    dt, dev = x.dtype, x.device
+    _cuda(w_gate, "w_gate", dtype=dt, ndim=3)
     E, d_e, _ = w_gate.shape
-    if tuple(w_gate.shape) != (E, d_e, d_h) or w_up.shape != w_gate.shape:
-        raise ValueError("w_gate / w_up must be [E, d_expert, d_hidden]")
-    if tuple(w_down.shape) != (E, d_h, d_e) or tuple(w_g.shape) != (E, d_h):
-        raise ValueError("w_down must be [E, d_hidden, d_expert] and w_g [E, d_hidden]")
+    _need(w_gate, "w_gate", dt, (E, d_e, d_h))
+    _need(w_up, "w_up", dt, (E, d_e, d_h))
+    _need(w_down, "w_down", dt, (E, d_h, d_e))
+    _need(w_g, "w_g", dt, (E, d_h))
     if bias is not None:
-        _cuda(bias, "bias", dtype=torch.float32, ndim=1)
-        if bias.numel() != E:
-            raise ValueError("bias must be [E]")
-    if ws is None:
-        ws = torch.empty(forward_few_workspace_bytes(T, d_h, d_e, E, k, x.dtype), dtype=torch.uint8, device=x.device)
-    _cuda(ws, "ws", dtype=torch.uint8)
-    out = torch.empty_like(x) if out is None else _like(out, x, "out")
-    if err is not None:
-        _cuda(err, "err", dtype=torch.int32)
-    with torch.cuda.device(x.device):
-        _check(lib().moe_forward_few(_ptr(x), _ptr(w_g), _ptr(bias), _ptr(w_gate), _ptr(w_up), _ptr(w_down), T, d_h,
-                                     d_e, E, k, _dtype_code(x, "x"), _ptr(ws), ws.numel(), _ptr(out), _ptr(err),
-                                     _stream(x.device)), "moe_forward_few")
+        _need(bias, "bias", torch.float32, (E,))
+    code = _dtype_code(x, "x")
+    ws, nws = _ws(ws, dev, "moe_forward_few", T, d_h, d_e, E, k, code)
+    out = _want(out, "out", dt, x.shape, dev)
+    _call("moe_forward_few", dev, _at(x), _at(w_g), _at(bias), _at(w_gate), _at(w_up), _at(w_down), T, d_h, d_e, E, k, code,
+          _at(ws), nws, _at(out), _err(err))
     return out
 
 
@@ -902,13 +916,13 @@ def moe_forward_few(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=Non
 
 def _mx4(q, sf, name, lead):
     """q [*lead, K / 2], sf [*lead, K / 32]: returns K."""
+    if isinstance(q, torch.Tensor) and q.dim() == len(lead) + 1 and (2 * q.shape[-1]) % 32 == 0:
+        half = q.shape[-1]
+        _need(q, f"q{name}", torch.uint8, (*lead, half))
+        _need(sf, f"sf{name}", torch.uint8, (*lead, half // 16))
+        return 2 * half
     _cuda(q, f"q{name}", dtype=torch.uint8, ndim=len(lead) + 1)
-    _cuda(sf, f"sf{name}", dtype=torch.uint8, ndim=len(lead) + 1)
-    K = 2 * q.shape[-1]
-    if K % 32 != 0 or tuple(q.shape[:-1]) != tuple(lead) or tuple(sf.shape) != (*lead, K // 32):
-        raise ValueError(f"q{name} / sf{name} must be {(*lead, 'K / 2')} / {(*lead, 'K / 32')} with K % 32 == 0, "
-                         f"got {tuple(q.shape)} / {tuple(sf.shape)}")
-    return K
+    raise ValueError(f"q{name} must be {(*lead, 'K / 2')} with K % 32 == 0, got {tuple(q.shape)}")
 
 
 def moe_quantize_mx4(x, row_idx=None, q=None, sf=None, err=None):
@@ -920,31 +934,20 @@ def moe_quantize_mx4(x, row_idx=None, q=None, sf=None, err=None):
         raise ValueError("K must be a multiple of 32")
     if row_idx is not None:
         _cuda(row_idx, "row_idx", dtype=torch.int32, ndim=1)
-    R = T if row_idx is None else row_idx.numel()
-    u8 = dict(dtype=torch.uint8, device=x.device)
-    q = torch.empty((R, K // 2), **u8) if q is None else q
-    sf = torch.empty((R, K // 32), **u8) if sf is None else sf
-    _mx4(q, sf, "", (R,))
-    if err is not None:
-        _cuda(err, "err", dtype=torch.int32)
-    with torch.cuda.device(x.device):
-        _check(lib().moe_quantize_mx4(_ptr(x), _ptr(row_idx), R, T, K, _dtype_code(x, "x"), _ptr(q), _ptr(sf),
-                                      _ptr(err), _stream(x.device)), "moe_quantize_mx4")
+    R, dev = T if row_idx is None else row_idx.shape[0], x.device
+    q = _want(q, "q", torch.uint8, (R, K // 2), dev)
+    sf = _want(sf, "sf", torch.uint8, (R, K // 32), dev)
+    _call("moe_quantize_mx4", dev, _at(x), _at(row_idx), R, T, K, _dtype_code(x, "x"), _at(q), _at(sf), _err(err))
     return q, sf
 
 
 def moe_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None):
     """The values of q [R, K / 2], sf [R, K / 32] as [R, K] in dtype."""
     _cuda(q, "q", dtype=torch.uint8, ndim=2)
-    K = _mx4(q, sf, "", (q.shape[0],))
-    if out is None:
-        out = torch.empty((q.shape[0], K), dtype=dtype, device=q.device)
-    _cuda(out, "out", dtype=dtype, ndim=2)
-    if tuple(out.shape) != (q.shape[0], K):
-        raise ValueError(f"out must be {(q.shape[0], K)}, got {tuple(out.shape)}")
-    with torch.cuda.device(q.device):
-        _check(lib().moe_dequantize_mx4(_ptr(q), _ptr(sf), q.shape[0], K, _dtype_code(out, "out"), _ptr(out),
-                                        _stream(q.device)), "moe_dequantize_mx4")
+    R = q.shape[0]
+    K = _mx4(q, sf, "", (R,))
+    out = _want(out, "out", dtype, (R, K), q.device)
+    _call("moe_dequantize_mx4", q.device, _at(q), _at(sf), R, K, _dtype_code(out, "out"), _at(out))
     return out
 
 
@@ -958,17 +961,9 @@ def moe_grouped_gemm_mx4(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16,
     if _mx4(q_b, sf_b, "_b", (E, N)) != K:
         raise ValueError("the two sides disagree on K")
     s, o, p, g = _tables(tables)
-    if out is None:
-        out = torch.empty((rows, N), dtype=out_dtype, device=q_a.device)
-    _cuda(out, "out", dtype=out_dtype)
-    if tuple(out.shape) != (rows, N):
-        raise ValueError(f"out must be [{rows}, {N}], got {tuple(out.shape)}")
-    if err is not None:
-        _cuda(err, "err", dtype=torch.int32)
-    with torch.cuda.device(q_a.device):
-        _check(lib().moe_grouped_gemm_mx4(_ptr(q_a), _ptr(sf_a), _ptr(q_b), _ptr(sf_b), _ptr(s), _ptr(o), _ptr(p),
-                                          _ptr(g), g.numel(), rows, N, K, E, _dtype_code(out, "out"), _ptr(out),
-                                          _ptr(err), _stream(q_a.device)), "moe_grouped_gemm_mx4")
+    out = _want(out, "out", out_dtype, (rows, N), q_a.device)
+    _call("moe_grouped_gemm_mx4", q_a.device, _at(q_a), _at(sf_a), _at(q_b), _at(sf_b), _at(s), _at(o), _at(p), _at(g),
+          g.shape[0], rows, N, K, E, _dtype_code(out, "out"), _at(out), _err(err))
     return out
 
 
@@ -1000,54 +995,36 @@ def moe_grouped_gate_up_silu_mx4(q_a, sf_a, experts: "Mx4Experts", tables, q_h=N
     """h = silu(A W_gate^T) * (A W_up^T) over the dispatch tables, quantised:
     returns q_h [rows, d_e / 2], sf_h [rows, d_e / 32]."""
     _cuda(q_a, "q_a", dtype=torch.uint8, ndim=2)
-    rows = q_a.shape[0]
-    if _mx4(q_a, sf_a, "_a", (rows,)) != experts.d_h:
+    rows, dev, e = q_a.shape[0], q_a.device, experts
+    if _mx4(q_a, sf_a, "_a", (rows,)) != e.d_h:
         raise ValueError("the rows and the experts disagree on d_hidden")
     s, o, p, g = _tables(tables)
-    u8 = dict(dtype=torch.uint8, device=q_a.device)
-    q_h = torch.empty((rows, experts.d_e // 2), **u8) if q_h is None else q_h
-    sf_h = torch.empty((rows, experts.d_e // 32), **u8) if sf_h is None else sf_h
-    if _mx4(q_h, sf_h, "_h", (rows,)) != experts.d_e:
-        raise ValueError("q_h must be [rows, d_expert / 2]")
-    if err is not None:
-        _cuda(err, "err", dtype=torch.int32)
-    e = experts
-    with torch.cuda.device(q_a.device):
-        _check(lib().moe_grouped_gate_up_silu_mx4(
-            _ptr(q_a), _ptr(sf_a), _ptr(e.q_gate), _ptr(e.sf_gate), _ptr(e.q_up), _ptr(e.sf_up), _ptr(s), _ptr(o),
-            _ptr(p), _ptr(g), g.numel(), rows, e.d_h, e.d_e, e.E, _ptr(q_h), _ptr(sf_h), _ptr(err),
-            _stream(q_a.device)), "moe_grouped_gate_up_silu_mx4")
+    q_h = _want(q_h, "q_h", torch.uint8, (rows, e.d_e // 2), dev)
+    sf_h = _want(sf_h, "sf_h", torch.uint8, (rows, e.d_e // 32), dev)
+    _call("moe_grouped_gate_up_silu_mx4", dev, _at(q_a), _at(sf_a), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
+          _at(s), _at(o), _at(p), _at(g), g.shape[0], rows, e.d_h, e.d_e, e.E, _at(q_h), _at(sf_h), _err(err))
     return q_h, sf_h
 
 
 def forward_mx4_workspace_bytes(T, d_h, d_e, E, k, dtype) -> int:
-    return _ws_bytes(lib().moe_forward_mx4_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]), "moe_forward_mx4")
+    return int(lib().moe_forward_mx4_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]))
 
 
 def moe_forward_mx4(x, w_g, bias, experts: "Mx4Experts", k: int, ws=None, out=None, err=None):
     """The routed forward with mx4 experts and activations; returns out [T, d_hidden]."""
     _cuda(x, "x", ndim=2)
-    _cuda(w_g, "w_g", dtype=x.dtype, ndim=2)
     T, d_h = x.shape
-    e = experts
-    if d_h != e.d_h or tuple(w_g.shape) != (e.E, d_h):
-        raise ValueError("x, w_g and the experts disagree on d_hidden or the number of experts")
+    e, dt, dev = experts, x.dtype, x.device
+    if d_h != e.d_h:
+        raise ValueError("x and the experts disagree on d_hidden")
+    _need(w_g, "w_g", dt, (e.E, d_h))
     if bias is not None:
-        _cuda(bias, "bias", dtype=torch.float32, ndim=1)
-        if bias.numel() != e.E:
-            raise ValueError("bias must be [E]")
-    if ws is None:
-        ws = torch.empty(forward_mx4_workspace_bytes(T, d_h, e.d_e, e.E, k, x.dtype), dtype=torch.uint8,
-                         device=x.device)
-    _cuda(ws, "ws", dtype=torch.uint8)
-    out = torch.empty_like(x) if out is None else _like(out, x, "out")
-    if err is not None:
-        _cuda(err, "err", dtype=torch.int32)
-    with torch.cuda.device(x.device):
-        _check(lib().moe_forward_mx4(_ptr(x), _ptr(w_g), _ptr(bias), _ptr(e.q_gate), _ptr(e.sf_gate), _ptr(e.q_up),
-                                     _ptr(e.sf_up), _ptr(e.q_down), _ptr(e.sf_down), T, d_h, e.d_e, e.E, k,
-                                     _dtype_code(x, "x"), _ptr(ws), ws.numel(), _ptr(out), _ptr(err),
-                                     _stream(x.device)), "moe_forward_mx4")
+        _need(bias, "bias", torch.float32, (e.E,))
+    code = _dtype_code(x, "x")
+    ws, nws = _ws(ws, dev, "moe_forward_mx4", T, d_h, e.d_e, e.E, k, code)
+    out = _want(out, "out", dt, x.shape, dev)
+    _call("moe_forward_mx4", dev, _at(x), _at(w_g), _at(bias), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
+          _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err))
     return out
 
 
