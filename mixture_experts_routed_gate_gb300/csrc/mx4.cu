@@ -25,6 +25,17 @@ template <> struct Unit<float> {
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(b[i]);
     }
+    // the bits of the largest magnitude: they order like the values, with
+    // infinities and then NaNs at the top
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t b[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+        uint32_t t = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t = max(t, b[i] & 0x7fffffffu);
+        return t;
+    }
+    static __device__ __forceinline__ float top_value(uint32_t t) { return __uint_as_float(t); }
+    __device__ __forceinline__ void clear() { w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u); }
 };
 template <int DT> struct HalfUnit {
     uint4 w;
@@ -38,31 +49,31 @@ template <int DT> struct HalfUnit {
             v[2 * i + 1] = f.y;
         }
     }
+    __device__ __forceinline__ uint32_t top() const {
+        const uint32_t a = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), b = __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
+        const uint32_t c = __vmaxu2(a, b);
+        return max(c >> 16, c & 0xffffu);
+    }
+    static __device__ __forceinline__ float top_value(uint32_t t) { return unpack2<DT>(t).x; }
+    __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
 };
 template <> struct Unit<__half> : HalfUnit<kF16> {};
 template <> struct Unit<__nv_bfloat16> : HalfUnit<kBF16> {};
 
 // Four lanes quantise 32 values, 8 each (every lane of the warp takes part):
 // returns the lane's 4 bytes of elements and, through s, the scale byte.
-__device__ __forceinline__ uint32_t quad_quantize(const float (&v)[8], uint32_t &s) {
-    // fmaxf drops a NaN, so a block that holds one is told by a flag
-    float top = 0.0f;
-    bool odd = false;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        top = fmaxf(top, fabsf(v[i]));
-        odd |= v[i] != v[i];
-    }
-    if (odd) top = INFINITY;
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    s = mx4_scale(top);
-    if (s == 255u) return 0u;
-    const float inv = mx4_inverse(s);
+template <typename T> __device__ __forceinline__ uint32_t quad_quantize(const Unit<T> &raw, uint32_t &s) {
+    uint32_t top = raw.top();
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    s = mx4_scale(Unit<T>::top_value(top));
+    const float inv = s == 255u ? 0.0f : mx4_inverse(s);
+    float v[8];
+    raw.values(v);
     uint32_t q = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) q |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
-    return q;
+    return s == 255u ? 0u : q;
 }
 
 // A CTA holds rows_per_cta rows at a time, `width` threads (a power of two,
@@ -89,16 +100,18 @@ __global__ void __launch_bounds__(MX_THREADS)
         for (int u = u0; u - u0 < units; u += width * MX_STEPS) {  // every lane the same number of steps
             Unit<T> raw[MX_STEPS];
 #pragma unroll
-            for (int i = 0; i < MX_STEPS; ++i)
-                if (in && u + i * width < units) raw[i].load(row + static_cast<int64_t>(u + i * width) * MX_UNIT);
+            for (int i = 0; i < MX_STEPS; ++i) {
+                if (in && u + i * width < units)
+                    raw[i].load(row + static_cast<int64_t>(u + i * width) * MX_UNIT);
+                else
+                    raw[i].clear();
+            }
 #pragma unroll
             for (int i = 0; i < MX_STEPS; ++i) {
                 const int at = u + i * width;
                 if (at - u0 >= units) break;  // the same for the whole CTA
-                float v[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
-                if (in && at < units) raw[i].values(v);
                 uint32_t s;
-                const uint32_t w = quad_quantize(v, s);
+                const uint32_t w = quad_quantize(raw[i], s);
                 if (here && at < units) {
                     qr[at] = w;
                     if ((at & 3) == 0) sr[at >> 2] = static_cast<uint8_t>(s);

@@ -158,29 +158,64 @@ template <int V> __device__ __forceinline__ uint2 load_scales(const uint8_t *row
     return v;
 }
 
-template <typename TOut, int CNT>
-__device__ __forceinline__ void store_row(TOut *dst, const uint32_t (&r)[CNT], int64_t left, bool wide) {
-    // `wide`: the row's start is 16-byte aligned
-    if (wide && left >= CNT) {
-        if constexpr (sizeof(TOut) == 4) {
+// 32 values of one row, whose place is 16-byte aligned
+template <typename TOut> __device__ __forceinline__ void store_row(TOut *dst, const uint32_t (&r)[32]) {
+    if constexpr (sizeof(TOut) == 4) {
 #pragma unroll
-            for (int i = 0; i < CNT / 4; ++i)
-                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-        } else {
-            constexpr int DT = std::is_same<TOut, __half>::value ? kF16 : kBF16;
+        for (int i = 0; i < 8; ++i)
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+    } else {
+        constexpr int DT = std::is_same<TOut, __half>::value ? kF16 : kBF16;
 #pragma unroll
-            for (int i = 0; i < CNT / 8; ++i) {
-                uint32_t w[4];
+        for (int i = 0; i < 4; ++i) {
+            uint32_t w[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = pack2<DT>(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]));
-                reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int j = 0; j < 4; ++j)
+                w[j] = pack2<DT>(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]));
+            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+}
+
+// A warp's `rows` rows (one a lane) by `cols` of 32 columns, where rows are
+// not 16-byte aligned or the columns end.  More than a few rows: 8 x 8 blocks
+// transposed among the lanes, so that a store writes 8 columns of 4 rows; with
+// one element of 32 rows a store, a 28 MB result of odd width took 166 us.
+template <typename TOut>
+__device__ __forceinline__ void store_block(TOut *dst, int64_t ld, const uint32_t (&r)[32], int rows, int cols, int lane) {
+    if (rows <= 8) {
+        if (lane < rows) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (i < cols) dst[lane * ld + i] = from_f32<TOut>(__uint_as_float(r[i]));
+        }
+        return;
+    }
+#pragma unroll
+    for (int c = 0; c < 32; c += 8) {
+        if (c >= cols) return;
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = r[c + i];
+#pragma unroll
+        for (int s = 4; s >= 1; s >>= 1) {
+            const bool high = lane & s;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                if (j & s) continue;
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, high ? w[j] : w[j | s], s);
+                if (high)
+                    w[j] = got;
+                else
+                    w[j | s] = got;
             }
         }
-    } else {
+        const int col = c + (lane & 7);
 #pragma unroll
-        for (int i = 0; i < CNT; ++i)
-            if (i < left) dst[i] = from_f32<TOut>(__uint_as_float(r[i]));
+        for (int i = 0; i < 8; ++i) {
+            const int row = (lane & 24) + i;
+            if (row < rows && col < cols) dst[row * ld + col] = from_f32<TOut>(__uint_as_float(w[i]));
+        }
     }
 }
 
@@ -512,9 +547,13 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                         }
                     } else {
                         tmem_ld_wait();
-                        if (valid) {
-                            constexpr int per16 = 16 / sizeof(TOut);
-                            store_row(static_cast<TOut *>(p.out) + r * p.N + n, v, p.N - n, p.N % per16 == 0);
+                        TOut *out = static_cast<TOut *>(p.out);
+                        if (p.N % (16 / static_cast<int>(sizeof(TOut))) == 0 && p.N - n >= 32) {
+                            if (valid) store_row(out + r * p.N + n, v);
+                        } else {
+                            const int64_t left = p.N - n;
+                            store_block(out + (static_cast<int64_t>(ti.m_start) + q * 32) * p.N + n, p.N, v, ti.rows - q * 32,
+                                        left < 32 ? static_cast<int>(left) : 32, lane);
                         }
                     }
                 }
