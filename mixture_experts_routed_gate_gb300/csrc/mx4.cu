@@ -9,9 +9,10 @@
 namespace moe {
 namespace {
 
-constexpr int MX_THREADS = 256;
+constexpr int MX_THREADS = 128;
 constexpr int MX_UNIT = 8;    // elements per thread and step: four lanes hold a block
-constexpr int MX_STEPS = 4;   // loads in flight per thread
+constexpr int MX_STEPS = 8;   // loads in flight per thread: a row of up to 8192 elements in one go
+constexpr int MX_BACK_STEPS = 4;
 
 template <typename T> struct Unit;  // 8 elements as loaded
 template <> struct Unit<float> {
@@ -127,10 +128,10 @@ __global__ void __launch_bounds__(MX_THREADS)
     dequantize_kernel(const uint32_t *__restrict__ q, const uint8_t *__restrict__ sf, int64_t words, T *__restrict__ out) {
     griddep_wait();
     griddep_launch_dependents();
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * (MX_THREADS * MX_STEPS) + threadIdx.x;
-    uint32_t w[MX_STEPS], s[MX_STEPS];
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * (MX_THREADS * MX_BACK_STEPS) + threadIdx.x;
+    uint32_t w[MX_BACK_STEPS], s[MX_BACK_STEPS];
 #pragma unroll
-    for (int i = 0; i < MX_STEPS; ++i) {
+    for (int i = 0; i < MX_BACK_STEPS; ++i) {
         const int64_t at = first + i * MX_THREADS;
         if (at < words) {
             w[i] = __ldg(q + at);
@@ -138,7 +139,7 @@ __global__ void __launch_bounds__(MX_THREADS)
         }
     }
 #pragma unroll
-    for (int i = 0; i < MX_STEPS; ++i) {
+    for (int i = 0; i < MX_BACK_STEPS; ++i) {
         const int64_t at = first + i * MX_THREADS;
         if (at >= words) return;
         const float f = mx4_factor(s[i]);
@@ -167,14 +168,14 @@ cudaError_t launch_quantize_typed(const void *x, const int32_t *row_idx, int64_t
     int width = 4;
     while (width < units && width < MX_THREADS) width *= 2;
     const int64_t groups = (n_rows + MX_THREADS / width - 1) / (MX_THREADS / width);
-    const int64_t most = static_cast<int64_t>(device_sm_count()) * 8;
+    const int64_t most = static_cast<int64_t>(device_sm_count()) * 512;
     return launch_pdl(quantize_kernel<T>, dim3(static_cast<unsigned>(groups < most ? groups : most)), dim3(MX_THREADS),
                       0, stream, static_cast<const T *>(x), row_idx, n_rows, T_rows, units, width, q, sf, err);
 }
 
 template <typename T>
 cudaError_t launch_dequantize_typed(const uint8_t *q, const uint8_t *sf, int64_t words, void *out, cudaStream_t stream) {
-    constexpr int64_t per_cta = MX_THREADS * MX_STEPS;
+    constexpr int64_t per_cta = MX_THREADS * MX_BACK_STEPS;
     return launch_pdl(dequantize_kernel<T>, dim3(static_cast<unsigned>((words + per_cta - 1) / per_cta)),
                       dim3(MX_THREADS), 0, stream, reinterpret_cast<const uint32_t *>(q), sf, words,
                       static_cast<T *>(out));
