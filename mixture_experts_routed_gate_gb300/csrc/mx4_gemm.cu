@@ -31,7 +31,7 @@ constexpr int MG_EPI_WARP0 = 2, MG_EPI_WARPS = 8, MG_SF_WARP0 = 10, MG_SF_GROUPS
 constexpr int MG_AHEAD = 4;         // slices of scales in registers ahead of the ring
 constexpr int MG_LIST = 512;        // M blocks with rows that the shared-memory list holds
 constexpr int MG_BN = 192;         // columns of a tile
-constexpr int MG_FEW_ROWS = 32;     // a block of at most so many rows loads a short box
+constexpr int MG_BOX_ROWS = 32;     // rows of a copy: a block loads as many as hold its rows
 
 template <int BN> struct MgLayout {
     static constexpr int B_BYTES = BN * 128;
@@ -221,9 +221,8 @@ __device__ __forceinline__ void store_block(TOut *dst, int64_t ld, const uint32_
 
 template <typename TOut, bool GATE_UP, int BN, int V>
 __global__ void __launch_bounds__(MG_THREADS, 1)
-    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmA_few,
-                    const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
-                    const MgParams p) {
+    mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB0,
+                    const __grid_constant__ CUtensorMap tmB1, const MgParams p) {
     using L = MgLayout<BN>;
     constexpr int OUT_N = GATE_UP ? BN / 2 : BN;  // output columns of a tile
     extern __shared__ uint8_t mg_smem_raw[];
@@ -315,17 +314,18 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             for (int64_t t = blockIdx.x; t < total && ok; t += gridDim.x) {
                 const MgTile ti = tile_at(t);
                 if (ti.rows == 0) continue;
-                const bool few = ti.rows <= MG_FEW_ROWS;
-                // one row block: its weights are read once
-                const uint64_t pol_b = few ? pass : keep;
+                const int boxes = (ti.rows + MG_BOX_ROWS - 1) / MG_BOX_ROWS;
+                // a short block is most often its expert's only one: its weights are read once
+                const uint64_t pol_b = boxes == 1 ? pass : keep;
                 for (int s = 0; s < p.slices; ++s) {
                     if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
                     const uint32_t a = smem_u32(smem + stage * L::STAGE), b = a + MG_A_BYTES, fb = full_bar(stage);
-                    mbar_arrive_expect_tx(fb, (few ? MG_FEW_ROWS * 128 : MG_A_BYTES) + L::B_BYTES);
-                    tma_load_2d_hint(a, few ? &tmA_few : &tmA, fb, s * 128, ti.m_start, keep);
+                    mbar_arrive_expect_tx(fb, boxes * MG_BOX_ROWS * 128 + L::B_BYTES);
+                    for (int i = 0; i < boxes; ++i)
+                        tma_load_2d_hint(a + i * MG_BOX_ROWS * 128, &tmA, fb, s * 128, ti.m_start + i * MG_BOX_ROWS, keep);
                     if (GATE_UP) {
                         tma_load_3d_hint(b, &tmB0, fb, s * 128, ti.n0, ti.g, pol_b);
                         tma_load_3d_hint(b + L::B_BYTES / 2, &tmB1, fb, s * 128, ti.n0, ti.g, pol_b);
@@ -602,7 +602,7 @@ cudaError_t launch_v(const CUtensorMap *maps, const MgParams &p, cudaStream_t st
     const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_tiles;
     const int64_t grid = tiles < device_sm_count() ? tiles : device_sm_count();
     return launch_pdl(kern, dim3(static_cast<unsigned>(grid)), dim3(MG_THREADS), L::SMEM, stream, maps[0], maps[1],
-                      maps[2], maps[3], p);
+                      maps[2], p);
 }
 
 // the widest scale loads that K and the bases' alignment allow
@@ -636,11 +636,10 @@ cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, con
                                     const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
                                     int64_t E, int out_dtype, void *C, int32_t *err, cudaStream_t stream) {
     constexpr int BN = MG_BN;
-    CUtensorMap maps[4];
-    if (!rows_map(&maps[0], q_a, K, n_rows, MG_BM) || !rows_map(&maps[1], q_a, K, n_rows, MG_FEW_ROWS) ||
-        !weights_map(&maps[2], q_b, K, N, E, BN))
+    CUtensorMap maps[3];
+    if (!rows_map(&maps[0], q_a, K, n_rows, MG_BOX_ROWS) || !weights_map(&maps[1], q_b, K, N, E, BN))
         return cudaErrorInvalidValue;
-    maps[3] = maps[2];
+    maps[2] = maps[1];
     MgParams p = params(sf_a, tab, m_blocks, n_rows, N, K, BN, err);
     p.sf_b0 = sf_b;
     p.sf_b1 = sf_b;
@@ -656,9 +655,9 @@ cudaError_t launch_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *s
                                             int64_t d_e, int64_t E, uint8_t *q_h, uint8_t *sf_h, int32_t *err,
                                             cudaStream_t stream) {
     constexpr int BN = MG_BN;
-    CUtensorMap maps[4];
-    if (!rows_map(&maps[0], q_a, d_h, n_rows, MG_BM) || !rows_map(&maps[1], q_a, d_h, n_rows, MG_FEW_ROWS) ||
-        !weights_map(&maps[2], q_gate, d_h, d_e, E, BN / 2) || !weights_map(&maps[3], q_up, d_h, d_e, E, BN / 2))
+    CUtensorMap maps[3];
+    if (!rows_map(&maps[0], q_a, d_h, n_rows, MG_BOX_ROWS) || !weights_map(&maps[1], q_gate, d_h, d_e, E, BN / 2) ||
+        !weights_map(&maps[2], q_up, d_h, d_e, E, BN / 2))
         return cudaErrorInvalidValue;
     MgParams p = params(sf_a, tab, m_blocks, n_rows, d_e, d_h, BN / 2, err);
     p.sf_b0 = sf_gate;
