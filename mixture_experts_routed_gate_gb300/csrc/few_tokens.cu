@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     const int rows = __popc(sm.act_mask[a]);
                     const int r = sm.act_base[a] + (lane < rows ? lane : lane - rows);
                     if (a > ready) {  // h of this expert: every stage-1 warp has stored it
-                        ready = experts_ready(p.counters + 1, a, n_act, tiles_e * 2 * NT, lane, abort_flag, p.err);
+                        ready = experts_ready(p.counters + 1, a, n_act, tiles_e * 2, lane, abort_flag, p.err);
                         ok = ready >= a;
                     }
                     const void *h = lane < rows ? p.h_hi : p.h_lo;
@@ -513,47 +513,63 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             const int buf = local % FEW_PARTS;
             if (!wait(pf_bar(buf), static_cast<uint32_t>(local / FEW_PARTS) & 1u)) break;
             const float *f = reinterpret_cast<const float *>(sm.partial + buf * FEW_CONSUMERS * NT * 32);
+            // the sums are free for the next tile as soon as they are read:
+            // making h visible takes 1 to 2 us, and two pairs of warps take
+            // the stage-1 tiles in turn for the same reason
+            auto release = [&]() {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(pe_bar(buf));
+            };
             if (tile < n1) {
-                const int a = tile / tiles_e;
-                // 2 NT warps have values; at NT = 1 two pairs of warps take the
-                // tiles in turn, since making h visible costs 1 to 2 us
-                if (NT == 2 || (fin >> 1) == (local & 1)) {
-                    const int i = (NT == 2 ? fin : fin & 1) * 32 + lane, n = i >> 6, feat = i & 7, t8 = (i >> 3) & 7, t = n * 8 + t8;
-                    const uint32_t m = sm.act_mask[a];
-                    if ((m >> t) & 1u) {
-                        float gate = 0.0f, up = 0.0f;
-                        const int at = (n * 32 + feat * 4 + (t8 >> 1)) * 4 + (t8 & 1);
-#pragma unroll
-                        for (int w = 0; w < FEW_CONSUMERS; ++w) {
-                            gate += f[w * NT * 128 + at];
-                            up += f[w * NT * 128 + at + 2];
-                        }
-                        const int r = sm.act_base[a] + __popc(m & ((1u << t) - 1u));
-                        const float h = gate / (1.0f + __expf(-gate)) * up * sm.pair_w[r];
-                        const El top = from_f32<El>(h);
-                        const int64_t o = static_cast<int64_t>(r) * p.d_e + (tile - a * tiles_e) * 8 + feat;
-                        static_cast<El *>(p.h_hi)[o] = top;
-                        static_cast<El *>(p.h_lo)[o] = from_f32<El>(h - to_f32(top));
-                    }
-                    asm volatile("fence.proxy.async.global;" ::: "memory");
-                    __syncwarp();  // the publishing add releases the whole warp's stores
-                    if (lane == 0) counter_publish(p.counters + 1 + a);
+                if ((fin >> 1) != (local & 1)) {
+                    release();
+                    continue;
                 }
-            } else {
+                const int a = tile / tiles_e, i = (fin & 1) * 32 + lane, feat = i & 7, t8 = i >> 3;
+                float gate[NT], up[NT];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const int i = fin * 32 + lane, r = i & 15, t8 = i >> 4, t = n * 8 + t8;
-                    if (t < p.T) {
-                        float v = 0.0f;
-                        const int at = (n * 32 + (r & 7) * 4 + (t8 >> 1)) * 4 + (t8 & 1) + (r >> 3) * 2;
+                    const int at = (n * 32 + feat * 4 + (t8 >> 1)) * 4 + (t8 & 1);
+                    gate[n] = up[n] = 0.0f;
 #pragma unroll
-                        for (int w = 0; w < FEW_CONSUMERS; ++w) v += f[w * NT * 128 + at];
-                        static_cast<El *>(p.out)[static_cast<int64_t>(t) * p.d_h + (tile - n1) * 16 + r] = from_f32<El>(v);
+                    for (int w = 0; w < FEW_CONSUMERS; ++w) {
+                        gate[n] += f[w * NT * 128 + at];
+                        up[n] += f[w * NT * 128 + at + 2];
                     }
                 }
+                release();
+                const uint32_t m = sm.act_mask[a];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int t = n * 8 + t8;
+                    if (!((m >> t) & 1u)) continue;
+                    const int r = sm.act_base[a] + __popc(m & ((1u << t) - 1u));
+                    const float h = gate[n] / (1.0f + __expf(-gate[n])) * up[n] * sm.pair_w[r];
+                    const El top = from_f32<El>(h);
+                    const int64_t o = static_cast<int64_t>(r) * p.d_e + (tile - a * tiles_e) * 8 + feat;
+                    static_cast<El *>(p.h_hi)[o] = top;
+                    static_cast<El *>(p.h_lo)[o] = from_f32<El>(h - to_f32(top));
+                }
+                asm volatile("fence.proxy.async.global;" ::: "memory");
+                __syncwarp();  // the publishing add releases the whole warp's stores
+                if (lane == 0) counter_publish(p.counters + 1 + a);
+            } else {
+                const int i = fin * 32 + lane, r = i & 15, t8 = i >> 4;
+                float v[NT];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int at = (n * 32 + (r & 7) * 4 + (t8 >> 1)) * 4 + (t8 & 1) + (r >> 3) * 2;
+                    v[n] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < FEW_CONSUMERS; ++w) v[n] += f[w * NT * 128 + at];
+                }
+                release();
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const int t = n * 8 + t8;
+                    if (t < p.T) static_cast<El *>(p.out)[static_cast<int64_t>(t) * p.d_h + (tile - n1) * 16 + r] = from_f32<El>(v[n]);
+                }
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pe_bar(buf));
         }
         return;
     }
