@@ -5,4 +5,4 @@ sm_103a CUDA kernels).  :mod:`.binding` is its thin Python binding; importing
 it loads the library and fails loudly when it has not been built.
 """
 
-__all__ = ["binding", "workloads", "roofline"]
+__all__ = ["binding", "block", "workloads", "roofline"]
