@@ -525,7 +525,8 @@ MOE_API moe_status_t moe_residual_norm_backward(const void *d_out, const void *d
  * tokens; h = silu(G) * U, scaled by its routing weight, is kept as two values
  * of `dtype` (the rounded value and the rest), the outputs are summed over the
  * experts in fp32 and rounded once, so the result is closer to exact than
- * moe_forward's, which rounds h and each expert's output.
+ * moe_forward's, which rounds h and each expert's output.  The order of every
+ * sum is fixed: the same inputs give the same bits.
  * Arguments as moe_forward; d_h % 256 == 0, d_e % 64 == 0, k <= min(E, 32),
  * E <= 1024.  ws: moe_forward_few_workspace_bytes(...) bytes, 256-byte aligned,
  * needs no clearing.

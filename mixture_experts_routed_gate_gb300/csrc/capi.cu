@@ -783,9 +783,9 @@ moe_status_t moe_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_r
                                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
-static moe_status_t check_mx4_gemm(std::initializer_list<const void *> need, int64_t N, int64_t K) {
+static moe_status_t check_mx4_gemm(std::initializer_list<const void *> need, int64_t N, int64_t K, int64_t E) {
     if (N < 1 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
-    if (N > (1 << 20) || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (N > (1 << 20) || K > (1 << 20) || E > (1 << 20)) return MOE_ERR_UNSUPPORTED;
     for (const void *p : need)
         if (!p) return MOE_ERR_INVALID_ARG;
     return MOE_OK;
@@ -800,7 +800,7 @@ moe_status_t moe_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const
     if (n_rows == 0) return MOE_OK;
     moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
                                         n_rows, E);
-    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_b, sf_b, C}, N, K);
+    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_b, sf_b, C}, N, K, E);
     if (st != MOE_OK) return st;
     if (!all_aligned16({q_a, q_b, C})) return MOE_ERR_INVALID_ARG;
     const moe::Mx4Tables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
@@ -817,7 +817,7 @@ moe_status_t moe_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_
     if (n_rows == 0) return MOE_OK;
     moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
                                         n_rows, E);
-    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h);
+    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h, E);
     if (st != MOE_OK) return st;
     if (d_e % 32 != 0 || !all_aligned16({q_a, q_gate, q_up, q_h})) return MOE_ERR_INVALID_ARG;
     const moe::Mx4Tables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};

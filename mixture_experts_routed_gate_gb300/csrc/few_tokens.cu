@@ -176,9 +176,10 @@ __device__ __forceinline__ int experts_ready(const int *counters, int a, int n_a
         const bool yes = a + lane < n_act && counter_load_acquire(counters + a + lane) >= target;
         const uint32_t done = __ballot_sync(0xffffffffu, yes);
         if (done & 1u) {
-            // the copies of h that follow read through the async proxy
-            asm volatile("fence.proxy.async.global;" ::: "memory");
+            // every lane's copies of h come after every lane's look at the
+            // counters, and read through the async proxy
             __syncwarp();
+            asm volatile("fence.proxy.async.global;" ::: "memory");
             return a + __ffs(~done) - 2 + (done == 0xffffffffu ? 33 : 0);
         }
         const bool late = *abort_flag || global_timer_ns() - start > kWaitTimeoutNs;
@@ -389,6 +390,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     const int tiles_e = p.d_e / 8;           // stage-1 tiles of an expert
     const int n1 = n_act * tiles_e, total = n1 + p.d_h / 16;
     const int steps1 = (p.d_h + FEW_COLS - 1) / FEW_COLS, steps2 = (p.d_e + FEW_COLS - 1) / FEW_COLS;
+    // A tile takes an even number of stages, so that its steps go to the groups
+    // in the same way in whatever order the tiles are taken: the order of the
+    // sums, and with it the result's bits, does not depend on it.
+    static_assert(FEW_GROUPS == 2, "padding to an even count");
+    auto pad_steps = [&](int tile) { return (tile < n1 ? steps1 : n_act * steps2) & 1; };
 
     if (warp == FEW_CONSUMERS) {
         // -------------------- weights: one thread, no broadcasts --------------------
@@ -415,6 +421,16 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             }
             return true;
         };
+        // the step that makes a tile's count even (see pad_steps)
+        auto pad = [&]() {
+            if (!mbar_wait_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) return false;
+            mbar_arrive(full_bar(stage));
+            if (++stage == stages) {
+                stage = 0;
+                phase ^= 1u;
+            }
+            return true;
+        };
         int next = atomicAdd(p.counters, 1);
         while (ok) {
             ok = mbar_wait_bounded(tqe_bar(slot), qphase ^ 1u, abort_flag, p.err);
@@ -437,6 +453,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     ok = copy(&tm_down, &tm_down, row, row + 8, steps2);
                 }
             }
+            for (int i = pad_steps(tile); i > 0 && ok; --i) ok = pad();
         }
         if (*abort_flag) few_drain(bar0, stages, stage, phase);
         return;
@@ -474,7 +491,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             for (int c = 0; c < steps; ++c) {
                 if (!wait(empty_bar(stage), phase ^ 1u)) return false;
                 const uint32_t bytes = static_cast<uint32_t>(min(FEW_COLS, K - c * FEW_COLS)) * 2u, bar = full_bar(stage);
-                if (lane == 0) mbar_arrive_expect_tx(bar, n * bytes);
+                if (lane == 0) mbar_arrive_expect_tx(bar, n * bytes);  // no rows: a padding step
                 if (lane < n)
                     row_copy(ring + stage * stage_bytes + 2 * FEW_HALF + lane * FEW_ROW, src + c * FEW_COLS * 2, bytes, bar, policy);
                 if (++stage == stages) {
@@ -501,6 +518,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     ok = ok && copy(2 * rows, p.d_e, static_cast<const uint8_t *>(h) + static_cast<int64_t>(r) * p.d_e * 2, steps2);
                 }
             }
+            if (ok && pad_steps(tile)) ok = copy(0, 0, nullptr, 1);
         }
         if (*abort_flag && lane == 0) few_drain(bar0, stages, stage, phase);
         return;
@@ -648,6 +666,13 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty_bar(stage));
             }
+        }
+        if (ok && pad_steps(tile)) {
+            if (turn == 0) {
+                ok = wait(full_bar(stage), phase);
+                if (ok && lane == 0) mbar_arrive(empty_bar(stage));
+            }
+            advance();
         }
         if (!ok) break;
         const int buf = local % FEW_PARTS;

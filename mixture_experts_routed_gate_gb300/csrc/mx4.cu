@@ -71,9 +71,7 @@ template <typename T> __device__ __forceinline__ uint32_t quad_quantize(const Un
     const float inv = s == 255u ? 0.0f : mx4_inverse(s);
     float v[8];
     raw.values(v);
-    uint32_t q = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q |= e2m1x2(v[2 * i] * inv, v[2 * i + 1] * inv) << (8 * i);
+    const uint32_t q = e2m1x8(v, inv);
     return s == 255u ? 0u : q;
 }
 

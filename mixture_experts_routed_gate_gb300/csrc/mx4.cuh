@@ -24,10 +24,19 @@ __device__ __forceinline__ float mx4_factor(uint32_t byte) {
     return __uint_as_float(byte ? byte << 23 : 1u << 22);
 }
 
-// two elements to a byte, `lo` in the low nibble: nearest even, limited to 6
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi) {
+// eight elements to a word, first in the lowest nibble: each times `by`, to
+// nearest even, limited to 6
+__device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8], float by) {
     uint32_t r;
-    asm("{\n\t.reg .b8 b;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %2, %1;\n\tcvt.u32.u8 %0, b;\n\t}" : "=r"(r) : "f"(lo), "f"(hi));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0] * by), "f"(v[1] * by), "f"(v[2] * by), "f"(v[3] * by), "f"(v[4] * by), "f"(v[5] * by), "f"(v[6] * by),
+          "f"(v[7] * by));
     return r;
 }
 

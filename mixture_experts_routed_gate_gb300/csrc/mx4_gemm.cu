@@ -536,9 +536,12 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                         uint32_t w[4] = {0u, 0u, 0u, 0u};
                         if (!odd) {
 #pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                w[i >> 2] |= e2m1x2(__uint_as_float(v[2 * i]) * inv, __uint_as_float(v[2 * i + 1]) * inv)
-                                             << (8 * (i & 3));
+                            for (int j = 0; j < 4; ++j) {
+                                float eight[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) eight[i] = __uint_as_float(v[8 * j + i]);
+                                w[j] = e2m1x8(eight, inv);
+                            }
                         }
                         if (valid) {
                             const int64_t o = r * (p.N / 32) + n / 32;

@@ -155,24 +155,28 @@ template <typename T, int EPT> struct Part<T, EPT, false> {
 struct RowSums {
     float2 *scratch;  // [2][32]
     int turn = 0;
-    __device__ __forceinline__ float2 operator()(float a, float b) {
-#pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) {
-            a += __shfl_xor_sync(0xffffffffu, a, s);
-            b += __shfl_xor_sync(0xffffffffu, b, s);
-        }
+    __device__ __forceinline__ float2 *barrier(float a, float b) {
         float2 *buf = scratch + turn * 32;
         turn ^= 1;
-        const int warps = static_cast<int>(blockDim.x) >> 5, lane = threadIdx.x & 31;
-        if (lane == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
+        if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = make_float2(a, b);
         __syncthreads();
-        float2 v = lane < warps ? buf[lane] : make_float2(0.0f, 0.0f);
+        return buf;
+    }
+    static __device__ __forceinline__ float lanes(float v) {
 #pragma unroll
-        for (int s = 16; s >= 1; s >>= 1) {
-            v.x += __shfl_xor_sync(0xffffffffu, v.x, s);
-            v.y += __shfl_xor_sync(0xffffffffu, v.y, s);
-        }
+        for (int s = 16; s >= 1; s >>= 1) v += __shfl_xor_sync(0xffffffffu, v, s);
         return v;
+    }
+    __device__ __forceinline__ float one(float a) {
+        const float2 *buf = barrier(lanes(a), 0.0f);
+        const int lane = threadIdx.x & 31;
+        return lanes(lane < static_cast<int>(blockDim.x) >> 5 ? buf[lane].x : 0.0f);
+    }
+    __device__ __forceinline__ float2 two(float a, float b) {
+        const float2 *buf = barrier(lanes(a), lanes(b));
+        const int lane = threadIdx.x & 31;
+        const float2 v = lane < static_cast<int>(blockDim.x) >> 5 ? buf[lane] : make_float2(0.0f, 0.0f);
+        return make_float2(lanes(v.x), lanes(v.y));
     }
 };
 
@@ -283,30 +287,32 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
         P res, y, gate;
         res.load(ring.tensor(0), H);
         if (has_y) y.load(ring.tensor(1), H);
-        if (p.gate_kind == 3) gate.load(ring.tensor(2), H);
-        if (p.gate_kind == 1) gate.load(gate_row, H);
         bool read = false;  // every thread has read the stage
         float o[EPT];
         if (has_y) {
+            // what is absent counts as ones: no test per element
+            if (p.gate_kind == 3)
+                gate.load(ring.tensor(2), H);
+            else if (p.gate_kind == 1)
+                gate.load(gate_row, H);
+            else
+                gate.fill(1.0f);
+            P w;
             float r2 = 1.0f;
             if (post) {
                 float s = 0.0f;
 #pragma unroll
-                for (int i = 0; i < EPT; ++i) s += y.get(i) * y.get(i);
-                r2 = rsqrtf(sums(s, 0.0f).x * per + p.eps);
+                for (int i = 0; i < EPT; ++i) s = fmaf(y.get(i), y.get(i), s);
+                r2 = rsqrtf(sums.one(s) * per + p.eps);
                 if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
                 ring.refill();
                 read = true;
+                w.load(w_post, H);
+            } else {
+                w.fill(1.0f);
             }
-            P w;
-            if (post) w.load(w_post, H);
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) {
-                float z = y.get(i);
-                if (post) z = z * r2 * w.get(i);
-                if (p.gate_kind & 1) z *= gate.get(i);
-                o[i] = res.get(i) + scale * z;
-            }
+            for (int i = 0; i < EPT; ++i) o[i] = fmaf(scale, y.get(i) * r2 * w.get(i) * gate.get(i), res.get(i));
             P::store(static_cast<T *>(p.out) + base, H, o);
         } else {
 #pragma unroll
@@ -315,8 +321,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
         if (nxt) {
             float s = 0.0f;
 #pragma unroll
-            for (int i = 0; i < EPT; ++i) s += o[i] * o[i];
-            const float r = rsqrtf(sums(s, 0.0f).x * per + p.eps);
+            for (int i = 0; i < EPT; ++i) s = fmaf(o[i], o[i], s);
+            const float r = rsqrtf(sums.one(s) * per + p.eps);
             if (p.rstd_next && threadIdx.x == 0) p.rstd_next[t] = r;
             if (!read) ring.refill();
             read = true;
@@ -383,7 +389,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
             w.load(w_next, H);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) s = fmaf(d_u.times(w, i), out.get(i), s);
-            const float back = -(sums(s, 0.0f).x * (r * r * r * per));
+            const float back = -(sums.one(s) * (r * r * r * per));
             ring.refill();
             read = true;
             d_u.again();
@@ -431,7 +437,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
                 s = fmaf(d[i], y.get(i), s);
             }
             if (post || TOKEN) {
-                const float2 row = sums(s, sg);
+                const float2 row = TOKEN ? sums.two(s, sg) : make_float2(sums.one(s), 0.0f);
                 if (!read) ring.refill();
                 read = true;
                 if (TOKEN && p.d_gate && threadIdx.x == 0) static_cast<float *>(p.d_gate)[t] = row.y;

@@ -161,6 +161,28 @@ def test_writes_stay_inside(T, d_h, d_e, E, k):
         assert bool((r[:4096] == 0xA5).all()) and bool((r[4096 + m:] == 0xA5).all())
 
 
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,d_h,d_e,E,k", [(8, 512, 128, 16, 4), (16, 512, 128, 16, 4), (3, 768, 576, 9, 3), (11, 1280, 64, 7, 1)])
+def test_the_bits_do_not_depend_on_the_order_of_work(T, d_h, d_e, E, k, dtype, monkeypatch):
+    """Tiles are taken from a shared counter: one CTA, a few, or more than fit at
+    once, on workspaces that hold other bytes every time, give the same bits."""
+    require_cuda()
+    s = make(T, d_h, d_e, E, k, dtype, seed=14)
+    n = binding.forward_few_workspace_bytes(T, d_h, d_e, E, k, DT[dtype])
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    ref, err = call(s, k, ws=ws)
+    check(s, k, dtype, ref, err)
+    outs = []
+    for grid in (None, "1", "7", "304"):
+        if grid is not None:
+            monkeypatch.setenv("MOE_MLP_GRID", grid)
+        for i in range(50 if grid is None else 5):
+            ws.fill_(0x7F if i % 2 else 0xFF)
+            outs.append(call(s, k, ws=ws)[0])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, ref) for o in outs)
+
+
 def test_near_the_forward():
     """moe_forward on the same tokens, within its own tolerance."""
     require_cuda()
