@@ -56,6 +56,7 @@ struct MgParams {
     uint8_t *q_h, *sf_h;
     int32_t *err;
     int m_blocks, n_tiles, slices;
+    int wide;  // rows of out start 32-byte aligned
     int64_t n_rows, N, K;
 };
 
@@ -158,27 +159,33 @@ template <int V> __device__ __forceinline__ uint2 load_scales(const uint8_t *row
     return v;
 }
 
-// 32 values of one row, whose place is 16-byte aligned
+__device__ __forceinline__ void store_32_bytes(void *dst, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
+// 32 values of one row, whose place is 32-byte aligned: whole sectors a store
 template <typename TOut> __device__ __forceinline__ void store_row(TOut *dst, const uint32_t (&r)[32]) {
-    if constexpr (sizeof(TOut) == 4) {
+    constexpr int per = 32 / sizeof(TOut);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
-    } else {
-        constexpr int DT = std::is_same<TOut, __half>::value ? kF16 : kBF16;
+    for (int i = 0; i < 32 / per; ++i) {
+        uint32_t w[8];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = pack2<DT>(__uint_as_float(r[8 * i + 2 * j]), __uint_as_float(r[8 * i + 2 * j + 1]));
-            reinterpret_cast<uint4 *>(dst)[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(TOut) == 4) {
+                w[j] = r[8 * i + j];
+            } else {
+                constexpr int DT = std::is_same<TOut, __half>::value ? kF16 : kBF16;
+                w[j] = pack2<DT>(__uint_as_float(r[16 * i + 2 * j]), __uint_as_float(r[16 * i + 2 * j + 1]));
+            }
         }
+        store_32_bytes(dst + per * i, w);
     }
 }
 
 // A warp's `rows` rows (one a lane) by `cols` of 32 columns, where rows are
-// not 16-byte aligned or the columns end.  More than a few rows: 8 x 8 blocks
+// not 32-byte aligned or the columns end.  More than a few rows: 8 x 8 blocks
 // transposed among the lanes, so that a store writes 8 columns of 4 rows; with
 // one element of 32 rows a store, a 28 MB result of odd width took 166 us.
 template <typename TOut>
@@ -551,7 +558,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                     } else {
                         tmem_ld_wait();
                         TOut *out = static_cast<TOut *>(p.out);
-                        if (p.N % (16 / static_cast<int>(sizeof(TOut))) == 0 && p.N - n >= 32) {
+                        if (p.wide && p.N - n >= 32) {
                             if (valid) store_row(out + r * p.N + n, v);
                         } else {
                             const int64_t left = p.N - n;
@@ -647,6 +654,8 @@ cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, con
     p.sf_b0 = sf_b;
     p.sf_b1 = sf_b;
     p.out = C;
+    const int64_t row_bytes = N * (out_dtype == kF32 ? 4 : 2);
+    p.wide = row_bytes % 32 == 0 && reinterpret_cast<uintptr_t>(C) % 32 == 0;
     if (out_dtype == kF32) return launch_n<float, false, BN>(maps, p, stream);
     if (out_dtype == kBF16) return launch_n<__nv_bfloat16, false, BN>(maps, p, stream);
     return launch_n<__half, false, BN>(maps, p, stream);
