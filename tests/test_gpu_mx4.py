@@ -105,6 +105,31 @@ def test_quantize_gathers_rows():
     assert torch.equal(values64(q, sf), want) and int(err.item()) == 5
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("T,K,rows", [(700, 1024, 1400), (1300, 1056, 5000), (617, 9216, 1301)])
+def test_quantize_gathers_repeated_rows(T, K, rows, dtype):
+    """Many rows of few tokens: some tokens have no row, one has thousands, some
+    indexes are out of range."""
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    x = torch.randn((T, K), generator=g, device="cuda").to(DT[dtype])
+    idx = torch.randint(0, T, (rows,), generator=g, device="cuda", dtype=torch.int32)
+    idx[100:rows - 300] = torch.where(idx[100:rows - 300] % 3 == 0, torch.full_like(idx[100:rows - 300], 5), idx[100:rows - 300])
+    idx[3], idx[rows - 1], idx[77] = T, -7, 2 ** 31 - 1
+    raw_q = torch.full((4096 + rows * K // 2 + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    raw_s = torch.full((4096 + rows * K // 32 + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, sf = binding.moe_quantize_mx4(x, idx, q=raw_q[4096:-4096].view(rows, K // 2), sf=raw_s[4096:-4096].view(rows, K // 32), err=err)
+    good = (idx >= 0) & (idx < T)
+    want = quantize64(x)[0][idx.long().clamp(0, T - 1)]
+    want[~good] = 0
+    assert torch.equal(values64(q, sf), want) and int(err.item()) == 5
+    one_q, one_sf = binding.moe_quantize_mx4(x)  # the scale bytes too
+    assert torch.equal(q[good], one_q[idx[good].long()]) and torch.equal(sf[good], one_sf[idx[good].long()])
+    for r in (raw_q, raw_s):
+        assert bool((r[:4096] == 0xA5).all()) and bool((r[-4096:] == 0xA5).all())
+
+
 def tables_for(sizes):
     """Dispatch tables of groups of these sizes (top-1 routing)."""
     idx = torch.cat([torch.full((n,), e, dtype=torch.int32) for e, n in enumerate(sizes)]).cuda().view(-1, 1)
