@@ -12,13 +12,20 @@
 // products of these.
 //
 // Memory bound: every tensor is read once and written once.  A CTA holds one
-// row at a time in registers, 8 (wide rows: 16) elements a thread, and walks
-// the rows with the grid's stride; the rows to come arrive through a ring of
-// shared-memory stages by bulk copies, so loads go on under the row's two
-// reductions.  Rows whose bytes are no multiple of 16, and rows too wide for
-// two stages, are loaded by the threads themselves.  The backward pass keeps
-// the column sums of its rows in registers; a second kernel adds the CTAs'
-// sums in a fixed order.
+// row at a time, 8 (wide rows: 16) elements a thread, and walks the rows with
+// the grid's stride; the rows to come arrive through a ring of shared-memory
+// slots, one tensor's row each, by bulk copies, so loads go on under the row's
+// two reductions.  Rows that start on 16 bytes are read from there as 16-byte
+// vectors, others (an odd H) element by element.  The backward pass keeps the
+// column sums of its rows in registers; a second kernel adds the CTAs' sums in
+// a fixed order.
+//
+// 4096 x 7168 bf16: forward 39 us (235 MB at 6.0 TB/s, against 35 at this
+// card's copy rate; 70% of the issue slots), gradients 88 us (52 at the copy
+// rate: there the instructions bound, about 500 a warp and row).  fp32: 81 and
+// 138 us of 69 and 104 (147 and 315 with rows from memory, as two rows' slots do
+// not fit; so the slots are single tensors', a part of a row ahead if need be).  Rows of 7167 bf16, by elements: 72 and 161 us; from
+// memory instead of through the ring 154 and 465.
 #include "common.cuh"
 #include "internal.h"
 
@@ -26,8 +33,8 @@ namespace moe {
 namespace {
 
 constexpr int NORM_MAX_TENSORS = 5;
-constexpr int NORM_MAX_STAGES = 8;
-constexpr int NORM_RING_BYTES = 200 * 1024;  // of one SM, shared by its CTAs
+constexpr int NORM_MAX_SLOTS = 32, NORM_MAX_BARS = NORM_MAX_SLOTS + 2;
+constexpr int NORM_RING_BYTES = 224 * 1024;  // of one SM, shared by its CTAs
 
 struct NormParams {
     const void *y, *res, *w_post, *gate, *w_next;
@@ -40,54 +47,113 @@ struct NormParams {
     float alpha, eps;
     int64_t T;
     int H;
-    int stages, tensors;  // the ring: tensors a row (in the order of the kernel's reads)
+    int slots, tensors;  // the ring; tensors a row (in the order of the kernel's reads)
+    int bars;
+    uint32_t slot_bytes, ring_bytes;
     const void *ring[NORM_MAX_TENSORS];
 };
 
-// A thread's EPT elements of a row.  RING: 16-byte vectors, `threads` apart,
-// kept packed; otherwise single elements, `threads` apart, in fp32.
-template <typename T, int EPT, bool RING> struct Part;
+// How rows are read: through the ring, as 16-byte vectors or (rows that do not
+// all start on 16 bytes) by elements; or, too wide for the ring, from memory.
+enum class Rows { kVectors, kOdd, kMemory };
 
-template <typename T, int EPT> struct Part<T, EPT, true> {
-    static constexpr int EV = 16 / sizeof(T), V = EPT / EV;
+// A thread's EPT elements of a row, packed in registers.  VEC: 16-byte vectors,
+// `threads` apart, of a row that starts on 16 bytes; otherwise single
+// elements, `threads` apart.
+template <typename T, int EPT, bool VEC> struct Part {
     static constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
-    uint4 q[V];
-    static __device__ __forceinline__ int at(int v) { return (v * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * EV; }
+    static constexpr int PER = 4 / sizeof(T), WORDS = EPT / PER;  // elements of a word
+    static constexpr int RUN = VEC ? 16 / sizeof(T) : 1;          // consecutive elements
+    using Bits = typename std::conditional<sizeof(T) == 4, uint32_t, uint16_t>::type;
+    uint32_t w[WORDS];
+    // the row's index of the thread's element i
+    static __device__ __forceinline__ int at(int i) {
+        return (i / RUN * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x)) * RUN + i % RUN;
+    }
     __device__ __forceinline__ void load(const void *row, int H) {  // global or shared
+        if constexpr (VEC) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            q[v] = at(v) < H ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + at(v)) : make_uint4(0u, 0u, 0u, 0u);
+            for (int v = 0; v < WORDS / 4; ++v) {
+                const int i = at(v * RUN);
+                const uint4 q = i < H ? *reinterpret_cast<const uint4 *>(static_cast<const T *>(row) + i) : make_uint4(0u, 0u, 0u, 0u);
+                w[4 * v] = q.x;
+                w[4 * v + 1] = q.y;
+                w[4 * v + 2] = q.z;
+                w[4 * v + 3] = q.w;
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < WORDS; ++k) {
+                w[k] = 0u;
+#pragma unroll
+                for (int j = 0; j < PER; ++j) {
+                    const int i = at(k * PER + j);
+                    if (i < H) w[k] |= static_cast<uint32_t>(static_cast<const Bits *>(row)[i]) << (16 * j);
+                }
+            }
+        }
     }
     __device__ __forceinline__ void put(void *row, int H) const {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (at(v) < H) *reinterpret_cast<uint4 *>(static_cast<T *>(row) + at(v)) = q[v];
+            for (int v = 0; v < WORDS / 4; ++v)
+                if (at(v * RUN) < H)
+                    *reinterpret_cast<uint4 *>(static_cast<T *>(row) + at(v * RUN)) =
+                        make_uint4(w[4 * v], w[4 * v + 1], w[4 * v + 2], w[4 * v + 3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i)
+                if (at(i) < H) static_cast<Bits *>(row)[at(i)] = static_cast<Bits>(w[i / PER] >> (16 * (i % PER)));
+        }
     }
     __device__ __forceinline__ void fill(float v) {
-        uint32_t w;
+        uint32_t x;
         if constexpr (sizeof(T) == 4)
-            w = __float_as_uint(v);
+            x = __float_as_uint(v);
         else
-            w = pack2<DT>(v, v);
+            x = pack2<DT>(v, v);
 #pragma unroll
-        for (int i = 0; i < V; ++i) q[i] = make_uint4(w, w, w, w);
+        for (int k = 0; k < WORDS; ++k) w[k] = x;
+    }
+    // the thread's words of its own in shared memory, and back
+    __device__ __forceinline__ void keep(uint8_t *room) const {
+        constexpr int N = VEC ? 4 : 1;
+#pragma unroll
+        for (int k = 0; k < WORDS; k += N) {
+            uint8_t *at = room + (k * blockDim.x + threadIdx.x * N) * 4;
+            if constexpr (VEC)
+                *reinterpret_cast<uint4 *>(at) = make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+            else
+                *reinterpret_cast<uint32_t *>(at) = w[k];
+        }
+    }
+    __device__ __forceinline__ void again(const void *room) {
+        constexpr int N = VEC ? 4 : 1;
+#pragma unroll
+        for (int k = 0; k < WORDS; k += N) {
+            const uint8_t *at = static_cast<const uint8_t *>(room) + (k * blockDim.x + threadIdx.x * N) * 4;
+            if constexpr (VEC) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(at);
+                w[k] = q.x;
+                w[k + 1] = q.y;
+                w[k + 2] = q.z;
+                w[k + 3] = q.w;
+            } else {
+                w[k] = *reinterpret_cast<const uint32_t *>(at);
+            }
+        }
     }
     // The packed words as if read anew: otherwise the compiler keeps the
     // unpacked values across the reductions, twice the registers, and spills.
     __device__ __forceinline__ void again() {
 #pragma unroll
-        for (int v = 0; v < V; ++v) asm volatile("" : "+r"(q[v].x), "+r"(q[v].y), "+r"(q[v].z), "+r"(q[v].w));
-    }
-    __device__ __forceinline__ uint32_t word(int i) const {  // the one that holds element i
-        const uint4 &w = q[i / EV];
-        const int j = i % EV * static_cast<int>(sizeof(T)) / 4;
-        return j == 0 ? w.x : j == 1 ? w.y : j == 2 ? w.z : w.w;
+        for (int k = 0; k < WORDS; ++k) asm volatile("" : "+r"(w[k]));
     }
     __device__ __forceinline__ float get(int i) const {
         if constexpr (sizeof(T) == 4) {
-            return __uint_as_float(word(i));
+            return __uint_as_float(w[i]);
         } else {
-            const float2 f = unpack2<DT>(word(i));
+            const float2 f = unpack2<DT>(w[i / 2]);
             return i & 1 ? f.y : f.x;
         }
     }
@@ -96,58 +162,28 @@ template <typename T, int EPT> struct Part<T, EPT, true> {
         if constexpr (sizeof(T) == 4)
             return get(i) * o.get(i);
         else
-            return i & 1 ? fma_mixed<DT, true>(word(i), o.word(i), 0.0f) : fma_mixed<DT, false>(word(i), o.word(i), 0.0f);
+            return i & 1 ? fma_mixed<DT, true>(w[i / 2], o.w[i / 2], 0.0f) : fma_mixed<DT, false>(w[i / 2], o.w[i / 2], 0.0f);
     }
     static __device__ __forceinline__ void store(void *row, int H, const float (&f)[EPT]) {
+        Part out;
 #pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if (at(v) >= H) continue;
-            uint4 w;
-            if constexpr (sizeof(T) == 4) {
-                w = make_uint4(__float_as_uint(f[4 * v]), __float_as_uint(f[4 * v + 1]), __float_as_uint(f[4 * v + 2]),
-                               __float_as_uint(f[4 * v + 3]));
-            } else {
-                w = make_uint4(pack2<DT>(f[8 * v], f[8 * v + 1]), pack2<DT>(f[8 * v + 2], f[8 * v + 3]),
-                               pack2<DT>(f[8 * v + 4], f[8 * v + 5]), pack2<DT>(f[8 * v + 6], f[8 * v + 7]));
-            }
-            *reinterpret_cast<uint4 *>(static_cast<T *>(row) + at(v)) = w;
+        for (int k = 0; k < WORDS; ++k) {
+            if constexpr (sizeof(T) == 4)
+                out.w[k] = __float_as_uint(f[k]);
+            else
+                out.w[k] = pack2<DT>(f[2 * k], f[2 * k + 1]);
         }
+        out.put(row, H);
     }
     static __device__ __forceinline__ void store_sums(float *row, int H, const float (&f)[EPT]) {
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int j = 0; j < EV; j += 4)
-                if (at(v) < H)
-                    *reinterpret_cast<float4 *>(row + at(v) + j) =
-                        make_float4(f[v * EV + j], f[v * EV + j + 1], f[v * EV + j + 2], f[v * EV + j + 3]);
-    }
-};
-
-template <typename T, int EPT> struct Part<T, EPT, false> {
-    float f[EPT];
-    static __device__ __forceinline__ int at(int i) { return i * static_cast<int>(blockDim.x) + static_cast<int>(threadIdx.x); }
-    __device__ __forceinline__ void load(const void *row, int H) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) f[i] = at(i) < H ? to_f32(static_cast<const T *>(row)[at(i)]) : 0.0f;
-    }
-    __device__ __forceinline__ void put(void *, int) const {}
-    __device__ __forceinline__ void fill(float v) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i) f[i] = v;
-    }
-    __device__ __forceinline__ void again() {}
-    __device__ __forceinline__ float get(int i) const { return f[i]; }
-    __device__ __forceinline__ float times(const Part &o, int i) const { return f[i] * o.f[i]; }
-    static __device__ __forceinline__ void store(void *row, int H, const float (&v)[EPT]) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i)
-            if (at(i) < H) static_cast<T *>(row)[at(i)] = from_f32<T>(v[i]);
-    }
-    static __device__ __forceinline__ void store_sums(float *row, int H, const float (&v)[EPT]) {
-#pragma unroll
-        for (int i = 0; i < EPT; ++i)
-            if (at(i) < H) row[at(i)] = v[i];
+        for (int i = 0; i < EPT; i += VEC ? 4 : 1) {
+            if (at(i) >= H) continue;
+            if constexpr (VEC)
+                *reinterpret_cast<float4 *>(row + at(i)) = make_float4(f[i], f[i + 1], f[i + 2], f[i + 3]);
+            else
+                row[at(i)] = f[i];
+        }
     }
 };
 
@@ -181,93 +217,168 @@ struct RowSums {
 };
 
 // The rows of p.ring's tensors, this CTA's in order.  next() waits for the
-// next row's stage; refill() is called once every thread has read it.
-template <bool RING> struct RowRing;
+// next row; refill() is called once every thread has read it.
+// Thread 0's: the next copy is the row at this byte of the tensors, of this
+// tensor, into this shared-memory address and for this barrier.  In shared
+// memory, as registers are what the backward pass lacks.
+struct RowAsk {
+    int64_t from;
+    int tensor;
+    uint32_t slot, bar;
+};
+struct RowState {
+    uint64_t bars[NORM_MAX_BARS];
+    RowAsk ask;
+};
 
-template <> struct RowRing<true> {
+template <Rows MODE> struct RowRing;
+
+template <> struct RowRing<Rows::kMemory> {
+    const NormParams &p;
+    int64_t row, row_bytes;
+    __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *, RowState &, int elem)
+        : p(p), row(blockIdx.x), row_bytes(static_cast<int64_t>(p.H) * elem) {}
+    __device__ __forceinline__ void start() {}
+    __device__ __forceinline__ bool next() {
+        tensor = 0;
+        return true;
+    }
+    int tensor = 0;
+    __device__ __forceinline__ const void *take() { return static_cast<const uint8_t *>(p.ring[tensor++]) + row * row_bytes; }
+    __device__ __forceinline__ void refill() {}
+};
+
+// p.slots slots of one tensor's row each, filled in the order of the reads, a
+// row ahead as far as they go (not a whole number of rows), and a barrier for
+// each row in flight.  kOdd copies from the 16 bytes a row starts in to those
+// it ends in; what is left of the tensors after their last 16 bytes is copied
+// by the threads.
+template <Rows MODE> struct RowRing {
     const NormParams &p;
     uint8_t *smem;
-    uint32_t bars, row_bytes, stage_bytes;
-    int64_t row, ahead;  // the current row; the next one to ask for
-    int stage = -1;
+    uint32_t bars;
+    int64_t row_bytes, row;
+    RowAsk &next_ask;
+    uint32_t slot = 0;  // of the next tensor, in bytes
+    int bar = -1;       // the row's
     uint32_t phase = 0;
-    __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *smem, uint64_t *bar, int elem)
-        : p(p), smem(smem), bars(smem_u32(bar)), row_bytes(static_cast<uint32_t>(p.H * elem)),
-          stage_bytes(row_bytes * p.tensors), row(blockIdx.x), ahead(blockIdx.x) {
+    __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *smem, RowState &state, int elem)
+        : p(p), smem(smem), bars(smem_u32(state.bars)), row_bytes(static_cast<int64_t>(p.H) * elem), row(blockIdx.x),
+          next_ask(state.ask) {
         if (threadIdx.x == 0) {
-            for (int i = 0; i < p.stages; ++i) mbar_init(bars + 8u * i, 1);
+            next_ask = RowAsk{blockIdx.x * row_bytes, 0, smem_u32(smem), bars};
+            for (int i = 0; i < p.bars; ++i) mbar_init(bars + 8u * i, 1);
             fence_mbar_init();
         }
         __syncthreads();
     }
-    __device__ __forceinline__ void ask(int st) {  // thread 0
-        if (ahead >= p.T) return;
-        const uint32_t bar = bars + 8u * st, dst = smem_u32(smem) + st * stage_bytes;
-        mbar_arrive_expect_tx(bar, stage_bytes);
-        for (int i = 0; i < p.tensors; ++i)
-            asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                             dst + i * row_bytes),
-                         "l"(static_cast<const uint8_t *>(p.ring[i]) + ahead * row_bytes), "r"(row_bytes), "r"(bar)
-                         : "memory");
-        ahead += gridDim.x;
+    __device__ __forceinline__ void ask(int copies) {
+        const int64_t total = p.T * row_bytes;
+        RowAsk a = next_ask;
+        for (int i = 0; i < copies && a.from < total; ++i) {
+            int64_t from = a.from;
+            uint32_t bytes = static_cast<uint32_t>(row_bytes);
+            if constexpr (MODE == Rows::kOdd) {
+                int64_t to = (from + row_bytes + 15) & ~int64_t{15};
+                to = to < total ? to : total & ~int64_t{15};
+                from &= ~int64_t{15};
+                bytes = static_cast<uint32_t>(to - from);
+            }
+            if (a.tensor == 0) mbar_arrive_expect_tx(a.bar, bytes * p.tensors);
+            if (MODE != Rows::kOdd || bytes > 0)
+                asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(a.slot),
+                             "l"(static_cast<const uint8_t *>(p.ring[a.tensor]) + from), "r"(bytes), "r"(a.bar)
+                             : "memory");
+            a.slot += p.slot_bytes;
+            if (a.slot == smem_u32(smem) + p.ring_bytes) a.slot = smem_u32(smem);
+            if (++a.tensor == p.tensors) {
+                a.tensor = 0;
+                a.from += gridDim.x * row_bytes;
+                a.bar += 8;
+                if (a.bar == bars + 8u * p.bars) a.bar = bars;
+            }
+        }
+        next_ask = a;
     }
     __device__ __forceinline__ void start() {
-        if (threadIdx.x == 0)
-            for (int i = 0; i < p.stages; ++i) ask(i);
+        if (threadIdx.x == 0) ask(p.slots);
     }
-    // A copy of this CTA's own, asked for before: bounded, and without an
-    // error word to report to a row that never came would be left as it is.
-    __device__ __forceinline__ bool next() {
-        if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-        }
+    // This CTA's own copies, asked for before: bounded, and without an error
+    // word to report to a row that never came would be left as it is.
+    __device__ __forceinline__ bool wait() {
         for (int i = 0; i < 64; ++i)  // before the slow read of the timer
-            if (mbar_try_wait(bars + 8u * stage, phase)) return true;
-        const unsigned long long start = global_timer_ns();
-        while (!mbar_try_wait(bars + 8u * stage, phase))
-            if (global_timer_ns() - start > kWaitTimeoutNs) return false;
+            if (mbar_try_wait(bars + 8u * bar, phase & 1u)) return true;
+        const unsigned long long begin = global_timer_ns();
+        while (!mbar_try_wait(bars + 8u * bar, phase & 1u))
+            if (global_timer_ns() - begin > kWaitTimeoutNs) return false;
         return true;
     }
-    __device__ __forceinline__ const void *tensor(int i) const { return smem + stage * stage_bytes + i * row_bytes; }
-    __device__ __forceinline__ void refill() {
-        if (threadIdx.x == 0) ask(stage);
+    __device__ __forceinline__ bool next() {
+        if (++bar == p.bars) {
+            bar = 0;
+            phase ^= 1u;
+        }
+        if (!wait()) return false;
+        if constexpr (MODE == Rows::kOdd) {
+            const int64_t total = p.T * row_bytes;
+            if (row == p.T - 1 && total % 16 != 0) {
+                int64_t from = total / 16 * 16 - row * row_bytes;
+                from = from < 0 ? 0 : from;
+                const uint32_t first = slot;
+                for (int i = 0; i < p.tensors; ++i) {
+                    uint8_t *to = take();
+                    if (threadIdx.x < row_bytes - from)
+                        to[from + threadIdx.x] = static_cast<const uint8_t *>(p.ring[i])[row * row_bytes + from + threadIdx.x];
+                }
+                slot = first;
+                __syncthreads();
+            }
+        }
+        return true;
     }
-};
-
-template <> struct RowRing<false> {
-    const NormParams &p;
-    int64_t row, bytes;
-    bool first = true;
-    __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *, uint64_t *, int elem)
-        : p(p), row(blockIdx.x), bytes(static_cast<int64_t>(p.H) * elem) {}
-    __device__ __forceinline__ void start() {}
-    __device__ __forceinline__ bool next() { return true; }
-    __device__ __forceinline__ const void *tensor(int i) const { return static_cast<const uint8_t *>(p.ring[i]) + row * bytes; }
-    __device__ __forceinline__ void refill() {}
+    // the row's tensors in their order
+    __device__ __forceinline__ uint8_t *take() {
+        uint8_t *at = smem + slot;
+        slot += p.slot_bytes;
+        if (slot == p.ring_bytes) slot = 0;
+        return MODE == Rows::kOdd ? at + (row * row_bytes & 15) : at;
+    }
+    __device__ __forceinline__ void refill() {
+        if (threadIdx.x == 0) ask(p.tensors);
+    }
 };
 
 // The [H] tensors (weights, gate per channel): with the ring, a thread keeps
-// its elements in shared memory after the stages, else it reads them again for
+// its elements in shared memory after the slots, else it reads them again for
 // every row; either way they take no registers between their uses.
-template <typename P, bool RING>
-__device__ __forceinline__ const void *keep_row(const void *row, uint8_t *&room, int H, int elem) {
-    if (!RING || !row) return row;
-    P part;
-    part.load(row, H);
-    uint8_t *at = room;
-    room += H * elem;
-    part.put(at, H);
-    return at;
-}
+template <typename P, Rows MODE> struct Kept {
+    const void *at = nullptr;
+    __device__ __forceinline__ Kept(const void *row, uint8_t *&room, int H) {
+        if constexpr (MODE == Rows::kMemory) {
+            at = row;
+        } else if (row) {
+            P part;
+            part.load(row, H);
+            at = room;
+            part.keep(room);
+            room += P::WORDS * 4 * blockDim.x;
+        }
+    }
+    __device__ __forceinline__ void load(P &part, int H) const {
+        if constexpr (MODE == Rows::kMemory)
+            part.load(at, H);
+        else
+            part.again(at);
+    }
+};
 
-template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __grid_constant__ NormParams p) {
-    using P = Part<T, EPT, RING>;
+    using P = Part<T, EPT, MODE == Rows::kVectors>;
     extern __shared__ __align__(128) uint8_t norm_smem[];
     __shared__ float2 scratch[64];
-    __shared__ uint64_t bars[NORM_MAX_STAGES];
-    RowRing<RING> ring(p, norm_smem, bars, sizeof(T));
+    __shared__ RowState state;
+    RowRing<MODE> ring(p, norm_smem, state, sizeof(T));
     RowSums sums{scratch};
     griddep_wait();
     griddep_launch_dependents();
@@ -275,26 +386,26 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
     const int H = p.H;
     const bool has_y = p.y != nullptr, post = p.w_post != nullptr, nxt = p.w_next != nullptr;
     const float per = 1.0f / static_cast<float>(H);
-    uint8_t *room = norm_smem + static_cast<int64_t>(p.stages) * p.tensors * H * sizeof(T);
-    const void *w_post = keep_row<P, RING>(p.w_post, room, H, sizeof(T));
-    const void *w_next = keep_row<P, RING>(p.w_next, room, H, sizeof(T));
-    const void *gate_row = keep_row<P, RING>(p.gate_kind == 1 ? p.gate : nullptr, room, H, sizeof(T));
+    uint8_t *room = norm_smem + p.ring_bytes;
+    const Kept<P, MODE> w_post(p.w_post, room, H);
+    const Kept<P, MODE> w_next(p.w_next, room, H);
+    const Kept<P, MODE> gate_row(p.gate_kind == 1 ? p.gate : nullptr, room, H);
     for (; ring.row < p.T; ring.row += gridDim.x) {
         const int64_t t = ring.row, base = t * H;
         if (!ring.next()) return;
         float scale = p.alpha;
         if (p.gate_kind == 2) scale *= to_f32(static_cast<const T *>(p.gate)[t]);
         P res, y, gate;
-        res.load(ring.tensor(0), H);
-        if (has_y) y.load(ring.tensor(1), H);
-        bool read = false;  // every thread has read the stage
+        res.load(ring.take(), H);
+        if (has_y) y.load(ring.take(), H);
+        bool read = false;  // every thread has read the row's slots
         float o[EPT];
         if (has_y) {
             // what is absent counts as ones: no test per element
             if (p.gate_kind == 3)
-                gate.load(ring.tensor(2), H);
+                gate.load(ring.take(), H);
             else if (p.gate_kind == 1)
-                gate.load(gate_row, H);
+                gate_row.load(gate, H);
             else
                 gate.fill(1.0f);
             P w;
@@ -307,7 +418,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
                 if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
                 ring.refill();
                 read = true;
-                w.load(w_post, H);
+                w_post.load(w, H);
             } else {
                 w.fill(1.0f);
             }
@@ -327,31 +438,31 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
             if (!read) ring.refill();
             read = true;
             P w;
-            w.load(w_next, H);
+            w_next.load(w, H);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) o[i] = o[i] * r * w.get(i);
             P::store(static_cast<T *>(p.u) + base, H, o);
         }
         if (!read) {
-            if (RING) __syncthreads();
+            __syncthreads();
             ring.refill();
         }
     }
 }
 
-// The instructions of a row take as long as its bytes, so what a call has or
+// The instructions of a row take longer than its bytes, so what a call has or
 // lacks is no test per element: an absent weight is a row of ones, and the
 // gate's three forms (a row, of ones where there is none; one factor a token;
 // a factor an element) are three kernels.  4096 x 7168 bf16: 117 us with the
-// tests, 84 us without.
-template <typename T, int EPT, bool RING, int GATE, int MAX_THREADS, int MIN_CTAS>
+// tests, 88 us without.
+template <typename T, int EPT, Rows MODE, int GATE, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(const __grid_constant__ NormParams p) {
-    using P = Part<T, EPT, RING>;
+    using P = Part<T, EPT, MODE == Rows::kVectors>;
     constexpr bool TOKEN = GATE == 2, FULL = GATE == 3, ROW = !TOKEN && !FULL;
     extern __shared__ __align__(128) uint8_t norm_smem[];
     __shared__ float2 scratch[64];
-    __shared__ uint64_t bars[NORM_MAX_STAGES];
-    RowRing<RING> ring(p, norm_smem, bars, sizeof(T));
+    __shared__ RowState state;
+    RowRing<MODE> ring(p, norm_smem, state, sizeof(T));
     RowSums sums{scratch};
     griddep_wait();
     griddep_launch_dependents();
@@ -359,34 +470,33 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
     const int H = p.H;
     const bool has_y = p.y != nullptr, post = p.w_post != nullptr, nxt = p.w_next != nullptr;
     const float per = 1.0f / static_cast<float>(H);
-    uint8_t *room = norm_smem + static_cast<int64_t>(p.stages) * p.tensors * H * sizeof(T);
-    const void *w_post = keep_row<P, RING>(p.w_post, room, H, sizeof(T));
-    const void *w_next = keep_row<P, RING>(p.w_next, room, H, sizeof(T));
-    const void *gate_row = keep_row<P, RING>(p.gate_kind == 1 ? p.gate : nullptr, room, H, sizeof(T));
+    uint8_t *room = norm_smem + p.ring_bytes;
+    const Kept<P, MODE> w_post(p.w_post, room, H);
+    const Kept<P, MODE> w_next(p.w_next, room, H);
+    const Kept<P, MODE> gate_row(p.gate_kind == 1 ? p.gate : nullptr, room, H);
     float sum_next[EPT], sum_post[EPT], sum_gate[EPT];  // columns, over this CTA's rows
 #pragma unroll
     for (int i = 0; i < EPT; ++i) sum_next[i] = sum_post[i] = sum_gate[i] = 0.0f;
     for (; ring.row < p.T; ring.row += gridDim.x) {
         const int64_t t = ring.row, base = t * H;
         if (!ring.next()) return;
-        int at = 0;
-        bool read = false;  // every thread has read the stage
+        bool read = false;  // every thread has read the row's slots
         float d[EPT];
         P d_out, d_u, out, y, gate, w;
         if (p.d_out)
-            d_out.load(ring.tensor(at++), H);
+            d_out.load(ring.take(), H);
         else
             d_out.fill(0.0f);
         if (nxt) {
-            d_u.load(ring.tensor(at++), H);
-            out.load(ring.tensor(at++), H);
+            d_u.load(ring.take(), H);
+            out.load(ring.take(), H);
         }
-        if (has_y) y.load(ring.tensor(at++), H);
-        if (FULL) gate.load(ring.tensor(at), H);
+        if (has_y) y.load(ring.take(), H);
+        if (FULL) gate.load(ring.take(), H);
         if (nxt) {
             const float r = p.r_next[t];
             float s = 0.0f;
-            w.load(w_next, H);
+            w_next.load(w, H);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) s = fmaf(d_u.times(w, i), out.get(i), s);
             const float back = -(sums.one(s) * (r * r * r * per));
@@ -410,12 +520,12 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
             const float factor = TOKEN ? p.alpha * to_f32(static_cast<const T *>(p.gate)[t]) : p.alpha;
             float s = 0.0f, sg = 0.0f;
             if (post)
-                w.load(w_post, H);
+                w_post.load(w, H);
             else
                 w.fill(1.0f);
             if (ROW) {
                 if (p.gate_kind == 1)
-                    gate.load(gate_row, H);
+                    gate_row.load(gate, H);
                 else
                     gate.fill(1.0f);
             }
@@ -451,7 +561,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
             P::store(static_cast<T *>(p.d_y) + base, H, d);
         }
         if (!read) {
-            if (RING) __syncthreads();
+            __syncthreads();
             ring.refill();
         }
     }
@@ -485,41 +595,45 @@ __global__ void __launch_bounds__(256) norm_columns_kernel(const __grid_constant
     }
 }
 
-// Threads of a CTA, CTAs of an SM and of the grid, and whether the rows go
-// through the ring, by H, the type and the tensors of a row.
+// Threads of a CTA, CTAs of an SM and of the grid, and the ring, by H, the
+// type and the tensors of a row.
 struct NormShape {
-    int ept, threads, ctas, stages;
-    bool ring;
+    int ept, threads, ctas;
+    Rows mode;
     size_t smem;
 };
 
-NormShape norm_shape(const NormParams &p, int elem, bool backward) {
+NormShape norm_shape(NormParams &p, int elem, bool backward) {
     NormShape s{};
-    const int64_t row_bytes = static_cast<int64_t>(p.H) * elem, stage = row_bytes * p.tensors;
-    const int kept = (p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0);
-    int64_t room = 0;
-    int per_sm = 1;
-    auto size = [&](int ept) {
-        s.ept = ept;
-        s.threads = ((p.H + ept - 1) / ept + 31) / 32 * 32;
-        // narrow rows: several CTAs an SM (the backward pass holds more registers)
-        per_sm = (backward ? 896 : 1024) / s.threads;
-        per_sm = per_sm < 1 || (backward && ept == 16) ? 1 : per_sm > 16 ? 16 : per_sm;
-        room = NORM_RING_BYTES / per_sm - kept * row_bytes;
-        s.ring = row_bytes % 16 == 0 && room >= 2 * stage;
-    };
-    // Forward: 16 elements a thread above 4096, for two CTAs an SM.  Backward:
-    // 8 with the ring as long as the registers allow (72 at 896 threads).
-    size(p.H <= (backward ? 7168 : 4096) ? 8 : 16);
-    if (!s.ring && p.H > 4096) size(16);
+    const int64_t row_bytes = static_cast<int64_t>(p.H) * elem, padded = (row_bytes + 15) / 16 * 16;
+    // Forward, 16-bit types: 16 elements a thread above 4096, for two CTAs an
+    // SM; fp32 rows that wide leave two CTAs no room for a ring.  Backward: 8 as
+    // long as the registers allow (72 at 896 threads).
+    s.ept = p.H <= (backward ? 7168 : elem == 4 ? 8192 : 4096) ? 8 : 16;
+    s.threads = ((p.H + s.ept - 1) / s.ept + 31) / 32 * 32;
+    // narrow rows: several CTAs an SM (the backward pass holds more registers)
+    int per_sm = (backward ? 896 : 1024) / s.threads;
+    per_sm = per_sm < 1 || (backward && s.ept == 16) ? 1 : per_sm > 16 ? 16 : per_sm;
     const int64_t all = static_cast<int64_t>(device_sm_count()) * per_sm;
     s.ctas = static_cast<int>(p.T < all ? p.T : all);
-    if (s.ring) {
-        const int64_t rows = (p.T + s.ctas - 1) / (s.ctas > 0 ? s.ctas : 1), fit = room / stage;
-        s.stages = static_cast<int>(fit < NORM_MAX_STAGES ? fit : NORM_MAX_STAGES);
-        if (rows < s.stages) s.stages = static_cast<int>(rows);
-        s.smem = static_cast<size_t>(s.stages * stage + kept * row_bytes);
+    const int64_t room = NORM_RING_BYTES / per_sm - 2048;
+    const int64_t kept = ((p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0)) *
+                         static_cast<int64_t>(s.ept) * s.threads * elem;
+    const bool odd = row_bytes % 16 != 0;
+    p.slot_bytes = static_cast<uint32_t>(odd ? padded + 16 : row_bytes);
+    const int64_t rows = s.ctas > 0 ? (p.T + s.ctas - 1) / s.ctas : 0;
+    int64_t slots = (room - kept) / static_cast<int64_t>(p.slot_bytes);
+    if (slots > NORM_MAX_SLOTS) slots = NORM_MAX_SLOTS;
+    if (slots < p.tensors) {
+        s.mode = Rows::kMemory;
+        return s;
     }
+    if (slots > rows * p.tensors) slots = rows * p.tensors;
+    s.mode = odd ? Rows::kOdd : Rows::kVectors;
+    p.slots = static_cast<int>(slots);
+    p.ring_bytes = p.slots * p.slot_bytes;
+    p.bars = p.slots / p.tensors + 2;  // the rows in the slots, wholly or in part, and the current one's
+    s.smem = static_cast<size_t>(p.ring_bytes + kept);
     return s;
 }
 
@@ -527,7 +641,8 @@ cudaError_t launch_kernel(void (*kern)(NormParams), std::atomic<bool> *attr_done
                           cudaStream_t stream) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
-    if (s.ring && (dev < 0 || dev >= 64 || !attr_done[dev])) {
+    // 48 KB need no leave, the kernel's own arrays included
+    if (s.smem > 40 * 1024 && (dev < 0 || dev >= 64 || !attr_done[dev])) {
         cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, NORM_RING_BYTES);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev] = true;
@@ -535,47 +650,56 @@ cudaError_t launch_kernel(void (*kern)(NormParams), std::atomic<bool> *attr_done
     return launch_pdl(kern, dim3(static_cast<unsigned>(s.ctas)), dim3(static_cast<unsigned>(s.threads)), s.smem, stream, p);
 }
 
-template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 cudaError_t launch_forward(const NormParams &p, const NormShape &s, cudaStream_t stream) {
     static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
-    return launch_kernel(norm_kernel<T, EPT, RING, MAX_THREADS, MIN_CTAS>, attr_done, p, s, stream);
+    return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS>, attr_done, p, s, stream);
 }
 
-template <typename T, int EPT, bool RING, int MAX_THREADS, int MIN_CTAS>
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 cudaError_t launch_backward(const NormParams &p, const NormShape &s, cudaStream_t stream) {
     static std::atomic<bool> attr_done[3][64];  // zero-initialised; several host threads may launch
     if (p.gate_kind == 2)
-        return launch_kernel(norm_backward_kernel<T, EPT, RING, 2, MAX_THREADS, MIN_CTAS>, attr_done[1], p, s, stream);
+        return launch_kernel(norm_backward_kernel<T, EPT, MODE, 2, MAX_THREADS, MIN_CTAS>, attr_done[1], p, s, stream);
     if (p.gate_kind == 3)
-        return launch_kernel(norm_backward_kernel<T, EPT, RING, 3, MAX_THREADS, MIN_CTAS>, attr_done[2], p, s, stream);
-    return launch_kernel(norm_backward_kernel<T, EPT, RING, 1, MAX_THREADS, MIN_CTAS>, attr_done[0], p, s, stream);
+        return launch_kernel(norm_backward_kernel<T, EPT, MODE, 3, MAX_THREADS, MIN_CTAS>, attr_done[2], p, s, stream);
+    return launch_kernel(norm_backward_kernel<T, EPT, MODE, 1, MAX_THREADS, MIN_CTAS>, attr_done[0], p, s, stream);
 }
 
 // Registers by the CTA's threads: the forward pass has 64; the backward pass
 // 80 up to 256 threads, 128 up to 512, 72 up to 896 (rows of 7168), 64 above.
 template <typename T> cudaError_t launch_shape(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
+    constexpr Rows kVectors = Rows::kVectors, kOdd = Rows::kOdd, kMemory = Rows::kMemory;
+    const bool odd = s.mode == kOdd;
     if (!backward) {
+        if (s.mode == kMemory) return launch_forward<T, 16, kMemory, 1024, 1>(p, s, stream);
         if (s.ept == 16) {
-            if (s.threads <= 512)
-                return s.ring ? launch_forward<T, 16, true, 512, 2>(p, s, stream) : launch_forward<T, 16, false, 512, 2>(p, s, stream);
-            return s.ring ? launch_forward<T, 16, true, 1024, 1>(p, s, stream) : launch_forward<T, 16, false, 1024, 1>(p, s, stream);
+            if constexpr (sizeof(T) == 2)
+                if (s.threads <= 512)
+                    return odd ? launch_forward<T, 16, kOdd, 512, 2>(p, s, stream)
+                               : launch_forward<T, 16, kVectors, 512, 2>(p, s, stream);
+            return odd ? launch_forward<T, 16, kOdd, 1024, 1>(p, s, stream) : launch_forward<T, 16, kVectors, 1024, 1>(p, s, stream);
         }
-        return s.ring ? launch_forward<T, 8, true, 512, 2>(p, s, stream) : launch_forward<T, 8, false, 512, 2>(p, s, stream);
+        if constexpr (sizeof(T) == 4)
+            if (s.threads > 512)
+                return odd ? launch_forward<T, 8, kOdd, 1024, 1>(p, s, stream) : launch_forward<T, 8, kVectors, 1024, 1>(p, s, stream);
+        return odd ? launch_forward<T, 8, kOdd, 512, 2>(p, s, stream) : launch_forward<T, 8, kVectors, 512, 2>(p, s, stream);
     }
+    if (s.mode == kMemory) return launch_backward<T, 16, kMemory, 1024, 1>(p, s, stream);
     if (s.ept == 16) {
         if (s.threads <= 512)
-            return s.ring ? launch_backward<T, 16, true, 512, 1>(p, s, stream) : launch_backward<T, 16, false, 512, 1>(p, s, stream);
-        return s.ring ? launch_backward<T, 16, true, 1024, 1>(p, s, stream) : launch_backward<T, 16, false, 1024, 1>(p, s, stream);
+            return odd ? launch_backward<T, 16, kOdd, 512, 1>(p, s, stream) : launch_backward<T, 16, kVectors, 512, 1>(p, s, stream);
+        return odd ? launch_backward<T, 16, kOdd, 1024, 1>(p, s, stream) : launch_backward<T, 16, kVectors, 1024, 1>(p, s, stream);
     }
-    if (!s.ring) return launch_backward<T, 8, false, 512, 1>(p, s, stream);
-    if (s.threads <= 256) return launch_backward<T, 8, true, 256, 3>(p, s, stream);
-    if (s.threads <= 512) return launch_backward<T, 8, true, 512, 1>(p, s, stream);
-    return launch_backward<T, 8, true, 896, 1>(p, s, stream);
+    if (s.threads <= 256)
+        return odd ? launch_backward<T, 8, kOdd, 256, 3>(p, s, stream) : launch_backward<T, 8, kVectors, 256, 3>(p, s, stream);
+    if (s.threads <= 512)
+        return odd ? launch_backward<T, 8, kOdd, 512, 1>(p, s, stream) : launch_backward<T, 8, kVectors, 512, 1>(p, s, stream);
+    return odd ? launch_backward<T, 8, kOdd, 896, 1>(p, s, stream) : launch_backward<T, 8, kVectors, 896, 1>(p, s, stream);
 }
 
 template <typename T> cudaError_t launch_typed(NormParams p, bool backward, cudaStream_t stream) {
     const NormShape s = norm_shape(p, sizeof(T), backward);
-    p.stages = s.stages;
     if (p.T > 0) {
         const cudaError_t e = launch_shape<T>(p, s, backward, stream);
         if (e != cudaSuccess) return e;

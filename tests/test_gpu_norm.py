@@ -140,6 +140,28 @@ def test_forward_and_backward(T, H, dtype):
             check(back[k], want[k], mag[k], f"{k} {post} {nxt} {gate}")
 
 
+# several rows a CTA, tensors that end inside 16 bytes, rows of less than 16
+# bytes, rows that fit the staging buffers in part and not at all
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T,H", [(5001, 3), (4999, 7), (2501, 249), (1001, 2047), (457, 7167), (307, 9001), (305, 13001),
+                                 (306, 16382), (307, 7168), (304, 14336)])
+def test_many_rows_of_any_width(T, H, dtype):
+    require_cuda()
+    for i, (post, nxt, gate) in enumerate([(True, True, "channel"), (True, True, "full"), (False, False, "token")]):
+        s = make(T, H, dtype, post, nxt, gate, seed=i)
+        got = binding.moe_residual_norm(s["y"], s["res"], s["w_post"], s["gate"], ALPHA, s["w_next"], EPS)
+        check_forward(got, forward64(s))
+        g = torch.Generator(device="cuda").manual_seed(i)
+        d_out = torch.randn((T, H), generator=g, device="cuda").to(DT[dtype])
+        d_u = torch.randn((T, H), generator=g, device="cuda").to(DT[dtype]) if nxt else None
+        back = binding.moe_residual_norm_backward(d_out, d_u, s["y"], got["out"], s["w_post"], s["gate"], ALPHA, s["w_next"],
+                                                  got.get("rstd_post"), got.get("rstd_next"))
+        want, mag = backward64(s, d_out, d_u, got["out"], got.get("rstd_post"), got.get("rstd_next"))
+        assert set(back) == set(want)
+        for k in want:
+            check(back[k], want[k], mag[k], f"{k} {post} {nxt} {gate}")
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_norm_alone(dtype):
     """y None: the norm before the first block, and its gradients."""
