@@ -186,16 +186,6 @@ __device__ __forceinline__ bool mbar_wait_bounded(uint32_t bar, uint32_t parity,
     }
 }
 
-// The same wait for a wait that is usually short and on the critical path:
-// the global timer (a slow read) is looked at only after 64 tries.
-__device__ __forceinline__ bool mbar_wait_spin(uint32_t bar, uint32_t parity, volatile int *abort_flag,
-                                               int *err_flag) {
-#pragma unroll 1
-    for (int it = 0; it < 64; ++it)
-        if (mbar_try_wait(bar, parity)) return true;
-    return mbar_wait_bounded(bar, parity, abort_flag, err_flag);
-}
-
 // ----------------------------------------------------------------------------
 // Counters between CTAs of one persistent grid.  The writer's plain stores
 // are published with a gpu-scope release add; the reader acquires the count
