@@ -16,6 +16,13 @@
 //               tensor memory;
 //   warp 1      one elected lane: four K = 64 MMAs a slice;
 //   warps 2-9   epilogue, from one of two accumulators while the other fills.
+//
+// 32,768 rows, 64 experts, 7168 x 2048, bf16 out: 429 us, 2.2 PFLOP/s.  Shared
+// memory bounds it: a 128 x 192 slice brings 40 KB in and the tensor cores read
+// them once, 640 of its about 950 cycles at 128 bytes each, against 340 for
+// its MMAs alone; the rest is the hand-over between the roles.  192 columns take
+// the tensor memory that two accumulators and the stages' scales leave; 128
+// columns 690 us, 256 with a single accumulator 462.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"

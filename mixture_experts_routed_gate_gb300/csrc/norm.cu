@@ -21,11 +21,12 @@
 // a fixed order.
 //
 // 4096 x 7168 bf16: forward 39 us (235 MB at 6.0 TB/s, against 35 at this
-// card's copy rate; 70% of the issue slots), gradients 88 us (52 at the copy
+// card's copy rate; 67% of the issue slots), gradients 88 us (52 at the copy
 // rate: there the instructions bound, about 500 a warp and row).  fp32: 81 and
-// 138 us of 69 and 104 (147 and 315 with rows from memory, as two rows' slots do
-// not fit; so the slots are single tensors', a part of a row ahead if need be).  Rows of 7167 bf16, by elements: 72 and 161 us; from
-// memory instead of through the ring 154 and 465.
+// 138 us of 69 and 104; two rows' slots do not fit, so the slots are single
+// tensors', a part of a row ahead if need be (147 and 315 us with such rows read
+// from memory).  Rows of 7167 bf16, by elements: 72 and 161 us (from memory 154
+// and 465).
 #include "common.cuh"
 #include "internal.h"
 
@@ -607,8 +608,10 @@ NormShape norm_shape(NormParams &p, int elem, bool backward) {
     NormShape s{};
     const int64_t row_bytes = static_cast<int64_t>(p.H) * elem, padded = (row_bytes + 15) / 16 * 16;
     // Forward, 16-bit types: 16 elements a thread above 4096, for two CTAs an
-    // SM; fp32 rows that wide leave two CTAs no room for a ring.  Backward: 8 as
-    // long as the registers allow (72 at 896 threads).
+    // SM (4096 x 7168 bf16 with its graph's overhead 46 us, one CTA of 8 elements
+    // a thread 62); fp32 rows that wide leave two CTAs no room for a ring (81 us
+    // with one CTA, 145 with two).  Backward: 8 as long as the registers allow
+    // (72 at 896 threads).
     s.ept = p.H <= (backward ? 7168 : elem == 4 ? 8192 : 4096) ? 8 : 16;
     s.threads = ((p.H + s.ept - 1) / s.ept + 31) / 32 * 32;
     // narrow rows: several CTAs an SM (the backward pass holds more registers)
