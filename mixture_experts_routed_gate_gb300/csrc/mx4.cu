@@ -3,10 +3,14 @@
 //
 //   s = max(floor(log2 max|x|) - 2, -127),  q = e2m1(x * 2^-s)
 //
-// Quantising is bound by instruction issue (72% of the slots, about 0.4 a warp
-// and element): 4096 x 7168 bf16 to bits and back in 28 us, 22 at the copy rate;
-// 32,768 rows that 4096 tokens repeat, 105 us (one CTA a token that looks up its
-// rows: 90 to 104, the search eats what it saves).
+// A thread quantises whole blocks of 32, so the scale is worked out once for
+// them and no lane asks another.  32,768 rows of 7168 bf16 that 4096 tokens
+// repeat: 68 us, 125 MB written; with two lanes a block 77, with four
+// 100 (the loads are then contiguous over the warp, but the scale and the lanes'
+// maximum are most of the instructions); CTAs of 64 threads 68, of 256 80.  One
+// CTA a token that looks up its rows was no faster at four lanes a block (90 to
+// 104): the search eats what it saves.  4096 x 7168 to bits and back in 27 us, 22
+// at the copy rate.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"
@@ -15,78 +19,84 @@ namespace moe {
 namespace {
 
 constexpr int MX_THREADS = 128;
-constexpr int MX_UNIT = 8;    // elements per thread and step: four lanes hold a block
-constexpr int MX_STEPS = 8;   // loads in flight per thread: a row of up to 8192 elements in one go
+constexpr int MX_UNIT = 32;  // a thread quantises whole blocks
 constexpr int MX_BACK_STEPS = 4;
 
-template <typename T> struct Unit;  // 8 elements as loaded
-template <> struct Unit<float> {
-    uint4 w[2];
-    __device__ __forceinline__ void load(const float *p) {
-        w[0] = __ldg(reinterpret_cast<const uint4 *>(p));
-        w[1] = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
-    }
-    __device__ __forceinline__ void values(float (&v)[8]) const {
-        const uint32_t b[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
+template <typename T> struct Unit {  // a block's elements, packed
+    static constexpr int DT = std::is_same<T, __half>::value ? kF16 : kBF16;
+    static constexpr int VECS = MX_UNIT * static_cast<int>(sizeof(T)) / 16, WORDS = 4 * VECS;
+    static constexpr int STEPS = 8 / VECS;  // blocks in flight a thread: 128 bytes
+    uint32_t w[WORDS];
+    __device__ __forceinline__ void load(const T *p) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(b[i]);
-    }
-    // the bits of the largest magnitude: they order like the values, with
-    // infinities and then NaNs at the top
-    __device__ __forceinline__ uint32_t top() const {
-        const uint32_t b[8] = {w[0].x, w[0].y, w[0].z, w[0].w, w[1].x, w[1].y, w[1].z, w[1].w};
-        uint32_t t = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) t = max(t, b[i] & 0x7fffffffu);
-        return t;
-    }
-    static __device__ __forceinline__ float top_value(uint32_t t) { return __uint_as_float(t); }
-    __device__ __forceinline__ void clear() { w[0] = w[1] = make_uint4(0u, 0u, 0u, 0u); }
-};
-template <int DT> struct HalfUnit {
-    uint4 w;
-    __device__ __forceinline__ void load(const void *p) { w = __ldg(static_cast<const uint4 *>(p)); }
-    __device__ __forceinline__ void values(float (&v)[8]) const {
-        const uint32_t b[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2<DT>(b[i]);
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+        for (int i = 0; i < VECS; ++i) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(p) + i);
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
         }
     }
-    __device__ __forceinline__ uint32_t top() const {
-        const uint32_t a = __vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), b = __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu);
-        const uint32_t c = __vmaxu2(a, b);
-        return max(c >> 16, c & 0xffffu);
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = 0u;
     }
-    static __device__ __forceinline__ float top_value(uint32_t t) { return unpack2<DT>(t).x; }
-    __device__ __forceinline__ void clear() { w = make_uint4(0u, 0u, 0u, 0u); }
+    // The bits of the largest magnitude: they order like the values, with
+    // infinities and then NaNs at the top.
+    __device__ __forceinline__ float top() const {
+        uint32_t t = 0;
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) t = max(t, w[i] & 0x7fffffffu);
+        } else {
+#pragma unroll
+            for (int i = 0; i < WORDS; ++i) t = __vmaxu2(t, w[i] & 0x7fff7fffu);
+            t = max(t >> 16, t & 0xffffu);
+        }
+        if constexpr (sizeof(T) == 4)
+            return __uint_as_float(t);
+        else
+            return unpack2<DT>(t).x;
+    }
+    // eight elements times `by`, a power of two, as a word of 4-bit ones
+    __device__ __forceinline__ uint32_t word(int i, float by) const {
+        float v[8];
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[8 * i + j]) * by;
+        } else if constexpr (DT == kBF16) {
+            // two at a time: exact but for results that are zero in 4 bits anyway
+            const __nv_bfloat162 by2 = __float2bfloat162_rn(by);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                __nv_bfloat162 x;
+                memcpy(&x, &w[4 * i + j], 4);
+                x = __hmul2(x, by2);
+                uint32_t bits;
+                memcpy(&bits, &x, 4);
+                const float2 f = unpack2<kBF16>(bits);
+                v[2 * j] = f.x;
+                v[2 * j + 1] = f.y;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 f = unpack2<kF16>(w[4 * i + j]);
+                v[2 * j] = f.x * by;
+                v[2 * j + 1] = f.y * by;
+            }
+        }
+        return e2m1x8(v, 1.0f);
+    }
 };
-template <> struct Unit<__half> : HalfUnit<kF16> {};
-template <> struct Unit<__nv_bfloat16> : HalfUnit<kBF16> {};
 
-// Four lanes quantise 32 values, 8 each (every lane of the warp takes part):
-// returns the lane's 4 bytes of elements and, through s, the scale byte.
-template <typename T> __device__ __forceinline__ uint32_t quad_quantize(const Unit<T> &raw, uint32_t &s) {
-    uint32_t top = raw.top();
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    s = mx4_scale(Unit<T>::top_value(top));
-    const float inv = s == 255u ? 0.0f : mx4_inverse(s);
-    float v[8];
-    raw.values(v);
-    const uint32_t q = e2m1x8(v, inv);
-    return s == 255u ? 0u : q;
-}
-
-// A CTA holds rows_per_cta rows at a time, `width` threads (a power of two,
-// at least four) on each.  Memory bound: 2 bytes in, 0.53 out per 16-bit
-// element, every access 16 (4 out) bytes a lane and contiguous over the warp.
+// A CTA holds rows_per_cta rows at a time, `width` threads (a power of two) on
+// each.
 template <typename T>
 __global__ void __launch_bounds__(MX_THREADS)
     quantize_kernel(const T *__restrict__ x, const int32_t *__restrict__ row_idx, int64_t n_rows, int64_t T_rows,
                     int units, int width, uint8_t *__restrict__ q, uint8_t *__restrict__ sf, int32_t *err) {
+    using U = Unit<T>;
     griddep_wait();
     griddep_launch_dependents();
     const int rows_per_cta = MX_THREADS / width;
@@ -99,27 +109,33 @@ __global__ void __launch_bounds__(MX_THREADS)
         const bool in = here && src >= 0 && src < T_rows;
         if (here && !in && err && u0 == 0) atomicExch(err, kErrDeviceFlag);
         const T *row = x + (in ? src : 0) * units * MX_UNIT;
-        uint32_t *qr = reinterpret_cast<uint32_t *>(q) + (here ? r : 0) * units;
-        uint8_t *sr = sf + (here ? r : 0) * (units / 4);
-        for (int u = u0; u - u0 < units; u += width * MX_STEPS) {  // every lane the same number of steps
-            Unit<T> raw[MX_STEPS];
+        uint8_t *qr = q + (here ? r : 0) * units * 16;
+        uint8_t *sr = sf + (here ? r : 0) * units;
+        const int have = in ? units : 0, store = here ? units : 0;
+        for (int u = u0; u < store; u += width * U::STEPS) {
+            U raw[U::STEPS];
 #pragma unroll
-            for (int i = 0; i < MX_STEPS; ++i) {
-                if (in && u + i * width < units)
-                    raw[i].load(row + static_cast<int64_t>(u + i * width) * MX_UNIT);
+            for (int i = 0; i < U::STEPS; ++i) {
+                if (u + i * width < have)
+                    raw[i].load(row + (u + i * width) * MX_UNIT);
                 else
                     raw[i].clear();
             }
 #pragma unroll
-            for (int i = 0; i < MX_STEPS; ++i) {
+            for (int i = 0; i < U::STEPS; ++i) {
                 const int at = u + i * width;
-                if (at - u0 >= units) break;  // the same for the whole CTA
-                uint32_t s;
-                const uint32_t w = quad_quantize(raw[i], s);
-                if (here && at < units) {
-                    qr[at] = w;
-                    if ((at & 3) == 0) sr[at >> 2] = static_cast<uint8_t>(s);
+                if (at >= store) break;
+                const uint32_t s = mx4_scale(raw[i].top());
+                const bool bad = s == 255u;
+                const float by = bad ? 0.0f : mx4_inverse(s);
+                uint32_t out[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    out[j] = raw[i].word(j, by);
+                    out[j] = bad ? 0u : out[j];
                 }
+                reinterpret_cast<uint4 *>(qr)[at] = make_uint4(out[0], out[1], out[2], out[3]);
+                sr[at] = static_cast<uint8_t>(s);
             }
         }
     }
@@ -153,7 +169,7 @@ __global__ void __launch_bounds__(MX_THREADS)
             v[2 * j] = pair.x * f;
             v[2 * j + 1] = pair.y * f;
         }
-        uint4 *dst = reinterpret_cast<uint4 *>(out + at * MX_UNIT);
+        uint4 *dst = reinterpret_cast<uint4 *>(out + at * 8);
         if constexpr (sizeof(T) == 4) {
             dst[0] = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
             dst[1] = make_uint4(__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7]));
@@ -168,7 +184,7 @@ template <typename T>
 cudaError_t launch_quantize_typed(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T_rows, int64_t K,
                                   uint8_t *q, uint8_t *sf, int32_t *err, cudaStream_t stream) {
     const int units = static_cast<int>(K / MX_UNIT);
-    int width = 4;
+    int width = 1;
     while (width < units && width < MX_THREADS) width *= 2;
     const int64_t groups = (n_rows + MX_THREADS / width - 1) / (MX_THREADS / width);
     const int64_t most = static_cast<int64_t>(device_sm_count()) * 512;
@@ -195,7 +211,7 @@ cudaError_t launch_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n
 
 cudaError_t launch_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K, int dtype, void *out,
                                   cudaStream_t stream) {
-    const int64_t words = n_rows * (K / MX_UNIT);
+    const int64_t words = n_rows * (K / 8);
     if (dtype == kF32) return launch_dequantize_typed<float>(q, sf, words, out, stream);
     if (dtype == kBF16) return launch_dequantize_typed<__nv_bfloat16>(q, sf, words, out, stream);
     return launch_dequantize_typed<__half>(q, sf, words, out, stream);
