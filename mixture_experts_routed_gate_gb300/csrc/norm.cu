@@ -22,7 +22,7 @@
 //
 // 4096 x 7168 bf16: forward 39 us (235 MB at 6.0 TB/s, against 35 at this
 // card's copy rate; 67% of the issue slots), gradients 88 us (52 at the copy
-// rate: there the instructions bound, about 500 a warp and row).  fp32: 81 and
+// rate: there the instructions bound, about 500 a warp and row).  fp32: 81 to 87 and
 // 138 us of 69 and 104; two rows' slots do not fit, so the slots are single
 // tensors', a part of a row ahead if need be (147 and 315 us with such rows read
 // from memory).  Rows of 7167 bf16, by elements: 72 and 161 us (from memory 154
@@ -617,15 +617,16 @@ NormShape norm_shape(NormParams &p, int elem, bool backward) {
     // narrow rows: several CTAs an SM (the backward pass holds more registers)
     int per_sm = (backward ? 896 : 1024) / s.threads;
     per_sm = per_sm < 1 || (backward && s.ept == 16) ? 1 : per_sm > 16 ? 16 : per_sm;
-    const int64_t all = static_cast<int64_t>(device_sm_count()) * per_sm;
-    s.ctas = static_cast<int>(p.T < all ? p.T : all);
-    const int64_t room = NORM_RING_BYTES / per_sm - 2048;
     const int64_t kept = ((p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0)) *
                          static_cast<int64_t>(s.ept) * s.threads * elem;
     const bool odd = row_bytes % 16 != 0;
     p.slot_bytes = static_cast<uint32_t>(odd ? padded + 16 : row_bytes);
+    auto fit = [&](int ctas) { return (NORM_RING_BYTES / ctas - 2048 - kept) / static_cast<int64_t>(p.slot_bytes); };
+    while (per_sm > 1 && fit(per_sm) < p.tensors) --per_sm;
+    const int64_t all = static_cast<int64_t>(device_sm_count()) * per_sm;
+    s.ctas = static_cast<int>(p.T < all ? p.T : all);
     const int64_t rows = s.ctas > 0 ? (p.T + s.ctas - 1) / s.ctas : 0;
-    int64_t slots = (room - kept) / static_cast<int64_t>(p.slot_bytes);
+    int64_t slots = fit(per_sm);
     if (slots > NORM_MAX_SLOTS) slots = NORM_MAX_SLOTS;
     if (slots < p.tensors) {
         s.mode = Rows::kMemory;
@@ -675,7 +676,8 @@ template <typename T> cudaError_t launch_shape(const NormParams &p, const NormSh
     constexpr Rows kVectors = Rows::kVectors, kOdd = Rows::kOdd, kMemory = Rows::kMemory;
     const bool odd = s.mode == kOdd;
     if (!backward) {
-        if (s.mode == kMemory) return launch_forward<T, 16, kMemory, 1024, 1>(p, s, stream);
+        if constexpr (sizeof(T) == 4)  // 16-bit rows of 16384, the widest, fit the ring
+            if (s.mode == kMemory) return launch_forward<T, 16, kMemory, 1024, 1>(p, s, stream);
         if (s.ept == 16) {
             if constexpr (sizeof(T) == 2)
                 if (s.threads <= 512)

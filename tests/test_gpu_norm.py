@@ -143,7 +143,7 @@ def test_forward_and_backward(T, H, dtype):
 # several rows a CTA, tensors that end inside 16 bytes, rows of less than 16
 # bytes, rows that fit the staging buffers in part and not at all
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("T,H", [(5001, 3), (4999, 7), (2501, 249), (1001, 2047), (457, 7167), (307, 9001), (305, 13001),
+@pytest.mark.parametrize("T,H", [(5001, 3), (4999, 7), (2501, 249), (4403, 510), (4403, 511), (1001, 2047), (457, 7167), (307, 9001), (305, 13001),
                                  (306, 16382), (307, 7168), (304, 14336)])
 def test_many_rows_of_any_width(T, H, dtype):
     require_cuda()
