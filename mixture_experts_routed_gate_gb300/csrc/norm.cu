@@ -252,8 +252,9 @@ template <> struct RowRing<Rows::kMemory> {
 // p.slots slots of one tensor's row each, filled in the order of the reads, a
 // row ahead as far as they go (not a whole number of rows), and a barrier for
 // each row in flight.  kOdd copies from the 16 bytes a row starts in to those
-// it ends in; what is left of the tensors after their last 16 bytes is copied
-// by the threads.
+// it ends in; what is left of the tensors after their last whole 16 bytes is
+// copied by the threads, into slots that no bulk copy fills again (the rows that
+// come after have nothing left to copy).
 template <Rows MODE> struct RowRing {
     const NormParams &p;
     uint8_t *smem;
@@ -321,9 +322,10 @@ template <Rows MODE> struct RowRing {
         }
         if (!wait()) return false;
         if constexpr (MODE == Rows::kOdd) {
-            const int64_t total = p.T * row_bytes;
-            if (row == p.T - 1 && total % 16 != 0) {
-                int64_t from = total / 16 * 16 - row * row_bytes;
+            // rows of less than 16 bytes: several may reach past the last whole 16
+            const int64_t whole = p.T * row_bytes / 16 * 16;
+            if ((row + 1) * row_bytes > whole) {
+                int64_t from = whole - row * row_bytes;
                 from = from < 0 ? 0 : from;
                 const uint32_t first = slot;
                 for (int i = 0; i < p.tensors; ++i) {
