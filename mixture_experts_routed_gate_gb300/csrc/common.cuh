@@ -134,6 +134,18 @@ __device__ __forceinline__ float fma_mixed(uint32_t a, uint32_t b, float c) {
     return d;
 }
 
+// Order-preserving key of a logit: larger is better, 0 is below every logit's.
+// -0 counts as +0, a NaN comes first, so a selection by (key, then the lower
+// id) is a total order: whatever the logits hold, k distinct experts are chosen.
+__device__ __forceinline__ uint32_t order_key_number(float v) {  // v is not NaN
+    const uint32_t b = __float_as_uint(v + 0.0f);
+    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
+}
+__device__ __forceinline__ uint32_t order_key(float v) { return v != v ? 0xffffffffu : order_key_number(v); }
+__device__ __forceinline__ float key_value(uint32_t key) {
+    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
+}
+
 // ----------------------------------------------------------------------------
 // mbarrier
 // ----------------------------------------------------------------------------

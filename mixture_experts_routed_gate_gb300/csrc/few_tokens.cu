@@ -119,19 +119,6 @@ __global__ void __launch_bounds__(LOGIT_WARPS * 32)
     }
 }
 
-// Order-preserving key of a logit: larger is better, 0 is below every logit's.
-// -0 counts as +0, a NaN comes first, so whatever the logits hold, k distinct
-// experts in [0, E) are chosen.
-__device__ __forceinline__ uint32_t logit_key(float v) {
-    if (v != v) return 0xffffffffu;
-    const uint32_t b = __float_as_uint(v + 0.0f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-
-__device__ __forceinline__ float logit_of(uint32_t key) {
-    return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
-}
-
 // The k best of one token's E logits (descending, ties to the lower id) and
 // their softmax weights, by one warp; lane j < k gets slot j.
 template <int SLOTS>
@@ -140,14 +127,14 @@ __device__ __forceinline__ void warp_route(const float *row, int E, int k, int l
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
         const int e = s * 32 + lane;
-        key[s] = e < E ? logit_key(__ldcg(row + e)) : 0u;
+        key[s] = e < E ? order_key(__ldcg(row + e)) : 0u;
         most = max(most, key[s]);
     }
-    const float top = logit_of(__reduce_max_sync(0xffffffffu, most));
+    const float top = key_value(__reduce_max_sync(0xffffffffu, most));
     float sum = 0.0f;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s)
-        if (s * 32 + lane < E) sum += expf(logit_of(key[s]) - top);
+        if (s * 32 + lane < E) sum += expf(key_value(key[s]) - top);
     sum = warp_sum(sum);
     uint32_t mine = 0u;
     int id = 0;
@@ -171,7 +158,7 @@ __device__ __forceinline__ void warp_route(const float *row, int E, int k, int l
         }
     }
     *my_e = id;
-    *my_w = expf(logit_of(mine) - top) / sum;
+    *my_w = expf(key_value(mine) - top) / sum;
 }
 
 // Waits until counter `a` has reached `target` and returns the last expert up

@@ -383,16 +383,6 @@ __global__ void __launch_bounds__(GT_THREADS, 1)
     }
 }
 
-// Order-preserving key of a float that is not NaN (-0 taken as +0): a > b
-// as floats exactly when key(a) > key(b); 0 is below every key.
-__device__ __forceinline__ uint32_t order_key(float f) {
-    const uint32_t b = __float_as_uint(f + 0.0f);
-    return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
-}
-__device__ __forceinline__ float key_value(uint32_t k) {
-    return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
-}
-
 // One chunk of NG candidates' chains: the 8 elements in ascending order, each
 // a single-rounding fmaf on the exactly widened 16-bit values (the same bits
 // as the mixed-precision FMA of the CUDA-core gate); x is widened once for all
@@ -524,7 +514,7 @@ __global__ void __launch_bounds__(SEL_WARPS * 32)
         if (!bad) {
             uint32_t key[SLOTS];
 #pragma unroll
-            for (int s = 0; s < SLOTS; ++s) key[s] = s * 32 + lane < E ? order_key(lo[s]) : 0u;
+            for (int s = 0; s < SLOTS; ++s) key[s] = s * 32 + lane < E ? order_key_number(lo[s]) : 0u;
             uint32_t kth = 0u;
             for (int j = 0; j < k; ++j) {
                 uint32_t m = 0u;
@@ -587,66 +577,46 @@ __global__ void __launch_bounds__(SEL_WARPS * 32)
     __syncwarp();
 
     // top-k among the candidates by (logit desc, id asc); lane j keeps slot j.
-    // At most 32 candidates, none NaN: one per lane, each round a warp max of
-    // the keys and a warp min of the ids holding it.  Otherwise a scan.
+    // At most 32 candidates: one per lane; otherwise each lane scans its own.
+    // Each round is a warp max of the keys and a warp min of the ids holding it
+    // (the keys order NaN logits too, so every round takes one candidate).
     float top = 0.0f, my_v = 0.0f;
     int my_e = 0;
-    bool one_each = n <= 32;
-    float cv = 0.0f;
-    int ce = 0;
-    if (one_each) {
+    auto select = [&](int j, uint32_t key, int id) {  // whether the round took this lane's
+        const uint32_t m = __reduce_max_sync(0xffffffffu, key);
+        const uint32_t be =
+            __reduce_min_sync(0xffffffffu, key == m && key != 0u ? static_cast<uint32_t>(id) : 0xffffffffu);
+        const float bv = key_value(m);
+        if (j == 0) top = bv;
+        if (j == lane) {
+            my_v = bv;
+            my_e = static_cast<int>(be);
+        }
+        return key == m && static_cast<uint32_t>(id) == be;
+    };
+    if (n <= 32) {
+        uint32_t key = 0u;
+        int ce = 0;
         if (lane < n) {
-            cv = cand_val[lane];
+            key = order_key(cand_val[lane]);
             ce = cand_id[lane];
         }
-        one_each = !__any_sync(0xffffffffu, lane < n && isnan(cv));
-    }
-    if (one_each) {
-        uint32_t key = lane < n ? order_key(cv) : 0u;
-        for (int j = 0; j < k; ++j) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, key);
-            const uint32_t be =
-                __reduce_min_sync(0xffffffffu, key == m && key != 0u ? static_cast<uint32_t>(ce) : 0xffffffffu);
-            if (key == m && static_cast<uint32_t>(ce) == be) key = 0u;
-            const float bv = key_value(m);
-            if (j == 0) top = bv;
-            if (j == lane) {
-                my_v = bv;
-                my_e = static_cast<int>(be);
-            }
-        }
+        for (int j = 0; j < k; ++j)
+            if (select(j, key, ce)) key = 0u;
     } else {
         unsigned taken = 0;  // bit i: candidate lane + 32 i already selected
         for (int j = 0; j < k; ++j) {
-            float best = -INFINITY;
-            int best_e = 0x7fffffff, best_i = -1;
+            uint32_t best = 0u;
+            int best_e = 0, best_b = 0;
             for (int i = lane, b = 0; i < n; i += 32, ++b) {
-                if (taken & (1u << b)) continue;
-                const float v = cand_val[i];
-                const int e = cand_id[i];
-                if (best_i < 0 || v > best || (v == best && e < best_e)) {
-                    best = v;
-                    best_e = e;
-                    best_i = i;
+                const uint32_t c = order_key(cand_val[i]);
+                if (!((taken >> b) & 1u) && c > best) {  // ids ascend: ties stay with the first
+                    best = c;
+                    best_e = cand_id[i];
+                    best_b = b;
                 }
             }
-#pragma unroll
-            for (int sh = 16; sh >= 1; sh >>= 1) {
-                const float ob = __shfl_xor_sync(0xffffffffu, best, sh);
-                const int oe = __shfl_xor_sync(0xffffffffu, best_e, sh);
-                const int oi = __shfl_xor_sync(0xffffffffu, best_i, sh);
-                if (oi >= 0 && (best_i < 0 || ob > best || (ob == best && oe < best_e))) {
-                    best = ob;
-                    best_e = oe;
-                    best_i = oi;
-                }
-            }
-            if (best_i >= 0 && (best_i & 31) == lane) taken |= 1u << (best_i >> 5);
-            if (j == 0) top = best;
-            if (j == lane) {
-                my_v = best;
-                my_e = best_e;
-            }
+            if (select(j, best, best_e)) taken |= 1u << best_b;
         }
     }
     // softmax denominator over every expert (per lane in slot order, then the

@@ -43,32 +43,33 @@ __host__ __device__ constexpr int gate_stages(int rows, bool many_tokens) {
 }
 
 // Top-k by (logit desc, id asc) and the softmax weights of TOK tokens whose
-// 64 logits per token (E <= 64 valid) sit in shared memory, lsm[TOK][64],
-// with every thread of the CTA taking part (the single-token latency case).
-// Q = NT / (TOK * 64) threads rank one value, each against 64 / Q of the
-// token's values (4-wide shared loads, a short loop), and their counts are
-// added by shuffles; the value of rank r < k is selection slot r.  The
+// 64 logits per token (E <= 64 valid) sit in shared memory as their order
+// keys, ksm[TOK][64], with every thread of the CTA taking part (the
+// single-token latency case).  Q = NT / (TOK * 64) threads rank one key, each
+// against 64 / Q of the token's (4-wide shared loads, a short loop), and their
+// counts are added by shuffles; the key of rank r < k is selection slot r.
+// Keys and ids order totally, NaN included, so every slot is written.  The
 // softmax denominator is summed by the token's warp as in warp_topk_rounds
 // (per lane: its expert, then expert + 32; then the xor butterfly), so the
-// weights are the same bits either way.  Scratch after lsm: ranks and the
+// weights are the same bits either way.  Scratch after ksm: ranks and the
 // top logit per token.
 template <int TOK, int NT>
-__device__ __forceinline__ void cta_topk_softmax(float *lsm, int t0, int T, int E, int k,
+__device__ __forceinline__ void cta_topk_softmax(uint32_t *ksm, int t0, int T, int E, int k,
                                                  int32_t *__restrict__ topk_idx,
                                                  float *__restrict__ topk_w) {
     constexpr int EXP = 64, Q = NT / (TOK * EXP), PER = EXP / Q;
     static_assert(Q >= 1 && Q * TOK * EXP == NT && PER % 4 == 0, "ranking shape");
-    int *rank_s = reinterpret_cast<int *>(lsm + TOK * EXP);
+    int *rank_s = reinterpret_cast<int *>(ksm + TOK * EXP);
     float *top_s = reinterpret_cast<float *>(rank_s + TOK * EXP);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int vi = tid / Q, part = tid - vi * Q;
     const int tt = vi / EXP, e = vi - tt * EXP;
-    const float mine = lsm[vi];
-    const float4 *row4 = reinterpret_cast<const float4 *>(lsm + tt * EXP + part * PER);
+    const uint32_t mine = ksm[vi];
+    const uint4 *row4 = reinterpret_cast<const uint4 *>(ksm + tt * EXP + part * PER);
     int r = 0;
 #pragma unroll 1
     for (int q = 0; q < PER / 4; ++q) {
-        const float4 o = row4[q];
+        const uint4 o = row4[q];
         const int o0 = part * PER + q * 4;
         r += (o0 < E && (o.x > mine || (o.x == mine && o0 < e))) ? 1 : 0;
         r += (o0 + 1 < E && (o.y > mine || (o.y == mine && o0 + 1 < e))) ? 1 : 0;
@@ -79,13 +80,13 @@ __device__ __forceinline__ void cta_topk_softmax(float *lsm, int t0, int T, int 
     for (int sh = 1; sh < Q; sh <<= 1) r += __shfl_xor_sync(0xffffffffu, r, sh);
     if (part == 0) {
         rank_s[vi] = r;
-        if (e < E && r == 0) top_s[tt] = mine;
+        if (e < E && r == 0) top_s[tt] = key_value(mine);
     }
     __syncthreads();
     const int t = t0 + warp;
     if (warp < TOK && t < T) {
         const float top = top_s[warp];
-        const float v0 = lsm[warp * EXP + lane], v1 = lsm[warp * EXP + 32 + lane];
+        const float v0 = key_value(ksm[warp * EXP + lane]), v1 = key_value(ksm[warp * EXP + 32 + lane]);
         float sum = 0.0f;
         if (lane < E) sum += expf(v0 - top);
         if (32 + lane < E) sum += expf(v1 - top);
@@ -107,53 +108,45 @@ __device__ __forceinline__ void cta_topk_softmax(float *lsm, int t0, int T, int 
 
 // Warp argmax by (logit desc, id asc) over k rounds, then the softmax weights
 // (for many experts: k rounds cost less than ranking every value).
-// Lane holds v[s] = logit of expert s*32 + lane (or -inf past E).
+// Lane holds key[s] = the order key of expert s*32 + lane's logit (0 past E);
+// a round is a warp maximum and the lowest id that holds it.
 template <int SLOTS>
-__device__ __forceinline__ void warp_topk_rounds(float (&v)[SLOTS], int E, int k, int32_t *idx_out,
+__device__ __forceinline__ void warp_topk_rounds(uint32_t (&key)[SLOTS], int E, int k, int32_t *idx_out,
                                                  float *w_out, int lane) {
-    bool taken[SLOTS];
+    uint32_t most = 0u;
 #pragma unroll
-    for (int s = 0; s < SLOTS; ++s) taken[s] = s * 32 + lane >= E;
-    float top_logit = 0.0f, my_logit = 0.0f;
-    int my_id = 0;
-    for (int j = 0; j < k; ++j) {
-        float best = -INFINITY;
-        int best_id = 0x7fffffff;
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s) {
-            const int e = s * 32 + lane;
-            if (!taken[s] && (best_id == 0x7fffffff || v[s] > best || (v[s] == best && e < best_id))) {
-                best = v[s];
-                best_id = e;
-            }
-        }
-#pragma unroll
-        for (int sh = 16; sh >= 1; sh >>= 1) {
-            const float ob = __shfl_xor_sync(0xffffffffu, best, sh);
-            const int oid = __shfl_xor_sync(0xffffffffu, best_id, sh);
-            if (oid != 0x7fffffff && (best_id == 0x7fffffff || ob > best || (ob == best && oid < best_id))) {
-                best = ob;
-                best_id = oid;
-            }
-        }
-#pragma unroll
-        for (int s = 0; s < SLOTS; ++s)
-            if (s * 32 + lane == best_id) taken[s] = true;
-        if (j == 0) top_logit = best;
-        if (j == lane) {
-            my_logit = best;
-            my_id = best_id;
-        }
-    }
+    for (int s = 0; s < SLOTS; ++s) most = max(most, key[s]);
+    const float top_logit = key_value(__reduce_max_sync(0xffffffffu, most));
     float sum = 0.0f;
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s)
-        if (s * 32 + lane < E) sum += expf(v[s] - top_logit);
+        if (s * 32 + lane < E) sum += expf(key_value(key[s]) - top_logit);
 #pragma unroll
     for (int sh = 16; sh >= 1; sh >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, sh);
+    uint32_t my_key = 0u, my_id = 0u;
+    for (int j = 0; j < k; ++j) {
+        uint32_t best = 0u;
+        int slot = 0;
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s) {
+            if (key[s] > best) {
+                best = key[s];
+                slot = s;
+            }
+        }
+        const uint32_t win = __reduce_max_sync(0xffffffffu, best);
+        const uint32_t id = __reduce_min_sync(0xffffffffu, best == win ? slot * 32u + lane : 0xffffffffu);
+#pragma unroll
+        for (int s = 0; s < SLOTS; ++s)
+            if (s * 32u + lane == id) key[s] = 0u;
+        if (j == lane) {
+            my_key = win;
+            my_id = id;
+        }
+    }
     if (lane < k) {
-        idx_out[lane] = my_id;
-        w_out[lane] = expf(my_logit - top_logit) / sum;
+        idx_out[lane] = static_cast<int32_t>(my_id);
+        w_out[lane] = expf(key_value(my_key) - top_logit) / sum;
     }
 }
 
@@ -295,15 +288,15 @@ __global__ void __launch_bounds__(WT *WE * 32)
         // memory, then warp w selects the top-k of token t0 + w
         static_assert(!FUSE_TOPK || (WT == 1 && EXP == 64 && TPW <= WE), "fused shape");
         __syncthreads();  // the ring is no longer read
-        float *lsm = reinterpret_cast<float *>(smem);  // [TOK][EXP]
+        uint32_t *ksm = reinterpret_cast<uint32_t *>(smem);  // [TOK][EXP]
         if (lane < TPW * 8) {
             float l = mine;
             if (my_e < E && bias) l = l + bias[my_e];
-            lsm[(wt + my_i) * EXP + we + my_j] = l;
+            ksm[(wt + my_i) * EXP + we + my_j] = order_key(l);
             if (my_t < T && my_e < E) logits[static_cast<int64_t>(my_t) * E + my_e] = l;
         }
         __syncthreads();
-        cta_topk_softmax<TOK, WT * WE * 32>(lsm, t0, T, E, k, topk_idx, topk_w);
+        cta_topk_softmax<TOK, WT * WE * 32>(ksm, t0, T, E, k, topk_idx, topk_w);
     }
 }
 
@@ -320,13 +313,13 @@ __global__ void __launch_bounds__(TK_WARPS * 32)
     griddep_launch_dependents();
     if (t >= T) return;
     const float *row = logits + static_cast<int64_t>(t) * E;
-    float v[SLOTS];
+    uint32_t key[SLOTS];
 #pragma unroll
     for (int s = 0; s < SLOTS; ++s) {
         const int e = s * 32 + lane;
-        v[s] = e < E ? row[e] : -INFINITY;
+        key[s] = e < E ? order_key(row[e]) : 0u;
     }
-    warp_topk_rounds<SLOTS>(v, E, k, topk_idx + static_cast<int64_t>(t) * k,
+    warp_topk_rounds<SLOTS>(key, E, k, topk_idx + static_cast<int64_t>(t) * k,
                              topk_w + static_cast<int64_t>(t) * k, lane);
 }
 
