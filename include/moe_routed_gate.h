@@ -523,10 +523,13 @@ MOE_API moe_status_t moe_residual_norm_backward(const void *d_out, const void *d
  * 128-row tiles.  Routing as moe_gate_topk (the fixed summation order, ties to
  * the lower id).  Every chosen expert's weights are read once for all its
  * tokens; h = silu(G) * U, scaled by its routing weight, is kept as two values
- * of `dtype` (the rounded value and the rest), the outputs are summed over the
- * experts in fp32 and rounded once, so the result is closer to exact than
- * moe_forward's, which rounds h and each expert's output.  The order of every
- * sum is fixed: the same inputs give the same bits.
+ * of `dtype` (the rounded value and the rest; to 2^-22 of itself or 2^-35 in
+ * fp16, to 2^-17 of itself in bf16), the outputs are summed over the experts in
+ * fp32 and rounded once, so the result is closer to exact than moe_forward's,
+ * which rounds h and each expert's output.  As there, an h that fp16 does not
+ * hold (here after its weight, scaled so that the token's largest is in
+ * [0.5, 1)) counts as an infinity.  The order of every sum is fixed: the same
+ * inputs give the same bits.
  * Arguments as moe_forward; d_h % 256 == 0, d_e % 64 == 0, k <= min(E, 32),
  * E <= 1024.  ws: moe_forward_few_workspace_bytes(...) bytes, 256-byte aligned,
  * needs no clearing.

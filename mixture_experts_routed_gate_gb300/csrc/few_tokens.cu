@@ -23,7 +23,13 @@
 //    more warps join their sums in a fixed order.
 //    h is scaled by its routing weight and kept as a 16-bit value and the
 //    16-bit rest, both multiplied, so that the stage-2 accumulators hold the
-//    weighted sum over the experts and the output is rounded once.
+//    weighted sum over the experts and the output is rounded once.  The weights
+//    are a softmax over all experts, about 1 / E, and fp16 has few bits below
+//    2^-14, so a token's weights are scaled by the power of two that brings its
+//    largest to [0.5, 1), undone when the sums are joined, and in fp16 the rest
+//    is kept times 2^11, with sums of its own: h is held to 2^-22 of itself or
+//    2^-35, bf16's to 2^-17 of itself (its outputs round by 2^-9).  Without the
+//    scales an h of 1e-3 among 256 experts was off by up to 0.8%.
 // Tiles are taken in order, so a stage-2 tile waits only on tiles that running
 // CTAs hold: the launch completes whether or not all CTAs are resident.
 //
@@ -55,6 +61,8 @@ constexpr int FEW_QUEUE = 4;                         // tiles handed from the co
 constexpr int FEW_BARS = 2 * FEW_MAX_STAGES + 2 * FEW_QUEUE + 2 * FEW_PARTS;
 constexpr int FEW_SMEM_MAX = 232448 - 1024;
 constexpr int LOGIT_WARPS = 4;
+
+template <int DT> constexpr float FEW_REST = DT == kF16 ? 2048.0f : 1.0f;  // scale of h's rest: at most as large as h
 
 template <int DT>
 __device__ __forceinline__ float dot8(const uint4 &a, const uint4 &b, float c) {
@@ -250,13 +258,14 @@ struct FewSmem {
     float4 *partial;  // [FEW_PARTS][FEW_CONSUMERS][NT][32]
     int *queue, *act_e, *act_base, *topk_e;
     uint32_t *act_mask;
-    float *pair_w, *topk_w;
+    float *pair_w, *topk_w;  // times the token's power of two
+    float *undo;             // [16] and back
 };
 __host__ __device__ constexpr int few_stage_bytes(int tokens) {
     return (2 * FEW_HALF + 2 * tokens * FEW_ROW + 1023) / 1024 * 1024;
 }
 __host__ __device__ constexpr int few_fixed_bytes(int nt, int pairs) {
-    return FEW_BARS * 8 + FEW_ROW + FEW_PARTS * FEW_CONSUMERS * nt * 512 + FEW_QUEUE * 4 + pairs * 24;
+    return FEW_BARS * 8 + FEW_ROW + FEW_PARTS * FEW_CONSUMERS * nt * 512 + FEW_QUEUE * 4 + pairs * 24 + 64;
 }
 static_assert(1024 + FEW_GROUPS * few_stage_bytes(16) + few_fixed_bytes(2, 16 * 32) <= FEW_SMEM_MAX,
               "a stage for each group at least");
@@ -282,6 +291,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
     sm.act_mask = reinterpret_cast<uint32_t *>(sm.topk_e + pairs);
     sm.pair_w = reinterpret_cast<float *>(sm.act_mask + pairs);
     sm.topk_w = sm.pair_w + pairs;
+    sm.undo = sm.topk_w + pairs;
     __shared__ int abort_word, n_act_word, most_word;
     volatile int *abort_flag = &abort_word;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -329,11 +339,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             warp_route<8>(row, p.E, p.k, lane, &e, &w);
         else
             warp_route<32>(row, p.E, p.k, lane, &e, &w);
+        // the largest, in [2^(field - 127), 2^(field - 126)); a NaN stays one
+        const uint32_t field = min((__float_as_uint(__shfl_sync(0xffffffffu, w, 0)) >> 23) & 255u, 252u);
         if (lane < p.k) {
             sm.topk_e[t * p.k + lane] = e;
-            sm.topk_w[t * p.k + lane] = w;
+            sm.topk_w[t * p.k + lane] = w * __uint_as_float((253u - field) << 23);
             atomicOr(&mask[e], 1u << t);
         }
+        if (lane == 0) sm.undo[t] = __uint_as_float((field + 1u) << 23);
     }
     __syncthreads();
     if (warp == 0) {  // the chosen experts in ascending order, their tokens, their first row of h
@@ -561,8 +574,9 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     const float h = gate[n] / (1.0f + __expf(-gate[n])) * up[n] * sm.pair_w[r];
                     const El top = from_f32<El>(h);
                     const int64_t o = static_cast<int64_t>(r) * p.d_e + (tile - a * tiles_e) * 8 + feat;
+                    const float t32 = to_f32(top);
                     static_cast<El *>(p.h_hi)[o] = top;
-                    static_cast<El *>(p.h_lo)[o] = from_f32<El>(h - to_f32(top));
+                    static_cast<El *>(p.h_lo)[o] = from_f32<El>(fabsf(t32) == INFINITY ? 0.0f : (h - t32) * FEW_REST<DT>);
                 }
                 asm volatile("fence.proxy.async.global;" ::: "memory");
                 __syncwarp();  // the publishing add releases the whole warp's stores
@@ -581,7 +595,8 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int t = n * 8 + t8;
-                    if (t < p.T) static_cast<El *>(p.out)[static_cast<int64_t>(t) * p.d_h + (tile - n1) * 16 + r] = from_f32<El>(v[n]);
+                    if (t < p.T)
+                        static_cast<El *>(p.out)[static_cast<int64_t>(t) * p.d_h + (tile - n1) * 16 + r] = from_f32<El>(v[n] * sm.undo[t]);
                 }
             }
         }
@@ -643,18 +658,23 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     for (int n = 0; n < NT; ++n) {
                         if (!any[n]) continue;
                         const uint32_t b = here[n] ? st + token[n] : zeros;
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const uint4 v = ldmatrix_x4(b + j * 64);
-                            mma_16816<DT>(acc[n][j], w[2 * j], v.x, v.y);
-                            mma_16816<DT>(acc[n][2 + j], w[2 * j + 1], v.z, v.w);
-                        }
-                        if (!first) {
+                        if (first) {
 #pragma unroll
                             for (int j = 0; j < 2; ++j) {
-                                const uint4 v = ldmatrix_x4((here[n] ? b + rest : zeros) + j * 64);
-                                mma_16816<DT>(acc[n][2 + j], w[2 * j], v.x, v.y);
-                                mma_16816<DT>(acc[n][j], w[2 * j + 1], v.z, v.w);
+                                const uint4 v = ldmatrix_x4(b + j * 64);
+                                mma_16816<DT>(acc[n][j], w[2 * j], v.x, v.y);
+                                mma_16816<DT>(acc[n][2 + j], w[2 * j + 1], v.z, v.w);
+                            }
+                        } else {  // chains 0 and 1: h's values, 2 and 3: their rests
+                            const uint32_t b2 = here[n] ? b + rest : zeros;
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                uint4 v = ldmatrix_x4(b + j * 64);
+                                mma_16816<DT>(acc[n][0], w[2 * j], v.x, v.y);
+                                mma_16816<DT>(acc[n][1], w[2 * j + 1], v.z, v.w);
+                                v = ldmatrix_x4(b2 + j * 64);
+                                mma_16816<DT>(acc[n][2], w[2 * j], v.x, v.y);
+                                mma_16816<DT>(acc[n][3], w[2 * j + 1], v.z, v.w);
                             }
                         }
                     }
@@ -674,13 +694,14 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
         const int buf = local % FEW_PARTS;
         if (!wait(pe_bar(buf), (static_cast<uint32_t>(local / FEW_PARTS) & 1u) ^ 1u)) break;
         float4 *part = sm.partial + buf * FEW_CONSUMERS * NT * 32;
+        const float unscale = first ? 1.0f : 1.0f / FEW_REST<DT>;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-            part[(warp * NT + n) * 32 + lane] =
-                make_float4((acc[n][0][0] + acc[n][1][0]) + (acc[n][2][0] + acc[n][3][0]),
-                            (acc[n][0][1] + acc[n][1][1]) + (acc[n][2][1] + acc[n][3][1]),
-                            (acc[n][0][2] + acc[n][1][2]) + (acc[n][2][2] + acc[n][3][2]),
-                            (acc[n][0][3] + acc[n][1][3]) + (acc[n][2][3] + acc[n][3][3]));
+        for (int n = 0; n < NT; ++n) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = fmaf(acc[n][2][i] + acc[n][3][i], unscale, acc[n][0][i] + acc[n][1][i]);
+            part[(warp * NT + n) * 32 + lane] = make_float4(v[0], v[1], v[2], v[3]);
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(pf_bar(buf));
     }
