@@ -267,6 +267,29 @@ __host__ __device__ constexpr int few_stage_bytes(int tokens) {
 __host__ __device__ constexpr int few_fixed_bytes(int nt, int pairs) {
     return FEW_BARS * 8 + FEW_ROW + FEW_PARTS * FEW_CONSUMERS * nt * 512 + FEW_QUEUE * 4 + pairs * 24 + 64;
 }
+
+// One output of token t from its own experts alone, by a warp (every lane gets
+// it): the joining warps' way back from products that are not finite.
+template <int DT>
+__device__ __forceinline__ float few_output(const FewParams &p, const FewSmem &sm, int n_act, int t, int row, int lane) {
+    using El = typename Elem<DT>::T;
+    float s = 0.0f;
+#pragma unroll 1
+    for (int a = 0; a < n_act; ++a) {
+        const uint32_t m = sm.act_mask[a];
+        if (!((m >> t) & 1u)) continue;
+        const int r = sm.act_base[a] + __popc(m & ((1u << t) - 1u));
+        if (sm.pair_w[r] != sm.pair_w[r]) return sm.pair_w[r];
+        const El *w = static_cast<const El *>(p.w_down) + (static_cast<int64_t>(sm.act_e[a]) * p.d_h + row) * p.d_e;
+        const El *hi = static_cast<const El *>(p.h_hi) + static_cast<int64_t>(r) * p.d_e;
+        const El *lo = static_cast<const El *>(p.h_lo) + static_cast<int64_t>(r) * p.d_e;
+#pragma unroll 1
+        for (int c = lane; c < p.d_e; c += 32)  // h comes from other CTAs: past L1
+            s = fmaf(fmaf(to_f32(__ldcg(lo + c)), 1.0f / FEW_REST<DT>, to_f32(__ldcg(hi + c))), to_f32(__ldg(w + c)), s);
+    }
+    return warp_sum(s);
+}
+
 static_assert(1024 + FEW_GROUPS * few_stage_bytes(16) + few_fixed_bytes(2, 16 * 32) <= FEW_SMEM_MAX,
               "a stage for each group at least");
 static_assert(FEW_MAX_STAGES % FEW_GROUPS == 0, "stages belong to groups");
@@ -592,6 +615,20 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                     for (int w = 0; w < FEW_CONSUMERS; ++w) v[n] += f[w * NT * 128 + at];
                 }
                 release();
+                // A token takes part in every chosen expert's products, as a row of zeros
+                // where it is not routed: an infinity or a NaN among the weights would
+                // reach it.  And an infinite weight times h's two parts may be inf - inf.
+                // So an output that is not finite is summed again from the token's own
+                // experts, unless its routing is NaN already.
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const bool odd = n * 8 + t8 < p.T && !(fabsf(v[n]) < INFINITY);
+                    for (uint32_t todo = __ballot_sync(0xffffffffu, odd); todo != 0u; todo &= todo - 1u) {
+                        const int src = __ffs(todo) - 1, at = fin * 32 + src;
+                        const float whole = few_output<DT>(p, sm, n_act, n * 8 + (at >> 4), (tile - n1) * 16 + (at & 15), lane);
+                        if (lane == src) v[n] = whole;
+                    }
+                }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const int t = n * 8 + t8;

@@ -1,5 +1,5 @@
-"""moe_forward_few on activations that the 16-bit types barely hold, and past
-their range."""
+"""moe_forward_few on weights with infinities and NaN, on activations that the
+16-bit types barely hold, and past their range."""
 import pytest
 import torch
 
@@ -9,10 +9,11 @@ from test_gpu_few import DT, ULP, call, definition, make
 
 pytestmark = pytest.mark.gpu
 
+NAN, INF = float("nan"), float("inf")
 HALF_STEP = {"f16": 2.0 ** -25, "bf16": 0.0}  # half the distance of the smallest outputs
 
 
-def check(s, k, dtype, got, err):
+def check(s, k, dtype, got, err, pick=None):
     """As the layer's own tests, without their flat 1e-7."""
     torch.cuda.synchronize()
     assert int(err.item()) == 0
@@ -20,7 +21,46 @@ def check(s, k, dtype, got, err):
     want, off = definition(s, idx, w)
     bound = ULP[dtype] * want.abs() + off + HALF_STEP[dtype]
     bad = ~((got.double() - want).abs() <= bound)
+    if pick is not None:
+        bad &= pick
     assert not bad.any(), (int(bad.sum()), float(((got.double() - want).abs() / bound)[bad].max()))
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("T,d_h,d_e,E,k", [(3, 512, 192, 8, 2), (8, 768, 576, 12, 3), (16, 512, 128, 20, 4), (5, 1024, 2048, 6, 1)])
+def test_bad_weights_reach_the_tokens_routed_to_them(T, d_h, d_e, E, k, dtype):
+    require_cuda()
+    s = make(T, d_h, d_e, E, k, dtype, seed=21)
+    idx, _ = binding.moe_gate_topk(s["x"], s["w_g"], None, k)
+    ref, err = call(s, k)
+    check(s, k, dtype, ref, err)
+    counts = torch.bincount(idx.flatten().long(), minlength=E).tolist()
+    e = next(i for i, n in enumerate(counts) if 0 < n < T)
+    routed = (idx == e).any(1)
+    rows = (0, 17, d_h - 1)
+    for value in (INF, -INF, NAN):
+        t = {**s, "w_down": s["w_down"].clone()}
+        for row, col in zip(rows, (0, 65, d_e - 1)):
+            t["w_down"][e, row, col] = value
+        got, err = call(t, k)
+        torch.cuda.synchronize()
+        assert int(err.item()) == 0
+        hit = torch.zeros_like(ref, dtype=torch.bool)
+        hit[:, list(rows)] = True
+        assert torch.equal(got[~hit], ref[~hit])
+        assert not bool(got[hit & routed[:, None]].isfinite().any())
+        # the others' sums over their own experts, the definition's
+        check(s, k, dtype, got, err, pick=hit & ~routed[:, None])
+        for name in ("w_gate", "w_up"):
+            t = {**s, name: s[name].clone()}
+            t[name][e, 3, 9] = value
+            got, err = call(t, k)
+            torch.cuda.synchronize()
+            assert int(err.item()) == 0
+            assert torch.equal(got[~routed], ref[~routed])
+            assert not bool(got[routed].isfinite().all(1).any())
+        again, _ = call(t, k)
+        assert torch.equal(again.nan_to_num(7.0), got.nan_to_num(7.0))
 
 
 @pytest.mark.parametrize("dtype", ["f16", "bf16"])
