@@ -502,7 +502,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
             w_next.load(w, H);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) s = fmaf(d_u.times(w, i), out.get(i), s);
-            const float back = -(sums.one(s) * (r * r * r * per));
+            const float back = -(sums.one(s) * r * per) * r;  // r^3 alone leaves fp32 at an rms of 1e13
             ring.refill();
             read = true;
             d_u.again();
@@ -510,7 +510,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
             out.again();
 #pragma unroll
             for (int i = 0; i < EPT; ++i) {
-                d[i] = fmaf(out.get(i), back, fmaf(r, d_u.times(w, i), d_out.get(i)));
+                d[i] = fmaf(r, fmaf(out.get(i), back, d_u.times(w, i)), d_out.get(i));
                 sum_next[i] = fmaf(r, d_u.times(out, i), sum_next[i]);
             }
         } else {
@@ -555,10 +555,10 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
                 read = true;
                 if (TOKEN && p.d_gate && threadIdx.x == 0) static_cast<float *>(p.d_gate)[t] = row.y;
                 if (post) {
-                    const float back = -(row.x * (r2 * r2 * r2 * per));
+                    const float back = -(row.x * r2 * per) * r2;
                     y.again();
 #pragma unroll
-                    for (int i = 0; i < EPT; ++i) d[i] = fmaf(y.get(i), back, r2 * d[i]);
+                    for (int i = 0; i < EPT; ++i) d[i] = r2 * fmaf(y.get(i), back, d[i]);
                 }
             }
             P::store(static_cast<T *>(p.d_y) + base, H, d);

@@ -1,5 +1,6 @@
-"""The norms at their edges: rows of less than 16 bytes.  The references and
-their tolerances are those of the norms' own tests."""
+"""The norms at their edges: rows of less than 16 bytes, rows whose size
+lies far from one.  The references and their tolerances are those of the norms'
+own tests."""
 import pytest
 import torch
 
@@ -47,3 +48,25 @@ def test_rows_of_a_few_bytes(dtype, gate):
         assert set(back) == set(want)
         for k in want:
             check(back[k], want[k], mag[k], f"{k} {T} {H}")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e15, 1e-15])
+@pytest.mark.parametrize("post,nxt", [(True, False), (False, True), (True, True)])
+def test_gradients_of_very_large_and_very_small_rows(post, nxt, scale, dtype):
+    """eps = 0; no step on the way may hold rstd^3, 1e45 or 1e-45 here."""
+    require_cuda()
+    for T, H in ((9, 200), (5, 2047), (3, 7168)):
+        for gate in ("channel", "token", "full", "none"):
+            s = make(T, H, dtype, post, nxt, gate, seed=1)
+            s["y"], s["res"] = s["y"] * scale, s["res"] * scale
+            got = binding.moe_residual_norm(s["y"], s["res"], s["w_post"], s["gate"], ALPHA, s["w_next"], 0.0)
+            check_forward(got, forward64(s, eps=0.0), s["w_next"], 0.0)
+            g = torch.Generator(device="cuda").manual_seed(T)
+            d_out = (torch.randn((T, H), generator=g, device="cuda") / scale).to(DT[dtype])
+            d_u = torch.randn((T, H), generator=g, device="cuda").to(DT[dtype]) if nxt else None
+            back = binding.moe_residual_norm_backward(d_out, d_u, s["y"], got["out"], s["w_post"], s["gate"], ALPHA, s["w_next"],
+                                                      got.get("rstd_post"), got.get("rstd_next"))
+            want, mag = backward64(s, d_out, d_u, got["out"], got.get("rstd_post"), got.get("rstd_next"))
+            for k in want:
+                check(back[k], want[k], mag[k], f"{k} {T} {H} {gate}")
