@@ -627,7 +627,7 @@ NormShape norm_shape(NormParams &p, int elem, bool backward) {
     while (per_sm > 1 && fit(per_sm) < p.tensors) --per_sm;
     const int64_t all = static_cast<int64_t>(device_sm_count()) * per_sm;
     s.ctas = static_cast<int>(p.T < all ? p.T : all);
-    const int64_t rows = s.ctas > 0 ? (p.T + s.ctas - 1) / s.ctas : 0;
+    const int64_t rows = (p.T + s.ctas - 1) / s.ctas;
     int64_t slots = fit(per_sm);
     if (slots > NORM_MAX_SLOTS) slots = NORM_MAX_SLOTS;
     if (slots < p.tensors) {
@@ -706,13 +706,15 @@ template <typename T> cudaError_t launch_shape(const NormParams &p, const NormSh
 }
 
 template <typename T> cudaError_t launch_typed(NormParams p, bool backward, cudaStream_t stream) {
-    const NormShape s = norm_shape(p, sizeof(T), backward);
+    int ctas = 0;  // no rows: no tensors to shape a ring for, and column sums of zero
     if (p.T > 0) {
+        const NormShape s = norm_shape(p, sizeof(T), backward);
         const cudaError_t e = launch_shape<T>(p, s, backward, stream);
         if (e != cudaSuccess) return e;
+        ctas = s.ctas;
     }
     if (!backward || (!p.d_w_next && !p.d_w_post && !(p.d_gate && p.gate_kind == 1))) return cudaSuccess;
-    return launch_pdl(norm_columns_kernel, dim3(static_cast<unsigned>((p.H + 31) / 32), 3), dim3(256), 0, stream, p, s.ctas);
+    return launch_pdl(norm_columns_kernel, dim3(static_cast<unsigned>((p.H + 31) / 32), 3), dim3(256), 0, stream, p, ctas);
 }
 
 }  // namespace

@@ -1,6 +1,6 @@
-"""The norms at their edges: rows of less than 16 bytes, rows whose size
-lies far from one.  The references and their tolerances are those of the norms'
-own tests."""
+"""The norms at their edges: rows of less than 16 bytes, no rows at all, rows
+whose size lies far from one.  The references and their tolerances are those of
+the norms' own tests."""
 import pytest
 import torch
 
@@ -70,3 +70,20 @@ def test_gradients_of_very_large_and_very_small_rows(post, nxt, scale, dtype):
             want, mag = backward64(s, d_out, d_u, got["out"], got.get("rstd_post"), got.get("rstd_next"))
             for k in want:
                 check(back[k], want[k], mag[k], f"{k} {T} {H} {gate}")
+
+
+@pytest.mark.parametrize("post,nxt,gate", [(True, False, "none"), (True, False, "channel"), (False, False, "token"), (False, True, "full")])
+def test_no_rows(post, nxt, gate):
+    require_cuda()
+    H = 48
+    s = make(0, H, "bf16", post, nxt, gate)
+    none, stat = s["res"], torch.empty(0, device="cuda")
+    got = binding.moe_residual_norm(s["y"], none, s["w_post"], s["gate"], ALPHA, s["w_next"], EPS)
+    assert got["out"].shape == (0, H)
+    back = binding.moe_residual_norm_backward(none, none if nxt else None, s["y"], none, s["w_post"], s["gate"], ALPHA, s["w_next"],
+                                              stat if post else None, stat if nxt else None)
+    for k in ("d_w_post", "d_w_next"):
+        if k in back:
+            assert torch.equal(back[k], torch.zeros(H, device="cuda")), k
+    if gate == "channel":
+        assert torch.equal(back["d_gate"], torch.zeros(H, device="cuda"))
