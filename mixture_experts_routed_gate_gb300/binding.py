@@ -791,10 +791,10 @@ def _gate_kind(gate, T, H, dtype):
     shape = tuple(gate.shape)
     if shape == (H,):
         return GATE_CHANNEL
-    if shape == (T, H):
-        return GATE_FULL
     if shape == (T, 1):
         return GATE_TOKEN
+    if shape == (T, H):
+        return GATE_FULL
     raise ValueError(f"gate must be [{H}], [{T}, 1] or [{T}, {H}], got {list(shape)}")
 
 

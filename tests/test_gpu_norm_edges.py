@@ -72,6 +72,18 @@ def test_gradients_of_very_large_and_very_small_rows(post, nxt, scale, dtype):
                 check(back[k], want[k], mag[k], f"{k} {T} {H} {gate}")
 
 
+def test_gradient_of_a_gate_per_token_at_width_one():
+    """[T, 1] is a gate per token at any width: its gradient is fp32."""
+    require_cuda()
+    s = make(7, 1, "bf16", True, False, "token")
+    got = binding.moe_residual_norm(s["y"], s["res"], s["w_post"], s["gate"], ALPHA, None, EPS)
+    d_out = torch.randn((7, 1), device="cuda").bfloat16()
+    back = binding.moe_residual_norm_backward(d_out, None, s["y"], got["out"], s["w_post"], s["gate"], ALPHA, None, got["rstd_post"])
+    want, mag = backward64(s, d_out, None, got["out"], got["rstd_post"], None)
+    assert back["d_gate"].dtype is torch.float32
+    check(back["d_gate"], want["d_gate"], mag["d_gate"], "d_gate")
+
+
 @pytest.mark.parametrize("post,nxt,gate", [(True, False, "none"), (True, False, "channel"), (False, False, "token"), (False, True, "full")])
 def test_no_rows(post, nxt, gate):
     require_cuda()
