@@ -230,6 +230,7 @@ struct RowAsk {
 struct RowState {
     uint64_t bars[NORM_MAX_BARS];
     RowAsk ask;
+    int lost;  // a wait gave up
 };
 
 template <Rows MODE> struct RowRing;
@@ -240,10 +241,8 @@ template <> struct RowRing<Rows::kMemory> {
     __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *, RowState &, int elem)
         : p(p), row(blockIdx.x), row_bytes(static_cast<int64_t>(p.H) * elem) {}
     __device__ __forceinline__ void start() {}
-    __device__ __forceinline__ bool next() {
-        tensor = 0;
-        return true;
-    }
+    __device__ __forceinline__ void next() { tensor = 0; }
+    template <typename T> __device__ __forceinline__ void finish(bool) {}
     int tensor = 0;
     __device__ __forceinline__ const void *take() { return static_cast<const uint8_t *>(p.ring[tensor++]) + row * row_bytes; }
     __device__ __forceinline__ void refill() {}
@@ -260,15 +259,16 @@ template <Rows MODE> struct RowRing {
     uint8_t *smem;
     uint32_t bars;
     int64_t row_bytes, row;
-    RowAsk &next_ask;
+    RowState &state;
     uint32_t slot = 0;  // of the next tensor, in bytes
     int bar = -1;       // the row's
     uint32_t phase = 0;
     __device__ __forceinline__ RowRing(const NormParams &p, uint8_t *smem, RowState &state, int elem)
         : p(p), smem(smem), bars(smem_u32(state.bars)), row_bytes(static_cast<int64_t>(p.H) * elem), row(blockIdx.x),
-          next_ask(state.ask) {
+          state(state) {
         if (threadIdx.x == 0) {
-            next_ask = RowAsk{blockIdx.x * row_bytes, 0, smem_u32(smem), bars};
+            state.ask = RowAsk{blockIdx.x * row_bytes, 0, smem_u32(smem), bars};
+            state.lost = 0;
             for (int i = 0; i < p.bars; ++i) mbar_init(bars + 8u * i, 1);
             fence_mbar_init();
         }
@@ -276,7 +276,7 @@ template <Rows MODE> struct RowRing {
     }
     __device__ __forceinline__ void ask(int copies) {
         const int64_t total = p.T * row_bytes;
-        RowAsk a = next_ask;
+        RowAsk a = state.ask;
         for (int i = 0; i < copies && a.from < total; ++i) {
             int64_t from = a.from;
             uint32_t bytes = static_cast<uint32_t>(row_bytes);
@@ -300,27 +300,56 @@ template <Rows MODE> struct RowRing {
                 if (a.bar == bars + 8u * p.bars) a.bar = bars;
             }
         }
-        next_ask = a;
+        state.ask = a;
     }
+    __device__ __forceinline__ bool lost() const { return *static_cast<volatile int *>(&state.lost) != 0; }
     __device__ __forceinline__ void start() {
         if (threadIdx.x == 0) ask(p.slots);
     }
-    // This CTA's own copies, asked for before: bounded, and without an error
-    // word to report to a row that never came would be left as it is.
-    __device__ __forceinline__ bool wait() {
+    // For this CTA's own copies, asked for before; bounded all the same.  There is
+    // no error word to report to: once a wait gives up, nothing more is asked for,
+    // the CTA runs on with what its slots hold, and ends in finish().
+    __device__ __forceinline__ void wait() {
         for (int i = 0; i < 64; ++i)  // before the slow read of the timer
-            if (mbar_try_wait(bars + 8u * bar, phase & 1u)) return true;
+            if (mbar_try_wait(bars + 8u * bar, phase & 1u) || lost()) return;
         const unsigned long long begin = global_timer_ns();
-        while (!mbar_try_wait(bars + 8u * bar, phase & 1u))
-            if (global_timer_ns() - begin > kWaitTimeoutNs) return false;
-        return true;
+        while (!mbar_try_wait(bars + 8u * bar, phase & 1u) && !lost())
+            if (global_timer_ns() - begin > kWaitTimeoutNs) *static_cast<volatile int *>(&state.lost) = 1;
     }
-    __device__ __forceinline__ bool next() {
+    // After the last row.  If a row was lost: NaN for all of the CTA's rows and its
+    // column sums, and the copies still on their way land before shared memory
+    // goes (2 s in all).
+    template <typename T> __device__ __forceinline__ void finish(bool backward) {
+        __syncthreads();
+        if (!lost()) return;
+        T *const wide[] = {static_cast<T *>(backward ? p.d_res : p.out), static_cast<T *>(backward ? p.d_y : p.u),
+                           static_cast<T *>(p.gate_kind == 3 ? p.d_gate : nullptr)};
+        float *const narrow[] = {p.rstd_post, p.rstd_next, static_cast<float *>(p.gate_kind == 2 ? p.d_gate : nullptr)};
+#pragma unroll 1
+        for (int i = 0; i < 3; ++i) {
+#pragma unroll 1
+            for (int64_t t = blockIdx.x; t < p.T; t += gridDim.x) {
+#pragma unroll 1
+                for (int h = threadIdx.x; wide[i] && h < p.H; h += blockDim.x) wide[i][t * p.H + h] = from_f32<T>(NAN);
+                if (narrow[i] && threadIdx.x == 0) narrow[i][t] = NAN;
+            }
+        }
+#pragma unroll 1
+        for (int h = threadIdx.x; backward && h < 3 * p.H; h += blockDim.x)
+            p.partial[static_cast<int64_t>(blockIdx.x) * 3 * p.H + h] = NAN;
+        const int asked = static_cast<int>((state.ask.from / row_bytes - blockIdx.x) / gridDim.x) + (state.ask.tensor != 0);
+        const unsigned long long begin = global_timer_ns();
+#pragma unroll 1
+        for (int k = max(0, asked - p.bars); k < asked && threadIdx.x == 0; ++k)
+            while (!mbar_try_wait(bars + 8u * (k % p.bars), (k / p.bars) & 1))
+                if (global_timer_ns() - begin > kWaitTimeoutNs) return;
+    }
+    __device__ __forceinline__ void next() {
         if (++bar == p.bars) {
             bar = 0;
             phase ^= 1u;
         }
-        if (!wait()) return false;
+        wait();
         if constexpr (MODE == Rows::kOdd) {
             // rows of less than 16 bytes: several may reach past the last whole 16
             const int64_t whole = p.T * row_bytes / 16 * 16;
@@ -337,7 +366,6 @@ template <Rows MODE> struct RowRing {
                 __syncthreads();
             }
         }
-        return true;
     }
     // the row's tensors in their order
     __device__ __forceinline__ uint8_t *take() {
@@ -347,7 +375,7 @@ template <Rows MODE> struct RowRing {
         return MODE == Rows::kOdd ? at + (row * row_bytes & 15) : at;
     }
     __device__ __forceinline__ void refill() {
-        if (threadIdx.x == 0) ask(p.tensors);
+        if (threadIdx.x == 0 && !lost()) ask(p.tensors);
     }
 };
 
@@ -395,7 +423,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
     const Kept<P, MODE> gate_row(p.gate_kind == 1 ? p.gate : nullptr, room, H);
     for (; ring.row < p.T; ring.row += gridDim.x) {
         const int64_t t = ring.row, base = t * H;
-        if (!ring.next()) return;
+        ring.next();
         float scale = p.alpha;
         if (p.gate_kind == 2) scale *= to_f32(static_cast<const T *>(p.gate)[t]);
         P res, y, gate;
@@ -451,6 +479,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
             ring.refill();
         }
     }
+    ring.template finish<T>(false);
 }
 
 // The instructions of a row take longer than its bytes, so what a call has or
@@ -482,7 +511,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
     for (int i = 0; i < EPT; ++i) sum_next[i] = sum_post[i] = sum_gate[i] = 0.0f;
     for (; ring.row < p.T; ring.row += gridDim.x) {
         const int64_t t = ring.row, base = t * H;
-        if (!ring.next()) return;
+        ring.next();
         bool read = false;  // every thread has read the row's slots
         float d[EPT];
         P d_out, d_u, out, y, gate, w;
@@ -572,6 +601,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_backward_kernel(co
     if (p.d_w_next) P::store_sums(part, H, sum_next);
     if (p.d_w_post) P::store_sums(part + H, H, sum_post);
     if (p.gate_kind == 1 && p.d_gate) P::store_sums(part + 2 * H, H, sum_gate);
+    ring.template finish<T>(true);
 }
 
 // The CTAs' column sums added: 32 columns a CTA, 8 threads a column each with
