@@ -636,19 +636,27 @@ struct NormShape {
     size_t smem;
 };
 
+// Backward: 8 elements a thread as long as the registers allow (72 at 896
+// threads); narrow rows: several CTAs an SM (fewer than in the forward pass, as
+// it holds more registers).
+int norm_threads(int64_t H, int ept) { return static_cast<int>(((H + ept - 1) / ept + 31) / 32 * 32); }
+int backward_ept(int64_t H) { return H <= 7168 ? 8 : 16; }
+int backward_per_sm(int64_t H) {
+    const int n = backward_ept(H) == 16 ? 1 : 896 / norm_threads(H, 8);
+    return n < 1 ? 1 : n > 16 ? 16 : n;
+}
+
 NormShape norm_shape(NormParams &p, int elem, bool backward) {
     NormShape s{};
     const int64_t row_bytes = static_cast<int64_t>(p.H) * elem, padded = (row_bytes + 15) / 16 * 16;
     // Forward, 16-bit types: 16 elements a thread above 4096, for two CTAs an
     // SM (4096 x 7168 bf16 with its graph's overhead 46 us, one CTA of 8 elements
     // a thread 62); fp32 rows that wide leave two CTAs no room for a ring (81 us
-    // with one CTA, 145 with two).  Backward: 8 as long as the registers allow
-    // (72 at 896 threads).
-    s.ept = p.H <= (backward ? 7168 : elem == 4 ? 8192 : 4096) ? 8 : 16;
-    s.threads = ((p.H + s.ept - 1) / s.ept + 31) / 32 * 32;
-    // narrow rows: several CTAs an SM (the backward pass holds more registers)
-    int per_sm = (backward ? 896 : 1024) / s.threads;
-    per_sm = per_sm < 1 || (backward && s.ept == 16) ? 1 : per_sm > 16 ? 16 : per_sm;
+    // with one CTA, 145 with two).
+    s.ept = backward ? backward_ept(p.H) : p.H <= (elem == 4 ? 8192 : 4096) ? 8 : 16;
+    s.threads = norm_threads(p.H, s.ept);
+    int per_sm = 1024 / s.threads;
+    per_sm = backward ? backward_per_sm(p.H) : per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
     const int64_t kept = ((p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0)) *
                          static_cast<int64_t>(s.ept) * s.threads * elem;
     const bool odd = row_bytes % 16 != 0;
@@ -776,8 +784,8 @@ cudaError_t launch_residual_norm(const void *y, const void *res, const void *w_p
 }
 
 size_t residual_norm_backward_ws_bytes(int64_t T, int64_t H) {
-    // three rows of column sums for each CTA of the largest grid
-    const int64_t ctas = static_cast<int64_t>(device_sm_count()) * 16;
+    // three rows of column sums for each CTA of the largest grid at this width
+    const int64_t ctas = static_cast<int64_t>(device_sm_count()) * backward_per_sm(H);
     return static_cast<size_t>((T < ctas ? T : ctas) * 3 * H * 4 + 16);
 }
 
