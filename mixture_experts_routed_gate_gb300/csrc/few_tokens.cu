@@ -471,7 +471,11 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
             sm.queue[slot] = tile;
             mbar_arrive(tqf_bar(slot));
             if (tile >= total) break;
-            next = atomicAdd(p.counters, 1);  // its latency passes under this tile
+            // Claimed before the copies of a short stage-1 tile, under which the
+            // latency passes; after those of a stage-2 tile, which are a CTA's
+            // last 5 to 20 us: claimed ahead, some CTAs held two while others had
+            // none (8 x 2048 fp16 then took 68 or 89 us, by chance).
+            if (tile < n1) next = atomicAdd(p.counters, 1);
             if (++slot == FEW_QUEUE) {
                 slot = 0;
                 qphase ^= 1u;
@@ -486,6 +490,7 @@ __global__ void __launch_bounds__(FEW_THREADS, 1)
                 }
             }
             for (int i = pad_steps(tile); i > 0 && ok; --i) ok = pad();
+            if (tile >= n1) next = atomicAdd(p.counters, 1);
         }
         if (*abort_flag) few_drain(bar0, stages, stage, phase);
         return;
