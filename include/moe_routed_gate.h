@@ -86,7 +86,8 @@ MOE_API size_t moe_forward_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, 
  *   fixed: lane L = (j/8) mod 32 accumulates its 8-element chunks in ascending
  *   j with fmaf, then the 32 partials are combined by the xor butterfly
  *   s = 16, 8, 4, 2, 1; this makes the routing reproducible bit for bit.
- *   topk_idx[t, 0..k-1]: the k largest logits, descending, ties to the lower id.
+ *   topk_idx[t, 0..k-1]: the k largest logits, descending, ties to the lower id; a
+ *   NaN counts as the largest, so k distinct ids are written whatever the logits.
  *   topk_w[t, j] = softmax over all E logits at topk_idx[t, j] (no renormalisation).
  * x [T, d_h] and w_g [E, d_h] in `dtype` (f16 or bf16); bias [E] fp32 or NULL.
  * Requires d_h % 256 == 0, 1 <= k <= min(E, 32), E <= 1024.
@@ -481,8 +482,10 @@ MOE_API int64_t moe_forward_workspace_offset(int64_t T, int64_t d_h, int64_t d_e
  * MOE_GATE_TOKEN [T], MOE_GATE_FULL [T, H].  rstd_post, rstd_next: fp32 [T] or
  * NULL; a backward pass needs them.
  * y, res, out, u [T, H] and the weights and gate in `dtype` (f16, bf16, f32);
- * 1 <= H <= 16384, any T >= 0, eps >= 0.  `out` may be the same buffer as
- * `res`; no other output may overlap an input.
+ * 1 <= H <= 16384, any T >= 0, eps >= 0.  The sum of a row's squares is an fp32
+ * number: a row longer than 1.8e19 (its Euclidean norm) has rstd 0, and squares
+ * of elements below 1e-19 lose bits.  `out` may be the same buffer as `res`; no
+ * other output may overlap an input.
  */
 typedef enum { MOE_GATE_NONE = 0, MOE_GATE_CHANNEL = 1, MOE_GATE_TOKEN = 2, MOE_GATE_FULL = 3 } moe_gate_t;
 MOE_API moe_status_t moe_residual_norm(const void *y, const void *res, const void *w_post, const void *gate,

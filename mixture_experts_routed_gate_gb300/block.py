@@ -20,9 +20,10 @@ import torch
 from . import binding
 
 # Up to here moe_forward_few is the faster one at both layer sizes measured
-# (T = 8: 67 against 77 us at 2048 / 768, 64 experts, top-6, fp16, and 716
-# against 765 us at 7168 / 2048, 256 experts, top-8, bf16; at T = 12 it is 93
-# against 87 and 956 against 1022 us).
+# (T = 8: 68 against 78 us at 2048 / 768, 64 experts, top-6, fp16, and 726
+# against 778 us at 7168 / 2048, 256 experts, top-8, bf16; at T = 12 it is 91
+# against 87 and 956 against 1022 us).  4-bit experts take moe_forward_mx4 at any
+# T: at T = 8 48 and 263 us, at T = 1 34 (16-bit experts: 27) and 81 (122).
 FEW_TOKENS = 8
 
 

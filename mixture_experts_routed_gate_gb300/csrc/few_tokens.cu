@@ -34,13 +34,15 @@
 // CTAs hold: the launch completes whether or not all CTAs are resident.
 //
 // Bound by the weights' bytes once there are many: 2 tokens at 7168 / 2048, 256
-// experts, top-8, bf16: 1.39 GB in 199 us, 7.0 TB/s (a copy runs at 6.8); 8 at
-// 2048 / 768, 64 experts, top-6, fp16: 331 MB in 63 us, 5.2 TB/s, a CTA's few
-// tiles being too short to hide their ends.  One token there (57 MB, 8.4 us at
-// the copy rate) takes 23 us: two launches, the routing (about 2 us), the first
-// loads' latency and h on its way from CTA to CTA.  When the first two of these
-// took 210 and 72 us, stages of 256 columns took 343 and 117, of 1024 columns 206
-// and 74, and three groups of multiplying warps 212 and 79.
+// experts, top-8, bf16: 1.39 GB in 198 us, 7.0 TB/s (a copy runs at 6.8); 8 at
+// 2048 / 768, 64 experts, top-6, fp16: 331 MB in 67 us, 4.9 TB/s.  There stage 2
+// is 128 tiles, each 16 rows of all 35 or so chosen experts (860 KB, about 19 us
+// at a CTA's share of the memory), so 24 CTAs are idle for the last quarter.
+// One token there (57 MB, 8.4 us at the copy rate) takes 20 us: two launches, the
+// routing (about 2 us), the first loads' latency and h on its way from CTA to
+// CTA.  When the first two of these took 210 and 72 us, stages of 256 columns
+// took 343 and 117, of 1024 columns 206 and 74, and three groups of multiplying
+// warps 212 and 79.
 #include "common.cuh"
 #include "internal.h"
 

@@ -5,11 +5,12 @@
 //
 // A thread quantises whole blocks of 32, so the scale is worked out once for
 // them and no lane asks another.  32,768 rows of 7168 bf16 that 4096 tokens
-// repeat: 68 us, 125 MB written; with two lanes a block 77, with four
+// repeat: 61 to 68 us, 125 MB written, bound by L1 (86% of its rate: a warp's loads
+// are 64 bytes apart); when it took 68, two lanes a block took 77, four
 // 100 (the loads are then contiguous over the warp, but the scale and the lanes'
 // maximum are most of the instructions); CTAs of 64 threads 68, of 256 80.  One
 // CTA a token that looks up its rows was no faster at four lanes a block (90 to
-// 104): the search eats what it saves.  4096 x 7168 to bits and back in 27 us, 22
+// 104): the search eats what it saves.  4096 x 7168 to bits and back in 28 us, 22
 // at the copy rate.
 #include "common.cuh"
 #include "internal.h"

@@ -17,12 +17,15 @@
 //   warp 1      one elected lane: four K = 64 MMAs a slice;
 //   warps 2-9   epilogue, from one of two accumulators while the other fills.
 //
-// 32,768 rows, 64 experts, 7168 x 2048, bf16 out: 429 us, 2.2 PFLOP/s.  Shared
-// memory bounds it: a 128 x 192 slice brings 40 KB in and the tensor cores read
-// them once, 640 of its about 950 cycles at 128 bytes each, against 340 for
-// its MMAs alone; the rest is the hand-over between the roles.  192 columns take
-// the tensor memory that two accumulators and the stages' scales leave; 128
-// columns 690 us, 256 with a single accumulator 462.
+// 32,768 rows, 256 experts, 7168 x 2048, bf16 out: 423 us, 2.3 PFLOP/s (323 us
+// for its bytes).  Shared memory bounds a full tile: a 128 x 192 slice brings 40 KB
+// in and the tensor cores read them once, 640 of its about 950 cycles at 128
+// bytes each, against 340 for its MMAs alone; the rest is the hand-over between
+// the roles.  And blocks are not full: 256 groups make 409 blocks of 128, 60%
+// more rows than there are, each reading all of its expert's weights.  192
+// columns take the tensor memory that two accumulators and the stages' scales
+// leave; when that took 452 us, 128 columns took 690, 256 with a single
+// accumulator 462.  The gate/up form, twice the columns: 869 us.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"

@@ -22,11 +22,12 @@
 //
 // 4096 x 7168 bf16: forward 39 us (235 MB at 6.0 TB/s, against 35 at this
 // card's copy rate; 67% of the issue slots), gradients 88 us (52 at the copy
-// rate: there the instructions bound, about 500 a warp and row).  fp32: 81 to 87 and
-// 138 us of 69 and 104; two rows' slots do not fit, so the slots are single
-// tensors', a part of a row ahead if need be (147 and 315 us with such rows read
-// from memory).  Rows of 7167 bf16, by elements: 72 and 161 us (from memory 154
-// and 465).
+// rate; 57% of the issue slots at about 500 instructions a warp and row, and the
+// largest stall, 2.8 warps an issue, is on the row's statistics and gate, read
+// from memory in the row they serve).  fp32: 81 and 131 us of 69 and 104; two
+// rows' slots do not fit, so the slots are single tensors', a part of a row
+// ahead if need be (147 and 315 us with such rows read from memory).  Rows of
+// 7167 bf16, by elements: 68 and 150 us (from memory 154 and 465).
 #include "common.cuh"
 #include "internal.h"
 
