@@ -49,7 +49,8 @@ extern "C" {
 
 typedef struct CUstream_st *moe_stream_t; /* identical to cudaStream_t */
 
-/* MOE_E4M3 (float8 e4m3fn) is an output type of moe_reduce_fused_scaled only. */
+/* MOE_E4M3 (float8 e4m3fn) is an output type of moe_reduce_fused_scaled only (mx8 elements, which have their
+ * scales beside them, are uint8_t). */
 typedef enum { MOE_F16 = 0, MOE_BF16 = 1, MOE_F32 = 2, MOE_E4M3 = 3 } moe_dtype_t;
 
 typedef enum {
@@ -604,6 +605,105 @@ MOE_API moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float
                                      const uint8_t *q_down, const uint8_t *sf_down, int64_t T, int64_t d_h,
                                      int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype, void *ws,
                                      size_t ws_bytes, void *out, int32_t *err_flag, moe_stream_t stream);
+
+/*
+ * Microscaled 8-bit floating point ("mx8"): as mx4 with 8-bit e4m3 elements
+ * (float8 e4m3fn: magnitudes up to 448).  A matrix [R, K], K % 32 == 0, is
+ * q [R, K] and sf [R, K/32]; the scale 2^(s - 127) is the least power of two
+ * (s >= 0) that brings the largest magnitude of the 32 to 448 or less, so
+ * nothing saturates; elements are rounded to nearest even.  A block that holds
+ * a NaN or an infinity gets s = 255 (NaN) and elements of zero.
+ *
+ * moe_residual_norm_mx8: moe_residual_norm with u in 8 bits, quantised from its
+ * unrounded fp32 values: q [T, H], sf [T, H/32].  u may be NULL (the 8-bit form
+ * alone) or given (a gate needs it).  w_next is required and H % 32 == 0; the
+ * rest, the gradients included (moe_residual_norm_backward), as there.
+ *
+ * moe_quantize_mx8: rows of x [n_rows, K] in f16, bf16 or f32.
+ * moe_dequantize_mx8: the values, rounded to `dtype`.
+ *
+ * moe_sort_rows_mx8: for every token t and slot j < k, row
+ * token_topk_to_pos[t, j] of q_out, sf_out = row t of q, sf [T, K]: what
+ * moe_gather_rows_by_token is for 16-bit rows.  A position outside [0, n_rows)
+ * is skipped, rows that no position names are left as they were; every other
+ * position stands at one place only.  1 <= k <= 32.
+ *
+ * moe_grouped_gemm_mx8: C[r, :] = A_r B[g]^T for the rows r of expert g over the
+ * dispatch tables, as moe_grouped_gemm_mx4 with 8-bit operands: q_a, sf_a
+ * [n_rows, K], q_b, sf_b [E, N, K], sums in fp32, C [n_rows, N] rounded once to
+ * `out_dtype` (f16, bf16, f32).  N >= 1, K % 32 == 0.
+ * moe_grouped_gate_up_silu_mx8: h = silu(A W_gate^T) * (A W_up^T) from the fp32
+ * sums, quantised as moe_quantize_mx8 would its fp32 values: q_h, sf_h
+ * [n_rows, d_e].  d_h % 32 == 0, d_e % 32 == 0.
+ * q_* 16-byte aligned.
+ */
+MOE_API moe_status_t moe_residual_norm_mx8(const void *y, const void *res, const void *w_post, const void *gate,
+                                           moe_gate_t gate_kind, float alpha, const void *w_next, float eps,
+                                           int64_t T, int64_t H, moe_dtype_t dtype, void *out, void *u, uint8_t *q,
+                                           uint8_t *sf, float *rstd_post, float *rstd_next, moe_stream_t stream);
+MOE_API moe_status_t moe_quantize_mx8(const void *x, int64_t n_rows, int64_t K, moe_dtype_t dtype, uint8_t *q,
+                                      uint8_t *sf, moe_stream_t stream);
+MOE_API moe_status_t moe_dequantize_mx8(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K,
+                                        moe_dtype_t dtype, void *out, moe_stream_t stream);
+MOE_API moe_status_t moe_sort_rows_mx8(const uint8_t *q, const uint8_t *sf, const int32_t *token_topk_to_pos, int64_t T,
+                                       int64_t k, int64_t n_rows, int64_t K, uint8_t *q_out, uint8_t *sf_out,
+                                       moe_stream_t stream);
+MOE_API moe_status_t moe_grouped_gemm_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b,
+                                          const uint8_t *sf_b, const int32_t *group_sizes,
+                                          const int32_t *group_offsets, const int32_t *group_padded_offsets,
+                                          const int32_t *group_idx_for_bx, int64_t m_blocks, int64_t n_rows,
+                                          int64_t N, int64_t K, int64_t E, moe_dtype_t out_dtype, void *C,
+                                          int32_t *err_flag, moe_stream_t stream);
+MOE_API moe_status_t moe_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
+                                                  const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                                  const int32_t *group_sizes, const int32_t *group_offsets,
+                                                  const int32_t *group_padded_offsets,
+                                                  const int32_t *group_idx_for_bx, int64_t m_blocks,
+                                                  int64_t n_rows, int64_t d_h, int64_t d_e, int64_t E,
+                                                  uint8_t *q_h, uint8_t *sf_h, int32_t *err_flag,
+                                                  moe_stream_t stream);
+
+/*
+ * moe_forward with mx8 experts and mx8 activations: moe_gate_topk and
+ * moe_build_dispatch on x in `dtype`, moe_sort_rows_mx8 of the tokens' 8-bit rows,
+ * moe_grouped_gate_up_silu_mx8, moe_grouped_gemm_mx8 (down, into `dtype`) and
+ * moe_reduce_fused.  q, sf [T, d_h]: x in 8 bits, as moe_residual_norm_mx8 writes
+ * it beside x; both NULL: quantised from x by this call.  d_h % 256 == 0,
+ * d_e % 64 == 0.  ws: moe_forward_mx8_workspace_bytes(...) bytes, 256-byte
+ * aligned.
+ */
+MOE_API size_t moe_forward_mx8_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
+                                               moe_dtype_t dtype);
+MOE_API moe_status_t moe_forward_mx8(const void *x, const uint8_t *q, const uint8_t *sf, const void *w_g,
+                                     const float *bias, const uint8_t *q_gate, const uint8_t *sf_gate,
+                                     const uint8_t *q_up, const uint8_t *sf_up, const uint8_t *q_down,
+                                     const uint8_t *sf_down, int64_t T, int64_t d_h, int64_t d_e, int64_t E,
+                                     int64_t k, moe_dtype_t dtype, void *ws, size_t ws_bytes, void *out,
+                                     int32_t *err_flag, moe_stream_t stream);
+
+/*
+ * Gradient of moe_reduce_fused.  d_out [T, H]: gradient of its output, in
+ * `out_dtype`; x [n_rows, H] in `in_dtype` (the pairs of types that it takes):
+ *   d_x[r, h]      = (sum of w[t, j] over the j with pos[t, j] = r) * d_out[t, h],
+ *                    t = sorted_token_idx[r]; zeros where there is no such j or
+ *                    t lies outside [0, T)
+ *   d_topk_w[t, j] = sum over h of x[pos[t, j], h] * d_out[t, h]; zero for -1
+ * in fp32, d_x [n_rows, H] rounded once to `in_dtype`, d_topk_w fp32 [T, K].
+ * topk_weights NULL: unit weights.  d_topk_w NULL: not computed, and x, which
+ * nothing else reads, may be NULL.  sorted_token_idx [n_rows] as
+ * moe_build_dispatch writes it; it says which token writes a row, so positions
+ * may stand at several places of a token, and every row of d_x is written once
+ * whatever they hold: the same inputs give the same bits.  A pos < -1 or
+ * >= n_rows counts as -1, a pos that names another token's row reads that row
+ * and gives it no gradient; both set *err_flag = MOE_ERR_DEVICE_FLAG.
+ * H % 256 == 0, 1 <= K <= 32.  (The gradient of moe_gather_rows_by_token is
+ * moe_reduce_fused of the rows' gradients with unit weights.)
+ */
+MOE_API moe_status_t moe_reduce_fused_backward(const void *d_out, const void *x, int64_t n_rows,
+                                               const int32_t *token_topk_to_pos, const float *topk_weights,
+                                               const int32_t *sorted_token_idx, int64_t T, int64_t K, int64_t H,
+                                               moe_dtype_t in_dtype, moe_dtype_t out_dtype, void *d_x,
+                                               float *d_topk_w, int32_t *err_flag, moe_stream_t stream);
 
 #ifdef __cplusplus
 }

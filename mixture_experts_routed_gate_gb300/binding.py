@@ -88,6 +88,15 @@ def lib():
         "moe_grouped_gate_up_silu_mx4": (I, [P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, P, P]),
         "moe_forward_mx4_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
         "moe_forward_mx4": (I, [P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, P, SZ, P, P, P]),
+        "moe_residual_norm_mx8": (I, [P, P, P, P, I, F, P, F, I64, I64, I, P, P, P, P, P, P, P]),
+        "moe_reduce_fused_backward": (I, [P, P, I64, P, P, P, I64, I64, I64, I, I, P, P, P, P]),
+        "moe_quantize_mx8": (I, [P, I64, I64, I, P, P, P]),
+        "moe_dequantize_mx8": (I, [P, P, I64, I64, I, P, P]),
+        "moe_sort_rows_mx8": (I, [P, P, P, I64, I64, I64, I64, P, P, P]),
+        "moe_grouped_gemm_mx8": (I, [P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, P, P, P]),
+        "moe_grouped_gate_up_silu_mx8": (I, [P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, P, P, P, P]),
+        "moe_forward_mx8_workspace_bytes": (SZ, [I64, I64, I64, I64, I64, I]),
+        "moe_forward_mx8": (I, [P, P, P, P, P, P, P, P, P, P, P, I64, I64, I64, I64, I64, I, P, SZ, P, P, P]),
     }
     for name, (res, args) in sigs.items():
         fn = getattr(L, name)
@@ -111,7 +120,9 @@ def exported_symbols():
             "moe_residual_norm", "moe_residual_norm_backward_workspace_bytes", "moe_residual_norm_backward",
             "moe_forward_few_workspace_bytes", "moe_forward_few", "moe_quantize_mx4", "moe_dequantize_mx4",
             "moe_grouped_gemm_mx4", "moe_grouped_gate_up_silu_mx4", "moe_forward_mx4_workspace_bytes",
-            "moe_forward_mx4"]
+            "moe_forward_mx4", "moe_residual_norm_mx8", "moe_reduce_fused_backward", "moe_quantize_mx8",
+            "moe_dequantize_mx8", "moe_sort_rows_mx8", "moe_grouped_gemm_mx8", "moe_grouped_gate_up_silu_mx8",
+            "moe_forward_mx8_workspace_bytes", "moe_forward_mx8"]
 
 
 # --------------------------------------------------------------------------- helpers
@@ -805,7 +816,7 @@ def moe_residual_norm(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next
     u = out / rms(out) * w_next.  Returns a dict with ``out`` (unless y is None),
     ``u`` and ``rstd_next`` (with w_next) and ``rstd_post`` (with w_post).
     gate: [H], [T, 1], [T, H] or None; y None: u is the norm of res.  ``out``
-    may be ``res`` itself."""
+    may be ``res`` itself.  The gradients are :func:`moe_residual_norm_backward`."""
     _cuda(res, "res", ndim=2)
     shape, dt, dev = res.shape, res.dtype, res.device
     T, H = shape
@@ -830,6 +841,42 @@ def moe_residual_norm(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next
         got["rstd_next"] = r_next = torch.empty(T, dtype=torch.float32, device=dev)
     _call("moe_residual_norm", dev, _at(y), _at(res), _at(w_post), _at(gate), kind, alpha, _at(w_next), eps, T, H, code,
           _at(out), _at(u), _at(r_post), _at(r_next))
+    return got
+
+
+def moe_residual_norm_mx8(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next=None, eps: float = 1e-6,
+                          with_u: bool = True, out=None, q=None, sf=None):
+    """:func:`moe_residual_norm` with u in 8 bits: ``q`` float8 e4m3 [T, H] and
+    ``sf`` uint8 [T, H / 32], quantised from the unrounded u as
+    :func:`moe_quantize_mx8` would; ``u`` itself only with ``with_u``.  w_next is
+    needed and H % 32 == 0; everything else as there, the gradients
+    (:func:`moe_residual_norm_backward`, with d_u the gradient of the rows' values) too."""
+    _cuda(res, "res", ndim=2)
+    shape, dt, dev = res.shape, res.dtype, res.device
+    T, H = shape
+    if w_next is None:
+        raise ValueError("w_next is needed")
+    if y is None and (w_post is not None or gate is not None or out is not None):
+        raise ValueError("w_post, gate and out need y")
+    if H == 0 or H % 32 != 0:
+        raise ValueError("H must be a multiple of 32")
+    code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt)
+    got = {}
+    if y is not None:
+        _need(y, "y", dt, shape)
+        got["out"] = out = _want(out, "out", dt, shape, dev)
+    r_post = u = None
+    if w_post is not None:
+        _need(w_post, "w_post", dt, (H,))
+        got["rstd_post"] = r_post = torch.empty(T, dtype=torch.float32, device=dev)
+    _need(w_next, "w_next", dt, (H,))
+    if with_u:
+        got["u"] = u = torch.empty(shape, dtype=dt, device=dev)
+    got["q"] = q = _want(q, "q", torch.float8_e4m3fn, shape, dev)
+    got["sf"] = sf = _want(sf, "sf", torch.uint8, (T, H // 32), dev)
+    got["rstd_next"] = r_next = torch.empty(T, dtype=torch.float32, device=dev)
+    _call("moe_residual_norm_mx8", dev, _at(y), _at(res), _at(w_post), _at(gate), kind, alpha, _at(w_next), eps, T, H, code,
+          _at(out), _at(u), _at(q), _at(sf), _at(r_post), _at(r_next))
     return got
 
 
@@ -1025,6 +1072,166 @@ def moe_forward_mx4(x, w_g, bias, experts: "Mx4Experts", k: int, ws=None, out=No
     out = _want(out, "out", dt, x.shape, dev)
     _call("moe_forward_mx4", dev, _at(x), _at(w_g), _at(bias), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
           _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err))
+    return out
+
+
+# --------------------------------------------------------------------------- the gradient of the combine
+
+def moe_reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_token_idx, err=None):
+    """Gradients of :func:`moe_reduce_fused`: (d_x, d_topk_weights), d_x as x
+    [n_rows, H] and d_topk_weights fp32 [T, K].  d_out: gradient of its output,
+    in the output's dtype.  sorted_token_idx int32 [n_rows] names each row's
+    token, as the dispatch does; rows that no position names get zeros, positions
+    of -1 a zero weight gradient.  The gradient of the way to the experts
+    (:func:`moe_gather_rows_by_token`) is ``moe_reduce_fused(d_rows, token_topk_to_pos)``."""
+    _cuda(x, "x", ndim=2)
+    _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
+    n_rows, H = x.shape
+    T, K = token_topk_to_pos.shape
+    _cuda(d_out, "d_out", ndim=2)
+    _need(d_out, "d_out", d_out.dtype, (T, H))
+    if topk_weights is not None:
+        _need(topk_weights, "topk_weights", torch.float32, (T, K))
+    _need(sorted_token_idx, "sorted_token_idx", torch.int32, (n_rows,))
+    dev = x.device
+    d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
+    d_w = torch.empty((T, K), dtype=torch.float32, device=dev)
+    _call("moe_reduce_fused_backward", dev, _at(d_out), _at(x), n_rows, _at(token_topk_to_pos), _at(topk_weights),
+          _at(sorted_token_idx), T, K, H, _dtype_code(x, "x"), _dtype_code(d_out, "d_out"), _at(d_x), _at(d_w), _err(err))
+    return d_x, d_w
+
+
+# --------------------------------------------------------------------------- microscaled 8-bit floating point
+
+def _mx8(q, sf, name, lead):
+    """q float8 e4m3 [*lead, K], sf uint8 [*lead, K / 32]: returns K."""
+    if isinstance(q, torch.Tensor) and q.dim() == len(lead) + 1 and q.shape[-1] % 32 == 0:
+        K = q.shape[-1]
+        _need(q, f"q{name}", torch.float8_e4m3fn, (*lead, K))
+        _need(sf, f"sf{name}", torch.uint8, (*lead, K // 32))
+        return K
+    _cuda(q, f"q{name}", dtype=torch.float8_e4m3fn, ndim=len(lead) + 1)
+    raise ValueError(f"q{name} must be {(*lead, 'K')} with K % 32 == 0, got {tuple(q.shape)}")
+
+
+def moe_quantize_mx8(x, q=None, sf=None):
+    """Rows of x [R, K] as float8 e4m3 elements q [R, K] with one scale byte per
+    32, sf uint8 [R, K / 32]."""
+    _cuda(x, "x", ndim=2)
+    R, K = x.shape
+    if K == 0 or K % 32 != 0:
+        raise ValueError("K must be a multiple of 32")
+    dev = x.device
+    q = _want(q, "q", torch.float8_e4m3fn, (R, K), dev)
+    sf = _want(sf, "sf", torch.uint8, (R, K // 32), dev)
+    _call("moe_quantize_mx8", dev, _at(x), R, K, _dtype_code(x, "x"), _at(q), _at(sf))
+    return q, sf
+
+
+def moe_dequantize_mx8(q, sf, dtype=torch.bfloat16, out=None):
+    """The values of q [R, K], sf [R, K / 32] as [R, K] in dtype."""
+    _cuda(q, "q", dtype=torch.float8_e4m3fn, ndim=2)
+    R = q.shape[0]
+    K = _mx8(q, sf, "", (R,))
+    out = _want(out, "out", dtype, (R, K), q.device)
+    _call("moe_dequantize_mx8", q.device, _at(q), _at(sf), R, K, _dtype_code(out, "out"), _at(out))
+    return out
+
+
+def moe_sort_rows_mx8(q, sf, token_topk_to_pos, n_rows=None, q_out=None, sf_out=None):
+    """The tokens' 8-bit rows at the rows of their experts: row
+    token_topk_to_pos[t, j] of the result is row t of q, sf.  n_rows None: one for
+    each position.  Positions outside [0, n_rows) are skipped, rows that no
+    position names are left as they were; a position stands at one place only."""
+    _cuda(q, "q", dtype=torch.float8_e4m3fn, ndim=2)
+    _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
+    T, k = token_topk_to_pos.shape
+    K, dev = _mx8(q, sf, "", (T,)), q.device
+    n_rows = T * k if n_rows is None else n_rows
+    q_out = _want(q_out, "q_out", torch.float8_e4m3fn, (n_rows, K), dev)
+    sf_out = _want(sf_out, "sf_out", torch.uint8, (n_rows, K // 32), dev)
+    _call("moe_sort_rows_mx8", dev, _at(q), _at(sf), _at(token_topk_to_pos), T, k, n_rows, K, _at(q_out), _at(sf_out))
+    return q_out, sf_out
+
+
+def moe_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16, out=None, err=None):
+    """C[r] = A_r B[g]^T over the dispatch tables, both sides mx8: q_a, sf_a
+    [rows, .], q_b, sf_b [E, N, .]; returns C [rows, N] in out_dtype."""
+    _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
+    _cuda(q_b, "q_b", dtype=torch.float8_e4m3fn, ndim=3)
+    rows, (E, N, _) = q_a.shape[0], q_b.shape
+    K = _mx8(q_a, sf_a, "_a", (rows,))
+    if _mx8(q_b, sf_b, "_b", (E, N)) != K:
+        raise ValueError("the two sides disagree on K")
+    s, o, p, g = _tables(tables)
+    out = _want(out, "out", out_dtype, (rows, N), q_a.device)
+    _call("moe_grouped_gemm_mx8", q_a.device, _at(q_a), _at(sf_a), _at(q_b), _at(sf_b), _at(s), _at(o), _at(p), _at(g),
+          g.shape[0], rows, N, K, E, _dtype_code(out, "out"), _at(out), _err(err))
+    return out
+
+
+class Mx8Experts:
+    """The three expert weights of a layer as mx8 elements and scales."""
+
+    def __init__(self, q_gate, sf_gate, q_up, sf_up, q_down, sf_down):
+        self.E, self.d_e, self.d_h = q_gate.shape
+        for q, sf, name, lead in ((q_gate, sf_gate, "_gate", (self.E, self.d_e)), (q_up, sf_up, "_up", (self.E, self.d_e)),
+                                  (q_down, sf_down, "_down", (self.E, self.d_h))):
+            if _mx8(q, sf, name, lead) != (self.d_e if name == "_down" else self.d_h):
+                raise ValueError("q_gate / q_up must be [E, d_e, d_h] and q_down [E, d_h, d_e]")
+        self.q_gate, self.sf_gate, self.q_up, self.sf_up = q_gate, sf_gate, q_up, sf_up
+        self.q_down, self.sf_down = q_down, sf_down
+
+    @classmethod
+    def from_weights(cls, w_gate, w_up, w_down):
+        """Quantise the layer's weights [E, N, K] on the GPU."""
+        parts = []
+        for w in (w_gate, w_up, w_down):
+            E, N, K = w.shape
+            q, sf = moe_quantize_mx8(w.reshape(E * N, K))
+            parts += [q.view(E, N, K), sf.view(E, N, K // 32)]
+        return cls(*parts)
+
+
+def moe_grouped_gate_up_silu_mx8(q_a, sf_a, experts: "Mx8Experts", tables, q_h=None, sf_h=None, err=None):
+    """h = silu(A W_gate^T) * (A W_up^T) over the dispatch tables, quantised:
+    returns q_h [rows, d_e], sf_h [rows, d_e / 32]."""
+    _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
+    rows, dev, e = q_a.shape[0], q_a.device, experts
+    if _mx8(q_a, sf_a, "_a", (rows,)) != e.d_h:
+        raise ValueError("the rows and the experts disagree on d_hidden")
+    s, o, p, g = _tables(tables)
+    q_h = _want(q_h, "q_h", torch.float8_e4m3fn, (rows, e.d_e), dev)
+    sf_h = _want(sf_h, "sf_h", torch.uint8, (rows, e.d_e // 32), dev)
+    _call("moe_grouped_gate_up_silu_mx8", dev, _at(q_a), _at(sf_a), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
+          _at(s), _at(o), _at(p), _at(g), g.shape[0], rows, e.d_h, e.d_e, e.E, _at(q_h), _at(sf_h), _err(err))
+    return q_h, sf_h
+
+
+def forward_mx8_workspace_bytes(T, d_h, d_e, E, k, dtype) -> int:
+    return int(lib().moe_forward_mx8_workspace_bytes(T, d_h, d_e, E, k, _DT[dtype]))
+
+
+def moe_forward_mx8(x, w_g, bias, experts: "Mx8Experts", k: int, rows=None, ws=None, out=None, err=None):
+    """The routed forward with mx8 experts and activations; returns out [T,
+    d_hidden].  The gate reads x; the experts read ``rows`` = (q, sf), x in 8 bits
+    as :func:`moe_residual_norm_mx8` gives it (None: quantised from x here)."""
+    _cuda(x, "x", ndim=2)
+    T, d_h = x.shape
+    e, dt, dev = experts, x.dtype, x.device
+    if d_h != e.d_h:
+        raise ValueError("x and the experts disagree on d_hidden")
+    _need(w_g, "w_g", dt, (e.E, d_h))
+    if bias is not None:
+        _need(bias, "bias", torch.float32, (e.E,))
+    q, sf = (None, None) if rows is None else rows
+    if rows is not None and _mx8(q, sf, "", (T,)) != d_h:
+        raise ValueError("x and its 8-bit rows disagree on d_hidden")
+    code = _dtype_code(x, "x")
+    ws, nws = _ws(ws, dev, "moe_forward_mx8", T, d_h, e.d_e, e.E, k, code)
+    out = _want(out, "out", dt, x.shape, dev)
+    _call("moe_forward_mx8", dev, _at(x), _at(q), _at(sf), _at(w_g), _at(bias), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up),
+          _at(e.sf_up), _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err))
     return out
 
 

@@ -698,7 +698,22 @@ moe_status_t moe_residual_norm(const void *y, const void *res, const void *w_pos
     if ((rstd_post && !w_post) || (rstd_next && !w_next)) return MOE_ERR_INVALID_ARG;
     if (!all_aligned16({y, res, w_post, gate, w_next, out, u})) return MOE_ERR_INVALID_ARG;
     return cuda_status(moe::launch_residual_norm(y, res, w_post, gate, gate_kind, alpha, w_next, eps, T, H, dtype, out,
-                                                 u, rstd_post, rstd_next, reinterpret_cast<cudaStream_t>(stream)));
+                                                 u, nullptr, nullptr, rstd_post, rstd_next,
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_residual_norm_mx8(const void *y, const void *res, const void *w_post, const void *gate,
+                                   moe_gate_t gate_kind, float alpha, const void *w_next, float eps, int64_t T, int64_t H,
+                                   moe_dtype_t dtype, void *out, void *u, uint8_t *q, uint8_t *sf, float *rstd_post,
+                                   float *rstd_next, moe_stream_t stream) {
+    const moe_status_t st = check_norm(y, w_post, gate, gate_kind, alpha, T, H, dtype);
+    if (st != MOE_OK) return st;
+    if (!(eps >= 0.0f) || H % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!res || !w_next || !q || !sf || (y == nullptr) != (out == nullptr) || (rstd_post && !w_post)) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({y, res, w_post, gate, w_next, out, u, q})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_residual_norm(y, res, w_post, gate, gate_kind, alpha, w_next, eps, T, H, dtype, out, u, q,
+                                                 sf, rstd_post, rstd_next, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 size_t moe_residual_norm_backward_workspace_bytes(int64_t T, int64_t H) {
@@ -783,7 +798,7 @@ moe_status_t moe_dequantize_mx4(const uint8_t *q, const uint8_t *sf, int64_t n_r
                                                   reinterpret_cast<cudaStream_t>(stream)));
 }
 
-static moe_status_t check_mx4_gemm(std::initializer_list<const void *> need, int64_t N, int64_t K, int64_t E) {
+static moe_status_t check_mx_gemm(std::initializer_list<const void *> need, int64_t N, int64_t K, int64_t E) {
     if (N < 1 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
     if (N > (1 << 20) || K > (1 << 20) || E > (1 << 20)) return MOE_ERR_UNSUPPORTED;
     for (const void *p : need)
@@ -800,10 +815,10 @@ moe_status_t moe_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const
     if (n_rows == 0) return MOE_OK;
     moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
                                         n_rows, E);
-    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_b, sf_b, C}, N, K, E);
+    if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_b, sf_b, C}, N, K, E);
     if (st != MOE_OK) return st;
     if (!all_aligned16({q_a, q_b, C})) return MOE_ERR_INVALID_ARG;
-    const moe::Mx4Tables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
     return cuda_status(moe::launch_grouped_gemm_mx4(q_a, sf_a, q_b, sf_b, tab, m_blocks, n_rows, N, K, E, out_dtype, C,
                                                     err_flag, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -817,21 +832,22 @@ moe_status_t moe_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_
     if (n_rows == 0) return MOE_OK;
     moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
                                         n_rows, E);
-    if (st == MOE_OK) st = check_mx4_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h, E);
+    if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h, E);
     if (st != MOE_OK) return st;
     if (d_e % 32 != 0 || !all_aligned16({q_a, q_gate, q_up, q_h})) return MOE_ERR_INVALID_ARG;
-    const moe::Mx4Tables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
     return cuda_status(moe::launch_grouped_gate_up_silu_mx4(q_a, sf_a, q_gate, sf_gate, q_up, sf_up, tab, m_blocks,
                                                             n_rows, d_h, d_e, E, q_h, sf_h, err_flag,
                                                             reinterpret_cast<cudaStream_t>(stream)));
 }
 
-// the 16-bit forward's routing sections, then the 4-bit rows, h and y
-struct Mx4Layout {
-    size_t logits, idx, w, sizes, offsets, padded, gidx, stok, sw, pos, scratch, qa, sa, qh, sh, y, total;
+// the 16-bit forward's routing sections, then the rows and h in 4 or 8 bits (8
+// bits: the tokens' before the sort as well), and y
+struct MxLayout {
+    size_t logits, idx, w, sizes, offsets, padded, gidx, stok, sw, pos, scratch, qx, sx, qa, sa, qh, sh, y, total;
 };
 
-static bool mx4_layout(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype, Mx4Layout *L) {
+static bool mx_layout(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype, int bits, MxLayout *L) {
     if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || !is_half_type(dtype)) return false;
     const size_t Tk = static_cast<size_t>(T * k), e4 = static_cast<size_t>(E) * 4;
     size_t cur = 0;
@@ -851,9 +867,13 @@ static bool mx4_layout(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k
     L->sw = take(Tk * 4);
     L->pos = take(Tk * 4);
     L->scratch = take(moe::dispatch_scratch_bytes(static_cast<int64_t>(Tk), E));
-    L->qa = take(Tk * static_cast<size_t>(d_h / 2));
+    if (bits == 8) {
+        L->qx = take(static_cast<size_t>(T) * static_cast<size_t>(d_h));
+        L->sx = take(static_cast<size_t>(T) * static_cast<size_t>(d_h / 32));
+    }
+    L->qa = take(Tk * static_cast<size_t>(d_h) * bits / 8);
     L->sa = take(Tk * static_cast<size_t>(d_h / 32));
-    L->qh = take(Tk * static_cast<size_t>(d_e / 2));
+    L->qh = take(Tk * static_cast<size_t>(d_e) * bits / 8);
     L->sh = take(Tk * static_cast<size_t>(d_e / 32));
     L->y = take(Tk * static_cast<size_t>(d_h) * 2);
     L->total = cur;
@@ -861,8 +881,8 @@ static bool mx4_layout(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k
 }
 
 size_t moe_forward_mx4_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype) {
-    Mx4Layout L;
-    return mx4_layout(T, d_h, d_e, E, k, dtype, &L) ? L.total : static_cast<size_t>(-1);
+    MxLayout L;
+    return mx_layout(T, d_h, d_e, E, k, dtype, 4, &L) ? L.total : static_cast<size_t>(-1);
 }
 
 moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float *bias, const uint8_t *q_gate,
@@ -878,8 +898,8 @@ moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float *bias, 
         return MOE_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_INVALID_ARG;
     if (!all_aligned16({x, w_g, q_gate, q_up, q_down, out})) return MOE_ERR_INVALID_ARG;
-    Mx4Layout L;
-    if (!mx4_layout(T, d_h, d_e, E, k, dtype, &L)) return MOE_ERR_INVALID_ARG;
+    MxLayout L;
+    if (!mx_layout(T, d_h, d_e, E, k, dtype, 4, &L)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
     char *w = static_cast<char *>(ws);
     auto i32 = [w](size_t off) { return reinterpret_cast<int32_t *>(w + off); };
@@ -904,6 +924,146 @@ moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float *bias, 
     if (st != MOE_OK) return st;
     return reduce_common(w + L.y, Tk, i32(L.pos), topk_w, nullptr, nullptr, T, k, d_h, dtype, dtype, out, err_flag,
                          stream, false);
+}
+
+// ---------------------------------------------------------------------------
+// the gradient of the combine
+// ---------------------------------------------------------------------------
+moe_status_t moe_reduce_fused_backward(const void *d_out, const void *x, int64_t n_rows, const int32_t *token_topk_to_pos,
+                                       const float *topk_weights, const int32_t *sorted_token_idx, int64_t T, int64_t K,
+                                       int64_t H, moe_dtype_t in_dtype, moe_dtype_t out_dtype, void *d_x, float *d_topk_w,
+                                       int32_t *err_flag, moe_stream_t stream) {
+    if (!is_norm_type(in_dtype) || !is_norm_type(out_dtype) || (in_dtype != out_dtype && in_dtype != MOE_F32))
+        return MOE_ERR_UNSUPPORTED;
+    if (n_rows < 0 || T < 0 || K < 1 || K > 32 || H <= 0 || H % 256 != 0) return MOE_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX || T > INT32_MAX || H > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0 && T == 0) return MOE_OK;
+    if (n_rows > 0 && (!sorted_token_idx || !d_x)) return MOE_ERR_INVALID_ARG;
+    if (T > 0 && (!d_out || !token_topk_to_pos || (n_rows > 0 && d_topk_w && !x))) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({d_out, x, d_x})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_reduce_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_token_idx, T, K, H,
+                                                   n_rows, in_dtype, out_dtype, d_x, d_topk_w, err_flag,
+                                                   reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// ---------------------------------------------------------------------------
+// microscaled 8-bit floating point
+// ---------------------------------------------------------------------------
+moe_status_t moe_quantize_mx8(const void *x, int64_t n_rows, int64_t K, moe_dtype_t dtype, uint8_t *q, uint8_t *sf,
+                              moe_stream_t stream) {
+    if (!is_norm_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows < 0 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    if (!x || !q || !sf || !all_aligned16({x, q})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_quantize_mx8(x, n_rows, K, dtype, q, sf, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_dequantize_mx8(const uint8_t *q, const uint8_t *sf, int64_t n_rows, int64_t K, moe_dtype_t dtype,
+                                void *out, moe_stream_t stream) {
+    if (!is_norm_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows < 0 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    if (!q || !sf || !out || !all_aligned16({q, out})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_dequantize_mx8(q, sf, n_rows, K, dtype, out, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_sort_rows_mx8(const uint8_t *q, const uint8_t *sf, const int32_t *token_topk_to_pos, int64_t T, int64_t k,
+                               int64_t n_rows, int64_t K, uint8_t *q_out, uint8_t *sf_out, moe_stream_t stream) {
+    if (n_rows < 0 || T < 0 || k < 1 || k > 32 || K <= 0 || K % 32 != 0) return MOE_ERR_INVALID_ARG;
+    if (n_rows > INT32_MAX || T > INT32_MAX || K > (1 << 20)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0 || T == 0) return MOE_OK;
+    if (!q || !sf || !token_topk_to_pos || !q_out || !sf_out || !all_aligned16({q, q_out})) return MOE_ERR_INVALID_ARG;
+    return cuda_status(moe::launch_sort_rows_mx8(q, sf, token_topk_to_pos, T, k, n_rows, K, q_out, sf_out,
+                                                 reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gemm_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
+                                  const int32_t *group_sizes, const int32_t *group_offsets,
+                                  const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx,
+                                  int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K, int64_t E,
+                                  moe_dtype_t out_dtype, void *C, int32_t *err_flag, moe_stream_t stream) {
+    if (!is_norm_type(out_dtype)) return MOE_ERR_UNSUPPORTED;
+    if (n_rows == 0) return MOE_OK;
+    moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
+                                        n_rows, E);
+    if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_b, sf_b, C}, N, K, E);
+    if (st != MOE_OK) return st;
+    if (!all_aligned16({q_a, q_b, C})) return MOE_ERR_INVALID_ARG;
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
+    return cuda_status(moe::launch_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tab, m_blocks, n_rows, N, K, E, out_dtype, C,
+                                                    err_flag, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status_t moe_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
+                                          const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                                          const int32_t *group_sizes, const int32_t *group_offsets,
+                                          const int32_t *group_padded_offsets, const int32_t *group_idx_for_bx,
+                                          int64_t m_blocks, int64_t n_rows, int64_t d_h, int64_t d_e, int64_t E,
+                                          uint8_t *q_h, uint8_t *sf_h, int32_t *err_flag, moe_stream_t stream) {
+    if (n_rows == 0) return MOE_OK;
+    moe_status_t st = check_gemm_tables(group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, m_blocks,
+                                        n_rows, E);
+    if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h, E);
+    if (st != MOE_OK) return st;
+    if (d_e % 32 != 0 || !all_aligned16({q_a, q_gate, q_up, q_h})) return MOE_ERR_INVALID_ARG;
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx};
+    return cuda_status(moe::launch_grouped_gate_up_silu_mx8(q_a, sf_a, q_gate, sf_gate, q_up, sf_up, tab, m_blocks,
+                                                            n_rows, d_h, d_e, E, q_h, sf_h, err_flag,
+                                                            reinterpret_cast<cudaStream_t>(stream)));
+}
+
+size_t moe_forward_mx8_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype) {
+    MxLayout L;
+    return mx_layout(T, d_h, d_e, E, k, dtype, 8, &L) ? L.total : static_cast<size_t>(-1);
+}
+
+moe_status_t moe_forward_mx8(const void *x, const uint8_t *q, const uint8_t *sf, const void *w_g, const float *bias,
+                             const uint8_t *q_gate, const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
+                             const uint8_t *q_down, const uint8_t *sf_down, int64_t T, int64_t d_h, int64_t d_e, int64_t E,
+                             int64_t k, moe_dtype_t dtype, void *ws, size_t ws_bytes, void *out, int32_t *err_flag,
+                             moe_stream_t stream) {
+    if (!is_half_type(dtype)) return MOE_ERR_UNSUPPORTED;
+    if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || k > E || k > 32 || E > 1024) return MOE_ERR_INVALID_ARG;
+    if (d_h % 256 != 0 || d_e % 64 != 0 || (q == nullptr) != (sf == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (T == 0) return MOE_OK;
+    if (!x || !w_g || !q_gate || !sf_gate || !q_up || !sf_up || !q_down || !sf_down || !out || !ws)
+        return MOE_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(ws) & (kAlign - 1)) != 0) return MOE_ERR_INVALID_ARG;
+    if (!all_aligned16({x, q, w_g, q_gate, q_up, q_down, out})) return MOE_ERR_INVALID_ARG;
+    MxLayout L;
+    if (!mx_layout(T, d_h, d_e, E, k, dtype, 8, &L)) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+    char *w = static_cast<char *>(ws);
+    auto i32 = [w](size_t off) { return reinterpret_cast<int32_t *>(w + off); };
+    auto u8 = [w](size_t off) { return reinterpret_cast<uint8_t *>(w + off); };
+    float *topk_w = reinterpret_cast<float *>(w + L.w);
+    int32_t *sizes = i32(L.sizes), *offsets = i32(L.offsets), *padded = i32(L.padded), *gidx = i32(L.gidx);
+    const int64_t Tk = T * k, mb = m_blocks_of(T, k, E, MOE_BLOCK_M);
+    moe_status_t st = gate_topk(x, w_g, bias, T, d_h, E, k, dtype, i32(L.idx), topk_w, w + L.logits,
+                                moe_gate_topk_workspace_bytes(T, E), err_flag, stream);
+    if (st != MOE_OK) return st;
+    st = build_dispatch(i32(L.idx), topk_w, T, k, E, MOE_BLOCK_M, sizes, offsets, padded, gidx, i32(L.stok),
+                        reinterpret_cast<float *>(w + L.sw), i32(L.pos), w + L.scratch,
+                        moe::dispatch_scratch_bytes(Tk, E), nullptr, stream);
+    if (st != MOE_OK) return st;
+    if (!q) {
+        st = moe_quantize_mx8(x, T, d_h, dtype, u8(L.qx), u8(L.sx), stream);
+        if (st != MOE_OK) return st;
+        q = u8(L.qx);
+        sf = u8(L.sx);
+    }
+    st = moe_sort_rows_mx8(q, sf, i32(L.pos), T, k, Tk, d_h, u8(L.qa), u8(L.sa), stream);
+    if (st != MOE_OK) return st;
+    st = moe_grouped_gate_up_silu_mx8(u8(L.qa), u8(L.sa), q_gate, sf_gate, q_up, sf_up, sizes, offsets, padded, gidx, mb, Tk,
+                                      d_h, d_e, E, u8(L.qh), u8(L.sh), err_flag, stream);
+    if (st != MOE_OK) return st;
+    st = moe_grouped_gemm_mx8(u8(L.qh), u8(L.sh), q_down, sf_down, sizes, offsets, padded, gidx, mb, Tk, d_h, d_e, E, dtype,
+                              w + L.y, err_flag, stream);
+    if (st != MOE_OK) return st;
+    return reduce_common(w + L.y, Tk, i32(L.pos), topk_w, nullptr, nullptr, T, k, d_h, dtype, dtype, out, err_flag, stream,
+                         false);
 }
 
 }  // extern "C"

@@ -52,7 +52,7 @@ struct Mx4Block {
 };
 
 // rows of M block bx of the dispatch tables: expert, first row, count
-__device__ __forceinline__ Mx4Block mx4_block_of(const Mx4Tables &t, int bx) {
+__device__ __forceinline__ Mx4Block mx4_block_of(const MxTables &t, int bx) {
     Mx4Block b;
     b.g = t.gidx[bx];
     const int off = bx * 128 - t.padded[b.g];

@@ -61,7 +61,7 @@ template <int BN> struct MgLayout {
 
 struct MgParams {
     const uint8_t *sf_a, *sf_b0, *sf_b1;  // b1: the up weights of the gate/up form
-    Mx4Tables tab;
+    MxTables tab;
     void *out;
     uint8_t *q_h, *sf_h;
     int32_t *err;
@@ -635,7 +635,7 @@ cudaError_t launch_n(const CUtensorMap *maps, const MgParams &p, cudaStream_t st
     return launch_v<TOut, GATE_UP, BN, 1>(maps, p, stream);
 }
 
-MgParams params(const uint8_t *sf_a, const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
+MgParams params(const uint8_t *sf_a, const MxTables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
                 int out_n, int32_t *err) {
     MgParams p{};
     p.sf_a = sf_a;
@@ -653,7 +653,7 @@ MgParams params(const uint8_t *sf_a, const Mx4Tables &tab, int64_t m_blocks, int
 }  // namespace
 
 cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
-                                    const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
+                                    const MxTables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
                                     int64_t E, int out_dtype, void *C, int32_t *err, cudaStream_t stream) {
     constexpr int BN = MG_BN;
     CUtensorMap maps[3];
@@ -673,7 +673,7 @@ cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, con
 
 cudaError_t launch_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
                                             const uint8_t *sf_gate, const uint8_t *q_up, const uint8_t *sf_up,
-                                            const Mx4Tables &tab, int64_t m_blocks, int64_t n_rows, int64_t d_h,
+                                            const MxTables &tab, int64_t m_blocks, int64_t n_rows, int64_t d_h,
                                             int64_t d_e, int64_t E, uint8_t *q_h, uint8_t *sf_h, int32_t *err,
                                             cudaStream_t stream) {
     constexpr int BN = MG_BN;

@@ -30,6 +30,7 @@
 // 7167 bf16, by elements: 68 and 150 us (from memory 154 and 465).
 #include "common.cuh"
 #include "internal.h"
+#include "mx8.cuh"
 
 namespace moe {
 namespace {
@@ -44,6 +45,7 @@ struct NormParams {
     const float *r_post, *r_next;
     void *out, *u, *d_res, *d_y, *d_gate;
     float *rstd_post, *rstd_next, *d_w_post, *d_w_next;
+    uint8_t *q, *sf;  // u in 8 bits: elements and scale bytes
     float *partial;  // backward: [CTAs][3][H] column sums of d_w_next, d_w_post, d_gate
     int gate_kind;
     float alpha, eps;
@@ -189,6 +191,36 @@ template <typename T, int EPT, bool VEC> struct Part {
     }
 };
 
+// A row of u in 8 bits.  32 / RUN consecutive lanes hold a block of 32 elements
+// and find its largest magnitude among them; the blocks that cross H do not
+// exist (H % 32 == 0), so a block's lanes are all in the row or all past it.
+template <typename P, int EPT>
+__device__ __forceinline__ void store_mx8(const NormParams &p, int64_t t, const float (&o)[EPT]) {
+    constexpr int RUN = P::RUN, LANES = 32 / RUN;
+    uint8_t *q = p.q + t * p.H, *sf = p.sf + t * (p.H / 32);
+#pragma unroll
+    for (int v = 0; v < EPT; v += RUN) {
+        const int at = P::at(v);
+        uint32_t top = 0;
+#pragma unroll
+        for (int j = 0; j < RUN; ++j) top = max(top, magnitude_bits(o[v + j]));
+#pragma unroll
+        for (int s = LANES / 2; s >= 1; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
+        const uint32_t s = mx8_scale(top);
+        const float by = mx8_inverse(s);
+        const bool bad = s == 255u;
+        if (at >= p.H) continue;
+        if constexpr (RUN == 8)
+            *reinterpret_cast<uint2 *>(q + at) = make_uint2(e4m3x4(o[v], o[v + 1], o[v + 2], o[v + 3], by, bad),
+                                                            e4m3x4(o[v + 4], o[v + 5], o[v + 6], o[v + 7], by, bad));
+        else if constexpr (RUN == 4)
+            *reinterpret_cast<uint32_t *>(q + at) = e4m3x4(o[v], o[v + 1], o[v + 2], o[v + 3], by, bad);
+        else
+            q[at] = static_cast<uint8_t>(e4m3x4(o[v], 0.0f, 0.0f, 0.0f, by, bad));
+        if ((threadIdx.x & (LANES - 1)) == 0) sf[at / 32] = static_cast<uint8_t>(s);
+    }
+}
+
 // Sums over the CTA with one barrier each: two scratch buffers in turn.
 struct RowSums {
     float2 *scratch;  // [2][32]
@@ -243,7 +275,7 @@ template <> struct RowRing<Rows::kMemory> {
         : p(p), row(blockIdx.x), row_bytes(static_cast<int64_t>(p.H) * elem) {}
     __device__ __forceinline__ void start() {}
     __device__ __forceinline__ void next() { tensor = 0; }
-    template <typename T> __device__ __forceinline__ void finish(bool) {}
+    template <typename T, bool Q8 = false> __device__ __forceinline__ void finish(bool) {}
     int tensor = 0;
     __device__ __forceinline__ const void *take() { return static_cast<const uint8_t *>(p.ring[tensor++]) + row * row_bytes; }
     __device__ __forceinline__ void refill() {}
@@ -320,7 +352,7 @@ template <Rows MODE> struct RowRing {
     // After the last row.  If a row was lost: NaN for all of the CTA's rows and its
     // column sums, and the copies still on their way land before shared memory
     // goes (2 s in all).
-    template <typename T> __device__ __forceinline__ void finish(bool backward) {
+    template <typename T, bool Q8 = false> __device__ __forceinline__ void finish(bool backward) {
         __syncthreads();
         if (!lost()) return;
         T *const wide[] = {static_cast<T *>(backward ? p.d_res : p.out), static_cast<T *>(backward ? p.d_y : p.u),
@@ -335,6 +367,10 @@ template <Rows MODE> struct RowRing {
                 if (narrow[i] && threadIdx.x == 0) narrow[i][t] = NAN;
             }
         }
+#pragma unroll 1
+        for (int64_t t = blockIdx.x; Q8 && t < p.T; t += gridDim.x)
+#pragma unroll 1
+            for (int b = threadIdx.x; b < p.H / 32; b += blockDim.x) p.sf[t * (p.H / 32) + b] = 255u;
 #pragma unroll 1
         for (int h = threadIdx.x; backward && h < 3 * p.H; h += blockDim.x)
             p.partial[static_cast<int64_t>(blockIdx.x) * 3 * p.H + h] = NAN;
@@ -404,7 +440,8 @@ template <typename P, Rows MODE> struct Kept {
     }
 };
 
-template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
+// Q8: u comes in 8 bits too, and as u itself only where there is a place for it.
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS, bool Q8>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __grid_constant__ NormParams p) {
     using P = Part<T, EPT, MODE == Rows::kVectors>;
     extern __shared__ __align__(128) uint8_t norm_smem[];
@@ -473,14 +510,15 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
             w_next.load(w, H);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) o[i] = o[i] * r * w.get(i);
-            P::store(static_cast<T *>(p.u) + base, H, o);
+            if (!Q8 || p.u) P::store(static_cast<T *>(p.u) + base, H, o);
+            if constexpr (Q8) store_mx8<P>(p, t, o);
         }
         if (!read) {
             __syncthreads();
             ring.refill();
         }
     }
-    ring.template finish<T>(false);
+    ring.template finish<T, Q8>(false);
 }
 
 // The instructions of a row take longer than its bytes, so what a call has or
@@ -697,8 +735,10 @@ cudaError_t launch_kernel(void (*kern)(NormParams), std::atomic<bool> *attr_done
 
 template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 cudaError_t launch_forward(const NormParams &p, const NormShape &s, cudaStream_t stream) {
-    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
-    return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS>, attr_done, p, s, stream);
+    static std::atomic<bool> attr_done[2][64];  // zero-initialised; several host threads may launch
+    if constexpr (MODE != Rows::kOdd)  // rows of whole blocks of 32 start on 16 bytes
+        if (p.q) return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS, true>, attr_done[1], p, s, stream);
+    return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS, false>, attr_done[0], p, s, stream);
 }
 
 template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
@@ -760,7 +800,8 @@ template <typename T> cudaError_t launch_typed(NormParams p, bool backward, cuda
 
 cudaError_t launch_residual_norm(const void *y, const void *res, const void *w_post, const void *gate, int gate_kind,
                                  float alpha, const void *w_next, float eps, int64_t T, int64_t H, int dtype,
-                                 void *out, void *u, float *rstd_post, float *rstd_next, cudaStream_t stream) {
+                                 void *out, void *u, uint8_t *q, uint8_t *sf, float *rstd_post, float *rstd_next,
+                                 cudaStream_t stream) {
     NormParams p{};
     p.y = y;
     p.res = res;
@@ -774,6 +815,8 @@ cudaError_t launch_residual_norm(const void *y, const void *res, const void *w_p
     p.H = static_cast<int>(H);
     p.out = out;
     p.u = u;
+    p.q = q;
+    p.sf = sf;
     p.rstd_post = rstd_post;
     p.rstd_next = rstd_next;
     p.ring[p.tensors++] = res;

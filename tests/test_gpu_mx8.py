@@ -1,0 +1,479 @@
+"""Microscaled 8-bit rows: the quantiser, the norm that writes them, the sort, the
+grouped products, the layer of them and the block.
+
+Quantisation, dequantisation and the sort are held bit for bit to a list of what 8
+bits can hold.  The products' terms are exact, so their error is that of fp32 sums:
+2^-20 of the sum of the terms' magnitudes (the tensor cores add 32 products at a
+time, each aligned to the largest and cut at 24 bits or more, then up to 1024 such
+sums in fp32), plus half a step of the output's type."""
+import pytest
+import torch
+
+from gpu_helpers import require_cuda
+from mixture_experts_routed_gate_gb300 import binding
+from mixture_experts_routed_gate_gb300.block import MoEBlock, Rows8, run_blocks
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
+E4M3 = torch.float8_e4m3fn
+SUM = 2.0 ** -20
+
+
+def grid(device):
+    """The magnitudes of codes 0 to 126: 4 bits of exponent, 3 of mantissa."""
+    return torch.tensor([m * 2.0 ** -9 if e == 0 else (1 + m / 8) * 2.0 ** (e - 7) for e in range(16) for m in range(8)][:127],
+                        dtype=torch.float64, device=device)
+
+
+def power(e):
+    return ((e + 1023) << 52).view(torch.float64)
+
+
+def quantize64(x):
+    """Values and scale bytes of x [R, K] in 64 bits; NaN and 255 where the block has a NaN or an infinity."""
+    held = grid(x.device)
+    b = x.double().view(x.shape[0], -1, 32)
+    a = b.abs()
+    bad = ~a.isfinite().all(2, keepdim=True)
+    a = torch.where(bad, torch.zeros_like(a), a)
+    top = a.amax(2, keepdim=True)
+    e = torch.full_like(top, -127, dtype=torch.int64)
+    for n in range(-126, 121):  # the least power of two that brings the block to 448 or less
+        e += (top > 448 * 2.0 ** (n - 1)).long()
+    a = a / power(e)
+    low = torch.searchsorted(held, a.contiguous(), right=True) - 1  # held[low] <= a
+    high = (low + 1).clamp(max=126)
+    up = held[high] - a < a - held[low]
+    tie = held[high] - a == a - held[low]
+    code = torch.where(up | (tie & (low % 2 == 1)), high, low)
+    v = torch.sign(b) * held[code] * power(e)
+    return torch.where(bad, torch.full_like(v, float("nan")), v).view(x.shape), torch.where(bad, torch.full_like(e, 128), e)[:, :, 0] + 127
+
+
+def values64(q, sf):
+    """What elements and scale bytes stand for, from the format."""
+    bits = q.view(torch.uint8).long()
+    held = torch.cat((grid(q.device), torch.full((1,), float("nan"), dtype=torch.float64, device=q.device)))
+    v = torch.where(bits > 127, -1.0, 1.0).double() * held[bits % 128]
+    unit = torch.where(sf == 255, torch.full_like(sf, float("nan"), dtype=torch.float64), power(sf.long() - 127))
+    return (v.view(*q.shape[:-1], -1, 32) * unit[..., None]).view(q.shape)
+
+
+def same(a, b):
+    return bool(((a == b) | (a.isnan() & b.isnan())).all())
+
+
+def rows8(R, K, g):
+    x = torch.randn((R, K), generator=g, device="cuda")
+    x = x * torch.exp2(torch.randint(-6, 6, (R, K // 32), generator=g, device="cuda").float()).repeat_interleave(32, 1)
+    return binding.moe_quantize_mx8(x)
+
+
+# ----------------------------------------------------------------------------- to 8 bits and back
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("R,K", [(1, 32), (3, 96), (64, 2048), (5, 1056), (130, 288), (2, 7168), (33, 64)])
+def test_quantize(R, K, dtype):
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(R * 17 + K)
+    x = torch.randn((R, K), generator=g, device="cuda")
+    x = (x * torch.exp2(torch.randint(-6, 6, (R, K // 32), generator=g, device="cuda").float()).repeat_interleave(32, 1)).to(DT[dtype])
+    q, sf = binding.moe_quantize_mx8(x)
+    want, byte = quantize64(x)
+    assert q.dtype == E4M3 and torch.equal(sf.long(), byte)
+    assert same(values64(q, sf), want)
+    for out in ("bf16", "f32"):  # both hold every value
+        assert torch.equal(binding.moe_dequantize_mx8(q, sf, DT[out]).double(), want), out
+
+
+def test_quantize_ties_and_edges():
+    require_cuda()
+    ties = torch.tensor([448.0, 447.9, 432.0, 432.1, 17.0, 19.0, 2.0 ** -10, 3 * 2.0 ** -10, 2.0 ** -6, 15 * 2.0 ** -10, 1.0625, 1.1875, 0.5, 256.0, 8.5, 0.0],
+                        device="cuda")
+    rows = [torch.cat((ties, -ties)) * s for s in (1.0, 2.0 ** -20, 2.0 ** 100, 2.0 ** -126, 2.0 ** -135)]
+    over = torch.cat((ties, -ties))
+    over[5] = 448.00003  # one step over: the scale is 2
+    rows += [over, torch.zeros(32, device="cuda"), -torch.zeros(32, device="cuda"), torch.full((32,), 2.0 ** -149, device="cuda"),
+             torch.full((32,), 1.75 * 2.0 ** 127, device="cuda")]
+    for bad in (float("nan"), float("inf"), float("-inf"), -float("nan")):
+        r = torch.randn(32, device="cuda")
+        r[31] = bad
+        rows.append(r)
+    x = torch.stack(rows)
+    q, sf = binding.moe_quantize_mx8(x)
+    want, byte = quantize64(x)
+    assert torch.equal(sf.long(), byte)
+    assert same(values64(q, sf), want)
+    assert same(binding.moe_dequantize_mx8(q, sf, torch.float32).double(), want)
+    # every code with every scale byte, through the values' own types
+    q = torch.arange(256, device="cuda", dtype=torch.int32).to(torch.uint8).view(1, 256).expand(256, 256).contiguous().view(E4M3)
+    sf = torch.arange(256, device="cuda", dtype=torch.int32).to(torch.uint8).view(256, 1).expand(256, 8).contiguous()
+    for dtype in ("f32", "bf16", "f16"):
+        assert same(binding.moe_dequantize_mx8(q, sf, DT[dtype]), values64(q, sf).to(DT[dtype])), dtype
+
+
+# ----------------------------------------------------------------------------- the norm
+
+def norm_inputs(T, H, dt, gate, post, y, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    shape = dict(none=None, channel=(H,), token=(T, 1), full=(T, H))[gate]
+    return dict(y=(2 * n(T, H)).to(dt) if y else None, res=n(T, H).to(dt), w_post=(1 + 0.2 * n(H)).to(dt) if post else None,
+                gate=None if shape is None else (0.5 + 0.5 * n(*shape)).to(dt), alpha=0.7, w_next=(1 + 0.2 * n(H)).to(dt), eps=1e-5)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T,H,gate,post,y", [(1, 2048, "channel", True, True), (3, 32, "none", True, True), (7, 96, "token", True, True),
+                                             (333, 2080, "token", False, True), (65, 4128, "full", True, True), (129, 7168, "channel", True, True),
+                                             (5, 16384, "channel", True, True), (400, 64, "none", False, False), (2000, 1056, "full", True, True),
+                                             (3, 8224, "channel", True, True), (37, 14336, "none", False, False)])
+def test_norm(T, H, gate, post, y, dtype):
+    """out, u and the statistics are moe_residual_norm's; the rows are u's unrounded values in 8 bits: u itself
+    quantised in 32 bits, and for 16-bit types within the roundings of u in 64 bits.  Those: a row's sum of
+    squares is 26 additions of 16 or fewer, its rstd half of that and 2 units for the root, so 2^-19.5; five
+    products and sums more: 2^-18 of the terms' magnitudes a norm."""
+    require_cuda()
+    dt = DT[dtype]
+    a = norm_inputs(T, H, dt, gate, post, y, T + H)
+    want = binding.moe_residual_norm(**a)
+    got = binding.moe_residual_norm_mx8(**a)
+    for name in want:
+        assert torch.equal(got[name], want[name]), name
+    q, sf = got["q"], got["sf"]
+    alone = binding.moe_residual_norm_mx8(**a, with_u=False)
+    assert "u" not in alone
+    for name in alone:
+        assert torch.equal(alone[name].view(torch.uint8), got[name].view(torch.uint8)), name
+    if dtype == "f32":
+        eq, es = binding.moe_quantize_mx8(got["u"])
+        assert torch.equal(q.view(torch.uint8), eq.view(torch.uint8)) and torch.equal(sf, es)
+        return
+    d = {n: v.double() if isinstance(v, torch.Tensor) else v for n, v in a.items()}
+    z, o = torch.zeros_like(d["res"]), d["res"]
+    if y:
+        z = d["y"]
+        if post:
+            z = z * torch.rsqrt(z.square().mean(1, keepdim=True) + 1e-5) * d["w_post"]
+        if gate != "none":
+            z = z * d["gate"]
+        z = 0.7 * z
+        o = o + z
+    r = torch.rsqrt(o.square().mean(1, keepdim=True) + 1e-5)
+    u = o * r * d["w_next"]
+    off = 2 * 2.0 ** -18 * (d["res"].abs() + z.abs()) * r * d["w_next"].abs()
+    unit = power(sf.long() - 127).repeat_interleave(32, 1)
+    assert ((values64(q, sf) - u).abs() <= 2.0 ** -4 * (u.abs() + off) + 2.0 ** -10 * unit + off).all()
+    top, most = u.abs().view(T, -1, 32).amax(2), off.view(T, -1, 32).amax(2)
+    unit = unit.view(T, -1, 32)[:, :, 0]
+    assert (top - most <= 448 * unit).all() and ((top + most > 224 * unit) | (sf == 0)).all()
+
+
+def test_norm_odd_values():
+    """A row of zeros, a NaN, an infinity: each stays in its row, and in 8 bits in its block of 32 where the
+    statistics allow (a NaN in the weight)."""
+    require_cuda()
+    H = 128
+    x = torch.randn((5, H), device="cuda")
+    x[0] = 0
+    x[1, 5] = float("nan")
+    x[2, 70] = float("inf")
+    w = torch.ones(H, device="cuda")
+    w[33] = float("nan")
+    got = binding.moe_residual_norm_mx8(None, x, w_next=w)
+    assert same(values64(got["q"], got["sf"])[:, 32:64], torch.full((5, 32), float("nan"), dtype=torch.float64, device="cuda"))
+    assert (got["sf"][1] == 255).all() and (got["q"].view(torch.uint8)[1] == 0).all()
+    assert (got["sf"][0, [0, 2, 3]] == 0).all()
+    assert (got["sf"][2, 2] == 255).all()  # inf * rstd 0
+    assert (got["sf"][3:, [0, 2, 3]] != 255).all()
+    assert binding.moe_residual_norm_mx8(None, x[:0], w_next=w)["q"].shape == (0, H)
+
+
+def test_norm_in_place_and_its_gradient():
+    """out may be res; the gradient is moe_residual_norm_backward of the same saved values."""
+    require_cuda()
+    a = norm_inputs(50, 512, torch.bfloat16, "channel", True, True, 1)
+    want = binding.moe_residual_norm_mx8(**a)
+    res = a["res"].clone()
+    got = binding.moe_residual_norm_mx8(**{**a, "res": res}, out=res)
+    assert got["out"] is res and all(torch.equal(got[n].view(torch.uint8), want[n].view(torch.uint8)) for n in want)
+    d_out, d_u = torch.randn_like(res), torch.randn_like(res)
+    plain = binding.moe_residual_norm(**a)
+    g = [binding.moe_residual_norm_backward(d_out, d_u, a["y"], f["out"], a["w_post"], a["gate"], a["alpha"], a["w_next"],
+                                            f["rstd_post"], f["rstd_next"]) for f in (want, plain)]
+    assert all(torch.equal(g[0][n], g[1][n]) for n in g[1])
+
+
+# ----------------------------------------------------------------------------- the sort
+
+@pytest.mark.parametrize("T,K,k", [(1, 32, 1), (1, 7168, 8), (64, 2048, 6), (333, 1056, 5), (7, 96, 32), (1000, 160, 3), (50, 16384, 2)])
+def test_sort(T, K, k):
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(T)
+    q, sf = rows8(T, K, g)
+    n, more = T * k, 5
+    pos = torch.randperm(n + more, generator=g, device="cuda")[:n].to(torch.int32).view(T, k)
+    gone = torch.rand((T, k), generator=g, device="cuda") < 0.1
+    pos = torch.where(gone, torch.tensor([-1, n + more, -7, 2 ** 31 - 1], device="cuda", dtype=torch.int32)[torch.randint(0, 4, (T, k), generator=g, device="cuda")], pos)
+    out, osf = torch.full((n + more, K), 0x5a, dtype=torch.uint8, device="cuda"), torch.full((n + more, K // 32), 0xa5, dtype=torch.uint8, device="cuda")
+    want, wsf = out.clone(), osf.clone()
+    here = ~gone
+    t = torch.arange(T, device="cuda").view(T, 1).expand(T, k)[here]
+    want[pos[here].long()], wsf[pos[here].long()] = q.view(torch.uint8)[t], sf[t]
+    got = binding.moe_sort_rows_mx8(q, sf, pos, n + more, out.view(E4M3), osf)
+    assert torch.equal(got[0].view(torch.uint8), want) and torch.equal(got[1], wsf)
+
+
+def test_sort_unaligned_scales():
+    """The scales' bytes may start anywhere."""
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q, sf = rows8(20, 256, g)
+    pos = torch.randperm(40, generator=g, device="cuda").to(torch.int32).view(20, 2)
+    want = binding.moe_sort_rows_mx8(q, sf, pos)
+    room, place = torch.empty(20 * 8 + 3, dtype=torch.uint8, device="cuda"), torch.empty(40 * 8 + 1, dtype=torch.uint8, device="cuda")
+    odd = room[3:].view(20, 8).copy_(sf)
+    got = binding.moe_sort_rows_mx8(q, odd, pos, sf_out=place[1:].view(40, 8))
+    assert torch.equal(got[0].view(torch.uint8), want[0].view(torch.uint8)) and torch.equal(got[1], want[1])
+
+
+def test_sort_past_2_31_bytes():
+    require_cuda()
+    T, K, k = 40000, 7168, 8  # 2.3e9 bytes of rows
+    g = torch.Generator(device="cuda").manual_seed(2)
+    q = torch.randint(0, 127, (T, K), generator=g, device="cuda", dtype=torch.uint8).view(E4M3)
+    sf = torch.randint(0, 255, (T, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    pos = torch.randperm(T * k, generator=g, device="cuda").to(torch.int32).view(T, k)
+    out, osf = binding.moe_sort_rows_mx8(q, sf, pos)
+    for j in range(k):
+        p = pos[:, j].long()
+        assert torch.equal(out.view(torch.uint8)[p], q.view(torch.uint8)) and torch.equal(osf[p], sf)
+
+
+# ----------------------------------------------------------------------------- the products
+
+def routed(T, k, E, seed, spread=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    score = torch.randn((T, E), generator=g, device="cuda") + spread * torch.randn((E,), generator=g, device="cuda")
+    idx = score.topk(k, dim=1).indices.to(torch.int32).contiguous()
+    return binding.moe_build_dispatch(idx, None, E), g
+
+
+def by_group(t):
+    first = 0
+    for e, n in enumerate(t["group_sizes"].tolist()):
+        if n:
+            yield e, slice(first, first + n)
+        first += n
+
+
+def product_and_size(a, b, t):
+    """A_r B[g]^T in 64 bits, and the sum of the terms' magnitudes."""
+    out = torch.empty((a.shape[0], b.shape[1]), dtype=torch.float64, device="cuda")
+    mag = torch.empty_like(out)
+    for e, at in by_group(t):
+        out[at], mag[at] = a[at] @ b[e].t(), a[at].abs() @ b[e].abs().t()
+    return out, mag
+
+
+SHAPES = [(1, 1, 1, 32, 1), (1, 8, 8, 256, 128), (5, 2, 3, 64, 33), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 333), (130, 1, 1, 96, 257),
+          (700, 2, 3, 288, 200), (257, 4, 7, 1024, 512), (96, 2, 6, 7168, 160), (40, 2, 600, 160, 64), (128, 1, 1, 512, 300), (129, 1, 1, 544, 256)]
+
+
+@pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
+@pytest.mark.parametrize("T,k,E,K,N", SHAPES)
+def test_product(T, k, E, K, N, out):
+    require_cuda()
+    t, g = routed(T, k, E, T + K)
+    qa, sa = rows8(T * k, K, g)
+    qb, sb = (x.view(E, N, -1) for x in rows8(E * N, K, g))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = binding.moe_grouped_gemm_mx8(qa, sa, qb, sb, t, DT[out], err=err)
+    want, mag = product_and_size(values64(qa, sa), values64(qb, sb), t)
+    assert int(err.item()) == 0
+    top = torch.finfo(DT[out]).max
+    fits = want.abs() + SUM * mag < top
+    step = torch.finfo(DT[out]).eps / 2
+    bad = (got.double() - want).abs() > SUM * mag + step * want.abs() + torch.finfo(DT[out]).smallest_normal * step
+    assert not (bad & fits).any(), int((bad & fits).sum())
+
+
+def silu_products(t, qa, sa, gate, up):
+    """h in 64 bits and how far the kernel's fp32 h may be: from the two sums, each product's derivative, and
+    2^-20 of h for the exponential (2 + 1.2 |g| units), the quotient (2) and the product."""
+    a = values64(qa, sa)
+    g, mg = product_and_size(a, values64(*gate), t)
+    u, mu = product_and_size(a, values64(*up), t)
+    s = g * torch.sigmoid(g)
+    h = s * u
+    return h, 1.1 * SUM * mg * (u.abs() + SUM * mu) + SUM * mu * s.abs() + (2.0 ** -20 + 2.0 ** -22 * g.abs()) * h.abs()
+
+
+@pytest.mark.parametrize("T,k,E,K,N", [(1, 1, 1, 32, 32), (1, 8, 8, 256, 128), (5, 2, 3, 64, 96), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 352),
+                                       (700, 2, 3, 288, 224), (257, 4, 7, 1024, 512), (40, 2, 600, 160, 64), (129, 1, 1, 544, 256), (33, 1, 2, 7168, 160)])
+def test_gate_up(T, k, E, K, N):
+    require_cuda()
+    t, g = routed(T, k, E, T + K)
+    qa, sa = binding.moe_quantize_mx8(torch.randn((T * k, K), generator=g, device="cuda"))
+    w = [binding.moe_quantize_mx8(torch.randn((E * n, m), generator=g, device="cuda") * m ** -0.5) for n, m in ((N, K), (N, K), (K, N))]
+    parts = [x.view(E, n, -1) for (q, s), n in zip(w, (N, N, K)) for x in (q, s)]
+    e = binding.Mx8Experts(*parts)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, sf = binding.moe_grouped_gate_up_silu_mx8(qa, sa, e, t, err=err)
+    assert int(err.item()) == 0
+    h, off = silu_products(t, qa, sa, parts[0:2], parts[2:4])
+    unit = power(sf.long() - 127)
+    wide = unit.repeat_interleave(32, 1)
+    assert ((values64(q, sf) - h).abs() <= 2.0 ** -4 * (h.abs() + off) + 2.0 ** -10 * wide + off).all()
+    top, most = h.abs().view(T * k, -1, 32).amax(2), off.view(T * k, -1, 32).amax(2)
+    assert (top - most <= 448 * unit).all() and ((top + most > 224 * unit) | (sf == 0)).all()
+
+
+def test_products_of_odd_values():
+    """NaN scales, infinities in the sums and zeros stay in their rows and columns; rows of h in their blocks."""
+    require_cuda()
+    T, E, K, N = 200, 2, 320, 96
+    t, g = routed(T, 1, E, 3)
+    qa, sa = rows8(T, K, g)
+    qb, sb = (x.view(E, N, -1).clone() for x in rows8(E * N, K, g))
+    want, mag = product_and_size(values64(qa, sa), values64(qb, sb), t)
+    sa[3, 9] = 255
+    sa[150] = 255
+    sb[0, 40, 0] = 255
+    qa.view(torch.uint8)[10] = 0
+    got = binding.moe_grouped_gemm_mx8(qa, sa, qb, sb, t, torch.float32)
+    expert = torch.zeros(T, dtype=torch.long, device="cuda")
+    expert[int(t["group_sizes"][0]):] = 1
+    nan = torch.zeros((T, N), dtype=torch.bool, device="cuda")
+    nan[3] = nan[150] = True
+    nan[expert == 0, 40] = True
+    assert torch.equal(got.isnan(), nan)
+    assert (got[10][~nan[10]] == 0).all()
+    ok = ~nan
+    ok[10] = False
+    assert ((got.double() - want).abs() <= SUM * mag + 2.0 ** -24 * want.abs())[ok].all()
+    e = binding.Mx8Experts(qb, sb, qb, torch.full_like(sb, 127), *(x.view(E, K, -1) for x in rows8(E * K, N, g)))
+    q, sf = binding.moe_grouped_gate_up_silu_mx8(qa, sa, e, t)
+    bad = torch.zeros((T, N // 32), dtype=torch.bool, device="cuda")
+    bad[3] = bad[150] = True
+    bad[expert == 0, 1] = True  # feature 40's block
+    assert torch.equal(sf == 255, bad) and (q.view(torch.uint8).view(T, -1, 32)[bad] == 0).all()
+
+
+def test_rows_behind_the_last_group_are_left():
+    require_cuda()
+    T, E, K, N, more = 50, 3, 128, 96, 30
+    t, g = routed(T, 2, E, 4)
+    qa, sa = rows8(2 * T + more, K, g)
+    w = [x.view(E, n, -1) for n, m in ((N, K), (N, K), (K, N)) for x in rows8(E * n, m, g)]
+    for dt in (torch.float32, torch.float16):
+        out = torch.full((2 * T + more, N), 7.0, device="cuda", dtype=dt)
+        binding.moe_grouped_gemm_mx8(qa, sa, w[0], w[1], t, dt, out=out)
+        assert (out[2 * T:] == 7).all() and not (out[:2 * T] == 7).all()
+    q, s = torch.full((2 * T + more, N), 3, dtype=torch.uint8, device="cuda"), torch.full((2 * T + more, N // 32), 3, dtype=torch.uint8, device="cuda")
+    binding.moe_grouped_gate_up_silu_mx8(qa, sa, binding.Mx8Experts(*w), t, q.view(E4M3), s)
+    assert (q[2 * T:] == 3).all() and (s[2 * T:] == 3).all() and not (s[:2 * T] == 3).all()
+
+
+def test_unaligned_scales_and_results():
+    """Scale bytes and results may start where their types do."""
+    require_cuda()
+    T, E, K, N = 77, 3, 512, 130
+    t, g = routed(T, 2, E, 6)
+    qa, sa = rows8(2 * T, K, g)
+    qb, sb = (x.view(E, N, -1) for x in rows8(E * N, K, g))
+    want = binding.moe_grouped_gemm_mx8(qa, sa, qb, sb, t, torch.bfloat16)
+    for shift in (1, 2, 4):
+        def moved(s):
+            room = torch.empty(s.numel() + shift, dtype=torch.uint8, device="cuda")[shift:].view(s.shape)
+            return room.copy_(s)
+        assert torch.equal(binding.moe_grouped_gemm_mx8(qa, moved(sa), qb, moved(sb), t, torch.bfloat16), want)
+
+
+# ----------------------------------------------------------------------------- the layer and the block
+
+def layer(T, d_h, d_e, E, k, dtype, seed=0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    n = lambda *s: torch.randn(s, generator=g, device="cuda")  # noqa: E731
+    dt = DT[dtype]
+    x, w_g = n(T, d_h).to(dt), (n(E, d_h) * d_h ** -0.5).to(dt)
+    w = [(n(E, a, b) * b ** -0.5).to(dt) for a, b in ((d_e, d_h), (d_e, d_h), (d_h, d_e))]
+    return x, w_g, 0.2 * n(E), w
+
+
+@pytest.mark.parametrize("T,d_h,d_e,E,k,dtype", [(1, 256, 64, 4, 2, "f16"), (64, 512, 192, 16, 4, "bf16"), (300, 256, 320, 7, 3, "f16"),
+                                                 (1100, 512, 128, 24, 2, "bf16")])
+def test_forward_is_its_parts(T, d_h, d_e, E, k, dtype):
+    require_cuda()
+    x, w_g, bias, w = layer(T, d_h, d_e, E, k, dtype)
+    e = binding.Mx8Experts.from_weights(*w)
+    q, sf = binding.moe_quantize_mx8(x)
+    idx, tw = binding.moe_gate_topk(x, w_g, bias, k)
+    t = binding.moe_build_dispatch(idx, tw, E)
+    sq, ss = binding.moe_sort_rows_mx8(q, sf, t["token_topk_to_pos"])
+    y = binding.moe_grouped_gemm_mx8(*binding.moe_grouped_gate_up_silu_mx8(sq, ss, e, t), e.q_down, e.sf_down, t, DT[dtype])
+    want = binding.moe_reduce_fused(y, t["token_topk_to_pos"], tw)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert torch.equal(binding.moe_forward_mx8(x, w_g, bias, e, k, err=err), want)
+    assert torch.equal(binding.moe_forward_mx8(x, w_g, bias, e, k, (q, sf), err=err), want)
+    assert int(err.item()) == 0
+    # a replayed graph on other tokens
+    graph, ws = torch.cuda.CUDAGraph(), torch.empty(binding.forward_mx8_workspace_bytes(T, d_h, d_e, E, k, DT[dtype]), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(x)
+    with torch.cuda.graph(graph):
+        binding.moe_forward_mx8(x, w_g, bias, e, k, ws=ws, out=out)
+    x.copy_(x.flip(0))
+    graph.replay()
+    assert torch.equal(out, binding.moe_forward_mx8(x, w_g, bias, e, k))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = binding.moe_forward_mx8(x, w_g, bias, e, k)
+    side.synchronize()
+    assert torch.equal(other, out)
+
+
+def test_blocks_of_all_kinds():
+    """16-bit, 8-bit and 4-bit blocks in turn: each is the entry points' calls in order."""
+    require_cuda()
+    T, d_h, d_e, E, k = 70, 512, 128, 8, 2
+    x, w_g, bias, w = layer(T, d_h, d_e, E, k, "bf16")
+    one = torch.ones(d_h, dtype=torch.bfloat16, device="cuda")
+    e8, e4 = binding.Mx8Experts.from_weights(*w), binding.Mx4Experts.from_weights(*w)
+    make = lambda experts, last=False: MoEBlock(w_g, bias, experts, k, w_post=one, alpha=0.5, w_next=None if last else one * 0.9)  # noqa: E731
+    u, res = run_blocks([make(e8), make(tuple(w)), make(e8), make(e8), make(e4, True)], x, one)
+    assert u is None
+    r = x.clone()
+    f = binding.moe_residual_norm_mx8(None, r, w_next=one)
+    for kind, nxt in (("8", "16"), ("16", "8"), ("8", "8"), ("8", "4"), ("4", None)):
+        if kind == "8":
+            y = binding.moe_forward_mx8(f["u"], w_g, bias, e8, k, (f["q"], f["sf"]))
+        else:
+            y = binding.moe_forward(f["u"], w_g, bias, *w, k) if kind == "16" else binding.moe_forward_mx4(f["u"], w_g, bias, e4, k)
+        norm = binding.moe_residual_norm_mx8 if nxt == "8" else binding.moe_residual_norm
+        f = norm(y, r, one, None, 0.5, None if nxt is None else one * 0.9)
+        r = f["out"]
+    assert torch.equal(res, r)
+    rows = make(e8)(torch.zeros_like(x), x.clone(), rows8=True)[0]
+    assert isinstance(rows, Rows8) and rows.q.dtype == E4M3
+
+
+def test_refusals():
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(0)
+    q, sf = rows8(8, 64, g)
+    pos = torch.zeros((8, 2), dtype=torch.int32, device="cuda")
+    x = torch.randn((8, 64), device="cuda")
+    for call in (lambda: binding.moe_quantize_mx8(x[:, :40].contiguous()), lambda: binding.moe_quantize_mx8(x.t()),
+                 lambda: binding.moe_dequantize_mx8(q, sf[:4]), lambda: binding.moe_sort_rows_mx8(q[:4], sf[:4], pos),
+                 lambda: binding.moe_sort_rows_mx8(q, sf[:, :1].contiguous(), pos), lambda: binding.moe_residual_norm_mx8(x, x, w_next=None),
+                 lambda: binding.moe_residual_norm_mx8(None, x, w_post=x[0], w_next=x[0]), lambda: binding.moe_residual_norm_mx8(x, x, w_next=x[0, :32]),
+                 lambda: binding.moe_residual_norm_mx8(None, x[:, :40].contiguous(), w_next=x[0, :40]),
+                 lambda: binding.Mx8Experts(q[None], sf[None], q[None], sf[None], q[None], sf[None]),
+                 lambda: binding.moe_grouped_gemm_mx8(q, sf, q[None, :, :32].contiguous(), sf[None, :, :1].contiguous(), {})):
+        with pytest.raises(ValueError):
+            call()
+    for call in (lambda: binding.moe_dequantize_mx8(q.view(torch.uint8), sf), lambda: binding.moe_sort_rows_mx8(q, sf.int(), pos),
+                 lambda: binding.moe_sort_rows_mx8(q, sf, pos.long()), lambda: binding.moe_quantize_mx8(x.double())):
+        with pytest.raises(TypeError):
+            call()
