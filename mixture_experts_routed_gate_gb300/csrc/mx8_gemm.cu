@@ -1,10 +1,29 @@
-// mx8_gemm.cu -- the grouped product of 8-bit rows with 8-bit expert weights:
+// mx8_gemm.cu -- the grouped product of 8-bit rows with 8-bit expert weights on
+// the block-scaled tensor cores (tcgen05.mma kind::mxf8f6f4), on pairs of SMs:
 //
 //   C[r, n] = sum over k of (qa 2^sa)[r, k] * (qb 2^sb)[expert of r][n, k]
 //
 // and the gate/up form, h = silu(A Wg^T) * (A Wu^T), quantised to 8 bits.
 //
-// A warp holds 32 columns of a row, a lane a column; sums in fp32.
+// The weights are the M = 256 operand (128 rows in each SM), the rows of a
+// dispatch block the N operand (32 to 128, half in each SM): a tile costs what
+// its rows cost, and every weight byte enters one SM's shared memory once a
+// block.  The accumulator holds features in lanes and rows in columns, so a warp
+// stores 32 consecutive features of a row.
+//
+// A persistent pair works on tiles of one dispatch block by 256 features (128 in
+// the gate/up form: 64 of W_gate and 64 of W_up in each SM).  Roles in each CTA:
+//   warp 0      TMA: 256-element slices of its weights and of its half of the
+//               rows into a ring of 128-byte-swizzled stages, completing on the
+//               even CTA's barriers;
+//   warp 1      (even CTA) one elected lane: eight K = 32 MMAs a slice;
+//   warps 2-9   epilogue, from one of two accumulators while the other fills;
+//   warps 10-17 scales, a unit of four slices at a time, two groups in turn: each
+//               thread loads a weight row's and a row's 32 scale bytes, a unit
+//               ahead; through shared memory each warp gets every row's and
+//               stores them to its quarter of tensor memory.  Both CTAs hold all
+//               rows' scales.  The units have their own ring, of four, so that
+//               their way into tensor memory runs ahead of the slices.
 #include "common.cuh"
 #include "internal.h"
 #include "mx4.cuh"
@@ -13,62 +32,584 @@
 namespace moe {
 namespace {
 
-constexpr int G8_WARPS = 8;
+constexpr int G8_SLICE = 256;               // elements (bytes) of K per stage: two 128-byte halves
+constexpr int G8_A_HALF = 128 * 128;        // 128 weight rows of one half
+constexpr int G8_B_HALF = 64 * 128;         // up to 64 rows of one half
+constexpr int G8_STAGE = 2 * (G8_A_HALF + G8_B_HALF);
+constexpr int G8_STAGES = 4;
+constexpr int G8_THREADS = 576;
+constexpr int G8_EPI_WARP0 = 2, G8_EPI_WARPS = 8, G8_SF_WARP0 = 10, G8_SF_GROUPS = 2;
+constexpr int G8_UNIT = 4;                  // slices whose scales are stored together
+constexpr int G8_UNITS = 4;                 // units in tensor memory
+constexpr int G8_AHEAD = 2;                 // units in registers ahead of those, a group
+constexpr int G8_LIST = 512;                // M blocks with rows that the shared-memory list holds
+constexpr int G8_ACC = 128;                 // columns of an accumulator
+constexpr int G8_SF_COL0 = 2 * G8_ACC, G8_SF_COLS = 16;  // a stage's scales: two halves of 4 columns for each operand
+constexpr int G8_UNIT_COLS = G8_UNIT * G8_SF_COLS;
+constexpr int G8_SF_BYTES = 4 * G8_UNIT * 512;
+constexpr int G8_EXCHANGE = 4 * 2 * 8 * 32 * 4;  // gate/up: four pairs of epilogue warps, 8 rows by 32 features each way
+constexpr int G8_FIXED = 1024 + 512 + G8_LIST * 8 + G8_SF_GROUPS * G8_SF_BYTES + G8_EXCHANGE;
+constexpr int G8_SMEM = G8_STAGES * G8_STAGE + G8_FIXED;
+static_assert(G8_SMEM <= 232448 - 256, "shared memory");
+static_assert(G8_SF_COL0 + G8_UNITS * G8_UNIT_COLS <= 512, "tensor memory");
+static_assert(G8_UNITS % G8_SF_GROUPS == 0, "the groups alternate");
+static_assert((2 * G8_STAGES + 2 * G8_UNITS + 4) * 8 <= 512, "barriers");
 
-__device__ __forceinline__ float block_sum(const uint8_t *a, const uint8_t *b, float s) {
-    const uint4 *va = reinterpret_cast<const uint4 *>(a), *vb = reinterpret_cast<const uint4 *>(b);
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint4 x = __ldg(va + i), y = __ldg(vb + i);
-        const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int h = 0; h < 32; h += 16) {
-                const float2 f = e4m3x2_values(xs[j] >> h), g = e4m3x2_values(ys[j] >> h);
-                s = fmaf(f.x, g.x, s);
-                s = fmaf(f.y, g.y, s);
-            }
-    }
-    return s;
+struct G8Params {
+    const uint8_t *sf_a, *sf_b0, *sf_b1;  // b1: the up weights of the gate/up form
+    MxTables tab;
+    void *out;
+    uint8_t *q_h, *sf_h;
+    int32_t *err;
+    int m_blocks, n_tiles, slices, units;
+    int64_t N, K;
+};
+
+struct G8Tile {
+    int g, m_start, rows, n0;
+    bool single;  // the expert's only block
+};
+
+// kind::mxf8f6f4: e4m3 by e4m3 (format 0), e8m0 scales; the scale ids (which of
+// a cell's four bytes) are added per MMA.
+//   bits 4-5 B scale id; 7-9 A format, 10-12 B format; 17-22 N >> 3; 23 scale
+//   type (1 = e8m0); 24-28 M >> 4; 29-30 A scale id
+__device__ __forceinline__ uint32_t idesc_mxf8(uint32_t M, uint32_t N) { return ((N >> 3) << 17) | (1u << 23) | ((M >> 4) << 24); }
+
+// The MMA warp runs whole and one elected lane issues, so that the operands come
+// from uniform registers.
+__device__ __forceinline__ void tc_mma2_mxf8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                             uint32_t sfb, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
 }
 
-template <typename TOut, bool GATE_UP>
-__global__ void __launch_bounds__(G8_WARPS * 32)
-    mx8_gemm_kernel(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b0, const uint8_t *sf_b0, const uint8_t *q_b1,
-                    const uint8_t *sf_b1, const MxTables tab, int64_t N, int64_t K, TOut *out, uint8_t *q_h, uint8_t *sf_h) {
+__device__ __forceinline__ void tc_commit2_both_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(bar),
+        "h"(static_cast<uint16_t>(3))
+        : "memory");
+}
+
+// A barrier of COUNT threads: whether `yes` holds in all of them.
+template <int COUNT> __device__ __forceinline__ bool g8_all(int id, bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %2, 0;\n\t"
+        "barrier.cta.red.and.aligned.pred q, %1, %3, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"(id), "r"(yes ? 1u : 0u), "n"(COUNT)
+        : "memory");
+    return all != 0;
+}
+
+// the scales of rows i, 32 + i, 64 + i and 96 + i, p at row i
+__device__ __forceinline__ uint4 quarter_scales(const uint8_t *p) {
+    const uint32_t *w = reinterpret_cast<const uint32_t *>(p);
+    return make_uint4(w[0], w[32], w[64], w[96]);
+}
+
+// 8 consecutive columns of this warp's 32 lanes
+__device__ __forceinline__ void tmem_st8(uint32_t taddr, const uint4 &a, const uint4 &b) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(a.x),
+                 "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+}
+
+__device__ __forceinline__ void g8_drain(uint32_t bar, uint32_t parity) {
+    const unsigned long long start = global_timer_ns();
+    while (!mbar_try_wait_cluster(bar, parity))
+        if (global_timer_ns() - start > kWaitTimeoutNs) return;
+}
+
+// A unit's 32 scale bytes of a row.
+struct UnitScales {
+    uint32_t w[2 * G8_UNIT];  // a word for each 128 elements
+};
+
+// From byte `at` on of a row of kb bytes (null: zeros); bytes past kb are 0 (their
+// elements are not multiplied).  V: the load width that kb and the bases'
+// alignment allow.
+template <int V> __device__ __forceinline__ void load_scales(UnitScales &u, const uint8_t *row, int kb, int at) {
+    constexpr int WORDS = V < 4 ? 1 : V / 4;
+#pragma unroll
+    for (int i = 0; i < 2 * G8_UNIT; i += WORDS) {
+        const int byte = at + 4 * i;
+        const bool in = row != nullptr && byte < kb;
+        const uint8_t *p = row + byte;
+        if constexpr (V == 16) {
+            const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+            u.w[i] = v.x, u.w[i + 1] = v.y, u.w[i + 2] = v.z, u.w[i + 3] = v.w;
+        } else if constexpr (V == 8) {
+            const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
+            u.w[i] = v.x, u.w[i + 1] = v.y;
+        } else if constexpr (V == 4) {
+            u.w[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+        } else {
+            u.w[i] = 0u;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (in && byte + j < kb) u.w[i] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
+        }
+    }
+}
+
+// TOut void: the gate/up form
+template <typename TOut, int V>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
+    mx8_gemm_kernel(const __grid_constant__ CUtensorMap tmA16, const __grid_constant__ CUtensorMap tmA32,
+                    const __grid_constant__ CUtensorMap tmA64, const __grid_constant__ CUtensorMap tmB0,
+                    const __grid_constant__ CUtensorMap tmB1, const G8Params p) {
+    constexpr bool GATE_UP = std::is_same<TOut, void>::value;
+    constexpr int OWN = GATE_UP ? 64 : 128;  // features of a CTA's tile
+    extern __shared__ uint8_t g8_smem_raw[];
+    uint8_t *smem = g8_smem_raw + ((1024u - (smem_u32(g8_smem_raw) & 1023u)) & 1023u);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G8_STAGES * G8_STAGE);
+    int2 *list = reinterpret_cast<int2 *>(smem + G8_STAGES * G8_STAGE + 512);  // first row; expert, only block, row count
+    uint8_t *staging0 = smem + G8_STAGES * G8_STAGE + 512 + G8_LIST * 8;
+    float *exchange = reinterpret_cast<float *>(staging0 + G8_SF_GROUPS * G8_SF_BYTES);
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, warp_blocks[G8_THREADS / 32];
+    volatile int *abort_flag = &abort_word;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_cta_rank();
+    const bool leader = rank == 0;
+    const uint32_t bar0 = smem_u32(bars);
+    auto full_bar = [&](int i) { return bar0 + 8u * i; };  // the even CTA's, both CTAs' copies
+    auto empty_bar = [&](int i) { return bar0 + 8u * (G8_STAGES + i); };
+    auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + i); };
+    auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + 2 + i); };  // the even CTA's
+    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + 4 + i); };   // the even CTA's, both CTAs' scales
+    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + 4 + G8_UNITS + i); };
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < G8_STAGES; ++i) {
+            mbar_init(full_bar(i), 1);
+            mbar_init(empty_bar(i), 1);
+        }
+        for (int i = 0; i < G8_UNITS; ++i) {
+            mbar_init(sfull_bar(i), 2 * 4);  // a group's warps of each CTA
+            mbar_init(sempty_bar(i), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(tfull_bar(i), 1);
+            mbar_init(tempty_bar(i), 2 * G8_EPI_WARPS);
+        }
+        abort_word = 0;
+        fence_mbar_init();
+        tma_prefetch_desc(&tmA16);
+        tma_prefetch_desc(&tmA32);
+        tma_prefetch_desc(&tmA64);
+        tma_prefetch_desc(&tmB0);
+        if (GATE_UP) tma_prefetch_desc(&tmB1);
+    }
+    if (warp == 1) {
+        tmem_alloc2(smem_u32(&tmem_slot), 512);
+        tmem_relinquish2();
+    }
     griddep_wait();
     griddep_launch_dependents();
-    const Mx4Block b = mx4_block_of(tab, blockIdx.y);
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = static_cast<int64_t>(blockIdx.x) * 32 + lane, kb = K / 32;
-    const int64_t f = static_cast<int64_t>(b.g) * N + (n < N ? n : N - 1);
-    for (int i = warp; i < b.rows; i += G8_WARPS) {
-        const int64_t r = static_cast<int64_t>(b.m_start) + i;
-        float s0 = 0.0f, s1 = 0.0f;
-        for (int64_t c = 0; c < kb; ++c) {
-            const float sa = mx8_factor(__ldg(sf_a + r * kb + c));
-            s0 = fmaf(block_sum(q_a + r * K + c * 32, q_b0 + f * K + c * 32, 0.0f) * sa, mx8_factor(__ldg(sf_b0 + f * kb + c)), s0);
-            if (GATE_UP)
-                s1 = fmaf(block_sum(q_a + r * K + c * 32, q_b1 + f * K + c * 32, 0.0f) * sa, mx8_factor(__ldg(sf_b1 + f * kb + c)), s1);
+
+    // the blocks that hold rows, in order, when they fit the list (the whole CTA
+    // looks at G8_THREADS blocks at a time: the tables' latency is paid once);
+    // both CTAs of a pair build the same list
+    int n_blocks = 0;
+    for (int b0 = 0; b0 < p.m_blocks && n_blocks <= G8_LIST; b0 += G8_THREADS) {
+        const int bx = b0 + static_cast<int>(threadIdx.x);
+        const Mx4Block b = bx < p.m_blocks ? mx4_block_of(p.tab, bx) : Mx4Block{0, 0, 0};
+        const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
+        if (lane == 0) warp_blocks[warp] = __popc(has);
+        __syncthreads();
+        int at = n_blocks + __popc(has & ((1u << lane) - 1u));
+        for (int w = 0; w < G8_THREADS / 32; ++w) {
+            at += w < warp ? warp_blocks[w] : 0;
+            n_blocks += warp_blocks[w];
         }
-        if constexpr (GATE_UP) {
-            const float h = __fdividef(s0, 1.0f + __expf(-s0)) * s1;
-            const uint32_t s = mx8_scale(__reduce_max_sync(0xffffffffu, magnitude_bits(h)));
-            q_h[r * N + n] = static_cast<uint8_t>(e4m3x4(h, 0.0f, 0.0f, 0.0f, mx8_inverse(s), s == 255u));
-            if (lane == 0) sf_h[r * (N / 32) + blockIdx.x] = static_cast<uint8_t>(s);
-        } else if (n < N) {
-            out[r * N + n] = from_f32<TOut>(s0);
+        if (b.rows > 0 && at < G8_LIST) list[at] = make_int2(b.m_start, b.g << 9 | (p.tab.sizes[b.g] <= 128 ? 256 : 0) | b.rows);
+        __syncthreads();
+    }
+    const int listed = n_blocks <= G8_LIST ? n_blocks : -1;
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // the other CTA's barriers are initialised before any use
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+    const int64_t total = static_cast<int64_t>(listed >= 0 ? listed : p.m_blocks) * p.n_tiles;
+    const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
+    auto tile_at = [&](int64_t t) {
+        const int b = static_cast<int>(t / p.n_tiles);
+        G8Tile ti;
+        ti.n0 = static_cast<int>(t - static_cast<int64_t>(b) * p.n_tiles) * (2 * OWN) + static_cast<int>(rank) * OWN;
+        if (listed >= 0) {
+            const int2 e = list[b];
+            ti.g = e.y >> 9;
+            ti.m_start = e.x;
+            ti.rows = e.y & 255;
+            ti.single = (e.y & 256) != 0;
+        } else {
+            const Mx4Block k = mx4_block_of(p.tab, b);
+            ti.g = k.g;
+            ti.m_start = k.m_start;
+            ti.rows = k.rows;
+            ti.single = p.tab.sizes[k.g] <= 128;
         }
+        return ti;
+    };
+    auto columns_of = [](const G8Tile &ti) { return (ti.rows + 31) & ~31; };
+
+    if (warp == 0) {
+        // -------------------------------- copies --------------------------------
+        if (lane == 0) {
+            const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
+            int stage = 0;
+            uint32_t phase = 0;
+            long issued = 0;
+            bool ok = true;
+            for (int64_t t = first; t < total && ok; t += stride) {
+                const G8Tile ti = tile_at(t);
+                if (ti.rows == 0) continue;
+                const int half = columns_of(ti) / 2;  // 16, 32, 48 or 64 rows: one copy or two
+                const CUtensorMap *const box = half == 64 ? &tmA64 : half == 16 ? &tmA16 : &tmA32;
+                const int row0 = ti.m_start + static_cast<int>(rank) * half;
+                const uint64_t pol = ti.single ? pass : keep;  // an only block's weights are read once
+                for (int s = 0; s < p.slices; ++s) {
+                    if (!mbar_wait_cluster_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t a = smem_u32(smem + stage * G8_STAGE), b = a + 2 * G8_A_HALF;
+                    const int halves = s * G8_SLICE + 128 < p.K ? 2 : 1;
+                    if (leader)
+                        mbar_arrive_expect_tx(full_bar(stage), 2 * halves * (G8_A_HALF + half * 128));
+                    const uint32_t fb = smem_map_rank(full_bar(stage), 0);
+                    for (int h = 0; h < halves; ++h) {
+                        const int k0 = s * G8_SLICE + h * 128;
+                        tma2_load_3d_hint(a + h * G8_A_HALF, &tmB0, fb, k0, ti.n0, ti.g, pol);
+                        if (GATE_UP) tma2_load_3d_hint(a + h * G8_A_HALF + G8_A_HALF / 2, &tmB1, fb, k0, ti.n0, ti.g, pol);
+                        tma2_load_2d_hint(b + h * G8_B_HALF, box, fb, k0, row0, keep);
+                        if (half == 48) tma2_load_2d_hint(b + h * G8_B_HALF + 32 * 128, &tmA16, fb, k0, row0 + 32, keep);
+                    }
+                    ++issued;
+                    if (++stage == G8_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            if (leader && (!ok || *abort_flag)) {
+                // both CTAs' copies in flight land before shared memory goes away
+                for (long j = 1; j <= G8_STAGES && j <= issued; ++j) {
+                    const long i = issued - j;
+                    g8_drain(full_bar(static_cast<int>(i % G8_STAGES)), static_cast<uint32_t>((i / G8_STAGES) & 1));
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------ MMA issuer ------------------------------
+        if (leader) {
+            const uint32_t ring = smem_u32(smem);
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_wait_cluster_bounded(bar, parity, abort_flag, p.err)) != 0;
+            };
+            int stage = 0, local = 0, unit = 0;
+            uint32_t phase = 0, uphase = 0, last_bar = 0, last_parity = 0;
+            bool ok = true, committed = false;
+            for (int64_t t = first; t < total && ok; t += stride) {
+                const int columns = __shfl_sync(0xffffffffu, columns_of(tile_at(t)), 0);
+                if (columns == 0) continue;
+                const uint32_t idesc = idesc_mxf8(256, static_cast<uint32_t>(columns));
+                const int acc = local & 1;
+                ok = wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t d = tmem + static_cast<uint32_t>(acc * G8_ACC);
+                for (int s = 0; s < p.slices; ++s) {
+                    const int in_unit = s % G8_UNIT;
+                    if (in_unit == 0) ok = wait(sfull_bar(unit), uphase);
+                    ok = ok && wait(full_bar(stage), phase);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t a = ring + stage * G8_STAGE;
+                    const uint64_t a_desc = smem_desc_sw128(a), b_desc = smem_desc_sw128(a + 2 * G8_A_HALF);
+                    const uint32_t sfa = tmem + G8_SF_COL0 + unit * G8_UNIT_COLS + in_unit * G8_SF_COLS, sfb = sfa + 8u;
+                    const int left = static_cast<int>(p.K) - s * G8_SLICE;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (k * 32 >= left) break;
+                        const uint32_t id = k & 3, h = k >> 2;
+                        tc_mma2_mxf8(d, a_desc + (G8_A_HALF >> 4) * h + 2u * id, b_desc + (G8_B_HALF >> 4) * h + 2u * id,
+                                     idesc | (id << 29) | (id << 4), sfa + 4u * h, sfb + 4u * h, (s | k) != 0 ? 1u : 0u);
+                    }
+                    tc_commit2_both_elect(empty_bar(stage));  // frees the stage in both CTAs
+                    last_bar = empty_bar(stage);
+                    last_parity = phase;
+                    committed = true;
+                    if (++stage == G8_STAGES) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
+                    if (in_unit == G8_UNIT - 1 || s == p.slices - 1) {
+                        tc_commit2_both_elect(sempty_bar(unit));
+                        if (++unit == G8_UNITS) {
+                            unit = 0;
+                            uphase ^= 1u;
+                        }
+                    }
+                }
+                if (!ok) break;
+                tc_commit2_both_elect(tfull_bar(acc));
+                ++local;
+            }
+            if (!ok && committed && lane == 0) g8_drain(last_bar, last_parity);
+        }
+    } else if (warp >= G8_SF_WARP0) {
+        // -------------------------------- scales --------------------------------
+        // groups of four warps take the units in turn
+        const int r = (threadIdx.x - G8_SF_WARP0 * 32) & 127;
+        const int group = (warp - G8_SF_WARP0) >> 2;
+        const int kb = static_cast<int>(p.K / 32), span = p.units * 8 * G8_UNIT;
+        uint8_t *const staging = staging0 + group * G8_SF_BYTES;
+        UnitScales vw[G8_AHEAD], vr[G8_AHEAD];  // weights', rows'
+        int64_t lt = first;                     // next unit to load: its tile, its scale bytes
+        int at = group * 8 * G8_UNIT;           // byte offset of that unit in its row
+        const uint8_t *pw = nullptr, *pr = nullptr;  // the thread's rows; null where there is none
+        auto next_tile = [&]() {
+            for (; lt < total; lt += stride) {
+                const G8Tile ti = tile_at(lt);
+                if (ti.rows == 0) continue;
+                if (at >= span) {  // past this tile: the units go on in the next one
+                    at -= span;
+                    continue;
+                }
+                const bool up = GATE_UP && r >= OWN;
+                const int64_t f = ti.n0 + (up ? r - OWN : r);
+                pw = f < p.N ? (up ? p.sf_b1 : p.sf_b0) + (static_cast<int64_t>(ti.g) * p.N + f) * kb : nullptr;
+                pr = r < ti.rows ? p.sf_a + (static_cast<int64_t>(ti.m_start) + r) * kb : nullptr;
+                return;
+            }
+        };
+        next_tile();
+        auto load = [&](UnitScales &w, UnitScales &x) {
+            load_scales<V>(w, pw, kb, at);
+            load_scales<V>(x, pr, kb, at);
+            at += 8 * G8_UNIT * G8_SF_GROUPS;
+            if (at >= span) next_tile();
+        };
+        int ahead = 0;  // units in registers
+#pragma unroll
+        for (int j = 0; j < G8_AHEAD; ++j)
+            if (lt < total) {
+                load(vw[j], vr[j]);
+                ++ahead;
+            }
+        int unit = group;
+        uint32_t phase = 0;
+        bool ok = true;
+        while (ok && ahead > 0) {
+#pragma unroll
+            for (int j = 0; j < G8_AHEAD; ++j) {
+                if (!ok || ahead == 0) continue;
+                // 512 bytes for each 128 elements, the weights' then the rows': a row's word at 4 r
+                uint32_t *const mine = reinterpret_cast<uint32_t *>(staging) + r;
+#pragma unroll
+                for (int i = 0; i < 2 * G8_UNIT; ++i) {
+                    mine[((i & ~1) * 2 + (i & 1)) * 128] = vw[j].w[i];
+                    mine[((i & ~1) * 2 + 2 + (i & 1)) * 128] = vr[j].w[i];
+                }
+                int free = 1;
+                if (lane == 0) free = mbar_wait_cluster_bounded(sempty_bar(unit), phase ^ 1u, abort_flag, p.err) ? 1 : 0;
+                free = __shfl_sync(0xffffffffu, free, 0);
+                // every thread of the group has stored.  A warp whose wait gave up
+                // comes here too and takes the group along
+                ok = g8_all<128>(1 + group, free != 0);
+                if (!ok) continue;
+                // each warp puts all rows' scales into its own lane quarter:
+                // lane i, column c holds row 32 c + i
+                tc_fence_after();
+                const uint32_t col = tmem + ((warp & 3u) << 21) + G8_SF_COL0 + unit * G8_UNIT_COLS;
+#pragma unroll
+                for (int i = 0; i < 2 * G8_UNIT; ++i)
+                    tmem_st8(col + 8u * i, quarter_scales(staging + 1024 * i + lane * 4), quarter_scales(staging + 1024 * i + 512 + lane * 4));
+                tmem_st_wait();
+                tc_fence_before();
+                g8_all<128>(1 + group, true);  // the group has read: the next unit may be stored
+                if (lane == 0) {
+                    if (leader)
+                        mbar_arrive(sfull_bar(unit));
+                    else
+                        mbar_arrive_remote(smem_map_rank(sfull_bar(unit), 0));
+                }
+                unit += G8_SF_GROUPS;
+                if (unit >= G8_UNITS) {
+                    unit -= G8_UNITS;
+                    phase ^= 1u;
+                }
+                --ahead;
+                if (lt < total) {
+                    load(vw[j], vr[j]);
+                    ++ahead;
+                }
+            }
+        }
+    } else {
+        // ------------------------------- epilogue -------------------------------
+        // two warps to a lane quarter, each with every other 32 (gate/up: 16) columns,
+        // rows of the block; a lane is a feature
+        const int q = warp & 3, set = (warp - G8_EPI_WARP0) >> 2;
+        const uint32_t tempty_leader = smem_map_rank(tempty_bar(0), 0);  // + 8 * acc
+        // gate/up: quarters q and q + 2 hold the same features' gate and up sums
+        const int pair = set * 2 + (q & 1);
+        const bool up = GATE_UP && q >= 2;
+        float *send = exchange + pair * 512 + (up ? 256 : 0), *take = exchange + pair * 512 + (up ? 0 : 256);
+        int local = 0;
+        for (int64_t t = first; t < total; t += stride) {
+            const G8Tile ti = tile_at(t);
+            if (ti.rows == 0) continue;
+            const int acc = local & 1;
+            int ready = 1;
+            if (lane == 0)
+                ready = mbar_wait_cluster_bounded(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err) ? 1 : 0;
+            ready = __shfl_sync(0xffffffffu, ready, 0);
+            if constexpr (GATE_UP) ready = g8_all<64>(1 + G8_SF_GROUPS + pair, ready != 0);  // both or neither go on
+            if (!ready) break;
+            tc_fence_after();
+            const uint32_t d = tmem + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(acc * G8_ACC);
+            if constexpr (GATE_UP) {
+                const int f0 = ti.n0 + (q & 1) * 32;
+                uint8_t *const q_h = p.q_h + static_cast<int64_t>(ti.m_start) * p.N + f0 + lane;
+                uint8_t *const sf_h = p.sf_h + static_cast<int64_t>(ti.m_start) * (p.N / 32) + f0 / 32;
+                if (f0 < p.N) {
+#pragma unroll 1
+                    for (int c = set * 16; c < ti.rows; c += 32) {
+                        uint32_t v[16];
+                        tmem_ld16(d + c, v);
+                        tmem_ld_wait();
+                        // the gate's warp takes the first 8 rows, up's the others
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) send[i * 32 + lane] = __uint_as_float(up ? v[i] : v[8 + i]);
+                        g8_all<64>(1 + G8_SF_GROUPS + pair, true);
+                        const int row0 = c + (up ? 8 : 0);
+                        uint32_t scale = 0;
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float own = __uint_as_float(up ? v[8 + i] : v[i]), other = take[i * 32 + lane];
+                            const float g = up ? other : own, u = up ? own : other;
+                            const float h = __fdividef(g, 1.0f + __expf(-g)) * u;
+                            const uint32_t s = mx8_scale(__reduce_max_sync(0xffffffffu, magnitude_bits(h)));
+                            const uint32_t e = e4m3x4(h, 0.0f, 0.0f, 0.0f, mx8_inverse(s), s == 255u);
+                            if (row0 + i < ti.rows) q_h[static_cast<int64_t>(row0 + i) * p.N] = static_cast<uint8_t>(e);
+                            scale = lane == i ? s : scale;
+                        }
+                        if (lane < 8 && row0 + lane < ti.rows)
+                            sf_h[static_cast<int64_t>(row0 + lane) * (p.N / 32)] = static_cast<uint8_t>(scale);
+                        g8_all<64>(1 + G8_SF_GROUPS + pair, true);  // both have read
+                    }
+                }
+            } else {
+                const int64_t f = ti.n0 + q * 32 + lane;
+                TOut *const out = static_cast<TOut *>(p.out) + static_cast<int64_t>(ti.m_start) * p.N + f;
+#pragma unroll 1
+                for (int c = set * 32; c < ti.rows; c += 64) {
+                    uint32_t v[32];
+                    tmem_ld32(d + c, v);
+                    tmem_ld_wait();
+                    if (f < p.N) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (c + i < ti.rows) out[static_cast<int64_t>(c + i) * p.N] = from_f32<TOut>(__uint_as_float(v[i]));
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader)
+                    mbar_arrive(tempty_bar(acc));
+                else
+                    mbar_arrive_remote(tempty_leader + 8u * static_cast<uint32_t>(acc));
+            }
+            ++local;
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync_all();  // neither CTA leaves while the pair's MMAs or arrivals may touch it
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc2(tmem, 512);
     }
 }
 
+bool rows_map(CUtensorMap *m, const uint8_t *q, int64_t K, int64_t rows, uint32_t box_rows) {
+    const uint64_t dims[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(rows)};
+    const uint64_t strides[1] = {static_cast<uint64_t>(K)};
+    const uint32_t box[2] = {128, box_rows};
+    return encode_tma_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, q, dims, strides, box, 1);
+}
+
+// of 16, 32 and 64 rows
+bool rows_maps(CUtensorMap *m, const uint8_t *q, int64_t K, int64_t rows) {
+    return rows_map(m, q, K, rows, 16) && rows_map(m + 1, q, K, rows, 32) && rows_map(m + 2, q, K, rows, 64);
+}
+
+bool weights_map(CUtensorMap *m, const uint8_t *q, int64_t K, int64_t N, int64_t E, uint32_t box_rows) {
+    const uint64_t dims[3] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N), static_cast<uint64_t>(E)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(K), static_cast<uint64_t>(N * K)};
+    const uint32_t box[3] = {128, box_rows, 1};
+    return encode_tma_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box, 1);
+}
+
+template <typename TOut, int V>
+cudaError_t launch_v(const CUtensorMap *maps, const G8Params &p, cudaStream_t stream) {
+    auto kern = mx8_gemm_kernel<TOut, V>;
+    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
+    if (dev < 0 || dev >= 64 || !attr_done[dev]) {
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G8_SMEM);
+        if (e != cudaSuccess) return e;
+        if (dev >= 0 && dev < 64) attr_done[dev] = true;
+    }
+    const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_tiles, pairs = device_sm_count() / 2;
+    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), dim3(G8_THREADS), G8_SMEM, stream,
+                      maps[0], maps[1], maps[2], maps[3], maps[4], p);
+}
+
+// the widest scale loads that K and the bases' alignment allow
 template <typename TOut>
-cudaError_t launch_product(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b, const MxTables &tab,
-                           int64_t m_blocks, int64_t N, int64_t K, void *C, cudaStream_t stream) {
-    return launch_pdl(mx8_gemm_kernel<TOut, false>, dim3(static_cast<unsigned>((N + 31) / 32), static_cast<unsigned>(m_blocks)),
-                      dim3(G8_WARPS * 32), 0, stream, q_a, sf_a, q_b, sf_b, q_b, sf_b, tab, N, K, static_cast<TOut *>(C),
-                      static_cast<uint8_t *>(nullptr), static_cast<uint8_t *>(nullptr));
+cudaError_t launch_n(const CUtensorMap *maps, const G8Params &p, cudaStream_t stream) {
+    const uintptr_t bases = reinterpret_cast<uintptr_t>(p.sf_a) | reinterpret_cast<uintptr_t>(p.sf_b0) |
+                            reinterpret_cast<uintptr_t>(p.sf_b1);
+    if (p.K % 512 == 0 && (bases & 15u) == 0) return launch_v<TOut, 16>(maps, p, stream);
+    if (p.K % 256 == 0 && (bases & 7u) == 0) return launch_v<TOut, 8>(maps, p, stream);
+    if (p.K % 128 == 0 && (bases & 3u) == 0) return launch_v<TOut, 4>(maps, p, stream);
+    return launch_v<TOut, 1>(maps, p, stream);
+}
+
+G8Params params(const uint8_t *sf_a, const uint8_t *sf_b0, const uint8_t *sf_b1, const MxTables &tab, int64_t m_blocks,
+                int64_t N, int64_t K, int tile, int32_t *err) {
+    G8Params p{};
+    p.sf_a = sf_a;
+    p.sf_b0 = sf_b0;
+    p.sf_b1 = sf_b1;
+    p.tab = tab;
+    p.m_blocks = static_cast<int>(m_blocks);
+    p.N = N;
+    p.K = K;
+    p.n_tiles = static_cast<int>((N + tile - 1) / tile);
+    p.slices = static_cast<int>((K + G8_SLICE - 1) / G8_SLICE);
+    p.units = (p.slices + G8_UNIT - 1) / G8_UNIT;
+    p.err = err;
+    return p;
 }
 
 }  // namespace
@@ -76,9 +617,14 @@ cudaError_t launch_product(const uint8_t *q_a, const uint8_t *sf_a, const uint8_
 cudaError_t launch_grouped_gemm_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_b, const uint8_t *sf_b,
                                     const MxTables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
                                     int64_t E, int out_dtype, void *C, int32_t *err, cudaStream_t stream) {
-    if (out_dtype == kF32) return launch_product<float>(q_a, sf_a, q_b, sf_b, tab, m_blocks, N, K, C, stream);
-    if (out_dtype == kBF16) return launch_product<__nv_bfloat16>(q_a, sf_a, q_b, sf_b, tab, m_blocks, N, K, C, stream);
-    return launch_product<__half>(q_a, sf_a, q_b, sf_b, tab, m_blocks, N, K, C, stream);
+    CUtensorMap maps[5];
+    if (!rows_maps(maps, q_a, K, n_rows) || !weights_map(&maps[3], q_b, K, N, E, 128)) return cudaErrorInvalidValue;
+    maps[4] = maps[3];
+    G8Params p = params(sf_a, sf_b, sf_b, tab, m_blocks, N, K, 256, err);
+    p.out = C;
+    if (out_dtype == kF32) return launch_n<float>(maps, p, stream);
+    if (out_dtype == kBF16) return launch_n<__nv_bfloat16>(maps, p, stream);
+    return launch_n<__half>(maps, p, stream);
 }
 
 cudaError_t launch_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
@@ -86,9 +632,14 @@ cudaError_t launch_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *s
                                             const MxTables &tab, int64_t m_blocks, int64_t n_rows, int64_t d_h,
                                             int64_t d_e, int64_t E, uint8_t *q_h, uint8_t *sf_h, int32_t *err,
                                             cudaStream_t stream) {
-    return launch_pdl(mx8_gemm_kernel<float, true>, dim3(static_cast<unsigned>(d_e / 32), static_cast<unsigned>(m_blocks)),
-                      dim3(G8_WARPS * 32), 0, stream, q_a, sf_a, q_gate, sf_gate, q_up, sf_up, tab, d_e, d_h,
-                      static_cast<float *>(nullptr), q_h, sf_h);
+    CUtensorMap maps[5];
+    if (!rows_maps(maps, q_a, d_h, n_rows) || !weights_map(&maps[3], q_gate, d_h, d_e, E, 64) ||
+        !weights_map(&maps[4], q_up, d_h, d_e, E, 64))
+        return cudaErrorInvalidValue;
+    G8Params p = params(sf_a, sf_gate, sf_up, tab, m_blocks, d_e, d_h, 128, err);
+    p.q_h = q_h;
+    p.sf_h = sf_h;
+    return launch_n<void>(maps, p, stream);
 }
 
 }  // namespace moe

@@ -2,10 +2,14 @@
 grouped products, the layer of them and the block.
 
 Quantisation, dequantisation and the sort are held bit for bit to a list of what 8
-bits can hold.  The products' terms are exact, so their error is that of fp32 sums:
-2^-20 of the sum of the terms' magnitudes (the tensor cores add 32 products at a
-time, each aligned to the largest and cut at 24 bits or more, then up to 1024 such
-sums in fp32), plus half a step of the output's type."""
+bits can hold.  The products' terms are exact, so their error is that of the tensor
+cores' sums.  Those add 32 products and the sum so far at a time: each is cut at 2^-25
+of the largest one's power of two (2^16 + 16 2^-9 is exact, 2^16 + 16 2^-10 gives
+2^16) and the result at 24 bits (1 + 2^-23 is exact, 1 + 2^-24 gives 1).  No partial
+sum and no product exceeds m, the sum of the terms' magnitudes, so one step is off by
+at most (32 2^-25 + 2^-23) m = 1.125 2^-20 m, and K / 32 of them by that many times
+as much; to that comes half a step of the output's type.  Sums that need no more than
+24 bits are exact, which a test of whole numbers holds them to."""
 import pytest
 import torch
 
@@ -17,7 +21,11 @@ pytestmark = pytest.mark.gpu
 
 DT = {"f16": torch.float16, "bf16": torch.bfloat16, "f32": torch.float32}
 E4M3 = torch.float8_e4m3fn
-SUM = 2.0 ** -20
+
+
+def sum_off(K):
+    """How far a sum of K terms may be, relative to the sum of their magnitudes."""
+    return -(-K // 32) * 1.125 * 2.0 ** -20
 
 
 def grid(device):
@@ -292,21 +300,39 @@ def test_product(T, k, E, K, N, out):
     want, mag = product_and_size(values64(qa, sa), values64(qb, sb), t)
     assert int(err.item()) == 0
     top = torch.finfo(DT[out]).max
-    fits = want.abs() + SUM * mag < top
+    fits = want.abs() + sum_off(K) * mag < top
     step = torch.finfo(DT[out]).eps / 2
-    bad = (got.double() - want).abs() > SUM * mag + step * want.abs() + torch.finfo(DT[out]).smallest_normal * step
+    bad = (got.double() - want).abs() > sum_off(K) * mag + step * want.abs() + torch.finfo(DT[out]).smallest_normal * step
     assert not (bad & fits).any(), int((bad & fits).sum())
+
+
+@pytest.mark.parametrize("T,k,E,K,N", SHAPES + [(300, 2, 3, 7168, 300), (1000, 2, 5, 2080, 130)])
+def test_product_of_whole_numbers(T, k, E, K, N):
+    """Elements of up to 4, scales of 1, 2 and 4: every partial sum is a whole number of at most 7168 * 256 <
+    2^24, and the result is exact in fp32."""
+    require_cuda()
+    t, g = routed(T, k, E, T + K)
+
+    def whole(rows):
+        q = torch.randint(-4, 5, (rows, K), generator=g, device="cuda").float()
+        q *= torch.rand((rows, K), generator=g, device="cuda") < 0.5
+        return q.to(E4M3), torch.randint(127, 130, (rows, K // 32), generator=g, device="cuda").to(torch.uint8)
+    (qa, sa), (qb, sb) = whole(T * k), whole(E * N)
+    qb, sb = qb.view(E, N, K), sb.view(E, N, K // 32)
+    want, mag = product_and_size(values64(qa, sa), values64(qb, sb), t)
+    assert float(mag.max()) < 2 ** 24
+    assert torch.equal(binding.moe_grouped_gemm_mx8(qa, sa, qb, sb, t, torch.float32).double(), want)
 
 
 def silu_products(t, qa, sa, gate, up):
     """h in 64 bits and how far the kernel's fp32 h may be: from the two sums, each product's derivative, and
     2^-20 of h for the exponential (2 + 1.2 |g| units), the quotient (2) and the product."""
-    a = values64(qa, sa)
+    a, off = values64(qa, sa), sum_off(qa.shape[1])
     g, mg = product_and_size(a, values64(*gate), t)
     u, mu = product_and_size(a, values64(*up), t)
     s = g * torch.sigmoid(g)
     h = s * u
-    return h, 1.1 * SUM * mg * (u.abs() + SUM * mu) + SUM * mu * s.abs() + (2.0 ** -20 + 2.0 ** -22 * g.abs()) * h.abs()
+    return h, 1.1 * off * mg * (u.abs() + off * mu) + off * mu * s.abs() + (2.0 ** -20 + 2.0 ** -22 * g.abs()) * h.abs()
 
 
 @pytest.mark.parametrize("T,k,E,K,N", [(1, 1, 1, 32, 32), (1, 8, 8, 256, 128), (5, 2, 3, 64, 96), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 352),
@@ -351,7 +377,7 @@ def test_products_of_odd_values():
     assert (got[10][~nan[10]] == 0).all()
     ok = ~nan
     ok[10] = False
-    assert ((got.double() - want).abs() <= SUM * mag + 2.0 ** -24 * want.abs())[ok].all()
+    assert ((got.double() - want).abs() <= sum_off(K) * mag + 2.0 ** -24 * want.abs())[ok].all()
     e = binding.Mx8Experts(qb, sb, qb, torch.full_like(sb, 127), *(x.view(E, K, -1) for x in rows8(E * K, N, g)))
     q, sf = binding.moe_grouped_gate_up_silu_mx8(qa, sa, e, t)
     bad = torch.zeros((T, N // 32), dtype=torch.bool, device="cuda")
