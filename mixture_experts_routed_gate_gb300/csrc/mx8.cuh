@@ -29,6 +29,13 @@ __device__ __forceinline__ float mx8_factor(uint32_t byte) {
     return __uint_as_float(byte ? byte << 23 : 1u << 22);
 }
 
+// the largest magnitude of three, NaN if one of them is
+__device__ __forceinline__ float largest(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 __device__ __forceinline__ uint32_t magnitude_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 
 // two elements, a in the low byte: to nearest even

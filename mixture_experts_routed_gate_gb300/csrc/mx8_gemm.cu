@@ -5,24 +5,24 @@
 //
 // and the gate/up form, h = silu(A Wg^T) * (A Wu^T), quantised to 8 bits.
 //
-// The weights are the M = 256 operand (128 rows in each SM), the rows of a
-// dispatch block the N operand (32 to 128, half in each SM): a tile costs what
-// its rows cost, and every weight byte enters one SM's shared memory once a
-// block.  The accumulator holds features in lanes and rows in columns, so a warp
+// The weights are the M = 256 operand (128 rows in each SM), up to 128 or 256
+// rows of an expert the N operand (in steps of 32, half in each SM): a tile costs
+// what its rows cost, and every weight byte enters one SM's shared memory once a
+// tile.  The accumulator holds features in lanes and rows in columns, so a warp
 // stores 32 consecutive features of a row.
 //
-// A persistent pair works on tiles of one dispatch block by 256 features (128 in
-// the gate/up form: 64 of W_gate and 64 of W_up in each SM).  Roles in each CTA:
+// A persistent pair works on tiles of such rows by 256 features (128 in the
+// gate/up form: 64 of W_gate and 64 of W_up in each SM).  Roles in each CTA:
 //   warp 0      TMA: 256-element slices of its weights and of its half of the
 //               rows into a ring of 128-byte-swizzled stages, completing on the
 //               even CTA's barriers;
 //   warp 1      (even CTA) one elected lane: eight K = 32 MMAs a slice;
 //   warps 2-9   epilogue, from one of two accumulators while the other fills;
-//   warps 10-17 scales, a unit of four slices at a time, two groups in turn: each
-//               thread loads a weight row's and a row's 32 scale bytes, a unit
+//   warps 10-17 scales, a unit of two slices at a time, two groups in turn: each
+//               thread loads a weight row's and a row's 16 scale bytes, two units
 //               ahead; through shared memory each warp gets every row's and
 //               stores them to its quarter of tensor memory.  Both CTAs hold all
-//               rows' scales.  The units have their own ring, of four, so that
+//               rows' scales.  The units have their own ring, of eight, so that
 //               their way into tensor memory runs ahead of the slices.
 #include "common.cuh"
 #include "internal.h"
@@ -34,26 +34,32 @@ namespace {
 
 constexpr int G8_SLICE = 256;               // elements (bytes) of K per stage: two 128-byte halves
 constexpr int G8_A_HALF = 128 * 128;        // 128 weight rows of one half
-constexpr int G8_B_HALF = 64 * 128;         // up to 64 rows of one half
-constexpr int G8_STAGE = 2 * (G8_A_HALF + G8_B_HALF);
-constexpr int G8_STAGES = 4;
 constexpr int G8_THREADS = 576;
 constexpr int G8_EPI_WARP0 = 2, G8_EPI_WARPS = 8, G8_SF_WARP0 = 10, G8_SF_GROUPS = 2;
-constexpr int G8_UNIT = 4;                  // slices whose scales are stored together
-constexpr int G8_UNITS = 4;                 // units in tensor memory
-constexpr int G8_AHEAD = 2;                 // units in registers ahead of those, a group
-constexpr int G8_LIST = 512;                // M blocks with rows that the shared-memory list holds
-constexpr int G8_ACC = 128;                 // columns of an accumulator
-constexpr int G8_SF_COL0 = 2 * G8_ACC, G8_SF_COLS = 16;  // a stage's scales: two halves of 4 columns for each operand
-constexpr int G8_UNIT_COLS = G8_UNIT * G8_SF_COLS;
-constexpr int G8_SF_BYTES = 4 * G8_UNIT * 512;
-constexpr int G8_EXCHANGE = 4 * 2 * 8 * 32 * 4;  // gate/up: four pairs of epilogue warps, 8 rows by 32 features each way
-constexpr int G8_FIXED = 1024 + 512 + G8_LIST * 8 + G8_SF_GROUPS * G8_SF_BYTES + G8_EXCHANGE;
-constexpr int G8_SMEM = G8_STAGES * G8_STAGE + G8_FIXED;
-static_assert(G8_SMEM <= 232448 - 256, "shared memory");
-static_assert(G8_SF_COL0 + G8_UNITS * G8_UNIT_COLS <= 512, "tensor memory");
-static_assert(G8_UNITS % G8_SF_GROUPS == 0, "the groups alternate");
-static_assert((2 * G8_STAGES + 2 * G8_UNITS + 4) * 8 <= 512, "barriers");
+constexpr int G8_LIST = 512;                // units of rows that the shared-memory list holds
+constexpr int G8_ACC = 128;                 // columns of an accumulator slot; wider units take both
+constexpr int G8_UNIT = 2;                  // slices whose scales are stored together
+constexpr int G8_AHEAD = 2;                 // units of scales in registers ahead of tensor memory's, a group
+constexpr int G8_EXCHANGE = 4 * 2 * 2 * 8 * 32 * 4;  // gate/up: four pairs of epilogue warps, 8 rows by 32 features each way, twice
+
+// NT: the most rows of a tile, 128 or 256
+template <int NT> struct G8Layout {
+    static constexpr int B_HALF = NT / 2 * 128;  // up to NT / 2 rows of one half
+    static constexpr int STAGE = 2 * (G8_A_HALF + B_HALF);
+    static constexpr int STAGES = NT == 128 ? 4 : 3;
+    static constexpr int UNITS = NT == 128 ? 8 : 4;  // units of scales in tensor memory
+    static constexpr int ROWS = NT / 128;           // rows whose scales a thread loads
+    // a slice's scales: two halves of 4 columns for the weights, then two of 4 for each 128 rows
+    static constexpr int SF_COLS = 8 + 8 * ROWS, UNIT_COLS = G8_UNIT * SF_COLS;
+    static constexpr int SF_BYTES = UNIT_COLS * 128;
+    static constexpr int SF_COL0 = 2 * G8_ACC;
+    static constexpr int FIXED = 1024 + 512 + G8_LIST * 8 + G8_SF_GROUPS * SF_BYTES + G8_EXCHANGE;
+    static constexpr int SMEM = STAGES * STAGE + FIXED;
+    static_assert(SMEM <= 232448 - 256, "shared memory");
+    static_assert(SF_COL0 + UNITS * UNIT_COLS <= 512, "tensor memory");
+    static_assert(UNITS % G8_SF_GROUPS == 0, "the groups alternate");
+    static_assert((2 * STAGES + 2 * UNITS + 4) * 8 <= 512, "barriers");
+};
 
 struct G8Params {
     const uint8_t *sf_a, *sf_b0, *sf_b1;  // b1: the up weights of the gate/up form
@@ -61,13 +67,40 @@ struct G8Params {
     void *out;
     uint8_t *q_h, *sf_h;
     int32_t *err;
-    int m_blocks, n_tiles, slices, units;
+    int m_blocks, E, n_tiles, slices, units;
     int64_t N, K;
 };
 
 struct G8Tile {
     int g, m_start, rows, n0;
-    bool single;  // the expert's only block
+    bool single;  // the expert's only unit of rows
+};
+
+// Units of NT rows: every block of the dispatch tables, or every other one of an
+// expert with the block behind it.
+template <int NT> __device__ __forceinline__ Mx4Block unit_of(const MxTables &t, int bx, int m_blocks) {
+    Mx4Block b;
+    b.g = t.gidx[bx];
+    const int off = bx * 128 - t.padded[b.g];
+    b.m_start = off + t.offsets[b.g];
+    b.rows = off % NT ? 0 : max(0, min(min(t.sizes[b.g] - off, (m_blocks - bx) * 128), NT));
+    return b;
+}
+
+// The accumulator slots in turn; a unit of more rows than a slot's columns takes
+// both.  Every role follows the same sequence of tiles, and so of slots.
+struct G8Slots {
+    int cur = 0;
+    uint32_t used = 0;  // a bit a slot: how often, modulo 2
+    int first;
+    bool both;
+    __device__ __forceinline__ void take(int columns) {
+        both = columns > G8_ACC;
+        first = both ? 0 : cur;
+        cur = both ? 0 : cur ^ 1;
+    }
+    __device__ __forceinline__ uint32_t parity(int slot) const { return used >> slot & 1u; }
+    __device__ __forceinline__ void done() { used ^= both ? 3u : 1u << first; }
 };
 
 // kind::mxf8f6f4: e4m3 by e4m3 (format 0), e8m0 scales; the scale ids (which of
@@ -130,52 +163,61 @@ __device__ __forceinline__ void g8_drain(uint32_t bar, uint32_t parity) {
         if (global_timer_ns() - start > kWaitTimeoutNs) return;
 }
 
-// A unit's 32 scale bytes of a row.
-struct UnitScales {
-    uint32_t w[2 * G8_UNIT];  // a word for each 128 elements
-};
-
-// From byte `at` on of a row of kb bytes (null: zeros); bytes past kb are 0 (their
-// elements are not multiplied).  V: the load width that kb and the bases'
-// alignment allow.
-template <int V> __device__ __forceinline__ void load_scales(UnitScales &u, const uint8_t *row, int kb, int at) {
-    constexpr int WORDS = V < 4 ? 1 : V / 4;
+// A unit's scale bytes of a row, WORDS words of 128 elements, from byte `at` on of a
+// row of kb bytes (null: zeros); bytes past kb are 0 (their elements are not
+// multiplied).  V: the load width that kb and the bases' alignment allow.
+template <int V, int WORDS>
+__device__ __forceinline__ void load_scales(uint32_t (&w)[WORDS], const uint8_t *row, int kb, int at) {
+    constexpr int STEP = V < 4 ? 1 : V / 4;
+    if constexpr (V >= 4) {
 #pragma unroll
-    for (int i = 0; i < 2 * G8_UNIT; i += WORDS) {
-        const int byte = at + 4 * i;
-        const bool in = row != nullptr && byte < kb;
-        const uint8_t *p = row + byte;
-        if constexpr (V == 16) {
-            const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
-            u.w[i] = v.x, u.w[i + 1] = v.y, u.w[i + 2] = v.z, u.w[i + 3] = v.w;
-        } else if constexpr (V == 8) {
-            const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
-            u.w[i] = v.x, u.w[i + 1] = v.y;
-        } else if constexpr (V == 4) {
-            u.w[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
-        } else {
-            u.w[i] = 0u;
+        for (int i = 0; i < WORDS; i += STEP) {
+            const int byte = at + 4 * i;
+            const bool in = row != nullptr && byte < kb;
+            const uint8_t *p = row + byte;
+            if constexpr (V == 16) {
+                const uint4 v = in ? __ldg(reinterpret_cast<const uint4 *>(p)) : make_uint4(0u, 0u, 0u, 0u);
+                w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
+            } else if constexpr (V == 8) {
+                const uint2 v = in ? __ldg(reinterpret_cast<const uint2 *>(p)) : make_uint2(0u, 0u);
+                w[i] = v.x, w[i + 1] = v.y;
+            } else {
+                w[i] = in ? __ldg(reinterpret_cast<const uint32_t *>(p)) : 0u;
+            }
+        }
+    } else {
+        // rows that start anywhere: the aligned words that hold their bytes (a word
+        // with one of the row's bytes lies in its allocation), shifted together
+        const uintptr_t first = reinterpret_cast<uintptr_t>(row) + at;
+        const uint32_t *p = reinterpret_cast<const uint32_t *>(first & ~uintptr_t{3});
+        const int skip = static_cast<int>(first & 3), have = row != nullptr ? kb - at : 0;  // the row's bytes from `at` on
+        uint32_t last = have > 0 ? __ldg(p) : 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (in && byte + j < kb) u.w[i] |= static_cast<uint32_t>(__ldg(p + j)) << (8 * j);
+        for (int i = 0; i < WORDS; ++i) {
+            const uint32_t next = have > 4 * (i + 1) - skip ? __ldg(p + i + 1) : 0u;
+            const int left = have - 4 * i;
+            const uint32_t v = __funnelshift_r(last, next, 8 * skip);
+            w[i] = left >= 4 ? v : left <= 0 ? 0u : v & ((1u << (8 * left)) - 1u);
+            last = next;
         }
     }
 }
 
 // TOut void: the gate/up form
-template <typename TOut, int V>
+template <typename TOut, int NT, int V>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     mx8_gemm_kernel(const __grid_constant__ CUtensorMap tmA16, const __grid_constant__ CUtensorMap tmA32,
                     const __grid_constant__ CUtensorMap tmA64, const __grid_constant__ CUtensorMap tmB0,
                     const __grid_constant__ CUtensorMap tmB1, const G8Params p) {
+    using L = G8Layout<NT>;
     constexpr bool GATE_UP = std::is_same<TOut, void>::value;
     constexpr int OWN = GATE_UP ? 64 : 128;  // features of a CTA's tile
     extern __shared__ uint8_t g8_smem_raw[];
     uint8_t *smem = g8_smem_raw + ((1024u - (smem_u32(g8_smem_raw) & 1023u)) & 1023u);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + G8_STAGES * G8_STAGE);
-    int2 *list = reinterpret_cast<int2 *>(smem + G8_STAGES * G8_STAGE + 512);  // first row; expert, only block, row count
-    uint8_t *staging0 = smem + G8_STAGES * G8_STAGE + 512 + G8_LIST * 8;
-    float *exchange = reinterpret_cast<float *>(staging0 + G8_SF_GROUPS * G8_SF_BYTES);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::STAGES * L::STAGE);
+    int2 *list = reinterpret_cast<int2 *>(smem + L::STAGES * L::STAGE + 512);  // first row; expert, only block, row count
+    uint8_t *staging0 = smem + L::STAGES * L::STAGE + 512 + G8_LIST * 8;
+    float *exchange = reinterpret_cast<float *>(staging0 + G8_SF_GROUPS * L::SF_BYTES);
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, warp_blocks[G8_THREADS / 32];
     volatile int *abort_flag = &abort_word;
@@ -184,18 +226,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     const bool leader = rank == 0;
     const uint32_t bar0 = smem_u32(bars);
     auto full_bar = [&](int i) { return bar0 + 8u * i; };  // the even CTA's, both CTAs' copies
-    auto empty_bar = [&](int i) { return bar0 + 8u * (G8_STAGES + i); };
-    auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + i); };
-    auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + 2 + i); };  // the even CTA's
-    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + 4 + i); };   // the even CTA's, both CTAs' scales
-    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * G8_STAGES + 4 + G8_UNITS + i); };
+    auto empty_bar = [&](int i) { return bar0 + 8u * (L::STAGES + i); };
+    auto tfull_bar = [&](int i) { return bar0 + 8u * (2 * L::STAGES + i); };
+    auto tempty_bar = [&](int i) { return bar0 + 8u * (2 * L::STAGES + 2 + i); };  // the even CTA's
+    auto sfull_bar = [&](int i) { return bar0 + 8u * (2 * L::STAGES + 4 + i); };   // the even CTA's, both CTAs' scales
+    auto sempty_bar = [&](int i) { return bar0 + 8u * (2 * L::STAGES + 4 + L::UNITS + i); };
 
     if (threadIdx.x == 0) {
-        for (int i = 0; i < G8_STAGES; ++i) {
+        for (int i = 0; i < L::STAGES; ++i) {
             mbar_init(full_bar(i), 1);
             mbar_init(empty_bar(i), 1);
         }
-        for (int i = 0; i < G8_UNITS; ++i) {
+        for (int i = 0; i < L::UNITS; ++i) {
             mbar_init(sfull_bar(i), 2 * 4);  // a group's warps of each CTA
             mbar_init(sempty_bar(i), 1);
         }
@@ -218,22 +260,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     griddep_wait();
     griddep_launch_dependents();
 
-    // the blocks that hold rows, in order, when they fit the list (the whole CTA
-    // looks at G8_THREADS blocks at a time: the tables' latency is paid once);
-    // both CTAs of a pair build the same list
+    // the units that hold rows, in order, when they fit the list: each thread looks
+    // at an expert (its three entries need one round trip; through the blocks'
+    // expert they need two, 0.6 us more), and a scan places its units; both CTAs of
+    // a pair build the same list
     int n_blocks = 0;
-    for (int b0 = 0; b0 < p.m_blocks && n_blocks <= G8_LIST; b0 += G8_THREADS) {
-        const int bx = b0 + static_cast<int>(threadIdx.x);
-        const Mx4Block b = bx < p.m_blocks ? mx4_block_of(p.tab, bx) : Mx4Block{0, 0, 0};
-        const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
-        if (lane == 0) warp_blocks[warp] = __popc(has);
+    for (int e0 = 0; e0 < p.E && n_blocks <= G8_LIST; e0 += G8_THREADS) {
+        const int g = e0 + static_cast<int>(threadIdx.x);
+        const bool in = g < p.E;
+        const int size = in ? __ldg(p.tab.sizes + g) : 0, m = in ? __ldg(p.tab.offsets + g) : 0;
+        const int block = in ? __ldg(p.tab.padded + g) / 128 : 0;
+        const int rows = max(0, min(size, (p.m_blocks - block) * 128)), mine = (rows + NT - 1) / NT;
+        int upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int before = __shfl_up_sync(0xffffffffu, upto, o);
+            upto += lane >= o ? before : 0;
+        }
+        if (lane == 31) warp_blocks[warp] = upto;
         __syncthreads();
-        int at = n_blocks + __popc(has & ((1u << lane) - 1u));
+        int at = n_blocks + upto - mine;
         for (int w = 0; w < G8_THREADS / 32; ++w) {
             at += w < warp ? warp_blocks[w] : 0;
             n_blocks += warp_blocks[w];
         }
-        if (b.rows > 0 && at < G8_LIST) list[at] = make_int2(b.m_start, b.g << 9 | (p.tab.sizes[b.g] <= 128 ? 256 : 0) | b.rows);
+        for (int u = 0; u < mine && at + u < G8_LIST; ++u)
+            list[at + u] = make_int2(m + u * NT, g << 10 | (mine == 1 ? 512 : 0) | min(rows - u * NT, NT));
         __syncthreads();
     }
     const int listed = n_blocks <= G8_LIST ? n_blocks : -1;
@@ -250,16 +302,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         ti.n0 = static_cast<int>(t - static_cast<int64_t>(b) * p.n_tiles) * (2 * OWN) + static_cast<int>(rank) * OWN;
         if (listed >= 0) {
             const int2 e = list[b];
-            ti.g = e.y >> 9;
+            ti.g = e.y >> 10;
             ti.m_start = e.x;
-            ti.rows = e.y & 255;
-            ti.single = (e.y & 256) != 0;
+            ti.rows = e.y & 511;
+            ti.single = (e.y & 512) != 0;
         } else {
-            const Mx4Block k = mx4_block_of(p.tab, b);
+            const Mx4Block k = unit_of<NT>(p.tab, b, p.m_blocks);
             ti.g = k.g;
             ti.m_start = k.m_start;
             ti.rows = k.rows;
-            ti.single = p.tab.sizes[k.g] <= 128;
+            ti.single = p.tab.sizes[k.g] <= NT;
         }
         return ti;
     };
@@ -276,16 +328,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             for (int64_t t = first; t < total && ok; t += stride) {
                 const G8Tile ti = tile_at(t);
                 if (ti.rows == 0) continue;
-                const int half = columns_of(ti) / 2;  // 16, 32, 48 or 64 rows: one copy or two
-                const CUtensorMap *const box = half == 64 ? &tmA64 : half == 16 ? &tmA16 : &tmA32;
+                const int half = columns_of(ti) / 2;  // a multiple of 16 rows
                 const int row0 = ti.m_start + static_cast<int>(rank) * half;
-                const uint64_t pol = ti.single ? pass : keep;  // an only block's weights are read once
+                const uint64_t pol = ti.single ? pass : keep;  // an only unit's weights are read once
                 for (int s = 0; s < p.slices; ++s) {
                     if (!mbar_wait_cluster_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t a = smem_u32(smem + stage * G8_STAGE), b = a + 2 * G8_A_HALF;
+                    const uint32_t a = smem_u32(smem + stage * L::STAGE), b = a + 2 * G8_A_HALF;
                     const int halves = s * G8_SLICE + 128 < p.K ? 2 : 1;
                     if (leader)
                         mbar_arrive_expect_tx(full_bar(stage), 2 * halves * (G8_A_HALF + half * 128));
@@ -294,11 +345,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         const int k0 = s * G8_SLICE + h * 128;
                         tma2_load_3d_hint(a + h * G8_A_HALF, &tmB0, fb, k0, ti.n0, ti.g, pol);
                         if (GATE_UP) tma2_load_3d_hint(a + h * G8_A_HALF + G8_A_HALF / 2, &tmB1, fb, k0, ti.n0, ti.g, pol);
-                        tma2_load_2d_hint(b + h * G8_B_HALF, box, fb, k0, row0, keep);
-                        if (half == 48) tma2_load_2d_hint(b + h * G8_B_HALF + 32 * 128, &tmA16, fb, k0, row0 + 32, keep);
+                        for (int i = 0; i < half; i += 64) {  // copies of 64, 32 and 16 rows
+                            const int have = half - i;
+                            const uint32_t to = b + h * L::B_HALF + i * 128;
+                            if (have >= 64) {
+                                tma2_load_2d_hint(to, &tmA64, fb, k0, row0 + i, keep);
+                            } else {
+                                if (have & 32) tma2_load_2d_hint(to, &tmA32, fb, k0, row0 + i, keep);
+                                if (have & 16) tma2_load_2d_hint(to + (have & 32) * 128, &tmA16, fb, k0, row0 + i + (have & 32), keep);
+                            }
+                        }
                     }
                     ++issued;
-                    if (++stage == G8_STAGES) {
+                    if (++stage == L::STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
@@ -306,9 +365,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             }
             if (leader && (!ok || *abort_flag)) {
                 // both CTAs' copies in flight land before shared memory goes away
-                for (long j = 1; j <= G8_STAGES && j <= issued; ++j) {
+                for (long j = 1; j <= L::STAGES && j <= issued; ++j) {
                     const long i = issued - j;
-                    g8_drain(full_bar(static_cast<int>(i % G8_STAGES)), static_cast<uint32_t>((i / G8_STAGES) & 1));
+                    g8_drain(full_bar(static_cast<int>(i % L::STAGES)), static_cast<uint32_t>((i / L::STAGES) & 1));
                 }
             }
         }
@@ -319,54 +378,56 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             auto wait = [&](uint32_t bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, mbar_wait_cluster_bounded(bar, parity, abort_flag, p.err)) != 0;
             };
-            int stage = 0, local = 0, unit = 0;
+            int stage = 0, unit = 0;
+            G8Slots slots;
             uint32_t phase = 0, uphase = 0, last_bar = 0, last_parity = 0;
             bool ok = true, committed = false;
             for (int64_t t = first; t < total && ok; t += stride) {
                 const int columns = __shfl_sync(0xffffffffu, columns_of(tile_at(t)), 0);
                 if (columns == 0) continue;
                 const uint32_t idesc = idesc_mxf8(256, static_cast<uint32_t>(columns));
-                const int acc = local & 1;
-                ok = wait(tempty_bar(acc), (static_cast<uint32_t>(local >> 1) & 1u) ^ 1u);
+                slots.take(columns);
+                ok = wait(tempty_bar(slots.first), slots.parity(slots.first) ^ 1u);
+                if (slots.both) ok = ok && wait(tempty_bar(1), slots.parity(1) ^ 1u);
                 if (!ok) break;
                 tc_fence_after();
-                const uint32_t d = tmem + static_cast<uint32_t>(acc * G8_ACC);
+                const uint32_t d = tmem + static_cast<uint32_t>(slots.first * G8_ACC);
                 for (int s = 0; s < p.slices; ++s) {
                     const int in_unit = s % G8_UNIT;
                     if (in_unit == 0) ok = wait(sfull_bar(unit), uphase);
                     ok = ok && wait(full_bar(stage), phase);
                     if (!ok) break;
                     tc_fence_after();
-                    const uint32_t a = ring + stage * G8_STAGE;
+                    const uint32_t a = ring + stage * L::STAGE;
                     const uint64_t a_desc = smem_desc_sw128(a), b_desc = smem_desc_sw128(a + 2 * G8_A_HALF);
-                    const uint32_t sfa = tmem + G8_SF_COL0 + unit * G8_UNIT_COLS + in_unit * G8_SF_COLS, sfb = sfa + 8u;
+                    const uint32_t sfa = tmem + L::SF_COL0 + unit * L::UNIT_COLS + in_unit * L::SF_COLS, sfb = sfa + 8u;
                     const int left = static_cast<int>(p.K) - s * G8_SLICE;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
                         if (k * 32 >= left) break;
                         const uint32_t id = k & 3, h = k >> 2;
-                        tc_mma2_mxf8(d, a_desc + (G8_A_HALF >> 4) * h + 2u * id, b_desc + (G8_B_HALF >> 4) * h + 2u * id,
-                                     idesc | (id << 29) | (id << 4), sfa + 4u * h, sfb + 4u * h, (s | k) != 0 ? 1u : 0u);
+                        tc_mma2_mxf8(d, a_desc + (G8_A_HALF >> 4) * h + 2u * id, b_desc + (L::B_HALF >> 4) * h + 2u * id,
+                                     idesc | (id << 29) | (id << 4), sfa + 4u * h, sfb + 4u * L::ROWS * h, (s | k) != 0 ? 1u : 0u);
                     }
                     tc_commit2_both_elect(empty_bar(stage));  // frees the stage in both CTAs
                     last_bar = empty_bar(stage);
                     last_parity = phase;
                     committed = true;
-                    if (++stage == G8_STAGES) {
+                    if (++stage == L::STAGES) {
                         stage = 0;
                         phase ^= 1u;
                     }
                     if (in_unit == G8_UNIT - 1 || s == p.slices - 1) {
                         tc_commit2_both_elect(sempty_bar(unit));
-                        if (++unit == G8_UNITS) {
+                        if (++unit == L::UNITS) {
                             unit = 0;
                             uphase ^= 1u;
                         }
                     }
                 }
                 if (!ok) break;
-                tc_commit2_both_elect(tfull_bar(acc));
-                ++local;
+                tc_commit2_both_elect(tfull_bar(slots.first));
+                slots.done();
             }
             if (!ok && committed && lane == 0) g8_drain(last_bar, last_parity);
         }
@@ -376,11 +437,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         const int r = (threadIdx.x - G8_SF_WARP0 * 32) & 127;
         const int group = (warp - G8_SF_WARP0) >> 2;
         const int kb = static_cast<int>(p.K / 32), span = p.units * 8 * G8_UNIT;
-        uint8_t *const staging = staging0 + group * G8_SF_BYTES;
-        UnitScales vw[G8_AHEAD], vr[G8_AHEAD];  // weights', rows'
+        uint8_t *const staging = staging0 + group * L::SF_BYTES;
+        constexpr int WORDS = 2 * G8_UNIT;
+        uint32_t vw[G8_AHEAD][WORDS], vr[G8_AHEAD][L::ROWS][WORDS];  // weights', rows'
         int64_t lt = first;                     // next unit to load: its tile, its scale bytes
         int at = group * 8 * G8_UNIT;           // byte offset of that unit in its row
-        const uint8_t *pw = nullptr, *pr = nullptr;  // the thread's rows; null where there is none
+        const uint8_t *pw = nullptr, *pr[L::ROWS];  // the thread's rows; null where there is none
         auto next_tile = [&]() {
             for (; lt < total; lt += stride) {
                 const G8Tile ti = tile_at(lt);
@@ -392,14 +454,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 const bool up = GATE_UP && r >= OWN;
                 const int64_t f = ti.n0 + (up ? r - OWN : r);
                 pw = f < p.N ? (up ? p.sf_b1 : p.sf_b0) + (static_cast<int64_t>(ti.g) * p.N + f) * kb : nullptr;
-                pr = r < ti.rows ? p.sf_a + (static_cast<int64_t>(ti.m_start) + r) * kb : nullptr;
+#pragma unroll
+                for (int i = 0; i < L::ROWS; ++i)
+                    pr[i] = 128 * i + r < ti.rows ? p.sf_a + (static_cast<int64_t>(ti.m_start) + 128 * i + r) * kb : nullptr;
                 return;
             }
         };
         next_tile();
-        auto load = [&](UnitScales &w, UnitScales &x) {
+        auto load = [&](uint32_t(&w)[WORDS], uint32_t(&x)[L::ROWS][WORDS]) {
             load_scales<V>(w, pw, kb, at);
-            load_scales<V>(x, pr, kb, at);
+#pragma unroll
+            for (int i = 0; i < L::ROWS; ++i) load_scales<V>(x[i], pr[i], kb, at);
             at += 8 * G8_UNIT * G8_SF_GROUPS;
             if (at >= span) next_tile();
         };
@@ -417,12 +482,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
 #pragma unroll
             for (int j = 0; j < G8_AHEAD; ++j) {
                 if (!ok || ahead == 0) continue;
-                // 512 bytes for each 128 elements, the weights' then the rows': a row's word at 4 r
+                // a slice's 512 bytes for each half of the weights, then for each half and
+                // 128 rows: a row's word at 4 r
                 uint32_t *const mine = reinterpret_cast<uint32_t *>(staging) + r;
 #pragma unroll
-                for (int i = 0; i < 2 * G8_UNIT; ++i) {
-                    mine[((i & ~1) * 2 + (i & 1)) * 128] = vw[j].w[i];
-                    mine[((i & ~1) * 2 + 2 + (i & 1)) * 128] = vr[j].w[i];
+                for (int i = 0; i < WORDS; ++i) {
+                    uint32_t *const slice = mine + (i >> 1) * L::SF_COLS * 32;
+                    slice[(i & 1) * 128] = vw[j][i];
+#pragma unroll
+                    for (int n = 0; n < L::ROWS; ++n) slice[(2 + (i & 1) * L::ROWS + n) * 128] = vr[j][n][i];
                 }
                 int free = 1;
                 if (lane == 0) free = mbar_wait_cluster_bounded(sempty_bar(unit), phase ^ 1u, abort_flag, p.err) ? 1 : 0;
@@ -434,9 +502,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 // each warp puts all rows' scales into its own lane quarter:
                 // lane i, column c holds row 32 c + i
                 tc_fence_after();
-                const uint32_t col = tmem + ((warp & 3u) << 21) + G8_SF_COL0 + unit * G8_UNIT_COLS;
+                const uint32_t col = tmem + ((warp & 3u) << 21) + L::SF_COL0 + unit * L::UNIT_COLS;
 #pragma unroll
-                for (int i = 0; i < 2 * G8_UNIT; ++i)
+                for (int i = 0; i < L::UNIT_COLS / 8; ++i)
                     tmem_st8(col + 8u * i, quarter_scales(staging + 1024 * i + lane * 4), quarter_scales(staging + 1024 * i + 512 + lane * 4));
                 tmem_st_wait();
                 tc_fence_before();
@@ -448,8 +516,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                         mbar_arrive_remote(smem_map_rank(sfull_bar(unit), 0));
                 }
                 unit += G8_SF_GROUPS;
-                if (unit >= G8_UNITS) {
-                    unit -= G8_UNITS;
+                if (unit >= L::UNITS) {
+                    unit -= L::UNITS;
                     phase ^= 1u;
                 }
                 --ahead;
@@ -468,15 +536,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         // gate/up: quarters q and q + 2 hold the same features' gate and up sums
         const int pair = set * 2 + (q & 1);
         const bool up = GATE_UP && q >= 2;
-        float *send = exchange + pair * 512 + (up ? 256 : 0), *take = exchange + pair * 512 + (up ? 0 : 256);
-        int local = 0;
+        float *send = exchange + pair * 1024 + (up ? 256 : 0), *take = exchange + pair * 1024 + (up ? 0 : 256);
+        G8Slots slots;
+        uint32_t fills = 0;  // a bit a slot, modulo 2: a unit in both fills the first one's barrier only
         for (int64_t t = first; t < total; t += stride) {
             const G8Tile ti = tile_at(t);
             if (ti.rows == 0) continue;
-            const int acc = local & 1;
+            slots.take(columns_of(ti));
+            const int acc = slots.first;
             int ready = 1;
-            if (lane == 0)
-                ready = mbar_wait_cluster_bounded(tfull_bar(acc), static_cast<uint32_t>(local >> 1) & 1u, abort_flag, p.err) ? 1 : 0;
+            if (lane == 0) ready = mbar_wait_cluster_bounded(tfull_bar(acc), fills >> acc & 1u, abort_flag, p.err) ? 1 : 0;
+            fills ^= 1u << acc;
             ready = __shfl_sync(0xffffffffu, ready, 0);
             if constexpr (GATE_UP) ready = g8_all<64>(1 + G8_SF_GROUPS + pair, ready != 0);  // both or neither go on
             if (!ready) break;
@@ -487,30 +557,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 uint8_t *const q_h = p.q_h + static_cast<int64_t>(ti.m_start) * p.N + f0 + lane;
                 uint8_t *const sf_h = p.sf_h + static_cast<int64_t>(ti.m_start) * (p.N / 32) + f0 / 32;
                 if (f0 < p.N) {
+                    uint32_t v[16];
+                    int buffer = 0;
+                    if (set * 16 < ti.rows) tmem_ld16(d + set * 16, v);
 #pragma unroll 1
                     for (int c = set * 16; c < ti.rows; c += 32) {
-                        uint32_t v[16];
-                        tmem_ld16(d + c, v);
                         tmem_ld_wait();
-                        // the gate's warp takes the first 8 rows, up's the others
+                        // the gate's warp takes the first 8 rows, up's the others; two
+                        // buffers in turn, so the next exchange's stores cannot pass
+                        // this one's reads
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) send[i * 32 + lane] = __uint_as_float(up ? v[i] : v[8 + i]);
+                        for (int i = 0; i < 8; ++i) send[buffer + i * 32 + lane] = __uint_as_float(up ? v[i] : v[8 + i]);
+                        float own[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) own[i] = __uint_as_float(up ? v[8 + i] : v[i]);
+                        if (c + 32 < ti.rows) tmem_ld16(d + c + 32, v);
                         g8_all<64>(1 + G8_SF_GROUPS + pair, true);
                         const int row0 = c + (up ? 8 : 0);
                         uint32_t scale = 0;
+                        uint8_t *to = q_h + static_cast<int64_t>(row0) * p.N;
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float own = __uint_as_float(up ? v[8 + i] : v[i]), other = take[i * 32 + lane];
-                            const float g = up ? other : own, u = up ? own : other;
-                            const float h = __fdividef(g, 1.0f + __expf(-g)) * u;
-                            const uint32_t s = mx8_scale(__reduce_max_sync(0xffffffffu, magnitude_bits(h)));
-                            const uint32_t e = e4m3x4(h, 0.0f, 0.0f, 0.0f, mx8_inverse(s), s == 255u);
-                            if (row0 + i < ti.rows) q_h[static_cast<int64_t>(row0 + i) * p.N] = static_cast<uint8_t>(e);
-                            scale = lane == i ? s : scale;
+                        for (int i = 0; i < 8; i += 2) {  // two rows at a time
+                            float h[2];
+                            uint32_t s[2];
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const float other = take[buffer + (i + j) * 32 + lane];
+                                const float g = up ? other : own[i + j], u = up ? own[i + j] : other;
+                                h[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
+                                s[j] = mx8_scale(__reduce_max_sync(0xffffffffu, magnitude_bits(h[j])));
+                                scale = lane == i + j ? s[j] : scale;
+                            }
+                            const uint32_t e = e4m3x2(h[0] * mx8_inverse(s[0]), h[1] * mx8_inverse(s[1]));
+                            if (row0 + i < ti.rows) *to = static_cast<uint8_t>(s[0] == 255u ? 0u : e);
+                            to += p.N;
+                            if (row0 + i + 1 < ti.rows) *to = static_cast<uint8_t>(s[1] == 255u ? 0u : e >> 8);
+                            to += p.N;
                         }
                         if (lane < 8 && row0 + lane < ti.rows)
                             sf_h[static_cast<int64_t>(row0 + lane) * (p.N / 32)] = static_cast<uint8_t>(scale);
-                        g8_all<64>(1 + G8_SF_GROUPS + pair, true);  // both have read
+                        buffer ^= 512;
                     }
                 }
             } else {
@@ -522,21 +608,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                     tmem_ld32(d + c, v);
                     tmem_ld_wait();
                     if (f < p.N) {
+                        // a running pointer: with an address worked out for each store
+                        // this loop took longer than the stores (32768 rows of 16
+                        // experts, 7168 x 2048: 400 us, so 340)
+                        TOut *to = out + static_cast<int64_t>(c) * p.N;
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (c + i < ti.rows) out[static_cast<int64_t>(c + i) * p.N] = from_f32<TOut>(__uint_as_float(v[i]));
+                        for (int i = 0; i < 32; ++i) {
+                            if (c + i < ti.rows) *to = from_f32<TOut>(__uint_as_float(v[i]));
+                            to += p.N;
+                        }
                     }
                 }
             }
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                if (leader)
-                    mbar_arrive(tempty_bar(acc));
-                else
-                    mbar_arrive_remote(tempty_leader + 8u * static_cast<uint32_t>(acc));
+                for (int i = acc; i <= (slots.both ? 1 : acc); ++i) {
+                    if (leader)
+                        mbar_arrive(tempty_bar(i));
+                    else
+                        mbar_arrive_remote(tempty_leader + 8u * static_cast<uint32_t>(i));
+                }
             }
-            ++local;
         }
     }
     __syncwarp();
@@ -568,46 +661,64 @@ bool weights_map(CUtensorMap *m, const uint8_t *q, int64_t K, int64_t N, int64_t
     return encode_tma_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, q, dims, strides, box, 1);
 }
 
-template <typename TOut, int V>
-cudaError_t launch_v(const CUtensorMap *maps, const G8Params &p, cudaStream_t stream) {
-    auto kern = mx8_gemm_kernel<TOut, V>;
+template <typename TOut, int NT, int V>
+cudaError_t launch_v(const CUtensorMap *maps, G8Params p, cudaStream_t stream) {
+    using L = G8Layout<NT>;
+    p.units = (p.slices + G8_UNIT - 1) / G8_UNIT;
+    auto kern = mx8_gemm_kernel<TOut, NT, V>;
     static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return cudaErrorInvalidDevice;
     if (dev < 0 || dev >= 64 || !attr_done[dev]) {
-        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G8_SMEM);
+        cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::SMEM);
         if (e != cudaSuccess) return e;
         if (dev >= 0 && dev < 64) attr_done[dev] = true;
     }
     const int64_t tiles = static_cast<int64_t>(p.m_blocks) * p.n_tiles, pairs = device_sm_count() / 2;
-    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), dim3(G8_THREADS), G8_SMEM, stream,
+    return launch_pdl(kern, dim3(static_cast<unsigned>(2 * (tiles < pairs ? tiles : pairs))), dim3(G8_THREADS), L::SMEM, stream,
                       maps[0], maps[1], maps[2], maps[3], maps[4], p);
 }
 
 // the widest scale loads that K and the bases' alignment allow
-template <typename TOut>
+template <typename TOut, int NT>
 cudaError_t launch_n(const CUtensorMap *maps, const G8Params &p, cudaStream_t stream) {
     const uintptr_t bases = reinterpret_cast<uintptr_t>(p.sf_a) | reinterpret_cast<uintptr_t>(p.sf_b0) |
                             reinterpret_cast<uintptr_t>(p.sf_b1);
-    if (p.K % 512 == 0 && (bases & 15u) == 0) return launch_v<TOut, 16>(maps, p, stream);
-    if (p.K % 256 == 0 && (bases & 7u) == 0) return launch_v<TOut, 8>(maps, p, stream);
-    if (p.K % 128 == 0 && (bases & 3u) == 0) return launch_v<TOut, 4>(maps, p, stream);
-    return launch_v<TOut, 1>(maps, p, stream);
+    if (p.K % 512 == 0 && (bases & 15u) == 0) return launch_v<TOut, NT, 16>(maps, p, stream);
+    if (p.K % 256 == 0 && (bases & 7u) == 0) return launch_v<TOut, NT, 8>(maps, p, stream);
+    if (p.K % 128 == 0 && (bases & 3u) == 0) return launch_v<TOut, NT, 4>(maps, p, stream);
+    return launch_v<TOut, NT, 1>(maps, p, stream);
+}
+
+// Tiles of up to 256 rows where experts have many: the weights enter shared
+// memory half as often.  They leave three stages for four, and the wide tiles'
+// epilogue runs alone (both accumulator slots are one tile's), which the
+// gate/up form's longer one earns back only over a long K.  Narrow / wide, us:
+//   7168 x 2048, 256 experts, 128 rows each: 837 / 777, gate/up 1776 / 1639
+//   7168 x 2048, 64 experts: 32 rows each 153 / 156 and 326 / 328, 64 rows 184 / 175
+//   and 348 / 341, 256 rows 328 / 284 and 677 / 591; 16 experts, 2048 rows 507 / 347
+//   2048 x 768, 64 experts: 384 rows each 65 / 63, gate/up 129 / 140; 128 rows 32 / 34
+//   and 63 / 74; 2048 x 2048, 8 experts, 4096 rows 162 / 133, gate/up 340 / 347
+template <typename TOut>
+cudaError_t launch_typed(const CUtensorMap *maps, const G8Params &p, int64_t n_rows, int64_t E, cudaStream_t stream) {
+    const bool long_sums = !std::is_same<TOut, void>::value || p.K >= 4096;
+    if (n_rows > 64 * E && long_sums) return launch_n<TOut, 256>(maps, p, stream);
+    return launch_n<TOut, 128>(maps, p, stream);
 }
 
 G8Params params(const uint8_t *sf_a, const uint8_t *sf_b0, const uint8_t *sf_b1, const MxTables &tab, int64_t m_blocks,
-                int64_t N, int64_t K, int tile, int32_t *err) {
+                int64_t N, int64_t K, int64_t E, int tile, int32_t *err) {
     G8Params p{};
     p.sf_a = sf_a;
     p.sf_b0 = sf_b0;
     p.sf_b1 = sf_b1;
     p.tab = tab;
     p.m_blocks = static_cast<int>(m_blocks);
+    p.E = static_cast<int>(E);
     p.N = N;
     p.K = K;
     p.n_tiles = static_cast<int>((N + tile - 1) / tile);
     p.slices = static_cast<int>((K + G8_SLICE - 1) / G8_SLICE);
-    p.units = (p.slices + G8_UNIT - 1) / G8_UNIT;
     p.err = err;
     return p;
 }
@@ -620,11 +731,11 @@ cudaError_t launch_grouped_gemm_mx8(const uint8_t *q_a, const uint8_t *sf_a, con
     CUtensorMap maps[5];
     if (!rows_maps(maps, q_a, K, n_rows) || !weights_map(&maps[3], q_b, K, N, E, 128)) return cudaErrorInvalidValue;
     maps[4] = maps[3];
-    G8Params p = params(sf_a, sf_b, sf_b, tab, m_blocks, N, K, 256, err);
+    G8Params p = params(sf_a, sf_b, sf_b, tab, m_blocks, N, K, E, 256, err);
     p.out = C;
-    if (out_dtype == kF32) return launch_n<float>(maps, p, stream);
-    if (out_dtype == kBF16) return launch_n<__nv_bfloat16>(maps, p, stream);
-    return launch_n<__half>(maps, p, stream);
+    if (out_dtype == kF32) return launch_typed<float>(maps, p, n_rows, E, stream);
+    if (out_dtype == kBF16) return launch_typed<__nv_bfloat16>(maps, p, n_rows, E, stream);
+    return launch_typed<__half>(maps, p, n_rows, E, stream);
 }
 
 cudaError_t launch_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *sf_a, const uint8_t *q_gate,
@@ -636,10 +747,10 @@ cudaError_t launch_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *s
     if (!rows_maps(maps, q_a, d_h, n_rows) || !weights_map(&maps[3], q_gate, d_h, d_e, E, 64) ||
         !weights_map(&maps[4], q_up, d_h, d_e, E, 64))
         return cudaErrorInvalidValue;
-    G8Params p = params(sf_a, sf_gate, sf_up, tab, m_blocks, d_e, d_h, 128, err);
+    G8Params p = params(sf_a, sf_gate, sf_up, tab, m_blocks, d_e, d_h, E, 128, err);
     p.q_h = q_h;
     p.sf_h = sf_h;
-    return launch_n<void>(maps, p, stream);
+    return launch_typed<void>(maps, p, n_rows, E, stream);
 }
 
 }  // namespace moe

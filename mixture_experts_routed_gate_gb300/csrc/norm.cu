@@ -201,9 +201,13 @@ __device__ __forceinline__ void store_mx8(const NormParams &p, int64_t t, const 
 #pragma unroll
     for (int v = 0; v < EPT; v += RUN) {
         const int at = P::at(v);
-        uint32_t top = 0;
-#pragma unroll
-        for (int j = 0; j < RUN; ++j) top = max(top, magnitude_bits(o[v + j]));
+        float most = o[v];
+        if constexpr (RUN > 1) {
+            most = largest(o[v], o[v + 1], o[v + 2]);
+            if constexpr (RUN == 8) most = largest(largest(most, o[v + 3], o[v + 4]), o[v + 5], o[v + 6]);
+            most = largest(most, most, o[v + RUN - 1]);
+        }
+        uint32_t top = magnitude_bits(most);
 #pragma unroll
         for (int s = LANES / 2; s >= 1; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
         const uint32_t s = mx8_scale(top);
