@@ -755,16 +755,18 @@ def _at(t):
 # the current stream's handle without a Stream object (about 5 us a call)
 _raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
     lambda i: torch.cuda.current_stream(i).cuda_stream
+# the current device's number; a call has a CUDA tensor, so CUDA is up
+_device_now = torch._C._cuda_getDevice if hasattr(torch._C, "_cuda_getDevice") else torch.cuda.current_device
 
 
 def _call(what, dev, *args):
     """The library's `what` with these arguments and the device's current stream."""
-    fn = getattr(_lib or lib(), what)
-    if torch.cuda.current_device() == dev.index:
-        status = fn(*args, _raw_stream(dev.index))
+    fn, index = getattr(_lib or lib(), what), dev.index
+    if _device_now() == index:
+        status = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(*args, _raw_stream(dev.index))
+            status = fn(*args, _raw_stream(index))
     if status != 0:
         raise MoEError(status, what)
 
@@ -852,7 +854,7 @@ def moe_residual_norm_mx8(y, res, w_post=None, gate=None, alpha: float = 1.0, w_
     needed and H % 32 == 0; everything else as there, the gradients
     (:func:`moe_residual_norm_backward`, with d_u the gradient of the rows' values) too."""
     _cuda(res, "res", ndim=2)
-    shape, dt, dev = res.shape, res.dtype, res.device
+    shape, dt, dev, f32 = res.shape, res.dtype, res.device, torch.float32
     T, H = shape
     if w_next is None:
         raise ValueError("w_next is needed")
@@ -861,22 +863,25 @@ def moe_residual_norm_mx8(y, res, w_post=None, gate=None, alpha: float = 1.0, w_
     if H == 0 or H % 32 != 0:
         raise ValueError("H must be a multiple of 32")
     code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt)
-    got = {}
-    if y is not None:
-        _need(y, "y", dt, shape)
-        got["out"] = out = _want(out, "out", dt, shape, dev)
-    r_post = u = None
-    if w_post is not None:
-        _need(w_post, "w_post", dt, (H,))
-        got["rstd_post"] = r_post = torch.empty(T, dtype=torch.float32, device=dev)
     _need(w_next, "w_next", dt, (H,))
+    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else _need(q, "q", torch.float8_e4m3fn, shape)
+    sf = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if sf is None else _need(sf, "sf", torch.uint8, (T, H // 32))
+    r_next = torch.empty(T, dtype=f32, device=dev)
+    got = {"q": q, "sf": sf, "rstd_next": r_next}
+    a_y = a_out = a_u = a_post = a_r = None
+    if y is not None:
+        a_y = _need(y, "y", dt, shape).data_ptr()
+        got["out"] = out = torch.empty(shape, dtype=dt, device=dev) if out is None else _need(out, "out", dt, shape)
+        a_out = out.data_ptr()
+    if w_post is not None:
+        a_post = _need(w_post, "w_post", dt, (H,)).data_ptr()
+        got["rstd_post"] = r_post = torch.empty(T, dtype=f32, device=dev)
+        a_r = r_post.data_ptr()
     if with_u:
         got["u"] = u = torch.empty(shape, dtype=dt, device=dev)
-    got["q"] = q = _want(q, "q", torch.float8_e4m3fn, shape, dev)
-    got["sf"] = sf = _want(sf, "sf", torch.uint8, (T, H // 32), dev)
-    got["rstd_next"] = r_next = torch.empty(T, dtype=torch.float32, device=dev)
-    _call("moe_residual_norm_mx8", dev, _at(y), _at(res), _at(w_post), _at(gate), kind, alpha, _at(w_next), eps, T, H, code,
-          _at(out), _at(u), _at(q), _at(sf), _at(r_post), _at(r_next))
+        a_u = u.data_ptr()
+    _call("moe_residual_norm_mx8", dev, a_y, res.data_ptr(), a_post, None if gate is None else gate.data_ptr(), kind, alpha,
+          w_next.data_ptr(), eps, T, H, code, a_out, a_u, q.data_ptr(), sf.data_ptr(), a_r, r_next.data_ptr())
     return got
 
 
@@ -1086,18 +1091,20 @@ def moe_reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_
     (:func:`moe_gather_rows_by_token`) is ``moe_reduce_fused(d_rows, token_topk_to_pos)``."""
     _cuda(x, "x", ndim=2)
     _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
-    n_rows, H = x.shape
-    T, K = token_topk_to_pos.shape
     _cuda(d_out, "d_out", ndim=2)
-    _need(d_out, "d_out", d_out.dtype, (T, H))
+    shape, pairs, dev, f32 = x.shape, token_topk_to_pos.shape, x.device, torch.float32
+    n_rows, H = shape
+    T, K = pairs
+    if d_out.shape != (T, H):
+        raise ValueError(f"d_out must be {[T, H]}, got {list(d_out.shape)}")
     if topk_weights is not None:
-        _need(topk_weights, "topk_weights", torch.float32, (T, K))
+        _need(topk_weights, "topk_weights", f32, pairs)
     _need(sorted_token_idx, "sorted_token_idx", torch.int32, (n_rows,))
-    dev = x.device
-    d_x = torch.empty(x.shape, dtype=x.dtype, device=dev)
-    d_w = torch.empty((T, K), dtype=torch.float32, device=dev)
-    _call("moe_reduce_fused_backward", dev, _at(d_out), _at(x), n_rows, _at(token_topk_to_pos), _at(topk_weights),
-          _at(sorted_token_idx), T, K, H, _dtype_code(x, "x"), _dtype_code(d_out, "d_out"), _at(d_x), _at(d_w), _err(err))
+    d_x = torch.empty(shape, dtype=x.dtype, device=dev)
+    d_w = torch.empty(pairs, dtype=f32, device=dev)
+    _call("moe_reduce_fused_backward", dev, d_out.data_ptr(), x.data_ptr(), n_rows, token_topk_to_pos.data_ptr(),
+          None if topk_weights is None else topk_weights.data_ptr(), sorted_token_idx.data_ptr(), T, K, H, _dtype_code(x, "x"),
+          _dtype_code(d_out, "d_out"), d_x.data_ptr(), d_w.data_ptr(), None if err is None else _err(err))
     return d_x, d_w
 
 
@@ -1105,12 +1112,14 @@ def moe_reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_
 
 def _mx8(q, sf, name, lead):
     """q float8 e4m3 [*lead, K], sf uint8 [*lead, K / 32]: returns K."""
-    if isinstance(q, torch.Tensor) and q.dim() == len(lead) + 1 and q.shape[-1] % 32 == 0:
-        K = q.shape[-1]
-        _need(q, f"q{name}", torch.float8_e4m3fn, (*lead, K))
-        _need(sf, f"sf{name}", torch.uint8, (*lead, K // 32))
-        return K
-    _cuda(q, f"q{name}", dtype=torch.float8_e4m3fn, ndim=len(lead) + 1)
+    if isinstance(q, torch.Tensor):
+        shape = q.shape
+        if len(shape) == len(lead) + 1 and shape[-1] % 32 == 0:
+            K = shape[-1]
+            _need(q, "q" + name, torch.float8_e4m3fn, lead + (K,))
+            _need(sf, "sf" + name, torch.uint8, lead + (K // 32,))
+            return K
+    _cuda(q, "q" + name, dtype=torch.float8_e4m3fn, ndim=len(lead) + 1)
     raise ValueError(f"q{name} must be {(*lead, 'K')} with K % 32 == 0, got {tuple(q.shape)}")
 
 
@@ -1143,15 +1152,28 @@ def moe_sort_rows_mx8(q, sf, token_topk_to_pos, n_rows=None, q_out=None, sf_out=
     token_topk_to_pos[t, j] of the result is row t of q, sf.  n_rows None: one for
     each position.  Positions outside [0, n_rows) are skipped, rows that no
     position names are left as they were; a position stands at one place only."""
-    _cuda(q, "q", dtype=torch.float8_e4m3fn, ndim=2)
     _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
     T, k = token_topk_to_pos.shape
     K, dev = _mx8(q, sf, "", (T,)), q.device
     n_rows = T * k if n_rows is None else n_rows
     q_out = _want(q_out, "q_out", torch.float8_e4m3fn, (n_rows, K), dev)
     sf_out = _want(sf_out, "sf_out", torch.uint8, (n_rows, K // 32), dev)
-    _call("moe_sort_rows_mx8", dev, _at(q), _at(sf), _at(token_topk_to_pos), T, k, n_rows, K, _at(q_out), _at(sf_out))
+    _call("moe_sort_rows_mx8", dev, q.data_ptr(), sf.data_ptr(), token_topk_to_pos.data_ptr(), T, k, n_rows, K, q_out.data_ptr(),
+          sf_out.data_ptr())
     return q_out, sf_out
+
+
+def _table_addresses(t, E):
+    """The four tables' addresses, in the entry points' order, and the number of blocks;
+    the first three have an entry for each expert."""
+    s, o, p, g = t["group_sizes"], t["group_offsets"], t["group_padded_offsets"], t["group_idx_for_bx"]
+    i32 = torch.int32
+    for x in (s, o, p, g):
+        if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is i32 and x.is_contiguous()):
+            _tables(t)  # says which
+    if s.numel() != E or o.numel() != E or p.numel() != E:
+        raise ValueError(f"group_sizes, group_offsets and group_padded_offsets must have an entry for each of {E} experts")
+    return s.data_ptr(), o.data_ptr(), p.data_ptr(), g.data_ptr(), g.shape[0]
 
 
 def moe_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16, out=None, err=None):
@@ -1160,13 +1182,13 @@ def moe_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16,
     _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
     _cuda(q_b, "q_b", dtype=torch.float8_e4m3fn, ndim=3)
     rows, (E, N, _) = q_a.shape[0], q_b.shape
-    K = _mx8(q_a, sf_a, "_a", (rows,))
+    K, dev = _mx8(q_a, sf_a, "_a", (rows,)), q_a.device
     if _mx8(q_b, sf_b, "_b", (E, N)) != K:
         raise ValueError("the two sides disagree on K")
-    s, o, p, g = _tables(tables)
-    out = _want(out, "out", out_dtype, (rows, N), q_a.device)
-    _call("moe_grouped_gemm_mx8", q_a.device, _at(q_a), _at(sf_a), _at(q_b), _at(sf_b), _at(s), _at(o), _at(p), _at(g),
-          g.shape[0], rows, N, K, E, _dtype_code(out, "out"), _at(out), _err(err))
+    s, o, p, g, blocks = _table_addresses(tables, E)
+    out = _want(out, "out", out_dtype, (rows, N), dev)
+    _call("moe_grouped_gemm_mx8", dev, q_a.data_ptr(), sf_a.data_ptr(), q_b.data_ptr(), sf_b.data_ptr(), s, o, p, g, blocks,
+          rows, N, K, E, _dtype_code(out, "out"), out.data_ptr(), None if err is None else _err(err))
     return out
 
 
@@ -1200,11 +1222,12 @@ def moe_grouped_gate_up_silu_mx8(q_a, sf_a, experts: "Mx8Experts", tables, q_h=N
     rows, dev, e = q_a.shape[0], q_a.device, experts
     if _mx8(q_a, sf_a, "_a", (rows,)) != e.d_h:
         raise ValueError("the rows and the experts disagree on d_hidden")
-    s, o, p, g = _tables(tables)
+    s, o, p, g, blocks = _table_addresses(tables, e.E)
     q_h = _want(q_h, "q_h", torch.float8_e4m3fn, (rows, e.d_e), dev)
     sf_h = _want(sf_h, "sf_h", torch.uint8, (rows, e.d_e // 32), dev)
-    _call("moe_grouped_gate_up_silu_mx8", dev, _at(q_a), _at(sf_a), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
-          _at(s), _at(o), _at(p), _at(g), g.shape[0], rows, e.d_h, e.d_e, e.E, _at(q_h), _at(sf_h), _err(err))
+    _call("moe_grouped_gate_up_silu_mx8", dev, q_a.data_ptr(), sf_a.data_ptr(), e.q_gate.data_ptr(), e.sf_gate.data_ptr(),
+          e.q_up.data_ptr(), e.sf_up.data_ptr(), s, o, p, g, blocks, rows, e.d_h, e.d_e, e.E, q_h.data_ptr(), sf_h.data_ptr(),
+          None if err is None else _err(err))
     return q_h, sf_h
 
 

@@ -286,6 +286,8 @@ def product_and_size(a, b, t):
 
 SHAPES = [(1, 1, 1, 32, 1), (1, 8, 8, 256, 128), (5, 2, 3, 64, 33), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 333), (130, 1, 1, 96, 257),
           (700, 2, 3, 288, 200), (257, 4, 7, 1024, 512), (96, 2, 6, 7168, 160), (40, 2, 600, 160, 64), (128, 1, 1, 512, 300), (129, 1, 1, 544, 256)]
+# more units of rows than a CTA lists: of up to 128 rows, and of up to 256
+SHAPES += [(1100, 2, 900, 96, 40), (10000, 4, 600, 32, 40)]
 
 
 @pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
@@ -336,7 +338,8 @@ def silu_products(t, qa, sa, gate, up):
 
 
 @pytest.mark.parametrize("T,k,E,K,N", [(1, 1, 1, 32, 32), (1, 8, 8, 256, 128), (5, 2, 3, 64, 96), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 352),
-                                       (700, 2, 3, 288, 224), (257, 4, 7, 1024, 512), (40, 2, 600, 160, 64), (129, 1, 1, 544, 256), (33, 1, 2, 7168, 160)])
+                                       (700, 2, 3, 288, 224), (257, 4, 7, 1024, 512), (40, 2, 600, 160, 64), (129, 1, 1, 544, 256), (33, 1, 2, 7168, 160),
+                                       (1100, 2, 900, 96, 64), (400, 2, 3, 4128, 96), (600, 1, 2, 4096, 160), (39000, 1, 600, 4096, 32)])
 def test_gate_up(T, k, E, K, N):
     require_cuda()
     t, g = routed(T, k, E, T + K)
@@ -399,6 +402,53 @@ def test_rows_behind_the_last_group_are_left():
     q, s = torch.full((2 * T + more, N), 3, dtype=torch.uint8, device="cuda"), torch.full((2 * T + more, N // 32), 3, dtype=torch.uint8, device="cuda")
     binding.moe_grouped_gate_up_silu_mx8(qa, sa, binding.Mx8Experts(*w), t, q.view(E4M3), s)
     assert (q[2 * T:] == 3).all() and (s[2 * T:] == 3).all() and not (s[:2 * T] == 3).all()
+
+
+def test_past_2_31_elements():
+    """Weights of more than 2^31 bytes and a result of more than 2^31 elements, at places on both sides of it."""
+    require_cuda()
+    T, k, E, K, N = 64, 4, 300, 4096, 2048
+    t, g = routed(T, k, E, 1)
+    qa, sa = rows8(T * k, K, g)
+    qb = torch.randint(0, 100, (E, N, K), generator=g, device="cuda", dtype=torch.uint8).view(E4M3)
+    sb = torch.randint(120, 130, (E, N, K // 32), generator=g, device="cuda", dtype=torch.uint8)
+    got = binding.moe_grouped_gemm_mx8(qa, sa, qb, sb, t, torch.float32)
+    for e, at in by_group(t):
+        if e < 5 or e > E - 5:
+            a, b = values64(qa[at], sa[at]), values64(qb[e], sb[e])
+            off = sum_off(K) * (a.abs() @ b.abs().t()) + 2.0 ** -24 * (a @ b.t()).abs()
+            assert ((got[at].double() - a @ b.t()).abs() <= off).all(), e
+    del qb, sb
+    T, E, K, N = 90000, 3, 32, 24001
+    t, g = routed(T, 1, E, 2)
+    (qa, sa), (qb, sb) = rows8(T, K, g), (x.view(E, N, -1) for x in rows8(E * N, K, g))
+    got = binding.moe_grouped_gemm_mx8(qa, sa, qb, sb, t, torch.bfloat16)
+    for e, at in by_group(t):
+        for r in (at.start, at.stop - 1):
+            a, b = values64(qa[r:r + 1], sa[r:r + 1]), values64(qb[e], sb[e])
+            want = (a @ b.t())[0]
+            off = sum_off(K) * (a.abs() @ b.abs().t())[0] + 2.0 ** -8 * want.abs() + 2.0 ** -134
+            assert ((got[r].double() - want).abs() <= off).all(), r
+
+
+def test_two_streams_at_once():
+    """No call keeps state: products of different sizes on two streams, in turn and together, give the same bits."""
+    require_cuda()
+    calls = []
+    for T, k, E, K, N in ((700, 2, 3, 1024, 512), (64, 6, 64, 512, 256)):
+        t, g = routed(T, k, E, T)
+        a, b = rows8(T * k, K, g), [x.view(E, N, -1) for x in rows8(E * N, K, g)]
+        calls.append(lambda a=a, b=b, t=t: binding.moe_grouped_gemm_mx8(*a, *b, t, torch.float32))
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    got = [[], []]
+    for _ in range(20):
+        for i, (c, s) in enumerate(zip(calls, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(c())
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, w) for g, w in zip(got, want) for x in g)
 
 
 def test_unaligned_scales_and_results():
@@ -496,6 +546,7 @@ def test_refusals():
                  lambda: binding.moe_residual_norm_mx8(None, x, w_post=x[0], w_next=x[0]), lambda: binding.moe_residual_norm_mx8(x, x, w_next=x[0, :32]),
                  lambda: binding.moe_residual_norm_mx8(None, x[:, :40].contiguous(), w_next=x[0, :40]),
                  lambda: binding.Mx8Experts(q[None], sf[None], q[None], sf[None], q[None], sf[None]),
+                 lambda: binding.moe_grouped_gemm_mx8(q, sf, q[None], sf[None], binding.moe_build_dispatch(pos, None, 2)),
                  lambda: binding.moe_grouped_gemm_mx8(q, sf, q[None, :, :32].contiguous(), sf[None, :, :1].contiguous(), {})):
         with pytest.raises(ValueError):
             call()
