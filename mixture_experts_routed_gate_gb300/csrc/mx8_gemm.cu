@@ -257,6 +257,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         tmem_alloc2(smem_u32(&tmem_slot), 512);
         tmem_relinquish2();
     }
+    tc_fence_before();
+    cluster_sync_all();  // the other CTA's barriers are initialised before any use
+    tc_fence_after();
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
     griddep_wait();
     griddep_launch_dependents();
 
@@ -289,25 +293,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         __syncthreads();
     }
     const int listed = n_blocks <= G8_LIST ? n_blocks : -1;
-    tc_fence_before();
-    __syncthreads();
-    cluster_sync_all();  // the other CTA's barriers are initialised before any use
-    tc_fence_after();
-    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
-    const int64_t total = static_cast<int64_t>(listed >= 0 ? listed : p.m_blocks) * p.n_tiles;
-    const int64_t first = blockIdx.x >> 1, stride = gridDim.x >> 1;
-    auto tile_at = [&](int64_t t) {
-        const int b = static_cast<int>(t / p.n_tiles);
+    // Tile b * n_tiles + n is unit (or block) b by feature tile n; a pair takes every
+    // `pairs`-th.
+    const int n_units = listed >= 0 ? listed : p.m_blocks, pairs = static_cast<int>(gridDim.x >> 1);
+    const int step_b = pairs / p.n_tiles, step_n = pairs % p.n_tiles;
+    struct Cursor {
+        int b, n;
+    };
+    const Cursor first = {static_cast<int>(blockIdx.x >> 1) / p.n_tiles, static_cast<int>(blockIdx.x >> 1) % p.n_tiles};
+    auto live = [&](const Cursor &c) { return c.b < n_units; };
+    auto advance = [&](Cursor &c) {
+        c.b += step_b;
+        c.n += step_n;
+        if (c.n >= p.n_tiles) {
+            c.n -= p.n_tiles;
+            ++c.b;
+        }
+    };
+    auto tile_at = [&](const Cursor &c) {
         G8Tile ti;
-        ti.n0 = static_cast<int>(t - static_cast<int64_t>(b) * p.n_tiles) * (2 * OWN) + static_cast<int>(rank) * OWN;
+        ti.n0 = c.n * (2 * OWN) + static_cast<int>(rank) * OWN;
         if (listed >= 0) {
-            const int2 e = list[b];
+            const int2 e = list[c.b];
             ti.g = e.y >> 10;
             ti.m_start = e.x;
             ti.rows = e.y & 511;
             ti.single = (e.y & 512) != 0;
         } else {
-            const Mx4Block k = unit_of<NT>(p.tab, b, p.m_blocks);
+            const Mx4Block k = unit_of<NT>(p.tab, c.b, p.m_blocks);
             ti.g = k.g;
             ti.m_start = k.m_start;
             ti.rows = k.rows;
@@ -325,7 +338,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             uint32_t phase = 0;
             long issued = 0;
             bool ok = true;
-            for (int64_t t = first; t < total && ok; t += stride) {
+            for (Cursor t = first; live(t) && ok; advance(t)) {
                 const G8Tile ti = tile_at(t);
                 if (ti.rows == 0) continue;
                 const int half = columns_of(ti) / 2;  // a multiple of 16 rows
@@ -382,7 +395,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             G8Slots slots;
             uint32_t phase = 0, uphase = 0, last_bar = 0, last_parity = 0;
             bool ok = true, committed = false;
-            for (int64_t t = first; t < total && ok; t += stride) {
+            for (Cursor t = first; live(t) && ok; advance(t)) {
                 const int columns = __shfl_sync(0xffffffffu, columns_of(tile_at(t)), 0);
                 if (columns == 0) continue;
                 const uint32_t idesc = idesc_mxf8(256, static_cast<uint32_t>(columns));
@@ -440,11 +453,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         uint8_t *const staging = staging0 + group * L::SF_BYTES;
         constexpr int WORDS = 2 * G8_UNIT;
         uint32_t vw[G8_AHEAD][WORDS], vr[G8_AHEAD][L::ROWS][WORDS];  // weights', rows'
-        int64_t lt = first;                     // next unit to load: its tile, its scale bytes
+        Cursor lt = first;                      // next unit to load: its tile, its scale bytes
         int at = group * 8 * G8_UNIT;           // byte offset of that unit in its row
         const uint8_t *pw = nullptr, *pr[L::ROWS];  // the thread's rows; null where there is none
         auto next_tile = [&]() {
-            for (; lt < total; lt += stride) {
+            for (; live(lt); advance(lt)) {
                 const G8Tile ti = tile_at(lt);
                 if (ti.rows == 0) continue;
                 if (at >= span) {  // past this tile: the units go on in the next one
@@ -471,7 +484,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         int ahead = 0;  // units in registers
 #pragma unroll
         for (int j = 0; j < G8_AHEAD; ++j)
-            if (lt < total) {
+            if (live(lt)) {
                 load(vw[j], vr[j]);
                 ++ahead;
             }
@@ -521,7 +534,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                     phase ^= 1u;
                 }
                 --ahead;
-                if (lt < total) {
+                if (live(lt)) {
                     load(vw[j], vr[j]);
                     ++ahead;
                 }
@@ -539,7 +552,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         float *send = exchange + pair * 1024 + (up ? 256 : 0), *take = exchange + pair * 1024 + (up ? 0 : 256);
         G8Slots slots;
         uint32_t fills = 0;  // a bit a slot, modulo 2: a unit in both fills the first one's barrier only
-        for (int64_t t = first; t < total; t += stride) {
+        for (Cursor t = first; live(t); advance(t)) {
             const G8Tile ti = tile_at(t);
             if (ti.rows == 0) continue;
             slots.take(columns_of(ti));
