@@ -20,6 +20,9 @@
 // column sums of its rows in registers; a second kernel adds the CTAs' sums in
 // a fixed order.
 //
+// With u in 8 bits beside it (norm_mx8_kernel): 4096 x 7168 bf16 45 us (265 MB, 39 at
+// the copy rate), u in 8 bits alone 40 (30); fp32 82 (74); bound by instructions
+// below about 4096 elements (4096 x 2048: 15.4 us, 11.2 at the copy rate).
 // 4096 x 7168 bf16: forward 39 us (235 MB at 6.0 TB/s, against 35 at this
 // card's copy rate; 67% of the issue slots), gradients 88 us (52 at the copy
 // rate; 57% of the issue slots at about 500 instructions a warp and row, and the
@@ -161,6 +164,13 @@ template <typename T, int EPT, bool VEC> struct Part {
             return i & 1 ? f.y : f.x;
         }
     }
+    // elements 2 k and 2 k + 1
+    __device__ __forceinline__ float2 pair(int k) const {
+        if constexpr (sizeof(T) == 4)
+            return make_float2(get(2 * k), get(2 * k + 1));
+        else
+            return unpack2<DT>(w[k]);
+    }
     // this[i] * o[i], exact for 16-bit types: one mixed FMA, no unpacking
     __device__ __forceinline__ float times(const Part &o, int i) const {
         if constexpr (sizeof(T) == 4)
@@ -191,6 +201,24 @@ template <typename T, int EPT, bool VEC> struct Part {
     }
 };
 
+// Two fp32 products, or two sums of products, an instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, w;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+
 // A row of u in 8 bits.  32 / RUN consecutive lanes hold a block of 32 elements
 // and find its largest magnitude among them; the blocks that cross H do not
 // exist (H % 32 == 0), so a block's lanes are all in the row or all past it.
@@ -213,14 +241,24 @@ __device__ __forceinline__ void store_mx8(const NormParams &p, int64_t t, const 
         const uint32_t s = mx8_scale(top);
         const float by = mx8_inverse(s);
         const bool bad = s == 255u;
+        uint32_t w[RUN >= 4 ? RUN / 4 : 1];
+        if constexpr (RUN >= 4) {
+#pragma unroll
+            for (int j = 0; j < RUN / 4; ++j) {
+                const float2 a = mul2(make_float2(o[v + 4 * j], o[v + 4 * j + 1]), both(by));
+                const float2 b = mul2(make_float2(o[v + 4 * j + 2], o[v + 4 * j + 3]), both(by));
+                w[j] = bad ? 0u : e4m3x2(a.x, a.y) | e4m3x2(b.x, b.y) << 16;
+            }
+        } else {
+            w[0] = bad ? 0u : e4m3x2(o[v] * by, 0.0f);
+        }
         if (at >= p.H) continue;
         if constexpr (RUN == 8)
-            *reinterpret_cast<uint2 *>(q + at) = make_uint2(e4m3x4(o[v], o[v + 1], o[v + 2], o[v + 3], by, bad),
-                                                            e4m3x4(o[v + 4], o[v + 5], o[v + 6], o[v + 7], by, bad));
+            *reinterpret_cast<uint2 *>(q + at) = make_uint2(w[0], w[1]);
         else if constexpr (RUN == 4)
-            *reinterpret_cast<uint32_t *>(q + at) = e4m3x4(o[v], o[v + 1], o[v + 2], o[v + 3], by, bad);
+            *reinterpret_cast<uint32_t *>(q + at) = w[0];
         else
-            q[at] = static_cast<uint8_t>(e4m3x4(o[v], 0.0f, 0.0f, 0.0f, by, bad));
+            q[at] = static_cast<uint8_t>(w[0]);
         if ((threadIdx.x & (LANES - 1)) == 0) sf[at / 32] = static_cast<uint8_t>(s);
     }
 }
@@ -444,8 +482,7 @@ template <typename P, Rows MODE> struct Kept {
     }
 };
 
-// Q8: u comes in 8 bits too, and as u itself only where there is a place for it.
-template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS, bool Q8>
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __grid_constant__ NormParams p) {
     using P = Part<T, EPT, MODE == Rows::kVectors>;
     extern __shared__ __align__(128) uint8_t norm_smem[];
@@ -514,15 +551,119 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
             w_next.load(w, H);
 #pragma unroll
             for (int i = 0; i < EPT; ++i) o[i] = o[i] * r * w.get(i);
-            if (!Q8 || p.u) P::store(static_cast<T *>(p.u) + base, H, o);
-            if constexpr (Q8) store_mx8<P>(p, t, o);
+            P::store(static_cast<T *>(p.u) + base, H, o);
         }
         if (!read) {
             __syncthreads();
             ring.refill();
         }
     }
-    ring.template finish<T, Q8>(false);
+    ring.template finish<T>(false);
+}
+
+// The same with u in 8 bits.  What a row costs here is instructions, so they are
+// fewer: two elements a product (f32x2), products of 16-bit weights and gates and
+// the squares of y by mixed FMAs (exact, no unpacking), alpha, a token's gate and
+// rstd(y) one factor; with that its sums and products round less often than
+// norm_kernel's, and its results differ from them by as much.  Wide rows of many
+// tokens take 32 elements a thread (norm_shape): a row's two reductions, waits and
+// addresses are then shared by the fewest warps.  (Left out one at a time, of the
+// 1040 instructions a warp and row of 7168 elements that norm_kernel's arithmetic
+// took with 32 elements a thread: the 8-bit store 221, out 48, u 46, a reduction 42.)
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
+__global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const __grid_constant__ NormParams p) {
+    using P = Part<T, EPT, MODE == Rows::kVectors>;
+    extern __shared__ __align__(128) uint8_t norm_smem[];
+    __shared__ float2 scratch[64];
+    __shared__ RowState state;
+    RowRing<MODE> ring(p, norm_smem, state, sizeof(T));
+    RowSums sums{scratch};
+    griddep_wait();
+    griddep_launch_dependents();
+    ring.start();
+    const int H = p.H;
+    const bool has_y = p.y != nullptr, post = p.w_post != nullptr;
+    const float per = 1.0f / static_cast<float>(H);
+    uint8_t *room = norm_smem + p.ring_bytes;
+    const Kept<P, MODE> w_post(p.w_post, room, H);
+    const Kept<P, MODE> w_next(p.w_next, room, H);
+    const Kept<P, MODE> gate_row(p.gate_kind == 1 ? p.gate : nullptr, room, H);
+    for (; ring.row < p.T; ring.row += gridDim.x) {
+        const int64_t t = ring.row, base = t * H;
+        ring.next();
+        float factor = p.alpha;
+        if (p.gate_kind == 2) factor *= to_f32(static_cast<const T *>(p.gate)[t]);
+        P res, w;
+        res.load(ring.take(), H);
+        bool read = false;  // every thread has read the row's slots
+        float o[EPT];
+        if (has_y) {
+            P y, gate;
+            y.load(ring.take(), H);
+            if (p.gate_kind == 3) gate.load(ring.take(), H);
+            if (post) {
+                float a = 0.0f, b = 0.0f;
+#pragma unroll
+                for (int i = 0; i < EPT; i += 2) {
+                    if constexpr (sizeof(T) == 4) {
+                        a = fmaf(y.get(i), y.get(i), a);
+                        b = fmaf(y.get(i + 1), y.get(i + 1), b);
+                    } else {
+                        a = fma_mixed<P::DT, false>(y.w[i / 2], y.w[i / 2], a);
+                        b = fma_mixed<P::DT, true>(y.w[i / 2], y.w[i / 2], b);
+                    }
+                }
+                const float r2 = rsqrtf(sums.one(a + b) * per + p.eps);
+                if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
+                ring.refill();
+                read = true;
+                factor *= r2;
+                w_post.load(w, H);
+            }
+            if (p.gate_kind == 1) gate_row.load(gate, H);
+            // the factors that an element has of its own: w_post * gate, one of them, or none
+            const float2 f = both(factor);
+            if (post && (p.gate_kind & 1)) {
+#pragma unroll
+                for (int k = 0; k < EPT / 2; ++k) {
+                    const float2 v = fma2(mul2(y.pair(k), f), make_float2(w.times(gate, 2 * k), w.times(gate, 2 * k + 1)), res.pair(k));
+                    o[2 * k] = v.x;
+                    o[2 * k + 1] = v.y;
+                }
+            } else {
+                if (p.gate_kind & 1)
+                    w = gate;
+                else if (!post)
+                    w.fill(1.0f);
+#pragma unroll
+                for (int k = 0; k < EPT / 2; ++k) {
+                    const float2 v = fma2(mul2(y.pair(k), f), w.pair(k), res.pair(k));
+                    o[2 * k] = v.x;
+                    o[2 * k + 1] = v.y;
+                }
+            }
+            P::store(static_cast<T *>(p.out) + base, H, o);
+        } else {
+#pragma unroll
+            for (int i = 0; i < EPT; ++i) o[i] = res.get(i);
+        }
+        float2 s = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int i = 0; i < EPT; i += 2) s = fma2(make_float2(o[i], o[i + 1]), make_float2(o[i], o[i + 1]), s);
+        const float r = rsqrtf(sums.one(s.x + s.y) * per + p.eps);
+        if (p.rstd_next && threadIdx.x == 0) p.rstd_next[t] = r;
+        if (!read) ring.refill();
+        w_next.load(w, H);
+#pragma unroll
+        for (int i = 0; i < EPT; i += 2) {
+            const float2 v = mul2(mul2(make_float2(o[i], o[i + 1]), both(r)), w.pair(i / 2));
+            o[i] = v.x;
+            o[i + 1] = v.y;
+        }
+        if (p.u) P::store(static_cast<T *>(p.u) + base, H, o);
+        store_mx8<P>(p, t, o);
+    }
+    ring.template finish<T, true>(false);
 }
 
 // The instructions of a row take longer than its bytes, so what a call has or
@@ -697,8 +838,14 @@ NormShape norm_shape(NormParams &p, int elem, bool backward) {
     // a thread 62); fp32 rows that wide leave two CTAs no room for a ring (81 us
     // with one CTA, 145 with two).
     s.ept = backward ? backward_ept(p.H) : p.H <= (elem == 4 ? 8192 : 4096) ? 8 : 16;
+    // The 8-bit form, 16-bit types: 32 elements a thread where rows are wide and
+    // many.  4096 rows of 1024 / 2048 / 4096 / 7168: 8.7 / 15.4 / 27.8 / 45.5 us, with the
+    // widths above 10.7 / 18.5 / 33.7 / 45.0; of 512: 7.7 and 7.1; 320 rows of 1024: 3.9
+    // and 3.1, of 7168: 7.1 and 6.6; 700 rows the same.  (fp32 with 16 instead of 8: 136
+    // us for 82, spilled.)
+    if (p.q && elem == 2 && p.H >= 1024 && p.T >= 4 * device_sm_count()) s.ept = 32;
     s.threads = norm_threads(p.H, s.ept);
-    int per_sm = 1024 / s.threads;
+    int per_sm = (s.ept == 32 ? 512 : 1024) / s.threads;
     per_sm = backward ? backward_per_sm(p.H) : per_sm < 1 ? 1 : per_sm > 16 ? 16 : per_sm;
     const int64_t kept = ((p.w_post ? 1 : 0) + (p.w_next ? 1 : 0) + (p.gate_kind == 1 ? 1 : 0)) *
                          static_cast<int64_t>(s.ept) * s.threads * elem;
@@ -739,10 +886,14 @@ cudaError_t launch_kernel(void (*kern)(NormParams), std::atomic<bool> *attr_done
 
 template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 cudaError_t launch_forward(const NormParams &p, const NormShape &s, cudaStream_t stream) {
-    static std::atomic<bool> attr_done[2][64];  // zero-initialised; several host threads may launch
-    if constexpr (MODE != Rows::kOdd)  // rows of whole blocks of 32 start on 16 bytes
-        if (p.q) return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS, true>, attr_done[1], p, s, stream);
-    return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS, false>, attr_done[0], p, s, stream);
+    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
+    return launch_kernel(norm_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS>, attr_done, p, s, stream);
+}
+
+template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
+cudaError_t launch_mx8(const NormParams &p, const NormShape &s, cudaStream_t stream) {
+    static std::atomic<bool> attr_done[64];  // zero-initialised; several host threads may launch
+    return launch_kernel(norm_mx8_kernel<T, EPT, MODE, MAX_THREADS, MIN_CTAS>, attr_done, p, s, stream);
 }
 
 template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
@@ -760,6 +911,18 @@ cudaError_t launch_backward(const NormParams &p, const NormShape &s, cudaStream_
 template <typename T> cudaError_t launch_shape(const NormParams &p, const NormShape &s, bool backward, cudaStream_t stream) {
     constexpr Rows kVectors = Rows::kVectors, kOdd = Rows::kOdd, kMemory = Rows::kMemory;
     const bool odd = s.mode == kOdd;
+    if (p.q) {  // rows of whole blocks of 32: never odd
+        if constexpr (sizeof(T) == 2) {
+            if (s.ept == 32)
+                return s.threads <= 256 ? launch_mx8<T, 32, kVectors, 256, 2>(p, s, stream) : launch_mx8<T, 32, kVectors, 512, 1>(p, s, stream);
+        } else {
+            if (s.mode == kMemory) return launch_mx8<T, 16, kMemory, 1024, 1>(p, s, stream);
+            if (s.ept == 8 && s.threads > 512) return launch_mx8<T, 8, kVectors, 1024, 1>(p, s, stream);
+        }
+        if (s.ept == 16)
+            return s.threads <= 512 ? launch_mx8<T, 16, kVectors, 512, 2>(p, s, stream) : launch_mx8<T, 16, kVectors, 1024, 1>(p, s, stream);
+        return launch_mx8<T, 8, kVectors, 512, 2>(p, s, stream);
+    }
     if (!backward) {
         if constexpr (sizeof(T) == 4)  // 16-bit rows of 16384, the widest, fit the ring
             if (s.mode == kMemory) return launch_forward<T, 16, kMemory, 1024, 1>(p, s, stream);
