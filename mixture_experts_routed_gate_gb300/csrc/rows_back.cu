@@ -9,6 +9,15 @@
 // token's CTA writes it, whatever the positions hold: nothing is added by
 // atomics and the same inputs give the same bits.  A CTA takes a token: d_out's
 // row is read once and stays in registers over the token's rows.
+//
+// Bound by its bytes: 4096 tokens, 8 rows of 7168 bf16 each, 157 us (999 MB, 147 at
+// the copy rate); 333 tokens, 5 rows of 2304 fp32, 6.1 us (4.8); 64 tokens, 6 rows of
+// 2048 fp16, 2.9 us.  What it takes is bytes in flight: 8 elements a thread and
+// row, 191 us; four pieces of 16 bytes, one row at a time, four CTAs an SM, 157
+// (two rows at a time 154, but 4096 x 6 x 2048 37 us for 35; three CTAs 160; two 173).
+// Fewer tokens than twice the SMs: a piece a thread where that covers a row, and
+// the token's rows over several CTAs (64 tokens: 4.6 us by one CTA a token; 1
+// token, 8 rows of 7168: 6.9, so 2.8).
 #include "common.cuh"
 #include "internal.h"
 
