@@ -163,7 +163,8 @@ def norm64(a):
                                              (5, 16384, "channel", True, True), (400, 64, "none", False, False), (2000, 1056, "full", True, True),
                                              (3, 8224, "channel", True, True), (37, 14336, "none", False, False), (900, 7168, "channel", True, True),
                                              (700, 4096, "channel", False, True), (1500, 1024, "token", True, True), (320, 16384, "full", True, True),
-                                             (310, 3104, "none", True, True), (1300, 2048, "none", False, False)])
+                                             (310, 3104, "none", True, True), (1300, 2048, "none", False, False),
+                                             (650, 16384, "full", True, True), (640, 9248, "channel", True, True)])
 def test_norm(T, H, gate, post, y, dtype):
     """out, u and the statistics are within the roundings of fp32 (and a half step of their type) of the formula in
     64 bits; the rows are u's unrounded values in 8 bits: u itself quantised in 32 bits, and for 16-bit types
@@ -214,6 +215,12 @@ def test_norm_odd_values():
     assert (got["sf"][2, 2] == 255).all()  # inf * rstd 0
     assert (got["sf"][3:, [0, 2, 3]] != 255).all()
     assert binding.moe_residual_norm_mx8(None, x[:0], w_next=w)["q"].shape == (0, H)
+    # statistics without a finite root: a row of zeros without eps, rows too long for fp32 and too short
+    x = torch.stack([torch.zeros(H, device="cuda"), torch.full((H,), 1e25, device="cuda"), torch.full((H,), 1e-18, device="cuda")])
+    got = binding.moe_residual_norm_mx8(None, x, w_next=torch.ones(H, device="cuda"), eps=0.0)
+    assert got["rstd_next"][0] == float("inf") and got["rstd_next"][1] == 0
+    assert (got["sf"][0] == 255).all() and (got["q"].view(torch.uint8)[:2] == 0).all() and (got["sf"][1] == 0).all()
+    assert ((values64(got["q"], got["sf"])[2] - 1).abs() <= 2.0 ** -4).all()
 
 
 def test_norm_in_place_and_its_gradient():
