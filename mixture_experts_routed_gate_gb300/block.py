@@ -83,7 +83,8 @@ def run_blocks(blocks, x, w_first, eps: float = 1e-6, err=None):
     """x [T, d_hidden], the residual stream, through the blocks; w_first: weight
     of the norm before the first one.  Returns (u, res): the last block's u' (or
     None) and the residual stream; x is left as it was."""
-    eight = [isinstance(block.experts, binding.Mx8Experts) for block in blocks] + [False]
+    blocks = list(blocks)
+    eight = [isinstance(getattr(block, "experts", None), binding.Mx8Experts) for block in blocks] + [False]
     if eight[0]:
         got = binding.moe_residual_norm_mx8(None, x, w_next=w_first, eps=eps)
         u = Rows8(got["u"], got["q"], got["sf"])
@@ -93,5 +94,5 @@ def run_blocks(blocks, x, w_first, eps: float = 1e-6, err=None):
     for block, rows8 in zip(blocks, eight[1:]):
         if u is None:
             raise ValueError("only the last block may have no w_next")
-        u, res = block(u, res, err, rows8)
+        u, res = block(u, res, err, rows8=True) if rows8 else block(u, res, err)
     return u, res

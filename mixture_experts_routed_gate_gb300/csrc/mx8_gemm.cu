@@ -612,7 +612,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                             for (int j = 0; j < 2; ++j) {
                                 const float other = take[buffer + (i + j) * 32 + lane];
                                 const float g = up ? other : own[i + j], u = up ? own[i + j] : other;
-                                h[j] = __fdividef(g, 1.0f + __expf(-g)) * u;
+                                // silu from exp(-|g|), which neither overflows nor leaves the quotient's range
+                                const float e = __expf(-fabsf(g));
+                                h[j] = __fdividef(g < 0.0f ? g * e : g, 1.0f + e) * u;
                                 s[j] = mx8_scale(__reduce_max_sync(0xffffffffu, magnitude_bits(h[j])));
                                 scale = lane == i + j ? s[j] : scale;
                             }

@@ -422,6 +422,50 @@ def test_products_of_odd_values():
     assert torch.equal(sf == 255, bad) and (q.view(torch.uint8).view(T, -1, 32)[bad] == 0).all()
 
 
+def test_gate_up_of_large_gates():
+    """Gates from -448 to 448: silu where exp(-g) leaves fp32, down to its least numbers, times an up of 2^80.  Each sum is
+    one product, exact; exp's and the quotient's errors are far below half a step of 8 bits, but exp's result loses
+    bits below 2^-126, where a gate counts with an error of 2^-149."""
+    require_cuda()
+    values = torch.tensor([0.0, 0.5, 1, 4, 16, 30, 60, 80, 88, 96, 104, 112, 256, 448], device="cuda")
+    values = torch.cat((values, -values, values[:4]))
+    K, N = 32, 32
+    t, _ = routed(1, 1, 1, 0)
+    qa = torch.zeros((1, K), device="cuda")
+    qa[0, 0] = 1
+    gate, up = torch.zeros((1, N, K), device="cuda"), torch.zeros((1, N, K), device="cuda")
+    gate[0, :, 0], up[0, :, 0] = values, 1
+    one = torch.full((1, N, 1), 127, dtype=torch.uint8, device="cuda")
+    for pick in range(N):  # one feature at a time: the others' magnitudes would set the block's scale
+        only = up.clone()
+        only[0, :pick] = 0
+        only[0, pick + 1:] = 0
+        e = binding.Mx8Experts(gate.to(E4M3), one, only.to(E4M3), one + 80, torch.zeros((1, K, N), device="cuda").to(E4M3), one)
+        q, sf = binding.moe_grouped_gate_up_silu_mx8(qa.to(E4M3), one[0, :1, 0].view(1, 1), e, t)
+        g = float(values[pick])
+        want = torch.tensor(g, dtype=torch.float64)
+        want = float(want * torch.sigmoid(want)) * 2.0 ** 80
+        got = float(values64(q, sf)[0, pick])
+        assert abs(got - want) <= 2.0 ** -4 * abs(want) * 1.001 + abs(g) * 2.0 ** -149 * 2.0 ** 80 + 2.0 ** -136, (g, got, want)
+
+
+def test_nothing_to_do():
+    """No tokens, no rows: empty results, at every entry point."""
+    require_cuda()
+    t, g = routed(3, 2, 4, 0)
+    q, sf = torch.empty((0, 64), device="cuda").to(E4M3), torch.empty((0, 2), dtype=torch.uint8, device="cuda")
+    w = [x.view(4, n, -1) for n, m in ((96, 64), (96, 64), (64, 96)) for x in rows8(4 * n, m, g)]
+    e = binding.Mx8Experts(*w)
+    none = torch.empty((0, 2), dtype=torch.int32, device="cuda")
+    assert binding.moe_quantize_mx8(torch.empty((0, 64), device="cuda"))[0].shape == (0, 64)
+    assert binding.moe_dequantize_mx8(q, sf).shape == (0, 64)
+    assert binding.moe_sort_rows_mx8(q, sf, none)[0].shape == (0, 64)
+    assert binding.moe_grouped_gate_up_silu_mx8(q, sf, e, t)[0].shape == (0, 96)
+    assert binding.moe_grouped_gemm_mx8(q, sf, w[0], w[1], t).shape == (0, 96)
+    x, w_g, bias, w = layer(2, 256, 64, 4, 2, "f16")
+    assert binding.moe_forward_mx8(x[:0], w_g, bias, binding.Mx8Experts.from_weights(*w), 2).shape == (0, 256)
+
+
 def test_rows_behind_the_last_group_are_left():
     require_cuda()
     T, E, K, N, more = 50, 3, 128, 96, 30
@@ -550,7 +594,7 @@ def test_blocks_of_all_kinds():
     one = torch.ones(d_h, dtype=torch.bfloat16, device="cuda")
     e8, e4 = binding.Mx8Experts.from_weights(*w), binding.Mx4Experts.from_weights(*w)
     make = lambda experts, last=False: MoEBlock(w_g, bias, experts, k, w_post=one, alpha=0.5, w_next=None if last else one * 0.9)  # noqa: E731
-    u, res = run_blocks([make(e8), make(tuple(w)), make(e8), make(e8), make(e4, True)], x, one)
+    u, res = run_blocks(iter([make(e8), make(tuple(w)), make(e8), make(e8), make(e4, True)]), x, one)
     assert u is None
     r = x.clone()
     f = binding.moe_residual_norm_mx8(None, r, w_next=one)
