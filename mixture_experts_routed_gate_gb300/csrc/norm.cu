@@ -572,7 +572,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
 // took with 32 elements a thread: the 8-bit store 221, out 48, u 46, a reduction 42.)
 template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const __grid_constant__ NormParams p) {
-    using P = Part<T, EPT, MODE == Rows::kVectors>;
+    using P = Part<T, EPT, true>;  // rows of whole blocks of 32 start on 16 bytes
     extern __shared__ __align__(128) uint8_t norm_smem[];
     __shared__ float2 scratch[64];
     __shared__ RowState state;
