@@ -3,14 +3,21 @@
 Each ``csrc/*.cu`` is compiled in parallel to an object under ``_build/`` and
 the objects are linked into one shared library next to this file.  A rebuild
 happens only when a source or header is newer than the library.
+
+``csrc/host_calls.cpp``, the binding's shortest calls as a Python extension, is
+compiled beside them against PyTorch's headers.  The binding makes the same calls
+without it, so where it cannot be built the compiler's words are printed and
+the build goes on.
 """
 from __future__ import annotations
 
 import concurrent.futures
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -18,6 +25,9 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(ROOT, "_build", "moe_routed_gb300")
 LIB = os.path.join(PKG, "libmoe_routed_gb300.so")
+HOST_SRC = os.path.join(CSRC, "host_calls.cpp")
+HOST_LIB = os.path.join(PKG, "_host_calls.so")
+HOST_DONE = os.path.join(BUILD, "host_calls.done")  # built, or tried, at this time
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -47,10 +57,53 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def host_is_stale() -> bool:
+    if not os.path.exists(HOST_DONE):
+        return True
+    t = os.path.getmtime(HOST_DONE)
+    return any(os.path.getmtime(p) > t for p in [HOST_SRC, LIB, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")))
+
+
+def _host_object() -> str | None:
+    """host_calls.cpp compiled; None where PyTorch or its headers are missing."""
+    spec = importlib.util.find_spec("torch")
+    if spec is None or not spec.submodule_search_locations:
+        return None
+    torch_inc = os.path.join(list(spec.submodule_search_locations)[0], "include")
+    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    obj = os.path.join(BUILD, "host_calls.o")
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", torch_inc, "-I", os.path.join(torch_inc, "torch", "csrc", "api", "include"),
+           "-I", sysconfig.get_paths()["include"], "-I", cuda_inc, "-c", HOST_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"host_calls.cpp not built (the binding goes without it):\n{r.stderr[-2000:]}")
+        return None
+    return obj
+
+
+def _link_host(obj: str | None) -> None:
+    if os.path.exists(HOST_LIB):
+        os.remove(HOST_LIB)
+    if obj is not None:
+        torch_lib = os.path.join(list(importlib.util.find_spec("torch").submodule_search_locations)[0], "lib")
+        tmp = HOST_LIB + f".tmp{os.getpid()}"
+        cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
+               "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode == 0:
+            os.replace(tmp, HOST_LIB)
+        else:
+            print(f"host_calls not linked (the binding goes without it):\n{r.stderr[-2000:]}")
+    with open(HOST_DONE, "w"):
+        pass
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    if not force and not is_stale():
-        return LIB
     os.makedirs(BUILD, exist_ok=True)
+    if not force and not is_stale():
+        if host_is_stale():
+            _link_host(_host_object())
+        return LIB
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -65,14 +118,17 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj
 
     srcs = sources()
-    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs))) as ex:
+    with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, len(srcs) + 1)) as ex:
+        host = ex.submit(_host_object)
         objs = list(ex.map(compile_one, srcs))
+        host = host.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs, "-Xcompiler", "-fvisibility=hidden"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_host(host)
     return LIB
 
 

@@ -18,6 +18,10 @@ from . import _build
 _DT = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
 _DT_NAME = {0: "f16", 1: "bf16", 2: "f32", 3: "e4m3"}
 _lib = None
+# The extension of the shortest calls (csrc/host_calls.cpp), loaded with the library;
+# None without it.  Each of its functions makes the call that the Python code
+# behind it would make, or makes none and returns None.
+_host = None
 
 BLOCK_M = 128
 WS_NAMES = ["logits", "topk_idx", "topk_w", "group_sizes", "group_offsets",
@@ -38,7 +42,7 @@ def library_path() -> str:
 
 def lib():
     """Load the CUDA library (build it first with ``__graft_entry__.build()``)."""
-    global _lib
+    global _lib, _host
     if _lib is not None:
         return _lib
     path = _build.LIB
@@ -103,6 +107,9 @@ def lib():
         fn.restype = res
         fn.argtypes = args
     _lib = L
+    if path == os.path.join(_build.PKG, os.path.basename(path)) and os.path.exists(_build.HOST_LIB):
+        from . import _host_calls
+        _host = _host_calls
     return L
 
 
@@ -853,6 +860,17 @@ def moe_residual_norm_mx8(y, res, w_post=None, gate=None, alpha: float = 1.0, w_
     :func:`moe_quantize_mx8` would; ``u`` itself only with ``with_u``.  w_next is
     needed and H % 32 == 0; everything else as there, the gradients
     (:func:`moe_residual_norm_backward`, with d_u the gradient of the rows' values) too."""
+    if _host is not None and q is None and sf is None:
+        made = _host.norm_mx8(y, res, w_post, gate, alpha, w_next, eps, with_u, out)
+        if made is not None:
+            got = {"q": made[2], "sf": made[3], "rstd_next": made[5]}
+            if y is not None:
+                got["out"] = made[0]
+            if with_u:
+                got["u"] = made[1]
+            if w_post is not None:
+                got["rstd_post"] = made[4]
+            return got
     _cuda(res, "res", ndim=2)
     shape, dt, dev, f32 = res.shape, res.dtype, res.device, torch.float32
     T, H = shape
@@ -1089,6 +1107,10 @@ def moe_reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_
     token, as the dispatch does; rows that no position names get zeros, positions
     of -1 a zero weight gradient.  The gradient of the way to the experts
     (:func:`moe_gather_rows_by_token`) is ``moe_reduce_fused(d_rows, token_topk_to_pos)``."""
+    if _host is not None:
+        made = _host.reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_token_idx, err)
+        if made is not None:
+            return made
     _cuda(x, "x", ndim=2)
     _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
     _cuda(d_out, "d_out", ndim=2)
@@ -1152,6 +1174,10 @@ def moe_sort_rows_mx8(q, sf, token_topk_to_pos, n_rows=None, q_out=None, sf_out=
     token_topk_to_pos[t, j] of the result is row t of q, sf.  n_rows None: one for
     each position.  Positions outside [0, n_rows) are skipped, rows that no
     position names are left as they were; a position stands at one place only."""
+    if _host is not None and n_rows is None and q_out is None and sf_out is None:
+        made = _host.sort_rows_mx8(q, sf, token_topk_to_pos)
+        if made is not None:
+            return made
     _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
     T, k = token_topk_to_pos.shape
     K, dev = _mx8(q, sf, "", (T,)), q.device
@@ -1161,6 +1187,14 @@ def moe_sort_rows_mx8(q, sf, token_topk_to_pos, n_rows=None, q_out=None, sf_out=
     _call("moe_sort_rows_mx8", dev, q.data_ptr(), sf.data_ptr(), token_topk_to_pos.data_ptr(), T, k, n_rows, K, q_out.data_ptr(),
           sf_out.data_ptr())
     return q_out, sf_out
+
+
+def _four(t):
+    """The four tables for the extension, which makes no call where one is missing."""
+    try:
+        return t["group_sizes"], t["group_offsets"], t["group_padded_offsets"], t["group_idx_for_bx"]
+    except (KeyError, TypeError):
+        return None, None, None, None
 
 
 def _table_addresses(t, E):
@@ -1179,6 +1213,10 @@ def _table_addresses(t, E):
 def moe_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16, out=None, err=None):
     """C[r] = A_r B[g]^T over the dispatch tables, both sides mx8: q_a, sf_a
     [rows, .], q_b, sf_b [E, N, .]; returns C [rows, N] in out_dtype."""
+    if _host is not None and out is None:
+        made = _host.grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, *_four(tables), _DT.get(out_dtype), err)
+        if made is not None:
+            return made
     _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
     _cuda(q_b, "q_b", dtype=torch.float8_e4m3fn, ndim=3)
     rows, (E, N, _) = q_a.shape[0], q_b.shape
@@ -1196,9 +1234,11 @@ class Mx8Experts:
     """The three expert weights of a layer as mx8 elements and scales."""
 
     def __init__(self, q_gate, sf_gate, q_up, sf_up, q_down, sf_down):
-        self.E, self.d_e, self.d_h = q_gate.shape
-        for q, sf, name, lead in ((q_gate, sf_gate, "_gate", (self.E, self.d_e)), (q_up, sf_up, "_up", (self.E, self.d_e)),
-                                  (q_down, sf_down, "_down", (self.E, self.d_h))):
+        sizes = None if _host is None else _host.experts_mx8(q_gate, sf_gate, q_up, sf_up, q_down, sf_down)
+        self.E, self.d_e, self.d_h = q_gate.shape if sizes is None else sizes
+        for q, sf, name, lead in () if sizes else (
+                (q_gate, sf_gate, "_gate", (self.E, self.d_e)), (q_up, sf_up, "_up", (self.E, self.d_e)),
+                (q_down, sf_down, "_down", (self.E, self.d_h))):
             if _mx8(q, sf, name, lead) != (self.d_e if name == "_down" else self.d_h):
                 raise ValueError("q_gate / q_up must be [E, d_e, d_h] and q_down [E, d_h, d_e]")
         self.q_gate, self.sf_gate, self.q_up, self.sf_up = q_gate, sf_gate, q_up, sf_up
@@ -1218,6 +1258,11 @@ class Mx8Experts:
 def moe_grouped_gate_up_silu_mx8(q_a, sf_a, experts: "Mx8Experts", tables, q_h=None, sf_h=None, err=None):
     """h = silu(A W_gate^T) * (A W_up^T) over the dispatch tables, quantised:
     returns q_h [rows, d_e], sf_h [rows, d_e / 32]."""
+    if _host is not None and q_h is None and sf_h is None:
+        e = experts
+        made = _host.grouped_gate_up_silu_mx8(q_a, sf_a, e.q_gate, e.sf_gate, e.q_up, e.sf_up, *_four(tables), err)
+        if made is not None:
+            return made
     _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
     rows, dev, e = q_a.shape[0], q_a.device, experts
     if _mx8(q_a, sf_a, "_a", (rows,)) != e.d_h:

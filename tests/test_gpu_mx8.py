@@ -631,3 +631,80 @@ def test_refusals():
                  lambda: binding.moe_sort_rows_mx8(q, sf, pos.long()), lambda: binding.moe_quantize_mx8(x.double())):
         with pytest.raises(TypeError):
             call()
+
+
+def test_the_extension_makes_the_same_calls(monkeypatch):
+    """With the extension of the short calls and without it: the same bits, the same refusals."""
+    require_cuda()
+    binding.lib()
+    host = binding._host
+    assert host is not None
+    T, k, E, K, N = 70, 3, 5, 256, 96
+    t, g = routed(T, k, E, 9)
+    (q, sf), w = rows8(T, K, g), [x.view(E, n, -1) for n, m in ((N, K), (N, K), (K, N)) for x in rows8(E * n, m, g)]
+    x, d_out, tw = torch.randn((T * k, K), device="cuda").half(), torch.randn((T, K), device="cuda").half(), torch.rand((T, k), device="cuda")
+    pos, token = t["token_topk_to_pos"], t["sorted_token_idx"]
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    made = []
+
+    def calls():
+        out = []
+        for gate in ("none", "channel", "token", "full"):
+            for post, y in ((True, True), (False, True), (False, False)):
+                if y or gate == "none":
+                    a = norm_inputs(T, K, torch.bfloat16, gate, post, y, 5)
+                    for with_u in (True, False):
+                        out.append(binding.moe_residual_norm_mx8(**a, with_u=with_u))
+        a = norm_inputs(T, K, torch.float16, "channel", True, True, 6)
+        res = a["res"].clone()
+        out.append(binding.moe_residual_norm_mx8(**{**a, "res": res}, out=res))
+        assert out[-1]["out"] is res or out[-1]["out"].data_ptr() == res.data_ptr()
+        out.append(binding.moe_sort_rows_mx8(q, sf, pos))
+        for weights, e in ((tw, err), (None, None)):
+            out.append(binding.moe_reduce_fused_backward(d_out, x, pos, weights, token, e))
+        e = binding.Mx8Experts(*w)
+        out.append((e.E, e.d_e, e.d_h))
+        rows = binding.moe_sort_rows_mx8(q, sf, pos)
+        h = binding.moe_grouped_gate_up_silu_mx8(*rows, e, t, err=err)
+        out += [h] + [binding.moe_grouped_gemm_mx8(*h, e.q_down, e.sf_down, t, d) for d in DT.values()]
+        return out
+
+    def bits(v):
+        if isinstance(v, dict):
+            return {n: bits(x) for n, x in v.items()}
+        if isinstance(v, (tuple, list)):
+            return [bits(x) for x in v]
+        return (v.dtype, v.shape, v.view(torch.uint8).tolist()) if isinstance(v, torch.Tensor) else v
+
+    class Counted:
+        def __getattr__(self, name):
+            def f(*a):
+                r = getattr(host, name)(*a)
+                made.append((name, r is not None))
+                return r
+            return f
+    monkeypatch.setattr(binding, "_host", Counted())
+    fast = bits(calls())
+    assert all(yes for _, yes in made) and {n for n, _ in made} == {"norm_mx8", "sort_rows_mx8", "reduce_fused_backward", "experts_mx8",
+                                                                    "grouped_gemm_mx8", "grouped_gate_up_silu_mx8"}
+    monkeypatch.setattr(binding, "_host", None)
+    assert bits(calls()) == fast
+    e = binding.Mx8Experts(*w)
+    wrong = [lambda: binding.moe_sort_rows_mx8(q, sf, pos.long()), lambda: binding.moe_sort_rows_mx8(q, sf[:, :4], pos),
+             lambda: binding.moe_sort_rows_mx8(q.view(torch.uint8), sf, pos), lambda: binding.moe_sort_rows_mx8(q, sf, pos[:5]),
+             lambda: binding.moe_reduce_fused_backward(d_out.float(), x, pos, tw, token), lambda: binding.moe_reduce_fused_backward(d_out, x, pos, tw, token[:4]),
+             lambda: binding.moe_reduce_fused_backward(d_out, x, pos, tw.half(), token), lambda: binding.moe_reduce_fused_backward(d_out.t(), x, pos, tw, token),
+             lambda: binding.moe_grouped_gemm_mx8(q, sf, *w[4:], t), lambda: binding.moe_grouped_gemm_mx8(q, sf, w[0], w[1], {}),
+             lambda: binding.moe_grouped_gemm_mx8(q, sf, w[0], w[1], t, torch.float64), lambda: binding.moe_grouped_gemm_mx8(q, sf, w[0], w[1], t, err=tw),
+             lambda: binding.moe_grouped_gate_up_silu_mx8(*rows8(4, 64, g), e, t), lambda: binding.Mx8Experts(*w[2:], *w[:2]),
+             lambda: binding.moe_residual_norm_mx8(d_out, x, w_next=x[0]), lambda: binding.moe_residual_norm_mx8(None, x, w_next=x[0].float()),
+             lambda: binding.moe_residual_norm_mx8(None, x, w_next=x[0], alpha="1"), lambda: binding.moe_residual_norm_mx8(None, x, w_next=x[0], eps=-1.0),
+             lambda: binding.moe_residual_norm_mx8(x, x, gate=x[0, :32], w_next=x[0]), lambda: binding.moe_residual_norm_mx8(None, x, None, x[0], w_next=x[0])]
+    told = []
+    for h in (None, host):
+        monkeypatch.setattr(binding, "_host", h)
+        for f in wrong:
+            with pytest.raises(Exception) as caught:
+                f()
+            told.append((type(caught.value), str(caught.value)))
+    assert told[:len(wrong)] == told[len(wrong):]

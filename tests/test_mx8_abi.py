@@ -96,3 +96,15 @@ def test_binding_refuses_what_is_not_on_the_gpu():
                  lambda: binding.moe_grouped_gemm_mx8(q, sf, q[None], sf[None], {}), lambda: binding.Mx8Experts(*(q[None], sf[None]) * 3)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_the_short_calls_extension_is_built(lib):
+    """Where PyTorch's headers are, the binding has the extension; without a GPU's tensors it makes no call."""
+    import torch
+    assert binding._host is not None
+    x, q = torch.zeros((4, 64)), torch.zeros((4, 64), dtype=torch.float8_e4m3fn)
+    assert binding._host.norm_mx8(None, x, None, None, 1.0, x[0], 1e-6, True, None) is None
+    assert binding._host.sort_rows_mx8(q, x, x) is None and binding._host.sort_rows_mx8(q) is None
+    assert binding._host.reduce_fused_backward(x, x, None, None, None, None) is None
+    assert binding._host.grouped_gemm_mx8(*[None] * 10) is None and binding._host.grouped_gate_up_silu_mx8(*[3] * 11) is None
+    assert binding._host.experts_mx8(*[q] * 6) is None
