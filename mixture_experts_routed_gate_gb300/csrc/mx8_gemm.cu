@@ -723,16 +723,21 @@ cudaError_t launch_n(const CUtensorMap *maps, const G8Params &p, cudaStream_t st
 // Tiles of up to 256 rows where experts have many: the weights enter shared
 // memory half as often.  They leave three stages for four, and the wide tiles'
 // epilogue runs alone (both accumulator slots are one tile's), which the
-// gate/up form's longer one earns back only over a long K.  Narrow / wide, us:
+// gate/up form's longer one earns back only over a long K, and the product's
+// over a short K only when there are several rounds of tiles; tiles that do not
+// fill a round are better narrow, and more.  Narrow / wide, us:
 //   7168 x 2048, 256 experts, 128 rows each: 837 / 777, gate/up 1776 / 1639
 //   7168 x 2048, 64 experts: 32 rows each 153 / 156 and 326 / 328, 64 rows 184 / 175
 //   and 348 / 341, 256 rows 328 / 284 and 677 / 591; 16 experts, 2048 rows 507 / 347
-//   2048 x 768, 64 experts: 384 rows each 65 / 63, gate/up 129 / 140; 128 rows 32 / 34
-//   and 63 / 74; 2048 x 2048, 8 experts, 4096 rows 162 / 133, gate/up 340 / 347
+//   2048 x 768, 64 experts: 384 rows each 65 / 63, gate/up 129 / 140; 128 rows 29 / 31
+//   and 59 / 64; 2048 x 2048, 8 experts, 4096 rows 162 / 133, gate/up 340 / 347
+//   rounds of wide tiles: 0.2 (600 rows, 7168 x 512) 24 / 26, 0.4 (4096 rows) 24 / 28,
+//   gate/up 0.8 of them 44 / 33; 1.7 (16 experts, 500 rows, 2048 x 1024) 28 / 30
 template <typename TOut>
 cudaError_t launch_typed(const CUtensorMap *maps, const G8Params &p, int64_t n_rows, int64_t E, cudaStream_t stream) {
-    const bool long_sums = !std::is_same<TOut, void>::value || p.K >= 4096;
-    if (n_rows > 64 * E && long_sums) return launch_n<TOut, 256>(maps, p, stream);
+    const int64_t tiles = (n_rows + 255) / 256 * p.n_tiles, pairs = device_sm_count() / 2;
+    const bool pays = p.K >= 4096 ? 4 * tiles >= 3 * pairs : !std::is_same<TOut, void>::value && tiles >= 4 * pairs;
+    if (n_rows > 64 * E && pays) return launch_n<TOut, 256>(maps, p, stream);
     return launch_n<TOut, 128>(maps, p, stream);
 }
 

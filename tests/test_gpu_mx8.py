@@ -319,8 +319,9 @@ def product_and_size(a, b, t):
 
 SHAPES = [(1, 1, 1, 32, 1), (1, 8, 8, 256, 128), (5, 2, 3, 64, 33), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 333), (130, 1, 1, 96, 257),
           (700, 2, 3, 288, 200), (257, 4, 7, 1024, 512), (96, 2, 6, 7168, 160), (40, 2, 600, 160, 64), (128, 1, 1, 512, 300), (129, 1, 1, 544, 256)]
-# more units of rows than a CTA lists: of up to 128 rows, and of up to 256
-SHAPES += [(1100, 2, 900, 96, 40), (10000, 4, 600, 32, 40)]
+# more units of rows than a CTA lists: of up to 128 rows, and of up to 256; several rounds of tiles of up to 256
+SHAPES += [(1100, 2, 900, 96, 40), (10000, 4, 600, 32, 40), (20000, 4, 600, 32, 300), (5000, 2, 7, 288, 4100), (3000, 2, 7, 4128, 700),
+           (2000, 1, 3, 4096, 2000)]
 
 
 @pytest.mark.parametrize("out", ["f16", "bf16", "f32"])
@@ -372,7 +373,8 @@ def silu_products(t, qa, sa, gate, up):
 
 @pytest.mark.parametrize("T,k,E,K,N", [(1, 1, 1, 32, 32), (1, 8, 8, 256, 128), (5, 2, 3, 64, 96), (64, 6, 64, 2048, 768), (301, 3, 5, 1056, 352),
                                        (700, 2, 3, 288, 224), (257, 4, 7, 1024, 512), (40, 2, 600, 160, 64), (129, 1, 1, 544, 256), (33, 1, 2, 7168, 160),
-                                       (1100, 2, 900, 96, 64), (400, 2, 3, 4128, 96), (600, 1, 2, 4096, 160), (39000, 1, 600, 4096, 32)])
+                                       (1100, 2, 900, 96, 64), (400, 2, 3, 4128, 96), (600, 1, 2, 4096, 160), (39000, 1, 600, 4096, 32),
+                                       (4000, 1, 3, 4128, 512), (2000, 2, 5, 4096, 1056)])
 def test_gate_up(T, k, E, K, N):
     require_cuda()
     t, g = routed(T, k, E, T + K)
