@@ -88,7 +88,7 @@ def _link_host(obj: str | None) -> None:
         torch_lib = os.path.join(list(importlib.util.find_spec("torch").submodule_search_locations)[0], "lib")
         tmp = HOST_LIB + f".tmp{os.getpid()}"
         cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
-               "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+               "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if r.returncode == 0:
             os.replace(tmp, HOST_LIB)

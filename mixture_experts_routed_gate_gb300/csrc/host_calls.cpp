@@ -12,12 +12,14 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
 #include <initializer_list>
+#include <optional>
 
 #include "../../include/moe_routed_gate.h"
 
@@ -63,7 +65,7 @@ void scaled(PyObject *o, const Tensor &q) {
 }
 
 Tensor made(const Tensor &on, at::ScalarType type, at::IntArrayRef shape) {
-    return at::empty(shape, at::TensorOptions().dtype(type).device(on.device()));
+    return at::detail::empty_cuda(shape, type, on.device(), std::nullopt);
 }
 
 moe_dtype_t code(at::ScalarType t) {

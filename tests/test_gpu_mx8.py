@@ -689,6 +689,8 @@ def test_the_extension_makes_the_same_calls(monkeypatch):
     fast = bits(calls())
     assert all(yes for _, yes in made) and {n for n, _ in made} == {"norm_mx8", "sort_rows_mx8", "reduce_fused_backward", "experts_mx8",
                                                                     "grouped_gemm_mx8", "grouped_gate_up_silu_mx8"}
+    with torch.inference_mode():
+        assert bits(calls()) == fast and binding.moe_sort_rows_mx8(q, sf, pos)[0].is_inference()
     monkeypatch.setattr(binding, "_host", None)
     assert bits(calls()) == fast
     e = binding.Mx8Experts(*w)
