@@ -635,7 +635,8 @@ MOE_API moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float
  * moe_grouped_gate_up_silu_mx8: h = silu(A W_gate^T) * (A W_up^T) from the fp32
  * sums, quantised as moe_quantize_mx8 would its fp32 values: q_h, sf_h
  * [n_rows, d_e].  d_h % 32 == 0, d_e % 32 == 0.
- * q_* 16-byte aligned.
+ * q_* 16-byte aligned; sf_* may start anywhere.  No output may overlap an input
+ * (out and res of the norm apart).
  */
 MOE_API moe_status_t moe_residual_norm_mx8(const void *y, const void *res, const void *w_post, const void *gate,
                                            moe_gate_t gate_kind, float alpha, const void *w_next, float eps,
@@ -696,7 +697,8 @@ MOE_API moe_status_t moe_forward_mx8(const void *x, const uint8_t *q, const uint
  * whatever they hold: the same inputs give the same bits.  A pos < -1 or
  * >= n_rows counts as -1, a pos that names another token's row reads that row
  * and gives it no gradient; both set *err_flag = MOE_ERR_DEVICE_FLAG.
- * H % 256 == 0, 1 <= K <= 32.  (The gradient of moe_gather_rows_by_token is
+ * H % 256 == 0, 1 <= K <= 32; no output may overlap an input.  (The gradient of
+ * moe_gather_rows_by_token is
  * moe_reduce_fused of the rows' gradients with unit weights.)
  */
 MOE_API moe_status_t moe_reduce_fused_backward(const void *d_out, const void *x, int64_t n_rows,

@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 import torch
 
@@ -108,8 +109,11 @@ def lib():
         fn.argtypes = args
     _lib = L
     if path == os.path.join(_build.PKG, os.path.basename(path)) and os.path.exists(_build.HOST_LIB):
-        from . import _host_calls
-        _host = _host_calls
+        try:
+            from . import _host_calls
+            _host = _host_calls
+        except ImportError as e:  # built against another PyTorch, say: the Python code makes the same calls
+            warnings.warn(f"short calls go through Python: {e}")
     return L
 
 
