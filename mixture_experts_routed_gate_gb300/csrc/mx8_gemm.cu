@@ -145,6 +145,27 @@ __device__ __forceinline__ void tc_commit2_both_elect(uint32_t bar) {
         : "memory");
 }
 
+// The copies' warp runs whole too.
+__device__ __forceinline__ void expect_elect(uint32_t bar, uint32_t bytes) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copy_2d_elect(uint32_t dst, const void *map, uint32_t bar_cluster, int c0, int c1, uint64_t policy) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".L2::cache_hint [%0], [%1, {%3, %4}], [%2], %5;\n\t}" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(bar_cluster), "r"(c0), "r"(c1), "l"(policy)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_3d_elect(uint32_t dst, const void *map, uint32_t bar_cluster, int c0, int c1, int c2,
+                                              uint64_t policy) {
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
+                 "@e cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                 ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;\n\t}" ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "l"(policy)
+                 : "memory");
+}
+
 // A barrier of COUNT threads: whether `yes` holds in all of them.
 template <int COUNT> __device__ __forceinline__ bool g8_all(int id, bool yes) {
     uint32_t all;
@@ -347,56 +368,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
 
     if (warp == 0) {
         // -------------------------------- copies --------------------------------
-        if (lane == 0) {
-            const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
-            int stage = 0;
-            uint32_t phase = 0;
-            long issued = 0;
-            bool ok = true;
-            for (Cursor t = first; live(t) && ok; advance(t)) {
-                const G8Tile ti = tile_at(t);
-                if (ti.rows == 0) continue;
-                const int half = columns_of(ti) / 2;  // a multiple of 16 rows
-                const int row0 = ti.m_start + static_cast<int>(rank) * half;
-                const uint64_t pol = ti.single ? pass : keep;  // an only unit's weights are read once
-                for (int s = 0; s < p.slices; ++s) {
-                    if (!mbar_wait_cluster_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t a = smem_u32(smem + stage * L::STAGE), b = a + 2 * G8_A_HALF;
-                    const int halves = s * G8_SLICE + 128 < p.K ? 2 : 1;
-                    if (leader)
-                        mbar_arrive_expect_tx(full_bar(stage), 2 * halves * (G8_A_HALF + half * 128));
-                    const uint32_t fb = smem_map_rank(full_bar(stage), 0);
-                    for (int h = 0; h < halves; ++h) {
-                        const int k0 = s * G8_SLICE + h * 128;
-                        tma2_load_3d_hint(a + h * G8_A_HALF, &tmB0, fb, k0, ti.n0, ti.g, pol);
-                        if (GATE_UP) tma2_load_3d_hint(a + h * G8_A_HALF + G8_A_HALF / 2, &tmB1, fb, k0, ti.n0, ti.g, pol);
-                        for (int i = 0; i < half; i += 64) {  // copies of 64, 32 and 16 rows
-                            const int have = half - i;
-                            const uint32_t to = b + h * L::B_HALF + i * 128;
-                            if (have >= 64) {
-                                tma2_load_2d_hint(to, &tmA64, fb, k0, row0 + i, keep);
-                            } else {
-                                if (have & 32) tma2_load_2d_hint(to, &tmA32, fb, k0, row0 + i, keep);
-                                if (have & 16) tma2_load_2d_hint(to + (have & 32) * 128, &tmA16, fb, k0, row0 + i + (have & 32), keep);
-                            }
+        const uint64_t keep = l2_policy_evict_last(), pass = l2_policy_evict_first();
+        const uint32_t ring = smem_u32(smem), full_leader = smem_map_rank(full_bar(0), 0);
+        int stage = 0;
+        uint32_t phase = 0;
+        long issued = 0;
+        bool ok = true;
+        for (Cursor t = first; live(t) && ok; advance(t)) {
+            const G8Tile ti = tile_at(t);
+            const int columns = __shfl_sync(0xffffffffu, columns_of(ti), 0);
+            if (columns == 0) continue;
+            const int half = columns / 2;  // a multiple of 16 rows
+            const int row0 = __shfl_sync(0xffffffffu, ti.m_start, 0) + static_cast<int>(rank) * half;
+            const int g = __shfl_sync(0xffffffffu, ti.g, 0), n0 = ti.n0;
+            const uint64_t pol = __shfl_sync(0xffffffffu, ti.single ? 1 : 0, 0) ? pass : keep;  // an only unit's weights are read once
+            for (int s = 0; s < p.slices; ++s) {
+                ok = __all_sync(0xffffffffu, mbar_wait_cluster_bounded(empty_bar(stage), phase ^ 1u, abort_flag, p.err)) != 0;
+                if (!ok) break;
+                const uint32_t a = ring + stage * L::STAGE, b = a + 2 * G8_A_HALF, fb = full_leader + 8u * stage;
+                const int halves = s * G8_SLICE + 128 < p.K ? 2 : 1;
+                if (leader) expect_elect(full_bar(stage), 2 * halves * (G8_A_HALF + half * 128));
+                for (int h = 0; h < halves; ++h) {
+                    const int k0 = s * G8_SLICE + h * 128;
+                    copy_3d_elect(a + h * G8_A_HALF, &tmB0, fb, k0, n0, g, pol);
+                    if (GATE_UP) copy_3d_elect(a + h * G8_A_HALF + G8_A_HALF / 2, &tmB1, fb, k0, n0, g, pol);
+                    for (int i = 0; i < half; i += 64) {  // copies of 64, 32 and 16 rows
+                        const int have = half - i;
+                        const uint32_t to = b + h * L::B_HALF + i * 128;
+                        if (have >= 64) {
+                            copy_2d_elect(to, &tmA64, fb, k0, row0 + i, keep);
+                        } else {
+                            if (have & 32) copy_2d_elect(to, &tmA32, fb, k0, row0 + i, keep);
+                            if (have & 16) copy_2d_elect(to + (have & 32) * 128, &tmA16, fb, k0, row0 + i + (have & 32), keep);
                         }
                     }
-                    ++issued;
-                    if (++stage == L::STAGES) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                ++issued;
+                if (++stage == L::STAGES) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            if (leader && (!ok || *abort_flag)) {
-                // both CTAs' copies in flight land before shared memory goes away
-                for (long j = 1; j <= L::STAGES && j <= issued; ++j) {
-                    const long i = issued - j;
-                    g8_drain(full_bar(static_cast<int>(i % L::STAGES)), static_cast<uint32_t>((i / L::STAGES) & 1));
-                }
+        }
+        if (leader && lane == 0 && (!ok || *abort_flag)) {
+            // both CTAs' copies in flight land before shared memory goes away
+            for (long j = 1; j <= L::STAGES && j <= issued; ++j) {
+                const long i = issued - j;
+                g8_drain(full_bar(static_cast<int>(i % L::STAGES)), static_cast<uint32_t>((i / L::STAGES) & 1));
             }
         }
     } else if (warp == 1) {
