@@ -27,14 +27,18 @@
 //               the slices: as a part of each slice it bound the kernel (1124 us
 //               where units took 788; without any scales 810).
 //
-// 32,768 rows, 256 experts, 7168 x 2048, bf16 out: 768 us for 4.25 GB (627 at the
+// 32,768 rows, 256 experts, 7168 x 2048, bf16 out: 718 us for 4.25 GB (627 at the
 // copy rate); its tiles bring 5.9 GB from L2 into shared memory, which gives out at
 // 10 to 12 TB/s (16 experts of 2048 rows: 3.8 GB in 347 us, 2.8 PFLOP/s), and the
-// tensor pipe is active for a quarter of the time.  8192 rows: 616 us, 95% of the
-// copy rate; the gate/up form of those 1260 us, twice the bytes.  384 rows of 64
-// experts, 2048 x 768, fp16: 25 us for 100 MB (15 at the copy rate): about 7 us are
-// the unit list, the first copies, the last epilogue and the exit, and 192 tiles
-// are 2.5 rounds of 76 pairs.
+// tensor pipe is active for a quarter of the time.  What paces a slice is the one
+// thread that asks for its copies: issued by one lane of a branch, each operand
+// is moved to it first (770 us), and any work more between them shows in all sizes
+// (chunks of shared memory handed out by need, so that a fourth narrow slice fits
+// the wide tiles' ring, 8 to 10% slower).  8192 rows: 600 us, 95% of the copy rate;
+// the gate/up form of those 1200 us, twice the bytes.  384 rows of 64 experts, 2048 x
+// 768, fp16: 23 us for 100 MB (15 at the copy rate): about 7 us are the unit list, the
+// first copies, the last epilogue and the exit, and 192 tiles are 2.5 rounds of 76
+// pairs.
 //
 // Slower, at 384 rows through both forms (63 us with the sort): the last round's
 // tiles cut by features into 2 or 4 parts 69; the weights' first slices
@@ -392,14 +396,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                     const int k0 = s * G8_SLICE + h * 128;
                     copy_3d_elect(a + h * G8_A_HALF, &tmB0, fb, k0, n0, g, pol);
                     if (GATE_UP) copy_3d_elect(a + h * G8_A_HALF + G8_A_HALF / 2, &tmB1, fb, k0, n0, g, pol);
-                    for (int i = 0; i < half; i += 64) {  // copies of 64, 32 and 16 rows
-                        const int have = half - i;
-                        const uint32_t to = b + h * L::B_HALF + i * 128;
-                        if (have >= 64) {
-                            copy_2d_elect(to, &tmA64, fb, k0, row0 + i, keep);
-                        } else {
-                            if (have & 32) copy_2d_elect(to, &tmA32, fb, k0, row0 + i, keep);
-                            if (have & 16) copy_2d_elect(to + (have & 32) * 128, &tmA16, fb, k0, row0 + i + (have & 32), keep);
+                    // copies of 64, 32 and 16 rows; the wide tiles' without a loop, which paces
+                    // them (32768 rows 744 us with it, 718 without), the others' with one
+                    // (384 rows 60.5 us with it, 61.0 without)
+                    uint32_t to = b + h * L::B_HALF;
+                    if constexpr (NT == 256) {
+                        int r = row0;
+                        if (half >= 64) {
+                            copy_2d_elect(to, &tmA64, fb, k0, r, keep);
+                            to += 64 * 128;
+                            r += 64;
+                            if (half == 128) copy_2d_elect(to, &tmA64, fb, k0, r, keep);
+                        }
+                        if (half & 32) {
+                            copy_2d_elect(to, &tmA32, fb, k0, r, keep);
+                            to += 32 * 128;
+                            r += 32;
+                        }
+                        if (half & 16) copy_2d_elect(to, &tmA16, fb, k0, r, keep);
+                    } else {
+                        for (int i = 0; i < half; i += 64) {
+                            const int have = half - i;
+                            const uint32_t at = to + i * 128;
+                            if (have >= 64) {
+                                copy_2d_elect(at, &tmA64, fb, k0, row0 + i, keep);
+                            } else {
+                                if (have & 32) copy_2d_elect(at, &tmA32, fb, k0, row0 + i, keep);
+                                if (have & 16) copy_2d_elect(at + (have & 32) * 128, &tmA16, fb, k0, row0 + i + (have & 32), keep);
+                            }
                         }
                     }
                 }
