@@ -764,21 +764,26 @@ cudaError_t launch_n(const CUtensorMap *maps, const G8Params &p, cudaStream_t st
 
 // Tiles of up to 256 rows where experts have many: the weights enter shared
 // memory half as often.  They leave three stages for four, and the wide tiles'
-// epilogue runs alone (both accumulator slots are one tile's), which the
-// gate/up form's longer one earns back only over a long K, and the product's
-// over a short K only when there are several rounds of tiles; tiles that do not
-// fill a round are better narrow, and more.  Narrow / wide, us:
-//   7168 x 2048, 256 experts, 128 rows each: 837 / 777, gate/up 1776 / 1639
-//   7168 x 2048, 64 experts: 32 rows each 153 / 156 and 326 / 328, 64 rows 184 / 175
-//   and 348 / 341, 256 rows 328 / 284 and 677 / 591; 16 experts, 2048 rows 507 / 347
-//   2048 x 768, 64 experts: 384 rows each 65 / 63, gate/up 129 / 140; 128 rows 29 / 31
-//   and 59 / 64; 2048 x 2048, 8 experts, 4096 rows 162 / 133, gate/up 340 / 347
+// epilogue runs alone (both accumulator slots are one tile's), which a long K earns
+// back, and a shorter one only when there are several rounds of tiles: the product
+// from K of 1024, the gate/up form, whose epilogue is longer, from 2048 and 512 rows
+// an expert; tiles that do not fill a round are better narrow, and more.  Narrow / wide, us:
+//   7168 x 2048, 256 experts, 128 rows each: 828 / 730, gate/up 1730 / 1455
+//   7168 x 2048, 64 experts: 32 rows each 166 / 165 and 316 / 313, 64 rows 177 / 174
+//   and 331 / 326, 256 rows 321 / 244 and 678 / 520; 16 experts, 2048 rows 515 / 370
+//   2048 x 768, 64 experts: 128 rows each 29 / 30, gate/up 61 / 65; 384 rows 57.5 / 62.5,
+//   124 / 128; gate/up 768 rows 222 / 210, 1024 rows 295 / 269
+//   2048 x 2048: 8 experts, 4096 rows 158 / 125, gate/up 352 / 327; gate/up 1024 rows
+//   97 / 90, 64 experts, 256 rows 221 / 223
+//   32 experts, 1024 rows, 1024 x 2048: 95.6 / 90.8, gate/up 248 / 274; 512 x 2048: 68.9 /
+//   70.0, gate/up 219 / 235; 64 experts, 128 rows, 256 x 4096: 43.8 / 48.9
 //   rounds of wide tiles: 0.2 (600 rows, 7168 x 512) 24 / 26, 0.4 (4096 rows) 24 / 28,
 //   gate/up 0.8 of them 44 / 33; 1.7 (16 experts, 500 rows, 2048 x 1024) 28 / 30
 template <typename TOut>
 cudaError_t launch_typed(const CUtensorMap *maps, const G8Params &p, int64_t n_rows, int64_t E, cudaStream_t stream) {
     const int64_t tiles = (n_rows + 255) / 256 * p.n_tiles, pairs = device_sm_count() / 2;
-    const bool pays = p.K >= 4096 ? 4 * tiles >= 3 * pairs : !std::is_same<TOut, void>::value && tiles >= 4 * pairs;
+    const bool deep = std::is_same<TOut, void>::value ? p.K >= 2048 && n_rows >= 512 * E : p.K >= 1024;
+    const bool pays = p.K >= 4096 ? 4 * tiles >= 3 * pairs : deep && tiles >= 4 * pairs;
     if (n_rows > 64 * E && pays) return launch_n<TOut, 256>(maps, p, stream);
     return launch_n<TOut, 128>(maps, p, stream);
 }

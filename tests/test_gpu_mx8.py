@@ -393,6 +393,11 @@ def test_gate_up(T, k, E, K, N):
     assert (top - most <= 448 * unit).all() and ((top + most > 224 * unit) | (sf == 0)).all()
 
 
+def test_gate_up_of_many_rows_over_short_sums():
+    """Tiles of 256 rows below 4096 features: many rows an expert and several rounds of tiles, none of them whole."""
+    test_gate_up(4100, 1, 2, 2080, 2336)
+
+
 def test_products_of_odd_values():
     """NaN scales, infinities in the sums and zeros stay in their rows and columns; rows of h in their blocks."""
     require_cuda()
