@@ -569,7 +569,9 @@ MOE_API moe_status_t moe_forward_few(const void *x, const void *w_g, const float
  * moe_grouped_gate_up_silu_mx4: h = silu(A W_gate^T) * (A W_up^T) from the fp32
  * sums, quantised as moe_quantize_mx4 would its fp32 values: q_h, sf_h
  * [n_rows, d_e].  d_h % 32 == 0, d_e % 32 == 0.
- * q_* 16-byte aligned.
+ * q_* 16-byte aligned.  Rows that the tables place outside [0, n_rows) (the tables
+ * of a larger batch) are left out and set *err_flag = MOE_ERR_DEVICE_FLAG; the
+ * others, and rows that the tables do not name, are as ever.
  */
 MOE_API moe_status_t moe_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T, int64_t K,
                                       moe_dtype_t dtype, uint8_t *q, uint8_t *sf, int32_t *err_flag,
@@ -631,7 +633,8 @@ MOE_API moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float
  * moe_grouped_gemm_mx8: C[r, :] = A_r B[g]^T for the rows r of expert g over the
  * dispatch tables, as moe_grouped_gemm_mx4 with 8-bit operands: q_a, sf_a
  * [n_rows, K], q_b, sf_b [E, N, K], sums in fp32, C [n_rows, N] rounded once to
- * `out_dtype` (f16, bf16, f32).  N >= 1, K % 32 == 0.
+ * `out_dtype` (f16, bf16, f32), rows outside [0, n_rows) left out as there.
+ * N >= 1, K % 32 == 0.
  * moe_grouped_gate_up_silu_mx8: h = silu(A W_gate^T) * (A W_up^T) from the fp32
  * sums, quantised as moe_quantize_mx8 would its fp32 values: q_h, sf_h
  * [n_rows, d_e].  d_h % 32 == 0, d_e % 32 == 0.

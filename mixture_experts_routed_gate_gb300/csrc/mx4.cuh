@@ -51,14 +51,25 @@ struct Mx4Block {
     int g, m_start, rows;
 };
 
-// rows of M block bx of the dispatch tables: expert, first row, count
-__device__ __forceinline__ Mx4Block mx4_block_of(const MxTables &t, int bx) {
-    Mx4Block b;
-    b.g = t.gidx[bx];
-    const int off = bx * 128 - t.padded[b.g];
-    b.m_start = off + t.offsets[b.g];
-    b.rows = max(0, min(t.sizes[b.g] - off, 128));
-    return b;
+// How many of an expert's `size` rows from row `first` on there are: the tables
+// lie on the device, and those of a larger batch name rows past the call's own,
+// which are neither read nor written.
+__device__ __forceinline__ int64_t rows_there(const MxTables &t, int size, int first, int32_t *err) {
+    const int64_t there = first < 0 ? 0 : t.n_rows - first;
+    if (size > there && err) atomicExch(err, kErrDeviceFlag);
+    return min(static_cast<int64_t>(size), there);
+}
+
+// Rows of M block bx of the dispatch tables: expert, first row, count.  Units of
+// ROWS rows: every block, or every other one of an expert with the block behind it.
+template <int ROWS> __device__ __forceinline__ Mx4Block mx_unit_of(const MxTables &t, int bx, int m_blocks, int32_t *err) {
+    const int g = t.gidx[bx];
+    if (g < 0 || g >= t.E) return {0, 0, 0};
+    const int64_t at = static_cast<int64_t>(bx) * 128, off = at - t.padded[g], here = static_cast<int64_t>(m_blocks) * 128 - at;
+    if (off < 0 || off % ROWS != 0) return {g, 0, 0};
+    const int first = t.offsets[g];
+    const int64_t rows = min(min(rows_there(t, t.sizes[g], first, err) - off, here), static_cast<int64_t>(ROWS));
+    return rows > 0 ? Mx4Block{g, static_cast<int>(first + off), static_cast<int>(rows)} : Mx4Block{g, 0, 0};
 }
 
 }  // namespace moe

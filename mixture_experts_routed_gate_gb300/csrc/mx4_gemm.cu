@@ -67,7 +67,7 @@ struct MgParams {
     int32_t *err;
     int m_blocks, n_tiles, slices;
     int wide;  // rows of out start 32-byte aligned
-    int64_t n_rows, N, K;
+    int64_t N, K;
 };
 
 struct MgTile {
@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     int n_blocks = 0;
     for (int b0 = 0; b0 < p.m_blocks && n_blocks <= MG_LIST; b0 += MG_THREADS) {
         const int bx = b0 + static_cast<int>(threadIdx.x);
-        const Mx4Block b = bx < p.m_blocks ? mx4_block_of(p.tab, bx) : Mx4Block{0, 0, 0};
+        const Mx4Block b = bx < p.m_blocks ? mx_unit_of<128>(p.tab, bx, p.m_blocks, p.err) : Mx4Block{0, 0, 0};
         const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
         if (lane == 0) warp_blocks[warp] = __popc(has);
         __syncthreads();
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             ti.m_start = e.x;
             ti.rows = e.y & 255;
         } else {
-            const Mx4Block k = mx4_block_of(p.tab, b);
+            const Mx4Block k = mx_unit_of<128>(p.tab, b, p.m_blocks, p.err);
             ti.g = k.g;
             ti.m_start = k.m_start;
             ti.rows = k.rows;
@@ -623,13 +623,12 @@ cudaError_t launch_n(const CUtensorMap *maps, const MgParams &p, cudaStream_t st
     return launch_v<TOut, GATE_UP, BN, 1>(maps, p, stream);
 }
 
-MgParams params(const uint8_t *sf_a, const MxTables &tab, int64_t m_blocks, int64_t n_rows, int64_t N, int64_t K,
-                int out_n, int32_t *err) {
+MgParams params(const uint8_t *sf_a, const MxTables &tab, int64_t m_blocks, int64_t N, int64_t K, int out_n,
+                int32_t *err) {
     MgParams p{};
     p.sf_a = sf_a;
     p.tab = tab;
     p.m_blocks = static_cast<int>(m_blocks);
-    p.n_rows = n_rows;
     p.N = N;
     p.K = K;
     p.n_tiles = static_cast<int>((N + out_n - 1) / out_n);
@@ -648,7 +647,7 @@ cudaError_t launch_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, con
     if (!rows_map(&maps[0], q_a, K, n_rows, MG_BOX_ROWS) || !weights_map(&maps[1], q_b, K, N, E, BN))
         return cudaErrorInvalidValue;
     maps[2] = maps[1];
-    MgParams p = params(sf_a, tab, m_blocks, n_rows, N, K, BN, err);
+    MgParams p = params(sf_a, tab, m_blocks, N, K, BN, err);
     p.sf_b0 = sf_b;
     p.sf_b1 = sf_b;
     p.out = C;
@@ -669,7 +668,7 @@ cudaError_t launch_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *s
     if (!rows_map(&maps[0], q_a, d_h, n_rows, MG_BOX_ROWS) || !weights_map(&maps[1], q_gate, d_h, d_e, E, BN / 2) ||
         !weights_map(&maps[2], q_up, d_h, d_e, E, BN / 2))
         return cudaErrorInvalidValue;
-    MgParams p = params(sf_a, tab, m_blocks, n_rows, d_e, d_h, BN / 2, err);
+    MgParams p = params(sf_a, tab, m_blocks, d_e, d_h, BN / 2, err);
     p.sf_b0 = sf_gate;
     p.sf_b1 = sf_up;
     p.q_h = q_h;

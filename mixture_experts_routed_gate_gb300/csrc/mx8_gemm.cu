@@ -86,7 +86,7 @@ struct G8Params {
     void *out;
     uint8_t *q_h, *sf_h;
     int32_t *err;
-    int m_blocks, E, n_tiles, slices, units;
+    int m_blocks, n_tiles, slices, units;
     int64_t N, K;
 };
 
@@ -94,17 +94,6 @@ struct G8Tile {
     int g, m_start, rows, n0;
     bool single;  // the expert's only unit of rows
 };
-
-// Units of NT rows: every block of the dispatch tables, or every other one of an
-// expert with the block behind it.
-template <int NT> __device__ __forceinline__ Mx4Block unit_of(const MxTables &t, int bx, int m_blocks) {
-    Mx4Block b;
-    b.g = t.gidx[bx];
-    const int off = bx * 128 - t.padded[b.g];
-    b.m_start = off + t.offsets[b.g];
-    b.rows = off % NT ? 0 : max(0, min(min(t.sizes[b.g] - off, (m_blocks - bx) * 128), NT));
-    return b;
-}
 
 // The accumulator slots in turn; a unit of more rows than a slot's columns takes
 // both.  Every role follows the same sequence of tiles, and so of slots.
@@ -309,12 +298,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
     // expert they need two, 0.6 us more), and a scan places its units; both CTAs of
     // a pair build the same list
     int n_blocks = 0;
-    for (int e0 = 0; e0 < p.E && n_blocks <= G8_LIST; e0 += G8_THREADS) {
+    for (int e0 = 0; e0 < p.tab.E && n_blocks <= G8_LIST; e0 += G8_THREADS) {
         const int g = e0 + static_cast<int>(threadIdx.x);
-        const bool in = g < p.E;
+        const bool in = g < p.tab.E;
         const int size = in ? __ldg(p.tab.sizes + g) : 0, m = in ? __ldg(p.tab.offsets + g) : 0;
-        const int block = in ? __ldg(p.tab.padded + g) / 128 : 0;
-        const int rows = max(0, min(size, (p.m_blocks - block) * 128)), mine = (rows + NT - 1) / NT;
+        const int64_t here = static_cast<int64_t>(p.m_blocks) * 128 - (in ? __ldg(p.tab.padded + g) : 0);  // to the end of the blocks
+        const int rows = static_cast<int>(max(min(rows_there(p.tab, size, m, p.err), here), int64_t{0}));
+        const int mine = static_cast<int>((static_cast<int64_t>(rows) + NT - 1) / NT);
         int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -360,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             ti.rows = e.y & 511;
             ti.single = (e.y & 512) != 0;
         } else {
-            const Mx4Block k = unit_of<NT>(p.tab, c.b, p.m_blocks);
+            const Mx4Block k = mx_unit_of<NT>(p.tab, c.b, p.m_blocks, p.err);
             ti.g = k.g;
             ti.m_start = k.m_start;
             ti.rows = k.rows;
@@ -789,14 +779,13 @@ cudaError_t launch_typed(const CUtensorMap *maps, const G8Params &p, int64_t n_r
 }
 
 G8Params params(const uint8_t *sf_a, const uint8_t *sf_b0, const uint8_t *sf_b1, const MxTables &tab, int64_t m_blocks,
-                int64_t N, int64_t K, int64_t E, int tile, int32_t *err) {
+                int64_t N, int64_t K, int tile, int32_t *err) {
     G8Params p{};
     p.sf_a = sf_a;
     p.sf_b0 = sf_b0;
     p.sf_b1 = sf_b1;
     p.tab = tab;
     p.m_blocks = static_cast<int>(m_blocks);
-    p.E = static_cast<int>(E);
     p.N = N;
     p.K = K;
     p.n_tiles = static_cast<int>((N + tile - 1) / tile);
@@ -813,7 +802,7 @@ cudaError_t launch_grouped_gemm_mx8(const uint8_t *q_a, const uint8_t *sf_a, con
     CUtensorMap maps[5];
     if (!rows_maps(maps, q_a, K, n_rows) || !weights_map(&maps[3], q_b, K, N, E, 128)) return cudaErrorInvalidValue;
     maps[4] = maps[3];
-    G8Params p = params(sf_a, sf_b, sf_b, tab, m_blocks, N, K, E, 256, err);
+    G8Params p = params(sf_a, sf_b, sf_b, tab, m_blocks, N, K, 256, err);
     p.out = C;
     if (out_dtype == kF32) return launch_typed<float>(maps, p, n_rows, E, stream);
     if (out_dtype == kBF16) return launch_typed<__nv_bfloat16>(maps, p, n_rows, E, stream);
@@ -829,7 +818,7 @@ cudaError_t launch_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *s
     if (!rows_maps(maps, q_a, d_h, n_rows) || !weights_map(&maps[3], q_gate, d_h, d_e, E, 64) ||
         !weights_map(&maps[4], q_up, d_h, d_e, E, 64))
         return cudaErrorInvalidValue;
-    G8Params p = params(sf_a, sf_gate, sf_up, tab, m_blocks, d_e, d_h, E, 128, err);
+    G8Params p = params(sf_a, sf_gate, sf_up, tab, m_blocks, d_e, d_h, 128, err);
     p.q_h = q_h;
     p.sf_h = sf_h;
     return launch_typed<void>(maps, p, n_rows, E, stream);
