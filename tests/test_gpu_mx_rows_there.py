@@ -79,3 +79,39 @@ def test_tables_that_name_no_row(form):
         form.product(*a, *(x.view(E, N, -1) for x in b), tables, torch.float32, out=out[-1], err=err)
         assert int(err.item()) == (0 if tables is ok else DEVICE_FLAG)
     assert torch.equal(*out)  # every row is written: a NaN is not equal to itself
+
+
+@pytest.mark.parametrize("form", [Eight, Four])
+def test_as_many_rows_as_there_may_be(form):
+    """2^31 - 256 rows of 32 elements, and blocks up to row 2^31: the products of the first rows and the last."""
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(1)
+    E, K, N, n, last, some = 3, 32, 1, 2 ** 31 - 256, 1000, 700
+    sizes = torch.tensor([n - last, 0, last])
+    padded = torch.tensor([0, 0, 0])
+    for i in (1, 2):
+        padded[i] = padded[i - 1] + (sizes[i - 1] + 128) // 128 * 128
+    blocks = -(-n // 128) + E
+    assert blocks * 128 > 2 ** 31 and int(padded[2]) + last < 2 ** 31
+    t = dict(group_sizes=sizes, group_offsets=torch.tensor([0, n - last, n - last]), group_padded_offsets=padded)
+    t = {name: v.to(torch.int32).cuda() for name, v in t.items()}
+    gidx = torch.zeros(blocks, dtype=torch.int32, device="cuda")
+    gidx[int(padded[1]) // 128:] = 1
+    gidx[int(padded[2]) // 128:] = 2
+    t["group_idx_for_bx"] = gidx
+    qa, sa = torch.zeros((n, K // form.per), dtype=torch.uint8, device="cuda"), torch.full((n, 1), 127, dtype=torch.uint8, device="cuda")
+    ends = [slice(0, some), slice(n - last - some, n - last), slice(n - last, n)]
+    parts = [form.quantize(torch.randn((at.stop - at.start, K), generator=g, device="cuda")) for at in ends]
+    for at, (q, s) in zip(ends, parts):
+        qa[at], sa[at] = q.view(torch.uint8), s
+    qb, sb = form.quantize(torch.randn((E * N, K), generator=g, device="cuda"))
+    qb, sb = qb.view(E, N, -1), sb.view(E, N, -1)
+    out, err = torch.full((n, N), 7.0, dtype=torch.float16, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    form.product(qa.view(form.dtype), sa, qb, sb, t, torch.float16, out=out, err=err)
+    assert int(err.item()) == 0
+    for at, e, (q, s) in zip(ends, (0, 0, 2), parts):
+        r = at.stop - at.start
+        one = dict(group_sizes=[r], group_offsets=[0], group_padded_offsets=[0], group_idx_for_bx=[0] * (r // 128 + 1))
+        one = {name: torch.tensor(v, dtype=torch.int32, device="cuda") for name, v in one.items()}
+        assert torch.equal(out[at], form.product(q, s, qb[e:e + 1], sb[e:e + 1], one, torch.float16)), (at, e)
+    assert not (out[some:some + 2 ** 20]).any() and not out[-last - some - 2 ** 20:-last - some].any()
