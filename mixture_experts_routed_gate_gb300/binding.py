@@ -146,11 +146,13 @@ def _stream(dev):
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
-def _cuda(t, name, dtype=None, ndim=None):
+def _cuda(t, name, dtype=None, ndim=None, dev=None):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    if dev is not None and t.device != dev:
+        raise ValueError(f"{name} must be on {dev}, got {t.device}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
@@ -351,10 +353,10 @@ def moe_gather_rows_by_token(x, token_topk_to_pos, n_rows: int, out=None, err=No
     return out
 
 
-def _tables(t):
+def _tables(t, dev=None):
     names = ("group_sizes", "group_offsets", "group_padded_offsets", "group_idx_for_bx")
     for n in names:
-        _cuda(t[n], n, dtype=torch.int32)
+        _cuda(t[n], n, dtype=torch.int32, dev=dev)
     return [t[n] for n in names]
 
 
@@ -744,19 +746,26 @@ def moe_forward(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=None, e
 
 # --------------------------------------------------------------------------- checks and calls of the entry points below
 # (a decode step's calls take about as long on the host as on the GPU: the
-# checks look at each tensor once, and a call switches devices only when it must)
+# checks look at each tensor once, and a call switches devices only when it must;
+# every tensor lies on the device of the call's first one, whose addresses and
+# stream the library gets)
 
-def _need(t, name, dtype, shape):
-    """t is a contiguous CUDA tensor of this dtype and shape."""
-    if isinstance(t, torch.Tensor) and t.is_cuda and t.dtype is dtype and t.shape == shape and t.is_contiguous():
+def _need(t, name, dtype, shape, dev):
+    """t is a contiguous tensor of this dtype and shape on this CUDA device."""
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.device == dev and t.dtype is dtype and t.shape == shape and t.is_contiguous():
         return t
-    _cuda(t, name, dtype=dtype)
+    _cuda(t, name, dtype=dtype, dev=dev)
     raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
 
 
 def _want(t, name, dtype, shape, dev):
     """An output: the caller's, checked, or a new one."""
-    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _need(t, name, dtype, shape)
+    return torch.empty(shape, dtype=dtype, device=dev) if t is None else _need(t, name, dtype, shape, dev)
+
+
+def _experts_on(e, dev):
+    """Experts whose weights, all on one device, are on this one."""
+    _cuda(e.q_gate, "the experts", dev=dev)
 
 
 def _at(t):
@@ -782,9 +791,9 @@ def _call(what, dev, *args):
         raise MoEError(status, what)
 
 
-def _err(err):
+def _err(err, dev):
     if err is not None:
-        _cuda(err, "err", dtype=torch.int32)
+        _cuda(err, "err", dtype=torch.int32, dev=dev)
     return _at(err)
 
 
@@ -795,7 +804,7 @@ def _ws(ws, dev, what, *sizes):
         if n == _NO_BYTES:
             raise ValueError(f"{what}: unsupported sizes or dtype")
         return torch.empty(n, dtype=torch.uint8, device=dev), n
-    _cuda(ws, "ws", dtype=torch.uint8)
+    _cuda(ws, "ws", dtype=torch.uint8, dev=dev)
     return ws, ws.numel()
 
 
@@ -807,11 +816,11 @@ _NO_BYTES = ctypes.c_size_t(-1).value
 GATE_NONE, GATE_CHANNEL, GATE_TOKEN, GATE_FULL = 0, 1, 2, 3
 
 
-def _gate_kind(gate, T, H, dtype):
+def _gate_kind(gate, T, H, dtype, dev):
     """[H] per channel, [T, 1] per token, [T, H] per element, None for 1."""
     if gate is None:
         return GATE_NONE
-    _cuda(gate, "gate", dtype=dtype)
+    _cuda(gate, "gate", dtype=dtype, dev=dev)
     shape = tuple(gate.shape)
     if shape == (H,):
         return GATE_CHANNEL
@@ -839,17 +848,17 @@ def moe_residual_norm(y, res, w_post=None, gate=None, alpha: float = 1.0, w_next
         raise ValueError("w_post, gate and out need y")
     if u is not None and w_next is None:
         raise ValueError("u needs w_next")
-    code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt)
+    code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt, dev)
     got = {}
     if y is not None:
-        _need(y, "y", dt, shape)
+        _need(y, "y", dt, shape, dev)
         got["out"] = out = _want(out, "out", dt, shape, dev)
     r_post = r_next = None
     if w_post is not None:
-        _need(w_post, "w_post", dt, (H,))
+        _need(w_post, "w_post", dt, (H,), dev)
         got["rstd_post"] = r_post = torch.empty(T, dtype=torch.float32, device=dev)
     if w_next is not None:
-        _need(w_next, "w_next", dt, (H,))
+        _need(w_next, "w_next", dt, (H,), dev)
         got["u"] = u = _want(u, "u", dt, shape, dev)
         got["rstd_next"] = r_next = torch.empty(T, dtype=torch.float32, device=dev)
     _call("moe_residual_norm", dev, _at(y), _at(res), _at(w_post), _at(gate), kind, alpha, _at(w_next), eps, T, H, code,
@@ -884,19 +893,19 @@ def moe_residual_norm_mx8(y, res, w_post=None, gate=None, alpha: float = 1.0, w_
         raise ValueError("w_post, gate and out need y")
     if H == 0 or H % 32 != 0:
         raise ValueError("H must be a multiple of 32")
-    code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt)
-    _need(w_next, "w_next", dt, (H,))
-    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else _need(q, "q", torch.float8_e4m3fn, shape)
-    sf = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if sf is None else _need(sf, "sf", torch.uint8, (T, H // 32))
+    code, kind = _dtype_code(res, "res"), _gate_kind(gate, T, H, dt, dev)
+    _need(w_next, "w_next", dt, (H,), dev)
+    q = torch.empty(shape, dtype=torch.float8_e4m3fn, device=dev) if q is None else _need(q, "q", torch.float8_e4m3fn, shape, dev)
+    sf = torch.empty((T, H // 32), dtype=torch.uint8, device=dev) if sf is None else _need(sf, "sf", torch.uint8, (T, H // 32), dev)
     r_next = torch.empty(T, dtype=f32, device=dev)
     got = {"q": q, "sf": sf, "rstd_next": r_next}
     a_y = a_out = a_u = a_post = a_r = None
     if y is not None:
-        a_y = _need(y, "y", dt, shape).data_ptr()
-        got["out"] = out = torch.empty(shape, dtype=dt, device=dev) if out is None else _need(out, "out", dt, shape)
+        a_y = _need(y, "y", dt, shape, dev).data_ptr()
+        got["out"] = out = torch.empty(shape, dtype=dt, device=dev) if out is None else _need(out, "out", dt, shape, dev)
         a_out = out.data_ptr()
     if w_post is not None:
-        a_post = _need(w_post, "w_post", dt, (H,)).data_ptr()
+        a_post = _need(w_post, "w_post", dt, (H,), dev).data_ptr()
         got["rstd_post"] = r_post = torch.empty(T, dtype=f32, device=dev)
         a_r = r_post.data_ptr()
     if with_u:
@@ -928,25 +937,25 @@ def moe_residual_norm_backward(d_out, d_u, y, out, w_post=None, gate=None, alpha
         raise ValueError("w_post and gate need y")
     if w_post is not None and rstd_post is None:
         raise ValueError("w_post needs rstd_post")
-    code, kind = _dtype_code(ref, "d_out"), _gate_kind(gate, T, H, dt)
+    code, kind = _dtype_code(ref, "d_out"), _gate_kind(gate, T, H, dt, dev)
     if out is not None:
-        _need(out, "out", dt, shape)
+        _need(out, "out", dt, shape, dev)
     d_res = torch.empty(shape, dtype=dt, device=dev)
     got = {"d_res": d_res}
     d_y = d_gate = d_w_post = d_w_next = None
     if y is not None:
-        _need(y, "y", dt, shape)
+        _need(y, "y", dt, shape, dev)
         got["d_y"] = d_y = torch.empty(shape, dtype=dt, device=dev)
     if kind != GATE_NONE:
         got["d_gate"] = d_gate = torch.empty(gate.shape, dtype=dt if kind == GATE_FULL else f32, device=dev)
     if w_post is not None:
-        _need(w_post, "w_post", dt, (H,))
-        _need(rstd_post, "rstd_post", f32, (T,))
+        _need(w_post, "w_post", dt, (H,), dev)
+        _need(rstd_post, "rstd_post", f32, (T,), dev)
         got["d_w_post"] = d_w_post = torch.empty(H, dtype=f32, device=dev)
     if w_next is not None:
-        _need(d_u, "d_u", dt, shape)
-        _need(w_next, "w_next", dt, (H,))
-        _need(rstd_next, "rstd_next", f32, (T,))
+        _need(d_u, "d_u", dt, shape, dev)
+        _need(w_next, "w_next", dt, (H,), dev)
+        _need(rstd_next, "rstd_next", f32, (T,), dev)
         got["d_w_next"] = d_w_next = torch.empty(H, dtype=f32, device=dev)
     ws, nws = _ws(ws, dev, "moe_residual_norm_backward", T, H)
     _call("moe_residual_norm_backward", dev, _at(d_out), _at(d_u), _at(y), _at(out), _at(w_post), _at(gate), kind, alpha,
@@ -970,32 +979,32 @@ def moe_forward_few(x, w_g, bias, w_gate, w_up, w_down, k: int, ws=None, out=Non
     _cuda(x, "x", ndim=2)
     T, d_h = x.shape
     dt, dev = x.dtype, x.device
-    _cuda(w_gate, "w_gate", dtype=dt, ndim=3)
+    _cuda(w_gate, "w_gate", dtype=dt, ndim=3, dev=dev)
     E, d_e, _ = w_gate.shape
-    _need(w_gate, "w_gate", dt, (E, d_e, d_h))
-    _need(w_up, "w_up", dt, (E, d_e, d_h))
-    _need(w_down, "w_down", dt, (E, d_h, d_e))
-    _need(w_g, "w_g", dt, (E, d_h))
+    _need(w_gate, "w_gate", dt, (E, d_e, d_h), dev)
+    _need(w_up, "w_up", dt, (E, d_e, d_h), dev)
+    _need(w_down, "w_down", dt, (E, d_h, d_e), dev)
+    _need(w_g, "w_g", dt, (E, d_h), dev)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (E,))
+        _need(bias, "bias", torch.float32, (E,), dev)
     code = _dtype_code(x, "x")
     ws, nws = _ws(ws, dev, "moe_forward_few", T, d_h, d_e, E, k, code)
     out = _want(out, "out", dt, x.shape, dev)
     _call("moe_forward_few", dev, _at(x), _at(w_g), _at(bias), _at(w_gate), _at(w_up), _at(w_down), T, d_h, d_e, E, k, code,
-          _at(ws), nws, _at(out), _err(err))
+          _at(ws), nws, _at(out), _err(err, dev))
     return out
 
 
 # --------------------------------------------------------------------------- microscaled 4-bit floating point
 
-def _mx4(q, sf, name, lead):
-    """q [*lead, K / 2], sf [*lead, K / 32]: returns K."""
+def _mx4(q, sf, name, lead, dev):
+    """q [*lead, K / 2], sf [*lead, K / 32] on dev: returns K."""
     if isinstance(q, torch.Tensor) and q.dim() == len(lead) + 1 and (2 * q.shape[-1]) % 32 == 0:
         half = q.shape[-1]
-        _need(q, f"q{name}", torch.uint8, (*lead, half))
-        _need(sf, f"sf{name}", torch.uint8, (*lead, half // 16))
+        _need(q, f"q{name}", torch.uint8, (*lead, half), dev)
+        _need(sf, f"sf{name}", torch.uint8, (*lead, half // 16), dev)
         return 2 * half
-    _cuda(q, f"q{name}", dtype=torch.uint8, ndim=len(lead) + 1)
+    _cuda(q, f"q{name}", dtype=torch.uint8, ndim=len(lead) + 1, dev=dev)
     raise ValueError(f"q{name} must be {(*lead, 'K / 2')} with K % 32 == 0, got {tuple(q.shape)}")
 
 
@@ -1006,12 +1015,13 @@ def moe_quantize_mx4(x, row_idx=None, q=None, sf=None, err=None):
     T, K = x.shape
     if K == 0 or K % 32 != 0:
         raise ValueError("K must be a multiple of 32")
+    dev = x.device
     if row_idx is not None:
-        _cuda(row_idx, "row_idx", dtype=torch.int32, ndim=1)
-    R, dev = T if row_idx is None else row_idx.shape[0], x.device
+        _cuda(row_idx, "row_idx", dtype=torch.int32, ndim=1, dev=dev)
+    R = T if row_idx is None else row_idx.shape[0]
     q = _want(q, "q", torch.uint8, (R, K // 2), dev)
     sf = _want(sf, "sf", torch.uint8, (R, K // 32), dev)
-    _call("moe_quantize_mx4", dev, _at(x), _at(row_idx), R, T, K, _dtype_code(x, "x"), _at(q), _at(sf), _err(err))
+    _call("moe_quantize_mx4", dev, _at(x), _at(row_idx), R, T, K, _dtype_code(x, "x"), _at(q), _at(sf), _err(err, dev))
     return q, sf
 
 
@@ -1019,7 +1029,7 @@ def moe_dequantize_mx4(q, sf, dtype=torch.bfloat16, out=None):
     """The values of q [R, K / 2], sf [R, K / 32] as [R, K] in dtype."""
     _cuda(q, "q", dtype=torch.uint8, ndim=2)
     R = q.shape[0]
-    K = _mx4(q, sf, "", (R,))
+    K = _mx4(q, sf, "", (R,), q.device)
     out = _want(out, "out", dtype, (R, K), q.device)
     _call("moe_dequantize_mx4", q.device, _at(q), _at(sf), R, K, _dtype_code(out, "out"), _at(out))
     return out
@@ -1031,13 +1041,14 @@ def moe_grouped_gemm_mx4(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16,
     _cuda(q_a, "q_a", dtype=torch.uint8, ndim=2)
     _cuda(q_b, "q_b", dtype=torch.uint8, ndim=3)
     rows, (E, N, _) = q_a.shape[0], q_b.shape
-    K = _mx4(q_a, sf_a, "_a", (rows,))
-    if _mx4(q_b, sf_b, "_b", (E, N)) != K:
+    dev = q_a.device
+    K = _mx4(q_a, sf_a, "_a", (rows,), dev)
+    if _mx4(q_b, sf_b, "_b", (E, N), dev) != K:
         raise ValueError("the two sides disagree on K")
-    s, o, p, g = _tables(tables)
-    out = _want(out, "out", out_dtype, (rows, N), q_a.device)
-    _call("moe_grouped_gemm_mx4", q_a.device, _at(q_a), _at(sf_a), _at(q_b), _at(sf_b), _at(s), _at(o), _at(p), _at(g),
-          g.shape[0], rows, N, K, E, _dtype_code(out, "out"), _at(out), _err(err))
+    s, o, p, g = _tables(tables, dev)
+    out = _want(out, "out", out_dtype, (rows, N), dev)
+    _call("moe_grouped_gemm_mx4", dev, _at(q_a), _at(sf_a), _at(q_b), _at(sf_b), _at(s), _at(o), _at(p), _at(g),
+          g.shape[0], rows, N, K, E, _dtype_code(out, "out"), _at(out), _err(err, dev))
     return out
 
 
@@ -1045,11 +1056,12 @@ class Mx4Experts:
     """The three expert weights of a layer as mx4 elements and scales."""
 
     def __init__(self, q_gate, sf_gate, q_up, sf_up, q_down, sf_down):
+        dev = _cuda(q_gate, "q_gate", ndim=3).device
         self.E, self.d_e, half = q_gate.shape
         self.d_h = 2 * half
         for q, sf, name, lead in ((q_gate, sf_gate, "_gate", (self.E, self.d_e)), (q_up, sf_up, "_up", (self.E, self.d_e)),
                                   (q_down, sf_down, "_down", (self.E, self.d_h))):
-            if _mx4(q, sf, name, lead) != (self.d_e if name == "_down" else self.d_h):
+            if _mx4(q, sf, name, lead, dev) != (self.d_e if name == "_down" else self.d_h):
                 raise ValueError("q_gate / q_up must be [E, d_e, d_h // 2] and q_down [E, d_h, d_e // 2]")
         self.q_gate, self.sf_gate, self.q_up, self.sf_up = q_gate, sf_gate, q_up, sf_up
         self.q_down, self.sf_down = q_down, sf_down
@@ -1070,13 +1082,14 @@ def moe_grouped_gate_up_silu_mx4(q_a, sf_a, experts: "Mx4Experts", tables, q_h=N
     returns q_h [rows, d_e / 2], sf_h [rows, d_e / 32]."""
     _cuda(q_a, "q_a", dtype=torch.uint8, ndim=2)
     rows, dev, e = q_a.shape[0], q_a.device, experts
-    if _mx4(q_a, sf_a, "_a", (rows,)) != e.d_h:
+    if _mx4(q_a, sf_a, "_a", (rows,), dev) != e.d_h:
         raise ValueError("the rows and the experts disagree on d_hidden")
-    s, o, p, g = _tables(tables)
+    _experts_on(e, dev)
+    s, o, p, g = _tables(tables, dev)
     q_h = _want(q_h, "q_h", torch.uint8, (rows, e.d_e // 2), dev)
     sf_h = _want(sf_h, "sf_h", torch.uint8, (rows, e.d_e // 32), dev)
     _call("moe_grouped_gate_up_silu_mx4", dev, _at(q_a), _at(sf_a), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
-          _at(s), _at(o), _at(p), _at(g), g.shape[0], rows, e.d_h, e.d_e, e.E, _at(q_h), _at(sf_h), _err(err))
+          _at(s), _at(o), _at(p), _at(g), g.shape[0], rows, e.d_h, e.d_e, e.E, _at(q_h), _at(sf_h), _err(err, dev))
     return q_h, sf_h
 
 
@@ -1091,14 +1104,15 @@ def moe_forward_mx4(x, w_g, bias, experts: "Mx4Experts", k: int, ws=None, out=No
     e, dt, dev = experts, x.dtype, x.device
     if d_h != e.d_h:
         raise ValueError("x and the experts disagree on d_hidden")
-    _need(w_g, "w_g", dt, (e.E, d_h))
+    _experts_on(e, dev)
+    _need(w_g, "w_g", dt, (e.E, d_h), dev)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (e.E,))
+        _need(bias, "bias", torch.float32, (e.E,), dev)
     code = _dtype_code(x, "x")
     ws, nws = _ws(ws, dev, "moe_forward_mx4", T, d_h, e.d_e, e.E, k, code)
     out = _want(out, "out", dt, x.shape, dev)
     _call("moe_forward_mx4", dev, _at(x), _at(w_g), _at(bias), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up), _at(e.sf_up),
-          _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err))
+          _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err, dev))
     return out
 
 
@@ -1115,37 +1129,37 @@ def moe_reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_
         made = _host.reduce_fused_backward(d_out, x, token_topk_to_pos, topk_weights, sorted_token_idx, err)
         if made is not None:
             return made
-    _cuda(x, "x", ndim=2)
-    _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
-    _cuda(d_out, "d_out", ndim=2)
-    shape, pairs, dev, f32 = x.shape, token_topk_to_pos.shape, x.device, torch.float32
+    dev = _cuda(x, "x", ndim=2).device
+    _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2, dev=dev)
+    _cuda(d_out, "d_out", ndim=2, dev=dev)
+    shape, pairs, f32 = x.shape, token_topk_to_pos.shape, torch.float32
     n_rows, H = shape
     T, K = pairs
     if d_out.shape != (T, H):
         raise ValueError(f"d_out must be {[T, H]}, got {list(d_out.shape)}")
     if topk_weights is not None:
-        _need(topk_weights, "topk_weights", f32, pairs)
-    _need(sorted_token_idx, "sorted_token_idx", torch.int32, (n_rows,))
+        _need(topk_weights, "topk_weights", f32, pairs, dev)
+    _need(sorted_token_idx, "sorted_token_idx", torch.int32, (n_rows,), dev)
     d_x = torch.empty(shape, dtype=x.dtype, device=dev)
     d_w = torch.empty(pairs, dtype=f32, device=dev)
     _call("moe_reduce_fused_backward", dev, d_out.data_ptr(), x.data_ptr(), n_rows, token_topk_to_pos.data_ptr(),
           None if topk_weights is None else topk_weights.data_ptr(), sorted_token_idx.data_ptr(), T, K, H, _dtype_code(x, "x"),
-          _dtype_code(d_out, "d_out"), d_x.data_ptr(), d_w.data_ptr(), None if err is None else _err(err))
+          _dtype_code(d_out, "d_out"), d_x.data_ptr(), d_w.data_ptr(), None if err is None else _err(err, dev))
     return d_x, d_w
 
 
 # --------------------------------------------------------------------------- microscaled 8-bit floating point
 
-def _mx8(q, sf, name, lead):
-    """q float8 e4m3 [*lead, K], sf uint8 [*lead, K / 32]: returns K."""
+def _mx8(q, sf, name, lead, dev):
+    """q float8 e4m3 [*lead, K], sf uint8 [*lead, K / 32] on dev: returns K."""
     if isinstance(q, torch.Tensor):
         shape = q.shape
         if len(shape) == len(lead) + 1 and shape[-1] % 32 == 0:
             K = shape[-1]
-            _need(q, "q" + name, torch.float8_e4m3fn, lead + (K,))
-            _need(sf, "sf" + name, torch.uint8, lead + (K // 32,))
+            _need(q, "q" + name, torch.float8_e4m3fn, lead + (K,), dev)
+            _need(sf, "sf" + name, torch.uint8, lead + (K // 32,), dev)
             return K
-    _cuda(q, "q" + name, dtype=torch.float8_e4m3fn, ndim=len(lead) + 1)
+    _cuda(q, "q" + name, dtype=torch.float8_e4m3fn, ndim=len(lead) + 1, dev=dev)
     raise ValueError(f"q{name} must be {(*lead, 'K')} with K % 32 == 0, got {tuple(q.shape)}")
 
 
@@ -1167,7 +1181,7 @@ def moe_dequantize_mx8(q, sf, dtype=torch.bfloat16, out=None):
     """The values of q [R, K], sf [R, K / 32] as [R, K] in dtype."""
     _cuda(q, "q", dtype=torch.float8_e4m3fn, ndim=2)
     R = q.shape[0]
-    K = _mx8(q, sf, "", (R,))
+    K = _mx8(q, sf, "", (R,), q.device)
     out = _want(out, "out", dtype, (R, K), q.device)
     _call("moe_dequantize_mx8", q.device, _at(q), _at(sf), R, K, _dtype_code(out, "out"), _at(out))
     return out
@@ -1182,9 +1196,9 @@ def moe_sort_rows_mx8(q, sf, token_topk_to_pos, n_rows=None, q_out=None, sf_out=
         made = _host.sort_rows_mx8(q, sf, token_topk_to_pos)
         if made is not None:
             return made
-    _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2)
+    dev = _cuda(token_topk_to_pos, "token_topk_to_pos", dtype=torch.int32, ndim=2).device
     T, k = token_topk_to_pos.shape
-    K, dev = _mx8(q, sf, "", (T,)), q.device
+    K = _mx8(q, sf, "", (T,), dev)
     n_rows = T * k if n_rows is None else n_rows
     q_out = _want(q_out, "q_out", torch.float8_e4m3fn, (n_rows, K), dev)
     sf_out = _want(sf_out, "sf_out", torch.uint8, (n_rows, K // 32), dev)
@@ -1201,14 +1215,14 @@ def _four(t):
         return None, None, None, None
 
 
-def _table_addresses(t, E):
+def _table_addresses(t, E, dev):
     """The four tables' addresses, in the entry points' order, and the number of blocks;
     the first three have an entry for each expert."""
     s, o, p, g = t["group_sizes"], t["group_offsets"], t["group_padded_offsets"], t["group_idx_for_bx"]
     i32 = torch.int32
     for x in (s, o, p, g):
-        if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dtype is i32 and x.is_contiguous()):
-            _tables(t)  # says which
+        if not (isinstance(x, torch.Tensor) and x.is_cuda and x.device == dev and x.dtype is i32 and x.is_contiguous()):
+            _tables(t, dev)  # says which
     if s.numel() != E or o.numel() != E or p.numel() != E:
         raise ValueError(f"group_sizes, group_offsets and group_padded_offsets must have an entry for each of {E} experts")
     return s.data_ptr(), o.data_ptr(), p.data_ptr(), g.data_ptr(), g.shape[0]
@@ -1224,13 +1238,14 @@ def moe_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tables, out_dtype=torch.bfloat16,
     _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
     _cuda(q_b, "q_b", dtype=torch.float8_e4m3fn, ndim=3)
     rows, (E, N, _) = q_a.shape[0], q_b.shape
-    K, dev = _mx8(q_a, sf_a, "_a", (rows,)), q_a.device
-    if _mx8(q_b, sf_b, "_b", (E, N)) != K:
+    dev = q_a.device
+    K = _mx8(q_a, sf_a, "_a", (rows,), dev)
+    if _mx8(q_b, sf_b, "_b", (E, N), dev) != K:
         raise ValueError("the two sides disagree on K")
-    s, o, p, g, blocks = _table_addresses(tables, E)
+    s, o, p, g, blocks = _table_addresses(tables, E, dev)
     out = _want(out, "out", out_dtype, (rows, N), dev)
     _call("moe_grouped_gemm_mx8", dev, q_a.data_ptr(), sf_a.data_ptr(), q_b.data_ptr(), sf_b.data_ptr(), s, o, p, g, blocks,
-          rows, N, K, E, _dtype_code(out, "out"), out.data_ptr(), None if err is None else _err(err))
+          rows, N, K, E, _dtype_code(out, "out"), out.data_ptr(), None if err is None else _err(err, dev))
     return out
 
 
@@ -1239,11 +1254,11 @@ class Mx8Experts:
 
     def __init__(self, q_gate, sf_gate, q_up, sf_up, q_down, sf_down):
         sizes = None if _host is None else _host.experts_mx8(q_gate, sf_gate, q_up, sf_up, q_down, sf_down)
-        self.E, self.d_e, self.d_h = q_gate.shape if sizes is None else sizes
+        self.E, self.d_e, self.d_h = _cuda(q_gate, "q_gate", ndim=3).shape if sizes is None else sizes
         for q, sf, name, lead in () if sizes else (
                 (q_gate, sf_gate, "_gate", (self.E, self.d_e)), (q_up, sf_up, "_up", (self.E, self.d_e)),
                 (q_down, sf_down, "_down", (self.E, self.d_h))):
-            if _mx8(q, sf, name, lead) != (self.d_e if name == "_down" else self.d_h):
+            if _mx8(q, sf, name, lead, q_gate.device) != (self.d_e if name == "_down" else self.d_h):
                 raise ValueError("q_gate / q_up must be [E, d_e, d_h] and q_down [E, d_h, d_e]")
         self.q_gate, self.sf_gate, self.q_up, self.sf_up = q_gate, sf_gate, q_up, sf_up
         self.q_down, self.sf_down = q_down, sf_down
@@ -1269,14 +1284,15 @@ def moe_grouped_gate_up_silu_mx8(q_a, sf_a, experts: "Mx8Experts", tables, q_h=N
             return made
     _cuda(q_a, "q_a", dtype=torch.float8_e4m3fn, ndim=2)
     rows, dev, e = q_a.shape[0], q_a.device, experts
-    if _mx8(q_a, sf_a, "_a", (rows,)) != e.d_h:
+    if _mx8(q_a, sf_a, "_a", (rows,), dev) != e.d_h:
         raise ValueError("the rows and the experts disagree on d_hidden")
-    s, o, p, g, blocks = _table_addresses(tables, e.E)
+    _experts_on(e, dev)
+    s, o, p, g, blocks = _table_addresses(tables, e.E, dev)
     q_h = _want(q_h, "q_h", torch.float8_e4m3fn, (rows, e.d_e), dev)
     sf_h = _want(sf_h, "sf_h", torch.uint8, (rows, e.d_e // 32), dev)
     _call("moe_grouped_gate_up_silu_mx8", dev, q_a.data_ptr(), sf_a.data_ptr(), e.q_gate.data_ptr(), e.sf_gate.data_ptr(),
           e.q_up.data_ptr(), e.sf_up.data_ptr(), s, o, p, g, blocks, rows, e.d_h, e.d_e, e.E, q_h.data_ptr(), sf_h.data_ptr(),
-          None if err is None else _err(err))
+          None if err is None else _err(err, dev))
     return q_h, sf_h
 
 
@@ -1293,17 +1309,18 @@ def moe_forward_mx8(x, w_g, bias, experts: "Mx8Experts", k: int, rows=None, ws=N
     e, dt, dev = experts, x.dtype, x.device
     if d_h != e.d_h:
         raise ValueError("x and the experts disagree on d_hidden")
-    _need(w_g, "w_g", dt, (e.E, d_h))
+    _experts_on(e, dev)
+    _need(w_g, "w_g", dt, (e.E, d_h), dev)
     if bias is not None:
-        _need(bias, "bias", torch.float32, (e.E,))
+        _need(bias, "bias", torch.float32, (e.E,), dev)
     q, sf = (None, None) if rows is None else rows
-    if rows is not None and _mx8(q, sf, "", (T,)) != d_h:
+    if rows is not None and _mx8(q, sf, "", (T,), dev) != d_h:
         raise ValueError("x and its 8-bit rows disagree on d_hidden")
     code = _dtype_code(x, "x")
     ws, nws = _ws(ws, dev, "moe_forward_mx8", T, d_h, e.d_e, e.E, k, code)
     out = _want(out, "out", dt, x.shape, dev)
     _call("moe_forward_mx8", dev, _at(x), _at(q), _at(sf), _at(w_g), _at(bias), _at(e.q_gate), _at(e.sf_gate), _at(e.q_up),
-          _at(e.sf_up), _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err))
+          _at(e.sf_up), _at(e.q_down), _at(e.sf_down), T, d_h, e.d_e, e.E, k, code, _at(ws), nws, _at(out), _err(err, dev))
     return out
 
 
