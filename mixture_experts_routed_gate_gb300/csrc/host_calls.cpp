@@ -165,7 +165,9 @@ PyObject *norm_mx8(PyObject *, PyObject *const *a, Py_ssize_t n) {
         const double alpha = PyFloat_AsDouble(a[4]), eps = PyFloat_AsDouble(a[6]);
         need(!PyErr_Occurred());
         const Tensor &w_next = like(a[5], res, type, {H});
-        const bool with_u = PyObject_IsTrue(a[7]) == 1;
+        const int truth = PyObject_IsTrue(a[7]);
+        need(truth >= 0);  // what has none is the Python code's to report
+        const bool with_u = truth != 0;
         Tensor out, u, r_post;
         if (has_y) out = a[8] != Py_None ? like(a[8], res, type, {T, H}) : made(res, type, {T, H});
         if (with_u) u = made(res, type, {T, H});
