@@ -13,10 +13,12 @@ from __future__ import annotations
 
 import concurrent.futures
 import glob
+import hashlib
 import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -27,7 +29,7 @@ BUILD = os.path.join(ROOT, "_build", "moe_routed_gb300")
 LIB = os.path.join(PKG, "libmoe_routed_gb300.so")
 HOST_SRC = os.path.join(CSRC, "host_calls.cpp")
 HOST_LIB = os.path.join(PKG, "_host_calls.so")
-HOST_DONE = os.path.join(BUILD, "host_calls.done")  # built, or tried, at this time
+HOST_DONE = os.path.join(BUILD, "host_calls.done")  # host_key() of the last build, or try, at this time
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -57,23 +59,41 @@ def is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in _deps())
 
 
+def _torch_dir() -> str | None:
+    spec = importlib.util.find_spec("torch")
+    return list(spec.submodule_search_locations)[0] if spec is not None and spec.submodule_search_locations else None
+
+
+def host_key() -> str:
+    """The PyTorch and the Python that the extension is compiled against, whose layouts it holds: it is
+    loaded by these alone."""
+    parts, where = [sys.version, str(sysconfig.get_config_var("EXT_SUFFIX"))], _torch_dir()
+    if where is not None:
+        with open(os.path.join(where, "version.py")) as f:
+            parts.append(f.read())
+    return hashlib.sha256("\0".join(parts).encode()).hexdigest()
+
+
 def host_is_stale() -> bool:
     if not os.path.exists(HOST_DONE):
         return True
+    with open(HOST_DONE) as f:
+        if f.read() != host_key():
+            return True
     t = os.path.getmtime(HOST_DONE)
     return any(os.path.getmtime(p) > t for p in [HOST_SRC, LIB, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
 def _host_object() -> str | None:
     """host_calls.cpp compiled; None where PyTorch or its headers are missing."""
-    spec = importlib.util.find_spec("torch")
-    if spec is None or not spec.submodule_search_locations:
+    where = _torch_dir()
+    if where is None:
         return None
-    torch_inc = os.path.join(list(spec.submodule_search_locations)[0], "include")
+    torch_inc = os.path.join(where, "include")
     cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
     obj = os.path.join(BUILD, "host_calls.o")
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-I", torch_inc, "-I", os.path.join(torch_inc, "torch", "csrc", "api", "include"),
-           "-I", sysconfig.get_paths()["include"], "-I", cuda_inc, "-c", HOST_SRC, "-o", obj]
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DMOE_BUILT_FOR="{host_key()}"',
+           "-I", torch_inc, "-I", os.path.join(torch_inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I", cuda_inc, "-c", HOST_SRC, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         print(f"host_calls.cpp not built (the binding goes without it):\n{r.stderr[-2000:]}")
@@ -85,7 +105,7 @@ def _link_host(obj: str | None) -> None:
     if os.path.exists(HOST_LIB):
         os.remove(HOST_LIB)
     if obj is not None:
-        torch_lib = os.path.join(list(importlib.util.find_spec("torch").submodule_search_locations)[0], "lib")
+        torch_lib = os.path.join(_torch_dir(), "lib")
         tmp = HOST_LIB + f".tmp{os.getpid()}"
         cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
                "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
@@ -94,8 +114,8 @@ def _link_host(obj: str | None) -> None:
             os.replace(tmp, HOST_LIB)
         else:
             print(f"host_calls not linked (the binding goes without it):\n{r.stderr[-2000:]}")
-    with open(HOST_DONE, "w"):
-        pass
+    with open(HOST_DONE, "w") as f:
+        f.write(host_key())
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

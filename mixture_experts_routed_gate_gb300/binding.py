@@ -111,8 +111,10 @@ def lib():
     if path == os.path.join(_build.PKG, os.path.basename(path)) and os.path.exists(_build.HOST_LIB):
         try:
             from . import _host_calls
+            if _host_calls.built_for != _build.host_key():
+                raise ImportError("the extension was built for another PyTorch or Python")
             _host = _host_calls
-        except ImportError as e:  # built against another PyTorch, say: the Python code makes the same calls
+        except ImportError as e:  # the Python code makes the same calls
             warnings.warn(f"short calls go through Python: {e}")
     return L
 

@@ -1,0 +1,71 @@
+"""The build of the short calls' extension: what it is compiled against, and what a build does that cannot
+make it.  Compilers are stand-ins."""
+import subprocess
+import types
+
+import pytest
+
+from mixture_experts_routed_gate_gb300 import _build, binding
+
+
+@pytest.fixture
+def place(tmp_path, monkeypatch):
+    """A tree of its own with an up-to-date library, and a compiler that writes what it is told to."""
+    build, pkg = tmp_path / "_build", tmp_path / "pkg"
+    build.mkdir(), pkg.mkdir()
+    monkeypatch.setattr(_build, "BUILD", str(build))
+    monkeypatch.setattr(_build, "PKG", str(pkg))
+    monkeypatch.setattr(_build, "LIB", str(pkg / "lib.so"))
+    monkeypatch.setattr(_build, "HOST_LIB", str(pkg / "_host_calls.so"))
+    monkeypatch.setattr(_build, "HOST_DONE", str(build / "host_calls.done"))
+    (pkg / "lib.so").write_text("library")
+    ran = []
+
+    def run(cmd, **kw):
+        ran.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("built")
+        return subprocess.CompletedProcess(cmd, 0, "", "")
+    monkeypatch.setattr(subprocess, "run", run)
+    monkeypatch.setattr(_build, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
+    return types.SimpleNamespace(ran=ran, lib=pkg / "_host_calls.so", done=build / "host_calls.done")
+
+
+def test_built_once(place):
+    _build.build()
+    assert place.lib.read_text() == "built" and len(place.ran) == 2 and not _build.host_is_stale()
+    _build.build()
+    assert len(place.ran) == 2
+
+
+def test_another_pytorch_or_python(place, monkeypatch):
+    """An extension of another PyTorch is built anew."""
+    _build.build()
+    key = _build.host_key()
+    monkeypatch.setattr(_build, "host_key", lambda: "another")
+    assert key != "another" and _build.host_is_stale()
+    _build.build()
+    assert len(place.ran) == 4 and not _build.host_is_stale() and '-DMOE_BUILT_FOR="another"' in place.ran[2]
+
+
+def test_the_key_is_pytorchs_version(tmp_path, monkeypatch):
+    keys = []
+    for version in ("1", "2", "1"):
+        (tmp_path / "version.py").write_text(version)
+        monkeypatch.setattr(_build, "_torch_dir", lambda: str(tmp_path))
+        keys.append(_build.host_key())
+    assert keys[0] == keys[2] != keys[1]
+    monkeypatch.setattr(_build.sysconfig, "get_config_var", lambda name: ".another.so")
+    assert _build.host_key() not in keys
+
+
+def test_an_extension_of_another_pytorch_is_not_used(monkeypatch):
+    _build.build()
+    lib, host = binding.lib(), binding._host
+    assert host is not None and host.built_for == _build.host_key()
+    monkeypatch.setattr(_build, "host_key", lambda: "another")
+    monkeypatch.setattr(binding, "_lib", None)
+    monkeypatch.setattr(binding, "_host", None)
+    with pytest.warns(UserWarning, match="another PyTorch"):
+        binding.lib()
+    assert binding._host is None and binding._lib._name == lib._name
