@@ -29,7 +29,7 @@ BUILD = os.path.join(ROOT, "_build", "moe_routed_gb300")
 LIB = os.path.join(PKG, "libmoe_routed_gb300.so")
 HOST_SRC = os.path.join(CSRC, "host_calls.cpp")
 HOST_LIB = os.path.join(PKG, "_host_calls.so")
-HOST_DONE = os.path.join(BUILD, "host_calls.done")  # host_key() of the last build, or try, at this time
+HOST_DONE = os.path.join(BUILD, "host_calls.done")  # host_key() of the extension there is
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
@@ -75,7 +75,7 @@ def host_key() -> str:
 
 
 def host_is_stale() -> bool:
-    if not os.path.exists(HOST_DONE):
+    if not os.path.exists(HOST_DONE) or not os.path.exists(HOST_LIB):
         return True
     with open(HOST_DONE) as f:
         if f.read() != host_key():
@@ -102,18 +102,22 @@ def _host_object() -> str | None:
 
 
 def _link_host(obj: str | None) -> None:
-    if os.path.exists(HOST_LIB):
-        os.remove(HOST_LIB)
-    if obj is not None:
-        torch_lib = os.path.join(_torch_dir(), "lib")
-        tmp = HOST_LIB + f".tmp{os.getpid()}"
-        cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
-               "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode == 0:
-            os.replace(tmp, HOST_LIB)
-        else:
-            print(f"host_calls not linked (the binding goes without it):\n{r.stderr[-2000:]}")
+    """The extension from its object; none at all where there is no object or it cannot be linked, so that the
+    next build tries again."""
+    for old in (HOST_DONE, HOST_LIB):
+        if os.path.exists(old):
+            os.remove(old)
+    if obj is None:
+        return
+    torch_lib = os.path.join(_torch_dir(), "lib")
+    tmp = HOST_LIB + f".tmp{os.getpid()}"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
+           "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        print(f"host_calls not linked (the binding goes without it):\n{r.stderr[-2000:]}")
+        return
+    os.replace(tmp, HOST_LIB)
     with open(HOST_DONE, "w") as f:
         f.write(host_key())
 

@@ -1,5 +1,6 @@
 """The build of the short calls' extension: what it is compiled against, and what a build does that cannot
 make it.  Compilers are stand-ins."""
+import os
 import subprocess
 import types
 
@@ -28,7 +29,7 @@ def place(tmp_path, monkeypatch):
         return subprocess.CompletedProcess(cmd, 0, "", "")
     monkeypatch.setattr(subprocess, "run", run)
     monkeypatch.setattr(_build, "nvcc", lambda: "/usr/local/cuda/bin/nvcc")
-    return types.SimpleNamespace(ran=ran, lib=pkg / "_host_calls.so", done=build / "host_calls.done")
+    return types.SimpleNamespace(run=run, ran=ran, lib=pkg / "_host_calls.so", done=build / "host_calls.done")
 
 
 def test_built_once(place):
@@ -69,3 +70,30 @@ def test_an_extension_of_another_pytorch_is_not_used(monkeypatch):
     with pytest.warns(UserWarning, match="another PyTorch"):
         binding.lib()
     assert binding._host is None and binding._lib._name == lib._name
+
+
+@pytest.mark.parametrize("fails", ["-c", "-shared"])
+def test_a_build_that_failed_is_tried_again(place, monkeypatch, capsys, fails):
+    """Neither an extension nor a stamp stays behind a failed compile or link; the next build makes both."""
+    _build.build()
+    assert place.lib.exists()
+    place.lib.with_name("lib.so").write_text("a newer library")
+    os.utime(place.lib.with_name("lib.so"), ns=(1 << 62, 1 << 62))
+    monkeypatch.setattr(subprocess, "run", lambda cmd, **kw: subprocess.CompletedProcess(cmd, 1, "", "no such header")
+                        if fails in cmd else place.run(cmd, **kw))
+    _build.build()
+    assert "no such header" in capsys.readouterr().out and not place.lib.exists() and not place.done.exists()
+    os.utime(place.lib.with_name("lib.so"))
+    monkeypatch.setattr(subprocess, "run", place.run)
+    _build.build()
+    assert place.lib.exists() and place.done.exists() and not _build.host_is_stale()
+
+
+def test_pytorch_that_comes_later(place, monkeypatch):
+    """Without PyTorch there is nothing to build, and nothing says that it was built."""
+    with monkeypatch.context() as m:
+        m.setattr(_build, "_torch_dir", lambda: None)
+        _build.build()
+    assert not place.ran and not place.lib.exists()
+    _build.build()
+    assert len(place.ran) == 2 and place.lib.exists()
