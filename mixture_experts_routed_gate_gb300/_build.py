@@ -84,19 +84,32 @@ def host_is_stale() -> bool:
     return any(os.path.getmtime(p) > t for p in [HOST_SRC, LIB, os.path.abspath(__file__)] + glob.glob(os.path.join(INCLUDE, "*.h")))
 
 
+def _run(cmd) -> str | None:
+    """What went wrong with a command; None if nothing."""
+    try:
+        r = subprocess.run(cmd, capture_output=True, text=True)
+    except OSError as e:  # there is no such program, say
+        return str(e)
+    return None if r.returncode == 0 else r.stderr[-2000:] or f"exit code {r.returncode}"
+
+
 def _host_object() -> str | None:
-    """host_calls.cpp compiled; None where PyTorch or its headers are missing."""
+    """host_calls.cpp compiled; None where PyTorch, a header or a compiler is missing."""
     where = _torch_dir()
     if where is None:
         return None
     torch_inc = os.path.join(where, "include")
-    cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    try:
+        cuda_inc = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+    except RuntimeError as e:
+        print(f"host_calls.cpp not built (the binding goes without it):\n{e}")
+        return None
     obj = os.path.join(BUILD, "host_calls.o")
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DMOE_BUILT_FOR="{host_key()}"',
            "-I", torch_inc, "-I", os.path.join(torch_inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I", cuda_inc, "-c", HOST_SRC, "-o", obj]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        print(f"host_calls.cpp not built (the binding goes without it):\n{r.stderr[-2000:]}")
+    wrong = _run(cmd)
+    if wrong is not None:
+        print(f"host_calls.cpp not built (the binding goes without it):\n{wrong}")
         return None
     return obj
 
@@ -113,9 +126,9 @@ def _link_host(obj: str | None) -> None:
     tmp = HOST_LIB + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
            "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        print(f"host_calls not linked (the binding goes without it):\n{r.stderr[-2000:]}")
+    wrong = _run(cmd)
+    if wrong is not None:
+        print(f"host_calls not linked (the binding goes without it):\n{wrong}")
         return
     os.replace(tmp, HOST_LIB)
     with open(HOST_DONE, "w") as f:

@@ -97,3 +97,23 @@ def test_pytorch_that_comes_later(place, monkeypatch):
     assert not place.ran and not place.lib.exists()
     _build.build()
     assert len(place.ran) == 2 and place.lib.exists()
+
+
+@pytest.mark.parametrize("missing", ["g++", "nvcc", "the linker"])
+def test_without_a_compiler(place, monkeypatch, capsys, missing):
+    """An up-to-date library and no g++ or no CUDA toolkit: the build says so and goes on without the extension."""
+    def run(cmd, **kw):
+        if missing == "g++" or (missing == "the linker" and "-shared" in cmd):
+            raise FileNotFoundError(2, "No such file or directory", cmd[0])
+        return place.run(cmd, **kw)
+
+    def nvcc():
+        if missing == "nvcc":
+            raise RuntimeError("nvcc not found")
+        return "/usr/local/cuda/bin/nvcc"
+    monkeypatch.setattr(subprocess, "run", run)
+    monkeypatch.setattr(_build, "nvcc", nvcc)
+    assert _build.build() == _build.LIB
+    told = capsys.readouterr().out
+    assert "goes without it" in told and ("nvcc not found" if missing == "nvcc" else "No such file") in told
+    assert not place.lib.exists() and not place.done.exists()
