@@ -12,6 +12,7 @@ the build goes on.
 from __future__ import annotations
 
 import concurrent.futures
+import contextlib
 import glob
 import hashlib
 import importlib.util
@@ -104,7 +105,7 @@ def _host_object() -> str | None:
     except RuntimeError as e:
         print(f"host_calls.cpp not built (the binding goes without it):\n{e}")
         return None
-    obj = os.path.join(BUILD, "host_calls.o")
+    obj = os.path.join(BUILD, f"host_calls.{os.getpid()}.o")  # several processes may build at once
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f'-DMOE_BUILT_FOR="{host_key()}"',
            "-I", torch_inc, "-I", os.path.join(torch_inc, "torch", "csrc", "api", "include"), "-I", sysconfig.get_paths()["include"], "-I", cuda_inc, "-c", HOST_SRC, "-o", obj]
     wrong = _run(cmd)
@@ -114,25 +115,33 @@ def _host_object() -> str | None:
     return obj
 
 
+def _remove(*paths) -> None:
+    for path in paths:
+        with contextlib.suppress(FileNotFoundError):  # another process may have been faster
+            os.remove(path)
+
+
 def _link_host(obj: str | None) -> None:
     """The extension from its object; none at all where there is no object or it cannot be linked, so that the
     next build tries again."""
-    for old in (HOST_DONE, HOST_LIB):
-        if os.path.exists(old):
-            os.remove(old)
     if obj is None:
+        _remove(HOST_DONE, HOST_LIB)
         return
     torch_lib = os.path.join(_torch_dir(), "lib")
     tmp = HOST_LIB + f".tmp{os.getpid()}"
     cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:" + os.path.basename(LIB), "-L", torch_lib, "-ltorch_python", "-ltorch_cpu",
            "-ltorch_cuda", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"]
     wrong = _run(cmd)
+    _remove(obj)
     if wrong is not None:
+        _remove(HOST_DONE, HOST_LIB, tmp)
         print(f"host_calls not linked (the binding goes without it):\n{wrong}")
         return
     os.replace(tmp, HOST_LIB)
-    with open(HOST_DONE, "w") as f:
+    done = HOST_DONE + f".tmp{os.getpid()}"
+    with open(done, "w") as f:
         f.write(host_key())
+    os.replace(done, HOST_DONE)
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:

@@ -117,3 +117,38 @@ def test_without_a_compiler(place, monkeypatch, capsys, missing):
     told = capsys.readouterr().out
     assert "goes without it" in told and ("nvcc not found" if missing == "nvcc" else "No such file") in told
     assert not place.lib.exists() and not place.done.exists()
+
+
+def test_two_builds_at_once(place, monkeypatch):
+    """A build from another process in the middle of this one, at every step of it: both end well, and neither
+    takes away what the other made."""
+    for step in range(2):
+        for old in (place.lib, place.done):
+            old.unlink(missing_ok=True)
+        others, pid = [], os.getpid()
+
+        def run(cmd, **kw):
+            if len(others) == 0 and ("-shared" in cmd) == (step == 1):
+                others.append(cmd)
+                with monkeypatch.context() as m:  # the other process
+                    m.setattr(os, "getpid", lambda: pid + 1)
+                    _build.build()
+                assert place.lib.exists() and place.done.exists()
+            return place.run(cmd, **kw)
+        monkeypatch.setattr(subprocess, "run", run)
+        _build.build()
+        assert others and place.lib.read_text() == "built" and not _build.host_is_stale()
+    made = [cmd[cmd.index("-o") + 1] for cmd in place.ran]
+    assert len(set(made)) == 4 and not [n for n in os.listdir(place.done.parent) if n.endswith(".o")]
+
+
+def test_what_another_build_has_removed(place, monkeypatch):
+    """Two failed builds remove the same files."""
+    _build.build()
+    monkeypatch.setattr(_build, "_host_object", lambda: None)
+    exists = os.path.exists
+    monkeypatch.setattr(os.path, "exists", lambda p: True if str(p).startswith(str(place.lib.parent)) else exists(p))
+    _build._link_host(None)
+    _build._link_host(None)
+    monkeypatch.undo()
+    assert not place.lib.exists()
