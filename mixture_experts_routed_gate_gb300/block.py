@@ -79,20 +79,28 @@ class MoEBlock:
         return got.get("u"), got["out"]
 
 
+def _reads_rows8(block) -> bool:
+    return isinstance(getattr(block, "experts", None), binding.Mx8Experts)
+
+
 def run_blocks(blocks, x, w_first, eps: float = 1e-6, err=None):
     """x [T, d_hidden], the residual stream, through the blocks; w_first: weight
     of the norm before the first one.  Returns (u, res): the last block's u' (or
-    None) and the residual stream; x is left as it was."""
-    blocks = list(blocks)
-    eight = [isinstance(getattr(block, "experts", None), binding.Mx8Experts) for block in blocks] + [False]
-    if eight[0]:
+    None) and the residual stream; x is left as it was.  ``blocks`` may make them
+    as they are needed: the next one is asked for when one runs, whose norm writes
+    what the next one reads, and none is held behind that."""
+    blocks = iter(blocks)
+    block = next(blocks, None)
+    if _reads_rows8(block):
         got = binding.moe_residual_norm_mx8(None, x, w_next=w_first, eps=eps)
         u = Rows8(got["u"], got["q"], got["sf"])
     else:
         u = binding.moe_residual_norm(None, x, w_next=w_first, eps=eps)["u"]
     res = x.clone()
-    for block, rows8 in zip(blocks, eight[1:]):
+    while block is not None:
         if u is None:
             raise ValueError("only the last block may have no w_next")
-        u, res = block(u, res, err, rows8=True) if rows8 else block(u, res, err)
+        following = next(blocks, None)
+        u, res = block(u, res, err, rows8=True) if _reads_rows8(following) else block(u, res, err)
+        block = following
     return u, res
