@@ -101,6 +101,7 @@ def run_blocks(blocks, x, w_first, eps: float = 1e-6, err=None):
         if u is None:
             raise ValueError("only the last block may have no w_next")
         following = next(blocks, None)
-        u, res = block(u, res, err, rows8=True) if _reads_rows8(following) else block(u, res, err)
+        # what is no MoEBlock gives u alone, which an 8-bit layer quantises for itself
+        u, res = block(u, res, err, rows8=True) if isinstance(block, MoEBlock) and _reads_rows8(following) else block(u, res, err)
         block = following
     return u, res

@@ -61,3 +61,15 @@ def test_what_each_block_gets_and_is_asked_for(norms, monkeypatch):
     with pytest.raises(ValueError, match="only the last block"):
         run_blocks([make(last=True), make()], x, 1)
     assert run_blocks((make(last=True),), x, 1)[0] is None
+
+
+def test_a_callable_before_an_8_bit_block(norms):
+    """A program's own (u, res, err) -> (u, res) among the blocks: it is asked for no 8-bit rows."""
+    seen = []
+
+    def own(u, res, err):
+        seen.append(u)
+        return u + 1, res
+    x = torch.zeros(2, 4)
+    u, _ = run_blocks([own, make(True), own], x, 1)
+    assert len(seen) == 2 and seen[0] is x and torch.equal(u, torch.ones(2, 4))
