@@ -21,8 +21,8 @@
 // a fixed order.
 //
 // With u in 8 bits beside it (norm_mx8_kernel): 4096 x 7168 bf16 45 us (265 MB, 39 at
-// the copy rate), u in 8 bits alone 40 (30); fp32 82 (74); bound by instructions
-// below about 4096 elements (4096 x 2048: 15.4 us, 11.2 at the copy rate).
+// the copy rate), u in 8 bits alone 40 (30); fp32 79 (74); bound by instructions
+// below about 4096 elements (4096 x 2048: 15.8 us, 11.2 at the copy rate).
 // 4096 x 7168 bf16: forward 39 us (235 MB at 6.0 TB/s, against 35 at this
 // card's copy rate; 67% of the issue slots), gradients 88 us (52 at the copy
 // rate; 57% of the issue slots at about 500 instructions a warp and row, and the
@@ -218,6 +218,10 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
     return d;
 }
 __device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <int EPT> __device__ __forceinline__ void put(float (&o)[EPT], int k, float2 v) {
+    o[2 * k] = v.x;
+    o[2 * k + 1] = v.y;
+}
 
 // A row of u in 8 bits.  32 / RUN consecutive lanes hold a block of 32 elements
 // and find its largest magnitude among them; the blocks that cross H do not
@@ -562,14 +566,15 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
 }
 
 // The same with u in 8 bits.  What a row costs here is instructions, so they are
-// fewer: two elements a product (f32x2), products of 16-bit weights and gates and
-// the squares of y by mixed FMAs (exact, no unpacking), alpha, a token's gate and
-// rstd(y) one factor; with that its sums and products round less often than
-// norm_kernel's, and its results differ from them by as much.  Wide rows of many
-// tokens take 32 elements a thread (norm_shape): a row's two reductions, waits and
-// addresses are then shared by the fewest warps.  (Left out one at a time, of the
-// 1040 instructions a warp and row of 7168 elements that norm_kernel's arithmetic
-// took with 32 elements a thread: the 8-bit store 221, out 48, u 46, a reduction 42.)
+// fewer: two elements a product (f32x2), the squares of y by mixed FMAs (exact, no
+// unpacking); its products are norm_kernel's and its sums are in another order.
+// The row's factors come one at a time, each into o: with a row of the weight and
+// one of the gate beside y and res, fp32 rows of more than 8192 spilled 340 bytes
+// (2000 x 10240 98 us, so 68; 4096 x 14336 241, so 199).  Wide rows of many tokens
+// take 32 elements a thread (norm_shape): a row's two reductions, waits and addresses
+// are then shared by the fewest warps.  (Left out one at a time, of the 1040
+// instructions a warp and row of 7168 elements that norm_kernel's arithmetic took
+// with 32 elements a thread: the 8-bit store 221, out 48, u 46, a reduction 42.)
 template <typename T, int EPT, Rows MODE, int MAX_THREADS, int MIN_CTAS>
 __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const __grid_constant__ NormParams p) {
     using P = Part<T, EPT, true>;  // rows of whole blocks of 32 start on 16 bytes
@@ -591,8 +596,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const _
     for (; ring.row < p.T; ring.row += gridDim.x) {
         const int64_t t = ring.row, base = t * H;
         ring.next();
-        float factor = p.alpha;
-        if (p.gate_kind == 2) factor *= to_f32(static_cast<const T *>(p.gate)[t]);
+        float scale = p.alpha;
+        if (p.gate_kind == 2) scale *= to_f32(static_cast<const T *>(p.gate)[t]);
         P res, w;
         res.load(ring.take(), H);
         bool read = false;  // every thread has read the row's slots
@@ -601,6 +606,8 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const _
             P y, gate;
             y.load(ring.take(), H);
             if (p.gate_kind == 3) gate.load(ring.take(), H);
+            // y rstd, w_post, gate and alpha in turn, as norm_kernel: a product of any two
+            // of the factors may leave fp32's range where these do not
             if (post) {
                 float a = 0.0f, b = 0.0f;
 #pragma unroll
@@ -617,31 +624,20 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const _
                 if (p.rstd_post && threadIdx.x == 0) p.rstd_post[t] = r2;
                 ring.refill();
                 read = true;
-                factor *= r2;
                 w_post.load(w, H);
-            }
-            if (p.gate_kind == 1) gate_row.load(gate, H);
-            // the factors that an element has of its own: w_post * gate, one of them, or none
-            const float2 f = both(factor);
-            if (post && (p.gate_kind & 1)) {
 #pragma unroll
-                for (int k = 0; k < EPT / 2; ++k) {
-                    const float2 v = fma2(mul2(y.pair(k), f), make_float2(w.times(gate, 2 * k), w.times(gate, 2 * k + 1)), res.pair(k));
-                    o[2 * k] = v.x;
-                    o[2 * k + 1] = v.y;
-                }
+                for (int k = 0; k < EPT / 2; ++k) put(o, k, mul2(mul2(y.pair(k), both(r2)), w.pair(k)));
             } else {
-                if (p.gate_kind & 1)
-                    w = gate;
-                else if (!post)
-                    w.fill(1.0f);
 #pragma unroll
-                for (int k = 0; k < EPT / 2; ++k) {
-                    const float2 v = fma2(mul2(y.pair(k), f), w.pair(k), res.pair(k));
-                    o[2 * k] = v.x;
-                    o[2 * k + 1] = v.y;
-                }
+                for (int k = 0; k < EPT / 2; ++k) put(o, k, y.pair(k));
             }
+            if (p.gate_kind & 1) {
+                if (p.gate_kind == 1) gate_row.load(gate, H);
+#pragma unroll
+                for (int k = 0; k < EPT / 2; ++k) put(o, k, mul2(make_float2(o[2 * k], o[2 * k + 1]), gate.pair(k)));
+            }
+#pragma unroll
+            for (int k = 0; k < EPT / 2; ++k) put(o, k, fma2(both(scale), make_float2(o[2 * k], o[2 * k + 1]), res.pair(k)));
             P::store(static_cast<T *>(p.out) + base, H, o);
         } else {
 #pragma unroll
@@ -655,11 +651,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_mx8_kernel(const _
         if (!read) ring.refill();
         w_next.load(w, H);
 #pragma unroll
-        for (int i = 0; i < EPT; i += 2) {
-            const float2 v = mul2(mul2(make_float2(o[i], o[i + 1]), both(r)), w.pair(i / 2));
-            o[i] = v.x;
-            o[i + 1] = v.y;
-        }
+        for (int i = 0; i < EPT; i += 2) put(o, i / 2, mul2(mul2(make_float2(o[i], o[i + 1]), both(r)), w.pair(i / 2)));
         if (p.u) P::store(static_cast<T *>(p.u) + base, H, o);
         store_mx8<P>(p, t, o);
     }
