@@ -229,40 +229,32 @@ template <int EPT> __device__ __forceinline__ void put(float (&o)[EPT], int k, f
 template <typename P, int EPT>
 __device__ __forceinline__ void store_mx8(const NormParams &p, int64_t t, const float (&o)[EPT]) {
     constexpr int RUN = P::RUN, LANES = 32 / RUN;
+    static_assert(RUN == 4 || RUN == 8, "16 bytes of a row");
     uint8_t *q = p.q + t * p.H, *sf = p.sf + t * (p.H / 32);
 #pragma unroll
     for (int v = 0; v < EPT; v += RUN) {
         const int at = P::at(v);
-        float most = o[v];
-        if constexpr (RUN > 1) {
-            most = largest(o[v], o[v + 1], o[v + 2]);
-            if constexpr (RUN == 8) most = largest(largest(most, o[v + 3], o[v + 4]), o[v + 5], o[v + 6]);
-            most = largest(most, most, o[v + RUN - 1]);
-        }
+        float most = largest(o[v], o[v + 1], o[v + 2]);
+        if constexpr (RUN == 8) most = largest(largest(most, o[v + 3], o[v + 4]), o[v + 5], o[v + 6]);
+        most = largest(most, most, o[v + RUN - 1]);
         uint32_t top = magnitude_bits(most);
 #pragma unroll
         for (int s = LANES / 2; s >= 1; s >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, s));
         const uint32_t s = mx8_scale(top);
         const float by = mx8_inverse(s);
         const bool bad = s == 255u;
-        uint32_t w[RUN >= 4 ? RUN / 4 : 1];
-        if constexpr (RUN >= 4) {
+        uint32_t w[RUN / 4];
 #pragma unroll
-            for (int j = 0; j < RUN / 4; ++j) {
-                const float2 a = mul2(make_float2(o[v + 4 * j], o[v + 4 * j + 1]), both(by));
-                const float2 b = mul2(make_float2(o[v + 4 * j + 2], o[v + 4 * j + 3]), both(by));
-                w[j] = bad ? 0u : e4m3x2(a.x, a.y) | e4m3x2(b.x, b.y) << 16;
-            }
-        } else {
-            w[0] = bad ? 0u : e4m3x2(o[v] * by, 0.0f);
+        for (int j = 0; j < RUN / 4; ++j) {
+            const float2 a = mul2(make_float2(o[v + 4 * j], o[v + 4 * j + 1]), both(by));
+            const float2 b = mul2(make_float2(o[v + 4 * j + 2], o[v + 4 * j + 3]), both(by));
+            w[j] = bad ? 0u : e4m3x2(a.x, a.y) | e4m3x2(b.x, b.y) << 16;
         }
         if (at >= p.H) continue;
         if constexpr (RUN == 8)
             *reinterpret_cast<uint2 *>(q + at) = make_uint2(w[0], w[1]);
-        else if constexpr (RUN == 4)
-            *reinterpret_cast<uint32_t *>(q + at) = w[0];
         else
-            q[at] = static_cast<uint8_t>(w[0]);
+            *reinterpret_cast<uint32_t *>(q + at) = w[0];
         if ((threadIdx.x & (LANES - 1)) == 0) sf[at / 32] = static_cast<uint8_t>(s);
     }
 }
@@ -907,12 +899,12 @@ template <typename T> cudaError_t launch_shape(const NormParams &p, const NormSh
         if constexpr (sizeof(T) == 2) {
             if (s.ept == 32)
                 return s.threads <= 256 ? launch_mx8<T, 32, kVectors, 256, 2>(p, s, stream) : launch_mx8<T, 32, kVectors, 512, 1>(p, s, stream);
-        } else {
+            if (s.ept == 16 && s.threads <= 512) return launch_mx8<T, 16, kVectors, 512, 2>(p, s, stream);
+        } else {  // 16 elements a thread from 8193 on: more than 512 threads
             if (s.mode == kMemory) return launch_mx8<T, 16, kMemory, 1024, 1>(p, s, stream);
             if (s.ept == 8 && s.threads > 512) return launch_mx8<T, 8, kVectors, 1024, 1>(p, s, stream);
         }
-        if (s.ept == 16)
-            return s.threads <= 512 ? launch_mx8<T, 16, kVectors, 512, 2>(p, s, stream) : launch_mx8<T, 16, kVectors, 1024, 1>(p, s, stream);
+        if (s.ept == 16) return launch_mx8<T, 16, kVectors, 1024, 1>(p, s, stream);
         return launch_mx8<T, 8, kVectors, 512, 2>(p, s, stream);
     }
     if (!backward) {
