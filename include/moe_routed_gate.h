@@ -597,8 +597,8 @@ MOE_API moe_status_t moe_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint
  * moe_forward with mx4 experts and mx4 activations: moe_gate_topk and
  * moe_build_dispatch on x in `dtype`, then moe_quantize_mx4 of the routed rows,
  * moe_grouped_gate_up_silu_mx4, moe_grouped_gemm_mx4 (down, into `dtype`) and
- * moe_reduce_fused.  d_h % 256 == 0, d_e % 64 == 0.  ws:
- * moe_forward_mx4_workspace_bytes(...) bytes, 256-byte aligned.
+ * moe_reduce_fused.  d_h % 256 == 0, d_e % 64 == 0, both up to 2^20, T k up to
+ * 2^31 - 256.  ws: moe_forward_mx4_workspace_bytes(...) bytes, 256-byte aligned.
  */
 MOE_API size_t moe_forward_mx4_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
                                                moe_dtype_t dtype);
@@ -673,8 +673,8 @@ MOE_API moe_status_t moe_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint
  * moe_grouped_gate_up_silu_mx8, moe_grouped_gemm_mx8 (down, into `dtype`) and
  * moe_reduce_fused.  q, sf [T, d_h]: x in 8 bits, as moe_residual_norm_mx8 writes
  * it beside x; both NULL: quantised from x by this call.  d_h % 256 == 0,
- * d_e % 64 == 0.  ws: moe_forward_mx8_workspace_bytes(...) bytes, 256-byte
- * aligned.
+ * d_e % 64 == 0, both up to 2^20, T k up to 2^31 - 256.  ws:
+ * moe_forward_mx8_workspace_bytes(...) bytes, 256-byte aligned.
  */
 MOE_API size_t moe_forward_mx8_workspace_bytes(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k,
                                                moe_dtype_t dtype);

@@ -849,8 +849,13 @@ struct MxLayout {
     size_t logits, idx, w, sizes, offsets, padded, gidx, stok, sw, pos, scratch, qx, sx, qa, sa, qh, sh, y, total;
 };
 
+// the sizes that every part of the forward takes, so that none refuses its own after others have been launched
+static bool mx_sizes(int64_t T, int64_t d_h, int64_t d_e, int64_t k) {
+    return T <= ((int64_t(1) << 31) - 256) / k && d_h <= (1 << 20) && d_e <= (1 << 20);
+}
+
 static bool mx_layout(int64_t T, int64_t d_h, int64_t d_e, int64_t E, int64_t k, moe_dtype_t dtype, int bits, MxLayout *L) {
-    if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || !is_half_type(dtype)) return false;
+    if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || !is_half_type(dtype) || !mx_sizes(T, d_h, d_e, k)) return false;
     const size_t Tk = static_cast<size_t>(T * k), e4 = static_cast<size_t>(E) * 4;
     size_t cur = 0;
     auto take = [&cur](size_t bytes) {
@@ -895,6 +900,7 @@ moe_status_t moe_forward_mx4(const void *x, const void *w_g, const float *bias, 
     if (!is_half_type(dtype)) return MOE_ERR_UNSUPPORTED;
     if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || k > E || k > 32 || E > 1024) return MOE_ERR_INVALID_ARG;
     if (d_h % 256 != 0 || d_e % 64 != 0) return MOE_ERR_INVALID_ARG;
+    if (!mx_sizes(T, d_h, d_e, k)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !w_g || !q_gate || !sf_gate || !q_up || !sf_up || !q_down || !sf_down || !out || !ws)
         return MOE_ERR_INVALID_ARG;
@@ -1031,6 +1037,7 @@ moe_status_t moe_forward_mx8(const void *x, const uint8_t *q, const uint8_t *sf,
     if (!is_half_type(dtype)) return MOE_ERR_UNSUPPORTED;
     if (T < 0 || d_h <= 0 || d_e <= 0 || E <= 0 || k <= 0 || k > E || k > 32 || E > 1024) return MOE_ERR_INVALID_ARG;
     if (d_h % 256 != 0 || d_e % 64 != 0 || (q == nullptr) != (sf == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (!mx_sizes(T, d_h, d_e, k)) return MOE_ERR_UNSUPPORTED;
     if (T == 0) return MOE_OK;
     if (!x || !w_g || !q_gate || !sf_gate || !q_up || !sf_up || !q_down || !sf_down || !out || !ws)
         return MOE_ERR_INVALID_ARG;
