@@ -818,8 +818,8 @@ moe_status_t moe_grouped_gemm_mx4(const uint8_t *q_a, const uint8_t *sf_a, const
     if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_b, sf_b, C}, N, K, E);
     if (st != MOE_OK) return st;
     if (!all_aligned16({q_a, q_b, C})) return MOE_ERR_INVALID_ARG;
-    const moe::MxTables tab = {group_sizes,      group_offsets, group_padded_offsets,
-                               group_idx_for_bx, n_rows,        static_cast<int>(E)};
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, static_cast<int>(n_rows),
+                               static_cast<int>(E)};
     return cuda_status(moe::launch_grouped_gemm_mx4(q_a, sf_a, q_b, sf_b, tab, m_blocks, n_rows, N, K, E, out_dtype, C,
                                                     err_flag, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -836,8 +836,8 @@ moe_status_t moe_grouped_gate_up_silu_mx4(const uint8_t *q_a, const uint8_t *sf_
     if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h, E);
     if (st != MOE_OK) return st;
     if (d_e % 32 != 0 || !all_aligned16({q_a, q_gate, q_up, q_h})) return MOE_ERR_INVALID_ARG;
-    const moe::MxTables tab = {group_sizes,      group_offsets, group_padded_offsets,
-                               group_idx_for_bx, n_rows,        static_cast<int>(E)};
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, static_cast<int>(n_rows),
+                               static_cast<int>(E)};
     return cuda_status(moe::launch_grouped_gate_up_silu_mx4(q_a, sf_a, q_gate, sf_gate, q_up, sf_up, tab, m_blocks,
                                                             n_rows, d_h, d_e, E, q_h, sf_h, err_flag,
                                                             reinterpret_cast<cudaStream_t>(stream)));
@@ -999,8 +999,8 @@ moe_status_t moe_grouped_gemm_mx8(const uint8_t *q_a, const uint8_t *sf_a, const
     if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_b, sf_b, C}, N, K, E);
     if (st != MOE_OK) return st;
     if (!all_aligned16({q_a, q_b, C})) return MOE_ERR_INVALID_ARG;
-    const moe::MxTables tab = {group_sizes,      group_offsets, group_padded_offsets,
-                               group_idx_for_bx, n_rows,        static_cast<int>(E)};
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, static_cast<int>(n_rows),
+                               static_cast<int>(E)};
     return cuda_status(moe::launch_grouped_gemm_mx8(q_a, sf_a, q_b, sf_b, tab, m_blocks, n_rows, N, K, E, out_dtype, C,
                                                     err_flag, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -1017,8 +1017,8 @@ moe_status_t moe_grouped_gate_up_silu_mx8(const uint8_t *q_a, const uint8_t *sf_
     if (st == MOE_OK) st = check_mx_gemm({q_a, sf_a, q_gate, sf_gate, q_up, sf_up, q_h, sf_h}, d_e, d_h, E);
     if (st != MOE_OK) return st;
     if (d_e % 32 != 0 || !all_aligned16({q_a, q_gate, q_up, q_h})) return MOE_ERR_INVALID_ARG;
-    const moe::MxTables tab = {group_sizes,      group_offsets, group_padded_offsets,
-                               group_idx_for_bx, n_rows,        static_cast<int>(E)};
+    const moe::MxTables tab = {group_sizes, group_offsets, group_padded_offsets, group_idx_for_bx, static_cast<int>(n_rows),
+                               static_cast<int>(E)};
     return cuda_status(moe::launch_grouped_gate_up_silu_mx8(q_a, sf_a, q_gate, sf_gate, q_up, sf_up, tab, m_blocks,
                                                             n_rows, d_h, d_e, E, q_h, sf_h, err_flag,
                                                             reinterpret_cast<cudaStream_t>(stream)));

@@ -189,7 +189,7 @@ cudaError_t launch_reduce_backward(const void *d_out, const void *x, const int32
 // mx4.cu: 4-bit rows with a power-of-two scale per 32 elements
 struct MxTables {
     const int32_t *sizes, *offsets, *padded, *gidx;
-    int64_t n_rows;  // of the call's rows and results, whatever the tables say
+    int n_rows;  // of the call's rows and results, whatever the tables say
     int E;
 };
 cudaError_t launch_quantize_mx4(const void *x, const int32_t *row_idx, int64_t n_rows, int64_t T, int64_t K,

@@ -272,7 +272,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
     int n_blocks = 0;
     for (int b0 = 0; b0 < p.m_blocks && n_blocks <= MG_LIST; b0 += MG_THREADS) {
         const int bx = b0 + static_cast<int>(threadIdx.x);
-        const Mx4Block b = bx < p.m_blocks ? mx_unit_of<128>(p.tab, bx, p.m_blocks, p.err) : Mx4Block{0, 0, 0};
+        const Mx4Block b = bx < p.m_blocks ? mx_unit_of<128>(p.tab, bx, p.m_blocks) : Mx4Block{0, 0, 0};
         const uint32_t has = __ballot_sync(0xffffffffu, b.rows > 0);
         if (lane == 0) warp_blocks[warp] = __popc(has);
         __syncthreads();
@@ -300,7 +300,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             ti.m_start = e.x;
             ti.rows = e.y & 255;
         } else {
-            const Mx4Block k = mx_unit_of<128>(p.tab, b, p.m_blocks, p.err);
+            const Mx4Block k = mx_unit_of<128>(p.tab, b, p.m_blocks);
             ti.g = k.g;
             ti.m_start = k.m_start;
             ti.rows = k.rows;
@@ -353,6 +353,8 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
                 }
             }
         }
+        __syncwarp();
+        flag_rows_past(p.tab, lane, p.err);
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         constexpr uint32_t IDESC = idesc_mxf4(MG_BM, BN);

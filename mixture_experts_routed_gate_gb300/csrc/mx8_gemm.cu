@@ -302,9 +302,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
         const int g = e0 + static_cast<int>(threadIdx.x);
         const bool in = g < p.tab.E;
         const int size = in ? __ldg(p.tab.sizes + g) : 0, m = in ? __ldg(p.tab.offsets + g) : 0;
-        const int64_t here = static_cast<int64_t>(p.m_blocks) * 128 - (in ? __ldg(p.tab.padded + g) : 0);  // to the end of the blocks
-        const int rows = static_cast<int>(max(min(rows_there(p.tab, size, m, p.err), here), int64_t{0}));
-        const int mine = static_cast<int>((static_cast<int64_t>(rows) + NT - 1) / NT);
+        const int blocks = p.m_blocks - (in ? __ldg(p.tab.padded + g) / 128 : 0);  // more hold no more rows than 2^24 - 1
+        const int rows = max(0, min(rows_there(p.tab, size, m), min(max(blocks, 0), (1 << 24) - 1) * 128));
+        const int mine = rows / NT + (rows % NT ? 1 : 0);
         int upto = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -350,7 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
             ti.rows = e.y & 511;
             ti.single = (e.y & 512) != 0;
         } else {
-            const Mx4Block k = mx_unit_of<NT>(p.tab, c.b, p.m_blocks, p.err);
+            const Mx4Block k = mx_unit_of<NT>(p.tab, c.b, p.m_blocks);
             ti.g = k.g;
             ti.m_start = k.m_start;
             ti.rows = k.rows;
@@ -431,6 +431,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(G8_THREADS, 1)
                 g8_drain(full_bar(static_cast<int>(i % L::STAGES)), static_cast<uint32_t>((i / L::STAGES) & 1));
             }
         }
+        __syncwarp();
+        flag_rows_past(p.tab, lane, p.err);
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         if (leader) {

@@ -115,3 +115,25 @@ def test_as_many_rows_as_there_may_be(form):
         one = {name: torch.tensor(v, dtype=torch.int32, device="cuda") for name, v in one.items()}
         assert torch.equal(out[at], form.product(q, s, qb[e:e + 1], sb[e:e + 1], one, torch.float16)), (at, e)
     assert not (out[some:some + 2 ** 20]).any() and not out[-last - some - 2 ** 20:-last - some].any()
+
+
+@pytest.mark.parametrize("form", [Eight, Four])
+def test_more_units_than_a_list_holds_and_experts_without_rows(form):
+    """First rows below 0 and past the end among more units of rows than a CTA lists."""
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    E, K, N, n = 700, 64, 32, 700 * 2
+    a, b = form.quantize(torch.randn((n, K), generator=g, device="cuda")), form.quantize(torch.randn((E * N, K), generator=g, device="cuda"))
+    sizes, offsets = torch.full((E,), 2), torch.arange(E) * 2
+    t = dict(group_sizes=sizes, group_offsets=offsets, group_padded_offsets=torch.arange(E) * 128, group_idx_for_bx=torch.arange(E))
+    gone = torch.tensor([0, 5, 350, 698])
+    ok = dict(t, group_sizes=sizes.index_fill(0, gone, 0))
+    bad = dict(t, group_offsets=offsets.index_copy(0, gone, torch.tensor([-2, -(2 ** 31), n, 2 ** 31 - 1])))
+    err, out = torch.zeros(1, dtype=torch.int32, device="cuda"), []
+    for tables in (ok, bad):
+        out.append(torch.full((n, N), -1000.5, device="cuda"))
+        form.product(*a, *(x.view(E, N, -1) for x in b), {i: v.to(torch.int32).cuda() for i, v in tables.items()}, torch.float32, out=out[-1], err=err)
+        assert int(err.item()) == (0 if tables is ok else DEVICE_FLAG)
+    left = torch.zeros(n, dtype=torch.bool, device="cuda")
+    left.view(E, 2)[gone.cuda()] = True
+    assert torch.equal(*out) and (out[0][left] == -1000.5).all() and not (out[0][~left] == -1000.5).any()
