@@ -56,7 +56,7 @@ struct Mx4Block {
 // which are neither read nor written; nor are rows below 0.  Minima alone: a selection
 // by one of an expert's entries becomes a branch with the loads of the others behind
 // it, and this stands before the first copy of every launch (a 4-bit product of 384
-// rows of 64 experts, 2048 x 768: 12.1 us, so 12.6).
+// rows of 64 experts, 2048 x 768: 12.6 us for 12.1).
 __device__ __forceinline__ int rows_there(const MxTables &t, int size, int first) {
     const int behind = static_cast<int>(static_cast<uint32_t>(t.n_rows) - static_cast<uint32_t>(first));
     return min(min(size, behind), first | INT32_MAX);  // the last: -1 below 0

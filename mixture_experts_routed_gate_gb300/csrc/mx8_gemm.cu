@@ -29,7 +29,7 @@
 //
 // 32,768 rows, 256 experts, 7168 x 2048, bf16 out: 718 us for 4.25 GB (627 at the
 // copy rate); its tiles bring 5.9 GB from L2 into shared memory, which gives out at
-// 10 to 12 TB/s (16 experts of 2048 rows: 3.8 GB in 347 us, 2.8 PFLOP/s), and the
+// 10 to 12 TB/s (16 experts of 2048 rows: 3.8 GB in 317 us, 3.0 PFLOP/s), and the
 // tensor pipe is active for a quarter of the time.  What paces a slice is the one
 // thread that asks for its copies: issued by one lane of a branch, each operand
 // is moved to it first (770 us), and any work more between them shows in all sizes
@@ -759,7 +759,8 @@ cudaError_t launch_n(const CUtensorMap *maps, const G8Params &p, cudaStream_t st
 // epilogue runs alone (both accumulator slots are one tile's), which a long K earns
 // back, and a shorter one only when there are several rounds of tiles: the product
 // from K of 1024, the gate/up form, whose epilogue is longer, from 2048 and 512 rows
-// an expert; tiles that do not fill a round are better narrow, and more.  Narrow / wide, us:
+// an expert; tiles that do not fill a round are better narrow, and more.  Narrow / wide, us,
+// of groups whose sizes differ as routing makes them (rows on average):
 //   7168 x 2048, 256 experts, 128 rows each: 828 / 730, gate/up 1730 / 1455
 //   7168 x 2048, 64 experts: 32 rows each 166 / 165 and 316 / 313, 64 rows 177 / 174
 //   and 331 / 326, 256 rows 321 / 244 and 678 / 520; 16 experts, 2048 rows 515 / 370

@@ -562,7 +562,7 @@ __global__ void __launch_bounds__(MAX_THREADS, MIN_CTAS) norm_kernel(const __gri
 // unpacking); its products are norm_kernel's and its sums are in another order.
 // The row's factors come one at a time, each into o: with a row of the weight and
 // one of the gate beside y and res, fp32 rows of more than 8192 spilled 340 bytes
-// (2000 x 10240 98 us, so 68; 4096 x 14336 241, so 199).  Wide rows of many tokens
+// (2000 x 10240 98 us for 68; 4096 x 14336 241 for 199).  Wide rows of many tokens
 // take 32 elements a thread (norm_shape): a row's two reductions, waits and addresses
 // are then shared by the fewest warps.  (Left out one at a time, of the 1040
 // instructions a warp and row of 7168 elements that norm_kernel's arithmetic took
@@ -823,10 +823,10 @@ NormShape norm_shape(NormParams &p, int elem, bool backward) {
     // with one CTA, 145 with two).
     s.ept = backward ? backward_ept(p.H) : p.H <= (elem == 4 ? 8192 : 4096) ? 8 : 16;
     // The 8-bit form, 16-bit types: 32 elements a thread where rows are wide and
-    // many.  4096 rows of 1024 / 2048 / 4096 / 7168: 8.7 / 15.4 / 27.8 / 45.5 us, with the
-    // widths above 10.7 / 18.5 / 33.7 / 45.0; of 512: 7.7 and 7.1; 320 rows of 1024: 3.9
-    // and 3.1, of 7168: 7.1 and 6.6; 700 rows the same.  (fp32 with 16 instead of 8: 136
-    // us for 82, spilled.)
+    // many.  4096 rows of 1024 / 2048 / 4096 / 7168: 8.6 / 15.8 / 28.1 / 45.6 us, with the
+    // widths above 11.1 / 19.4 / 34.0 / 44.9; of 512: 7.9 and 7.2; 320 rows of 1024: 3.9
+    // and 3.2, of 7168: 7.0 and 6.7; 700 rows 4.3 and 4.0, 11.3 and 11.1.  (fp32 with 16
+    // instead of 8: 100 us for 79.)
     if (p.q && elem == 2 && p.H >= 1024 && p.T >= 4 * device_sm_count()) s.ept = 32;
     s.threads = norm_threads(p.H, s.ept);
     int per_sm = (s.ept == 32 ? 512 : 1024) / s.threads;
