@@ -62,19 +62,6 @@ __device__ __forceinline__ int rows_there(const MxTables &t, int size, int first
     return min(min(size, behind), first | INT32_MAX);  // the last: -1 below 0
 }
 
-// Whether they name such rows, into the error word; by a warp of each CTA that has
-// nothing else left to do (in the loop over the entries that every CTA starts with
-// it took 0.24 us a launch).
-__device__ __forceinline__ void flag_rows_past(const MxTables &t, int lane, int32_t *err) {
-    if (!err) return;
-    bool past = false;
-    for (int g = static_cast<int>(blockIdx.x) * 32 + lane; g < t.E; g += static_cast<int>(gridDim.x) * 32) {
-        const int size = t.sizes[g], first = t.offsets[g];
-        past |= (size > 0) & (rows_there(t, size, first) < size);
-    }
-    if (past) atomicExch(err, kErrDeviceFlag);
-}
-
 // Rows of M block bx of the dispatch tables: expert, first row, count.  Units of
 // ROWS rows: every block, or every other one of an expert with the block behind it.
 // A block's end may pass 32 bits, its rows' offsets do not.

@@ -135,6 +135,21 @@ __device__ __forceinline__ void mg_drain(uint32_t bar, uint32_t parity) {
         if (global_timer_ns() - start > kWaitTimeoutNs) return;
 }
 
+// Whether the blocks name rows past the call's, into the error word; by a warp of each
+// CTA that has nothing else left to do.  By blocks: weights may have more experts than
+// the tables have entries, as long as no block is one's.
+__device__ __forceinline__ void mg_flag_rows_past(const MxTables &t, int m_blocks, int lane, int32_t *err) {
+    if (!err) return;
+    bool past = false;
+    for (int bx = static_cast<int>(blockIdx.x) * 32 + lane; bx < m_blocks; bx += static_cast<int>(gridDim.x) * 32) {
+        const int g = static_cast<int>(min(static_cast<unsigned>(t.gidx[bx]), static_cast<unsigned>(t.E - 1)));
+        const int off = static_cast<int>(static_cast<uint32_t>(bx) * 128u - static_cast<uint32_t>(t.padded[g]));
+        const int named = min(t.sizes[g] - off, 128);
+        past |= (named > 0) & (rows_there(t, named, off + t.offsets[g]) < named);
+    }
+    if (past) atomicExch(err, kErrDeviceFlag);
+}
+
 // 8 scale bytes from byte `at` on of a row of kb of them (null: zeros); bytes
 // past kb are 0 (their elements are zeros too).  V: the load width that kb and
 // the bases' alignment allow.
@@ -354,7 +369,7 @@ __global__ void __launch_bounds__(MG_THREADS, 1)
             }
         }
         __syncwarp();
-        flag_rows_past(p.tab, lane, p.err);
+        mg_flag_rows_past(p.tab, p.m_blocks, lane, p.err);
     } else if (warp == 1) {
         // ------------------------------ MMA issuer ------------------------------
         constexpr uint32_t IDESC = idesc_mxf4(MG_BM, BN);

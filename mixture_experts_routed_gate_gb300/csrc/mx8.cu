@@ -6,8 +6,9 @@
 //
 // All three are bound by the bytes they move.  4096 x 7168: from bf16 14.8 us (90 MB,
 // 13.2 at the copy rate), from fp32 22.7 (148 MB, 21.8); to bf16 11.4 (13.1; part of the
-// result stays in L2), to fp32 32.5 (21.8); sorted for 8 experts a token 42 us (273 MB, 40; the stores wait in the queue to L1), 64 tokens of 2048
-// for 6 experts 2.1 us, a launch.
+// result stays in L2), to fp32 32.5 (21.8); sorted for 8 experts a token 42 us (273 MB,
+// 40; the stores wait in the queue to L1), 64 tokens of 2048 for 6 experts 2.1 us, a
+// launch.
 #include "common.cuh"
 #include "internal.h"
 #include "mx8.cuh"

@@ -137,3 +137,20 @@ def test_more_units_than_a_list_holds_and_experts_without_rows(form):
     left = torch.zeros(n, dtype=torch.bool, device="cuda")
     left.view(E, 2)[gone.cuda()] = True
     assert torch.equal(*out) and (out[0][left] == -1000.5).all() and not (out[0][~left] == -1000.5).any()
+
+
+def test_tables_of_fewer_experts_than_the_weights():
+    """4-bit rows whose tables have no entry for the last experts, which no block names: what lies behind the
+    tables (here entries that would name rows past the call's) is not looked at."""
+    require_cuda()
+    g = torch.Generator(device="cuda").manual_seed(4)
+    E, more, K, N, n = 3, 40, 64, 64, 40
+    a, b = Four.quantize(torch.randn((n, K), generator=g, device="cuda")), Four.quantize(torch.randn(((E + more) * N, K), generator=g, device="cuda"))
+    b = [x.view(E + more, N, -1) for x in b]
+    behind = [2 ** 30] * more
+    t = dict(group_sizes=[20, 0, 20], group_offsets=[0, 20, 20], group_padded_offsets=[0, 128, 256], group_idx_for_bx=[0, 1, 2, 2])
+    t = {name: torch.tensor(v + behind, dtype=torch.int32, device="cuda")[:len(v)] for name, v in t.items()}
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = Four.product(*a, *b, t, torch.float32, err=err)
+    assert int(err.item()) == 0
+    assert torch.equal(got, Four.product(*a, *(x[:E].contiguous() for x in b), t, torch.float32))
